@@ -623,6 +623,185 @@ int zero_grad_norm_noalloc(const void* const* grads, int M, const int64_t* bucke
 double zero_state_bytes_per_param(int stage, int M, double param_bytes, double grad_bytes,
                                   double optim_bytes);
 
+/* ---- Training losses and gradient clipping ---------------------------------------------
+ * What stands directly before an optimizer step of a language model, as calls of their own:
+ * the log-probability of given tokens (from logits, or from hidden states and the vocabulary
+ * matrix without any logits in memory), a preference loss or a clipped policy loss with its
+ * gradient on the logits, and the global norm and clipping of gradients that are still
+ * separate tensors, written in place or into the flat gradient buffer of a step. The pages
+ * define none of these; they start where the gradients exist.
+ *
+ * Shared by these calls:
+ *  - Memory, streams, device and errors as at the top of this file: nothing is allocated, work
+ *    is enqueued on `stream` and the call returns; every pointer is device memory of one GPU
+ *    (or managed memory), which the call finds from its first buffer and makes current; a
+ *    pointer elsewhere, or a stream of another GPU, returns INVALID_ARG before anything is
+ *    enqueued. The calls only launch kernels, so they can be captured in a CUDA graph.
+ *  - Logits of token t are the row z_t = x_t / temperature, x_t[j] at logits[t * stride + j].
+ *    Rows may have any alignment that their element type has: an odd vocabulary is as good as
+ *    a padded one. Elements past `vocab` in a row are never read nor written.
+ *  - A target below 0 marks a token without a loss (a prompt token, padding): its row is not
+ *    read, its results are 0 and its gradient row is written as zeros. A target >= vocab is
+ *    not followed: that token's log-probability and gradient row are NaN.
+ *  - A logit of -inf has probability 0 and gradient -0 or 0. A row of -inf alone has lse = -inf,
+ *    logp = -inf, entropy 0 and gradient 0. NaN or +inf in a row makes its results NaN.
+ *  - All sums are kept in fp32 or fp64 and in a fixed order: equal calls give equal bits. */
+#define ZERO_T_BF16 0
+#define ZERO_T_FP16 1
+#define ZERO_T_FP32 2
+
+/* Rows of logits and the token that each is asked about. */
+typedef struct {
+    const void* logits;      /* device [rows, vocab] of `type`, aligned to the element size   */
+    const int64_t* targets;  /* device [rows]                                                 */
+    int64_t rows;            /* >= 0; 0 rows is a valid, empty call                           */
+    int64_t vocab;           /* 1 .. 2^31 - 1                                                 */
+    int64_t stride;          /* elements from one row to the next, >= vocab                   */
+    int32_t type;            /* ZERO_T_*                                                      */
+    double temperature;      /* > 0, finite                                                   */
+} zero_logits;
+
+/* logp[t] = z_t[y] - lse_t, lse_t = log sum_j exp(z_t[j]) and, where `entropy` is not NULL,
+ * entropy[t] = -sum_j p_j log p_j: fp32 [rows] each. Reads each row once.
+ * Errors: INVALID_ARG, MISALIGNED, CUDA. */
+int zero_token_logp(const zero_logits* x, float* logp, float* lse, float* entropy, void* stream);
+
+/* The gradient of a function of logp and entropy on the logits:
+ *   dlogits[t, j] = (dlogp[t] ([j = y_t] - p_j) - dentropy[t] p_j (log p_j + entropy[t])) / temperature
+ * rounded once to x->type. logp, lse (and, with dentropy, entropy) are what zero_token_logp gave
+ * for the same x; dentropy NULL: 0. dlogits: device [rows, vocab] of x->type, rows dstride elements
+ * apart (>= vocab); it may be x->logits itself with dstride = stride (in place). A row whose two
+ * coefficients are 0 is written as zeros and not read.
+ * Errors: INVALID_ARG (also: dentropy without entropy), MISALIGNED, CUDA. */
+int zero_token_logp_backward(const zero_logits* x, const float* logp, const float* lse,
+                             const float* entropy, const float* dlogp, const float* dentropy,
+                             void* dlogits, int64_t dstride, void* stream);
+
+/* Preference loss (paired log ratios). Tokens are packed; sequence s is tokens
+ * [offsets[s], offsets[s + 1]), and pair i is sequence 2i (chosen) against 2i + 1 (rejected).
+ *   d_s = sum over the sequence's tokens with a target of (logp_t - ref_logp[t]), divided by
+ *         their number where `average` is 1;  m_i = d_2i - d_2i+1
+ *   ZERO_PREF_SIGMOID  -(1 - e) log sigmoid(beta m) - e log sigmoid(-beta m), e = label_smoothing
+ *   ZERO_PREF_HINGE    max(0, 1 - beta m)          ZERO_PREF_IPO  (m - 1 / (2 beta))^2
+ * loss = the mean over pairs. */
+#define ZERO_PREF_SIGMOID 0
+#define ZERO_PREF_HINGE   1
+#define ZERO_PREF_IPO     2
+typedef struct {
+    const int64_t* offsets;  /* device [2 * pairs + 1], not decreasing, within [0, rows]      */
+    const float* ref_logp;   /* device [rows]; NULL: 0                                        */
+    int64_t pairs;           /* >= 1                                                          */
+    double beta;             /* > 0                                                           */
+    double label_smoothing;  /* in [0, 0.5], sigmoid only                                     */
+    int32_t kind;            /* ZERO_PREF_*                                                   */
+    int32_t average;         /* 1: divide each sequence's sum by its number of targets        */
+    /* results, device */
+    float* loss;             /* [1]                                                           */
+    float* pair_loss;        /* [pairs]                                                       */
+    float* chosen_reward;    /* [pairs] beta d_2i                                             */
+    float* rejected_reward;  /* [pairs] beta d_2i+1                                           */
+    float* logp;             /* [rows]                                                        */
+    void* dlogits;           /* [rows, vocab] of the logits' type: the gradient of loss; may be
+                                the logits (dstride = stride). Tokens of no pair: zeros       */
+    int64_t dstride;
+} zero_preference;
+/* Bytes of workspace for `rows` tokens (16-byte aligned device memory, contents free before and
+ * after the call); negative for a negative count. Host only. */
+int64_t zero_preference_workspace(int64_t rows);
+int zero_preference_loss(const zero_logits* x, const zero_preference* p, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/* Clipped policy loss with a KL term and an entropy bonus. Per token with a target, with
+ * r = exp(logp - old_logp) and A its advantage:
+ *   L = max(-r A, -clamp(r, 1 - clip_low, 1 + clip_high) A), and for A < 0 with dual_clip > 0
+ *       at most -dual_clip A;  L += kl_coef KL - entropy_coef entropy
+ *   KL, with d = ref_logp - logp: ZERO_KL_K1 -d, ZERO_KL_K2 d^2 / 2, ZERO_KL_K3 exp(d) - d - 1
+ * loss = sum of w_t L_t: w = 1 / (number of targets) (ZERO_REDUCE_TOKEN), 1 / (targets of the
+ * token's sequence x sequences that have any) (ZERO_REDUCE_SEQUENCE), or 1 (ZERO_REDUCE_SUM).
+ * The gradient follows r inside and on the clip's edges and is 0 past them; old_logp, ref_logp
+ * and the advantages are constants. */
+#define ZERO_KL_K1 0
+#define ZERO_KL_K2 1
+#define ZERO_KL_K3 2
+#define ZERO_REDUCE_TOKEN    0
+#define ZERO_REDUCE_SEQUENCE 1
+#define ZERO_REDUCE_SUM      2
+typedef struct {
+    const float* advantages;  /* device [rows], or [seqs] with per_sequence = 1               */
+    const float* old_logp;    /* device [rows]; NULL: the current logp (r = 1)                */
+    const float* ref_logp;    /* device [rows]; may be NULL when kl_coef = 0                  */
+    const int64_t* offsets;   /* device [seqs + 1] as for zero_preference; NULL: no sequences
+                                 (then reduce is not SEQUENCE and per_sequence is 0). Tokens
+                                 of no sequence carry no loss                                 */
+    int64_t seqs;             /* >= 0; ignored without offsets                                */
+    double clip_low, clip_high;  /* in [0, 1], >= 0                                           */
+    double dual_clip;         /* 0 (off) or > 1                                               */
+    double kl_coef, entropy_coef;  /* finite                                                  */
+    int32_t kl;               /* ZERO_KL_*                                                    */
+    int32_t reduce;           /* ZERO_REDUCE_*                                                */
+    int32_t per_sequence;     /* 1: one advantage per sequence                                */
+    /* results, device */
+    float* loss;              /* [1]                                                          */
+    float* clip_fraction;     /* [1] share of the targets whose ratio was clipped             */
+    float* kl_mean;           /* [1] mean KL over the targets; 0 without ref_logp             */
+    float* logp;              /* [rows]                                                       */
+    float* entropy;           /* [rows]; may be NULL when entropy_coef = 0                    */
+    void* dlogits;            /* [rows, vocab] as for zero_preference                         */
+    int64_t dstride;
+} zero_policy;
+int64_t zero_policy_workspace(int64_t rows);
+int zero_policy_loss(const zero_logits* x, const zero_policy* p, void* workspace,
+                     int64_t workspace_bytes, void* stream);
+
+/* Token log-probabilities straight from the last hidden states and the vocabulary matrix:
+ * logits[t, j] = sum_k hidden[t, k] weight[j, k], summed in fp32 and never written to memory;
+ * results as zero_token_logp's. For the frozen sides of the losses above (ref_logp, old_logp),
+ * which need no gradient.
+ *  hidden  device [rows, dim], rows ld_hidden elements apart, of `type` (BF16 or FP16)
+ *  weight  device [vocab, dim], rows ld_weight elements apart, of the same type
+ * Both 16-byte aligned with leading dimensions that are multiples of 8, >= dim >= 1.
+ * Errors: INVALID_ARG, MISALIGNED, SIZE_MISMATCH (workspace too small), CUDA. */
+typedef struct {
+    const void* hidden;
+    const void* weight;
+    const int64_t* targets;  /* device [rows]                                                 */
+    int64_t rows, vocab, dim, ld_hidden, ld_weight;
+    int32_t type;
+    double temperature;
+} zero_linear;
+int64_t zero_linear_logp_workspace(int64_t rows, int64_t vocab);
+int zero_linear_logp(const zero_linear* x, float* logp, float* lse, float* entropy, void* workspace,
+                     int64_t workspace_bytes, void* stream);
+
+/* Global L2 norm over many separate tensors, and clipping:
+ *   norm = sqrt(sum over all tensors of all squares), scale = max_norm / norm where norm >
+ *   max_norm, else 1 (also when the norm is not finite: the values then pass unchanged, and a
+ *   clipped step on them skips itself); dst_i = src_i * scale, rounded once to dst's type.
+ * A plan holds the list of tensors; it borrows them and its workspace like a context.
+ * src and dst may have different types; dst = src (same type) is in place, and then nothing is
+ * written when scale is 1. A dst must not overlap any src but its own. dst NULL: norm only. */
+typedef struct {
+    const void* src;    /* device, contiguous, aligned to its element size                    */
+    void* dst;          /* device, contiguous, aligned to its element size; or NULL           */
+    int64_t numel;      /* >= 0                                                               */
+    int32_t src_type;   /* ZERO_T_*                                                           */
+    int32_t dst_type;   /* ZERO_T_*                                                           */
+} zero_grad_tensor;
+typedef struct zero_grads zero_grads; /* opaque, library-owned */
+/* Bytes of workspace of a plan over n tensors; negative for n < 1. Host only. */
+int64_t zero_grads_workspace(int64_t n);
+/* Checks the list and uploads its table; waits for `stream` (as zero_init). The device is that
+ * of `workspace`. Errors: INVALID_ARG, MISALIGNED, SIZE_MISMATCH, CUDA; *out is NULL then. */
+int zero_grads_init(zero_grads** out, const zero_grad_tensor* tensors, int64_t n, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+/* max_norm > 0 (may be infinite: no clipping). norm, scale: device fp32 [1]; tensor_norms: device
+ * fp32 [n] or NULL. Asynchronous on `stream`; calls of one plan must be ordered (they share its
+ * workspace). Errors: BAD_CONTEXT, INVALID_ARG, MISALIGNED, CUDA. */
+int zero_grads_clip(zero_grads* plan, double max_norm, float* norm, float* scale, float* tensor_norms,
+                    void* stream);
+/* Releases the plan (not the caller's buffers). Waits for nothing. */
+int zero_grads_destroy(zero_grads* plan);
+
 #ifdef __cplusplus
 }
 #endif

@@ -137,6 +137,18 @@ SIGNATURES = {
     "zero_rank_partial_bucket": (ctypes.c_int, [_P, ctypes.c_int64, _P, _P, _P]),
     "zero_rank_step_bucket": (ctypes.c_int, [_P, _I64, _P, ctypes.c_int, ctypes.POINTER(Hyper), _P]),
     "zero_rank_reduce_bucket": (ctypes.c_int, [_P, _I64, _P, _P]),
+    "zero_token_logp": (ctypes.c_int, [_P] * 5),
+    "zero_token_logp_backward": (ctypes.c_int, [_P] * 7 + [_I64, _P]),
+    "zero_preference_workspace": (_I64, [_I64]),
+    "zero_preference_loss": (ctypes.c_int, [_P, _P, _P, _I64, _P]),
+    "zero_policy_workspace": (_I64, [_I64]),
+    "zero_policy_loss": (ctypes.c_int, [_P, _P, _P, _I64, _P]),
+    "zero_linear_logp_workspace": (_I64, [_I64, _I64]),
+    "zero_linear_logp": (ctypes.c_int, [_P] * 5 + [_I64, _P]),
+    "zero_grads_workspace": (_I64, [_I64]),
+    "zero_grads_init": (ctypes.c_int, [ctypes.POINTER(_P), _P, _I64, _P, _I64, _P]),
+    "zero_grads_clip": (ctypes.c_int, [_P, ctypes.c_double, _P, _P, _P, _P]),
+    "zero_grads_destroy": (ctypes.c_int, [_P]),
 }
 
 
@@ -609,3 +621,8 @@ class ZeroOptimizer:
 
 # process-per-rank mode (one process per GPU); imported last: it builds on the names above
 from .sharded import ShardedZeroOptimizer  # noqa: E402
+
+# training losses and gradient clipping: what stands before the step
+from .gradclip import Clipped, GradClip  # noqa: E402
+from .losses import (PolicyLoss, PreferenceLoss, TokenLogp, linear_logp, policy_loss, preference_loss,  # noqa: E402
+                     token_logp, token_logp_backward)

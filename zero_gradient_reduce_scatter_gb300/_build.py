@@ -1,6 +1,6 @@
 """Compiles the C-ABI library libzero_gb300.so (CUDA kernels + host API) for sm_103a.
 
-Two translation units are compiled in parallel with nvcc and linked into
+The translation units are compiled in parallel with nvcc and linked into
 zero_gradient_reduce_scatter_gb300/_build/libzero_gb300.so (in-tree, git-ignored). The CUDA
 runtime is linked as a shared library so that a process that also uses PyTorch runs a
 single runtime instance (same soname).
@@ -21,7 +21,8 @@ LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 # The bounds-checked variant (every kernel index tested before use; for tests).
 CHECKED_LIB_PATH = os.path.join(BUILD_DIR, "libzero_gb300_checked.so")
 
-SOURCES = ["zero_kernels.cu", "zero_api.cpp", "zero_noalloc.cu"]
+SOURCES = ["zero_kernels.cu", "zero_api.cpp", "zero_noalloc.cu", "zero_logits.cu", "zero_linear.cu", "zero_grads.cu"]
+HEADERS = ["zero_internal.h", "zero_host.h", "zero_softmax.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -38,7 +39,8 @@ def _cuda_lib_dir(nvcc: str) -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
-    files += [os.path.join(CSRC, "zero_internal.h"), os.path.join(INCLUDE, "zero_gb300.h"), __file__]
+    files += [os.path.join(CSRC, h) for h in HEADERS]
+    files += [os.path.join(INCLUDE, "zero_gb300.h"), __file__]
     return files
 
 

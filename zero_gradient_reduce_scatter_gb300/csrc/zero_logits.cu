@@ -1,0 +1,589 @@
+// zero_logits.cu -- token log-probabilities over a vocabulary and their gradient, and the
+// preference and policy losses on them, for sm_103a.
+//
+// All of it is bound by reading and writing [rows, vocab] logits; the arithmetic on them is a
+// softmax, so every row is read with its maximum and sums carried along (zero_softmax.cuh).
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "zero_host.h"
+#include "zero_softmax.cuh"
+
+namespace zg {
+namespace {
+
+constexpr int kRowThreads = 256;
+
+// Logits as the kernels take them.
+template <class T>
+struct Rows {
+    const T* x;
+    const int64_t* targets;
+    const float* weight;  // nullptr, or 0 for rows that carry no loss
+    int64_t rows, vocab, stride;
+    float c, inv_t;       // log2(e) / temperature, 1 / temperature
+};
+
+template <class T>
+__device__ __forceinline__ int64_t live_target(const Rows<T>& a, int64_t t) {
+    return a.weight && a.weight[t] == 0.0f ? -1 : a.targets[t];
+}
+
+// The sums of one row, read by a whole CTA.
+template <class T, bool ENTROPY>
+__device__ __forceinline__ RowStat read_row(const T* x, int64_t n, float c) {
+    RowStat a = empty_stat();
+    for (int64_t j = threadIdx.x; j < n; j += kRowThreads) {
+        const float v = widen(x[j]), m = fmaxf(a.m, v), base = base_of(m);
+        rebase<ENTROPY>(a, base, c);
+        a.m = m;
+        add_term<ENTROPY>(a, v, c, base);
+    }
+    return a;
+}
+
+template <class T, bool ENTROPY>
+__global__ void __launch_bounds__(kRowThreads) k_token_logp(const Rows<T> a, float* logp, float* lse, float* entropy) {
+    __shared__ RowStat sm[kRowThreads / 32];
+    for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
+        const int64_t y = live_target(a, t);
+        RowResult r = {0.0f, 0.0f, 0.0f};
+        if (y >= 0) {
+            const T* x = a.x + t * a.stride;
+            const RowStat s = cta_join<ENTROPY, kRowThreads>(read_row<T, ENTROPY>(x, a.vocab, a.c), a.c, sm);
+            r = finish_row(s, y < a.vocab ? widen(x[y]) : NAN, a.inv_t);
+            if (y >= a.vocab) r.logp = NAN;
+        }
+        if (threadIdx.x == 0) {
+            logp[t] = r.logp;
+            if (lse) lse[t] = r.lse;
+            if (ENTROPY) entropy[t] = r.entropy;
+        }
+    }
+}
+
+// dx_j = g [j = y] - 2^d_j (ka + kb d_j), d_j = log2 p_j = (x_j - base) c - off.
+// log p is rebuilt from whichever is the smaller number and so the more exact in fp32: the
+// target's log-probability (base = its logit) or lse.
+struct GradRow {
+    float g, ka, kb, base, off;
+};
+
+__device__ __forceinline__ GradRow grad_row(float g, float h, float x_y, float logp, float lse, float entropy, float inv_t) {
+    GradRow r;
+    if (fabsf(logp) <= fabsf(lse)) {
+        r.base = x_y;
+        r.off = -logp * kLog2e;
+    } else {
+        r.base = lse / inv_t;
+        r.off = (float)(((double)lse - (double)r.base * (double)inv_t) * 1.4426950408889634);
+    }
+    r.g = g * inv_t;
+    r.ka = inv_t * (h == 0.0f ? g : fmaf(h, entropy, g));
+    r.kb = inv_t * h * kLn2;
+    return r;
+}
+
+__device__ __forceinline__ float grad_term(const GradRow& r, float x, float c) {
+    const float d = fmaf(x - r.base, c, -r.off);
+    return -pow2(d) * fmaf(r.kb, fmaxf(d, kFar), r.ka);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kRowThreads)
+    k_token_grad(const Rows<T> a, const float* logp, const float* lse, const float* entropy, const float* dlogp,
+                 const float* dentropy, T* dx, int64_t dstride) {
+    for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
+        const int64_t y = live_target(a, t);
+        const float g = y < 0 ? 0.0f : dlogp[t], h = y < 0 || !dentropy ? 0.0f : dentropy[t];
+        T* out = dx + t * dstride;
+        if ((g == 0.0f && h == 0.0f) || lse[t] == -INFINITY) {
+            for (int64_t j = threadIdx.x; j < a.vocab; j += kRowThreads) out[j] = narrow<T>(0.0f);
+            continue;
+        }
+        const T* x = a.x + t * a.stride;
+        const GradRow r = grad_row(y < a.vocab ? g : NAN, h, y < a.vocab ? widen(x[y]) : NAN, logp[t], lse[t],
+                                   h != 0.0f ? entropy[t] : 0.0f, a.inv_t);
+        if (out == x) __syncthreads();  // the target's logit is read before any thread writes it
+        for (int64_t j = threadIdx.x; j < a.vocab; j += kRowThreads)
+            out[j] = narrow<T>(grad_term(r, widen(x[j]), a.c) + (j == y ? r.g : 0.0f));
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// Sums over a CTA in fp64, in a fixed order; valid in thread 0.
+// ---------------------------------------------------------------------------------------
+template <int THREADS>
+__device__ __forceinline__ double cta_sum(double x, double* sm) {
+    sm[threadIdx.x] = x;
+    __syncthreads();
+    for (int h = THREADS / 2; h > 0; h >>= 1) {
+        if (threadIdx.x < h) sm[threadIdx.x] += sm[threadIdx.x + h];
+        __syncthreads();
+    }
+    const double r = sm[0];
+    __syncthreads();
+    return r;
+}
+
+__device__ __forceinline__ int64_t clamp_offset(int64_t o, int64_t lo, int64_t hi) {
+    return o < lo ? lo : (o > hi ? hi : o);
+}
+
+// ---------------------------------------------------------------------------------------
+// Preference loss: one CTA per pair sums its two sequences and spreads the gradient over their
+// tokens. g holds 0 for the tokens of no pair (written before).
+// ---------------------------------------------------------------------------------------
+struct PairArgs {
+    const int64_t* targets;
+    const int64_t* offsets;
+    const float* logp;
+    const float* ref;
+    float* g;
+    float *pair_loss, *chosen, *rejected;
+    int64_t rows, pairs;
+    double beta, smoothing;
+    int32_t kind, average;
+};
+
+// log(1 + e^x) without overflow
+__device__ __forceinline__ double softplus(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
+
+__global__ void __launch_bounds__(kRowThreads) k_pairs(const PairArgs a) {
+    __shared__ double sm[kRowThreads];
+    __shared__ float g_side[2];
+    for (int64_t i = blockIdx.x; i < a.pairs; i += gridDim.x) {
+        int64_t lo[2], hi[2];
+        double d[2], n[2];
+        for (int k = 0; k < 2; ++k) {
+            lo[k] = clamp_offset(a.offsets[2 * i + k], 0, a.rows);
+            hi[k] = clamp_offset(a.offsets[2 * i + k + 1], lo[k], a.rows);
+            double sum = 0.0, count = 0.0;
+            for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kRowThreads) {
+                if (a.targets[t] < 0) continue;
+                sum += (double)a.logp[t] - (a.ref ? (double)a.ref[t] : 0.0);
+                count += 1.0;
+            }
+            d[k] = cta_sum<kRowThreads>(sum, sm);
+            n[k] = a.average ? fmax(cta_sum<kRowThreads>(count, sm), 1.0) : 1.0;
+            d[k] /= n[k];
+        }
+        if (threadIdx.x == 0) {
+            const double m = d[0] - d[1], b = a.beta, e = a.smoothing;
+            double loss, dm;
+            if (a.kind == ZERO_PREF_SIGMOID) {
+                loss = (1.0 - e) * softplus(-b * m) + e * softplus(b * m);
+                // sigmoid(s) - (1 - e), each half formed without cancellation
+                dm = b * (e / (1.0 + exp(-b * m)) - (1.0 - e) / (1.0 + exp(b * m)));
+            } else if (a.kind == ZERO_PREF_HINGE) {
+                const double gap = 1.0 - b * m;
+                loss = gap > 0.0 || gap != gap ? gap : 0.0;
+                dm = gap > 0.0 ? -b : gap * 0.0;
+            } else {
+                const double gap = m - 0.5 / b;
+                loss = gap * gap;
+                dm = 2.0 * gap;
+            }
+            a.pair_loss[i] = (float)loss;
+            a.chosen[i] = (float)(b * d[0]);
+            a.rejected[i] = (float)(b * d[1]);
+            g_side[0] = (float)(dm / n[0] / (double)a.pairs);
+            g_side[1] = (float)(-dm / n[1] / (double)a.pairs);
+        }
+        __syncthreads();
+        for (int k = 0; k < 2; ++k)
+            for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kRowThreads) a.g[t] = g_side[k];
+        __syncthreads();
+    }
+}
+
+__global__ void __launch_bounds__(1024) k_mean(const float* x, int64_t n, float* out) {
+    __shared__ double sm[1024];
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += 1024) s += (double)x[i];
+    s = cta_sum<1024>(s, sm);
+    if (threadIdx.x == 0) *out = (float)(s / (double)n);
+}
+
+__global__ void __launch_bounds__(kRowThreads) k_zero(float* x, int64_t n) {
+    for (int64_t i = blockIdx.x * (int64_t)kRowThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kRowThreads) x[i] = 0.0f;
+}
+
+// ---------------------------------------------------------------------------------------
+// Policy loss.
+// ---------------------------------------------------------------------------------------
+// What a token's loss needs beside its row: its weight (0: no loss) and its advantage.
+struct PolicyTokens {
+    const int64_t* targets;
+    const int64_t* offsets;
+    const float* advantages;
+    const float *old_logp, *ref_logp;
+    float *w, *adv;              // [rows]
+    float *lse, *g, *h;          // [rows]
+    float *loss, *kl, *clipped;  // [rows]
+    float *out_loss, *out_clip, *out_kl;
+    int64_t rows, seqs;
+    float lo, hi, dual, kl_coef, entropy_coef;
+    int32_t kl_kind, reduce, per_sequence;
+};
+
+constexpr int kSetupThreads = 1024;
+
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    return x;
+}
+
+// Weights and advantages of all tokens, by one CTA: a warp per sequence counts, then spreads.
+__global__ void __launch_bounds__(kSetupThreads) k_policy_setup(const PolicyTokens a) {
+    __shared__ unsigned long long total, nonempty;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = kSetupThreads / 32;
+    if (threadIdx.x == 0) total = nonempty = 0;
+    __syncthreads();
+    for (int64_t t = threadIdx.x; t < a.rows; t += kSetupThreads) a.w[t] = 0.0f;
+    if (a.offsets) {
+        for (int64_t s = warp; s < a.seqs; s += warps) {
+            const int64_t b = clamp_offset(a.offsets[s], 0, a.rows), e = clamp_offset(a.offsets[s + 1], b, a.rows);
+            int64_t n = 0;
+            for (int64_t t = b + lane; t < e; t += 32) n += a.targets[t] >= 0;
+            n = warp_sum(n);
+            if (lane == 0 && n) {
+                atomicAdd(&total, (unsigned long long)n);
+                atomicAdd(&nonempty, 1ull);
+            }
+        }
+    } else {
+        int64_t n = 0;
+        for (int64_t t = threadIdx.x; t < a.rows; t += kSetupThreads) n += a.targets[t] >= 0;
+        n = warp_sum(n);
+        if (lane == 0) atomicAdd(&total, (unsigned long long)n);
+    }
+    __syncthreads();
+    const float tokens = (float)(total ? total : 1), filled = (float)(nonempty ? nonempty : 1);
+    if (!a.offsets) {
+        const float w = a.reduce == ZERO_REDUCE_TOKEN ? 1.0f / tokens : 1.0f;
+        for (int64_t t = threadIdx.x; t < a.rows; t += kSetupThreads) {
+            a.w[t] = a.targets[t] >= 0 ? w : 0.0f;
+            a.adv[t] = a.advantages[t];
+        }
+        return;
+    }
+    for (int64_t s = warp; s < a.seqs; s += warps) {
+        const int64_t b = clamp_offset(a.offsets[s], 0, a.rows), e = clamp_offset(a.offsets[s + 1], b, a.rows);
+        float w = a.reduce == ZERO_REDUCE_TOKEN ? 1.0f / tokens : 1.0f;
+        if (a.reduce == ZERO_REDUCE_SEQUENCE) {
+            int64_t n = 0;
+            for (int64_t t = b + lane; t < e; t += 32) n += a.targets[t] >= 0;
+            n = warp_sum(n);
+            w = 1.0f / (float)(n ? n : 1) / filled;
+        }
+        for (int64_t t = b + lane; t < e; t += 32) {
+            a.w[t] = a.targets[t] >= 0 ? w : 0.0f;
+            a.adv[t] = a.advantages[a.per_sequence ? s : t];
+        }
+    }
+}
+
+struct TokenLoss {
+    float loss, kl, clipped, g, h;  // loss and the gradients on logp and entropy, weighted
+};
+
+__device__ __forceinline__ TokenLoss policy_token(const PolicyTokens& a, int64_t t, float w, float logp, float entropy) {
+    TokenLoss r;
+    const float A = a.adv[t], ratio = a.old_logp ? expf(logp - a.old_logp[t]) : expf(logp - logp);
+    const float plain = -ratio * A, clip = -fminf(fmaxf(ratio, a.lo), a.hi) * A;
+    float loss = !(plain < clip) ? plain : clip;  // a NaN stays
+    bool off = (A > 0.0f && ratio > a.hi) || (A < 0.0f && ratio < a.lo);
+    if (a.dual > 0.0f && A < 0.0f && ratio > a.dual) {
+        off = true;
+        loss = -a.dual * A;
+    }
+    float g = off ? 0.0f : plain;
+    r.kl = 0.0f;
+    if (a.ref_logp) {
+        const float d = a.ref_logp[t] - logp;
+        float dkl;
+        if (a.kl_kind == ZERO_KL_K1) {
+            r.kl = -d;
+            dkl = 1.0f;
+        } else if (a.kl_kind == ZERO_KL_K2) {
+            r.kl = 0.5f * d * d;
+            dkl = -d;
+        } else {
+            const float e = expm1f(d);
+            r.kl = e - d;
+            dkl = -e;
+        }
+        if (a.kl_coef != 0.0f) {
+            loss = fmaf(a.kl_coef, r.kl, loss);
+            g = fmaf(a.kl_coef, dkl, g);
+        }
+    }
+    if (a.entropy_coef != 0.0f) loss = fmaf(-a.entropy_coef, entropy, loss);
+    r.loss = loss * w;
+    r.clipped = off ? 1.0f : 0.0f;
+    r.g = g * w;
+    r.h = -a.entropy_coef * w;
+    return r;
+}
+
+__global__ void __launch_bounds__(kRowThreads) k_policy_tokens(const PolicyTokens a, const float* logp, const float* entropy) {
+    for (int64_t t = blockIdx.x * (int64_t)kRowThreads + threadIdx.x; t < a.rows; t += (int64_t)gridDim.x * kRowThreads) {
+        const float w = a.w[t];
+        TokenLoss r = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (w != 0.0f) r = policy_token(a, t, w, logp[t], entropy ? entropy[t] : 0.0f);
+        a.loss[t] = r.loss;
+        a.kl[t] = r.kl;
+        a.clipped[t] = r.clipped;
+        a.g[t] = r.g;
+        a.h[t] = r.h;
+    }
+}
+
+__global__ void __launch_bounds__(kSetupThreads) k_policy_finish(const PolicyTokens a) {
+    __shared__ double sm[kSetupThreads];
+    double loss = 0.0, kl = 0.0, clipped = 0.0, n = 0.0;
+    for (int64_t t = threadIdx.x; t < a.rows; t += kSetupThreads) {
+        loss += (double)a.loss[t];
+        kl += (double)a.kl[t];
+        clipped += (double)a.clipped[t];
+        n += a.w[t] != 0.0f ? 1.0 : 0.0;
+    }
+    loss = cta_sum<kSetupThreads>(loss, sm);
+    kl = cta_sum<kSetupThreads>(kl, sm);
+    clipped = cta_sum<kSetupThreads>(clipped, sm);
+    n = fmax(cta_sum<kSetupThreads>(n, sm), 1.0);
+    if (threadIdx.x == 0) {
+        *a.out_loss = (float)loss;
+        *a.out_kl = (float)(kl / n);
+        *a.out_clip = (float)(clipped / n);
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------------------
+int check_logits(const zero_logits* x) {
+    if (!x || x->rows < 0 || x->vocab < 1 || x->vocab > INT32_MAX || x->stride < x->vocab || !type_ok(x->type)) return ZERO_ERR_INVALID_ARG;
+    if (!(x->temperature > 0.0) || !std::isfinite(x->temperature)) return ZERO_ERR_INVALID_ARG;
+    if (x->rows > 0 && x->stride > INT64_MAX / 8 / x->rows) return ZERO_ERR_INVALID_ARG;
+    return ZERO_OK;
+}
+
+void need_logits(CallDevice& d, const zero_logits* x) {
+    d.need(x->logits, type_size(x->type));
+    d.need(x->targets, 8);
+}
+
+template <class T>
+Rows<T> rows_of(const zero_logits* x, const float* weight) {
+    Rows<T> a;
+    a.x = (const T*)x->logits;
+    a.targets = x->targets;
+    a.weight = weight;
+    a.rows = x->rows;
+    a.vocab = x->vocab;
+    a.stride = x->stride;
+    a.c = (float)(1.4426950408889634 / x->temperature);
+    a.inv_t = (float)(1.0 / x->temperature);
+    return a;
+}
+
+template <class F>
+int by_type(int32_t type, F f) {
+    if (type == ZERO_T_BF16) return f(__nv_bfloat16());
+    if (type == ZERO_T_FP16) return f(__half());
+    return f(float());
+}
+
+int row_grid(int64_t rows) { return (int)(rows < (1 << 20) ? rows : (1 << 20)); }
+
+int launch_token_logp(const zero_logits* x, const float* weight, float* logp, float* lse, float* entropy, cudaStream_t s) {
+    if (x->rows == 0) return ZERO_OK;
+    return by_type(x->type, [&](auto tag) {
+        using T = decltype(tag);
+        const Rows<T> a = rows_of<T>(x, weight);
+        if (entropy) k_token_logp<T, true><<<row_grid(x->rows), kRowThreads, 0, s>>>(a, logp, lse, entropy);
+        else k_token_logp<T, false><<<row_grid(x->rows), kRowThreads, 0, s>>>(a, logp, lse, entropy);
+        return launched();
+    });
+}
+
+int launch_token_grad(const zero_logits* x, const float* weight, const float* logp, const float* lse, const float* entropy,
+                      const float* g, const float* h, void* dx, int64_t dstride, cudaStream_t s) {
+    if (x->rows == 0) return ZERO_OK;
+    return by_type(x->type, [&](auto tag) {
+        using T = decltype(tag);
+        k_token_grad<T><<<row_grid(x->rows), kRowThreads, 0, s>>>(rows_of<T>(x, weight), logp, lse, entropy, g, h,
+                                                                  (T*)dx, dstride);
+        return launched();
+    });
+}
+
+int check_dlogits(const zero_logits* x, const void* dx, int64_t dstride) {
+    if (dstride < x->vocab || (x->rows > 0 && dstride > INT64_MAX / 8 / x->rows)) return ZERO_ERR_INVALID_ARG;
+    if (dx == x->logits && x->rows > 0 && dstride != x->stride) return ZERO_ERR_INVALID_ARG;
+    return ZERO_OK;
+}
+
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+}  // namespace
+}  // namespace zg
+
+using namespace zg;
+
+extern "C" int zero_token_logp(const zero_logits* x, float* logp, float* lse, float* entropy, void* stream) {
+    int rc = check_logits(x);
+    if (rc || x->rows == 0) return rc;
+    CallDevice d(x->logits, stream);
+    need_logits(d, x);
+    d.need(logp, 4);
+    d.need(lse, 4);
+    d.optional(entropy, 4);
+    if (d.rc) return d.rc;
+    return launch_token_logp(x, nullptr, logp, lse, entropy, (cudaStream_t)stream);
+}
+
+extern "C" int zero_token_logp_backward(const zero_logits* x, const float* logp, const float* lse, const float* entropy,
+                                        const float* dlogp, const float* dentropy, void* dlogits, int64_t dstride, void* stream) {
+    int rc = check_logits(x);
+    if (!rc) rc = check_dlogits(x, dlogits, dstride);
+    if (!rc && dentropy && !entropy) rc = ZERO_ERR_INVALID_ARG;
+    if (rc || x->rows == 0) return rc;
+    CallDevice d(x->logits, stream);
+    need_logits(d, x);
+    d.need(logp, 4);
+    d.need(lse, 4);
+    d.optional(entropy, 4);
+    d.need(dlogp, 4);
+    d.optional(dentropy, 4);
+    d.need(dlogits, type_size(x->type));
+    if (d.rc) return d.rc;
+    return launch_token_grad(x, nullptr, logp, lse, entropy, dlogp, dentropy, dlogits, dstride, (cudaStream_t)stream);
+}
+
+extern "C" int64_t zero_preference_workspace(int64_t rows) {
+    if (rows < 0 || rows > INT64_MAX / 64) return -1;
+    return 2 * 4 * round_up(rows, 4) + 64;
+}
+
+extern "C" int zero_preference_loss(const zero_logits* x, const zero_preference* p, void* workspace, int64_t workspace_bytes,
+                                    void* stream) {
+    int rc = check_logits(x);
+    if (!rc && (!p || p->pairs < 1 || p->pairs > INT32_MAX / 2 || !(p->beta > 0.0) || !std::isfinite(p->beta) ||
+                !(p->label_smoothing >= 0.0 && p->label_smoothing <= 0.5) || p->kind < ZERO_PREF_SIGMOID ||
+                p->kind > ZERO_PREF_IPO || p->average < 0 || p->average > 1))
+        rc = ZERO_ERR_INVALID_ARG;
+    if (!rc) rc = check_dlogits(x, p->dlogits, p->dstride);
+    if (rc) return rc;
+    if (workspace_bytes < zero_preference_workspace(x->rows)) return ZERO_ERR_SIZE_MISMATCH;
+    CallDevice d(p->loss, stream);
+    if (x->rows > 0) {
+        need_logits(d, x);
+        d.optional(p->ref_logp, 4);
+        d.need(p->logp, 4);
+        d.need(p->dlogits, type_size(x->type));
+    }
+    d.need(p->offsets, 8);
+    d.need(p->loss, 4);
+    d.need(p->pair_loss, 4);
+    d.need(p->chosen_reward, 4);
+    d.need(p->rejected_reward, 4);
+    d.need(workspace, 16);
+    if (d.rc) return d.rc;
+    cudaStream_t s = (cudaStream_t)stream;
+    float* lse = (float*)workspace;
+    float* g = lse + round_up(x->rows, 4);
+    if (x->rows > 0) {
+        k_zero<<<(int)std::min<int64_t>((x->rows + kRowThreads - 1) / kRowThreads, 1024), kRowThreads, 0, s>>>(g, x->rows);
+        if ((rc = launched())) return rc;
+    }
+    if ((rc = launch_token_logp(x, nullptr, p->logp, lse, nullptr, s))) return rc;
+    const PairArgs a = {x->targets, p->offsets, p->logp, p->ref_logp, g, p->pair_loss, p->chosen_reward, p->rejected_reward,
+                        x->rows, p->pairs, p->beta, p->kind == ZERO_PREF_SIGMOID ? p->label_smoothing : 0.0, p->kind, p->average};
+    k_pairs<<<(int)std::min<int64_t>(p->pairs, 1 << 20), kRowThreads, 0, s>>>(a);
+    if ((rc = launched())) return rc;
+    k_mean<<<1, 1024, 0, s>>>(p->pair_loss, p->pairs, p->loss);
+    if ((rc = launched())) return rc;
+    return launch_token_grad(x, nullptr, p->logp, lse, nullptr, g, nullptr, p->dlogits, p->dstride, s);
+}
+
+extern "C" int64_t zero_policy_workspace(int64_t rows) {
+    if (rows < 0 || rows > INT64_MAX / 64) return -1;
+    return 8 * 4 * round_up(rows, 4) + 64;
+}
+
+extern "C" int zero_policy_loss(const zero_logits* x, const zero_policy* p, void* workspace, int64_t workspace_bytes, void* stream) {
+    int rc = check_logits(x);
+    if (!rc && (!p || !(p->clip_low >= 0.0 && p->clip_low <= 1.0) || !(p->clip_high >= 0.0) || !std::isfinite(p->clip_high) ||
+                !(p->dual_clip == 0.0 || p->dual_clip > 1.0) || !std::isfinite(p->dual_clip) || !std::isfinite(p->kl_coef) ||
+                !std::isfinite(p->entropy_coef) || p->kl < ZERO_KL_K1 || p->kl > ZERO_KL_K3 || p->reduce < ZERO_REDUCE_TOKEN ||
+                p->reduce > ZERO_REDUCE_SUM || p->per_sequence < 0 || p->per_sequence > 1))
+        rc = ZERO_ERR_INVALID_ARG;
+    if (!rc && (p->offsets ? p->seqs < 0 : p->per_sequence || p->reduce == ZERO_REDUCE_SEQUENCE)) rc = ZERO_ERR_INVALID_ARG;
+    if (!rc && x->rows > 0 && ((p->kl_coef != 0.0 && !p->ref_logp) || (p->entropy_coef != 0.0 && !p->entropy))) rc = ZERO_ERR_INVALID_ARG;
+    if (!rc) rc = check_dlogits(x, p->dlogits, p->dstride);
+    if (rc) return rc;
+    if (workspace_bytes < zero_policy_workspace(x->rows)) return ZERO_ERR_SIZE_MISMATCH;
+    CallDevice d(p->loss, stream);
+    if (x->rows > 0) {
+        need_logits(d, x);
+        if (!p->per_sequence || p->seqs > 0) d.need(p->advantages, 4);
+        d.optional(p->old_logp, 4);
+        d.optional(p->ref_logp, 4);
+        d.need(p->logp, 4);
+        d.optional(p->entropy, 4);
+        d.need(p->dlogits, type_size(x->type));
+    }
+    d.optional(p->offsets, 8);
+    d.need(p->loss, 4);
+    d.need(p->clip_fraction, 4);
+    d.need(p->kl_mean, 4);
+    d.need(workspace, 16);
+    if (d.rc) return d.rc;
+    cudaStream_t s = (cudaStream_t)stream;
+    float* f = (float*)workspace;
+    const int64_t n = round_up(x->rows, 4);
+    PolicyTokens a;
+    a.targets = x->targets;
+    a.offsets = p->offsets;
+    a.advantages = p->advantages;
+    a.old_logp = p->old_logp;
+    a.ref_logp = p->ref_logp;
+    a.w = f;
+    a.adv = f + n;
+    a.lse = f + 2 * n;
+    a.g = f + 3 * n;
+    a.h = f + 4 * n;
+    a.loss = f + 5 * n;
+    a.kl = f + 6 * n;
+    a.clipped = f + 7 * n;
+    a.out_loss = p->loss;
+    a.out_clip = p->clip_fraction;
+    a.out_kl = p->kl_mean;
+    a.rows = x->rows;
+    a.seqs = p->seqs;
+    a.lo = (float)(1.0 - p->clip_low);
+    a.hi = (float)(1.0 + p->clip_high);
+    a.dual = (float)p->dual_clip;
+    a.kl_coef = (float)p->kl_coef;
+    a.entropy_coef = (float)p->entropy_coef;
+    a.kl_kind = p->kl;
+    a.reduce = p->reduce;
+    a.per_sequence = p->per_sequence;
+    if (x->rows > 0) {
+        k_policy_setup<<<1, kSetupThreads, 0, s>>>(a);
+        if ((rc = launched())) return rc;
+        if ((rc = launch_token_logp(x, a.w, p->logp, a.lse, p->entropy, s))) return rc;
+        k_policy_tokens<<<(int)std::min<int64_t>((x->rows + kRowThreads - 1) / kRowThreads, 1024), kRowThreads, 0, s>>>(a, p->logp, p->entropy);
+        if ((rc = launched())) return rc;
+        rc = launch_token_grad(x, a.w, p->logp, a.lse, p->entropy, a.g, a.entropy_coef != 0.0f ? a.h : nullptr, p->dlogits, p->dstride, s);
+        if (rc) return rc;
+    }
+    k_policy_finish<<<1, kSetupThreads, 0, s>>>(a);
+    return launched();
+}

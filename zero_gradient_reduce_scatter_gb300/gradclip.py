@@ -1,0 +1,92 @@
+"""Global norm and clipping of gradients that are still separate tensors.
+
+``ZeroOptimizer.step`` clips by the norm of the averaged gradient. ``GradClip`` serves the step
+before that: a rank's own gradients, as autograd leaves them (any mix of bfloat16, float16 and
+float32, any sizes), are measured and clipped in place or straight into the rank's flat bf16
+gradient buffer, with no host synchronisation.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+import torch
+
+from . import _check, _lib
+from .losses import TYPES, _handle, _on
+
+
+class GradTensor(ctypes.Structure):
+    """zero_grad_tensor."""
+
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("numel", ctypes.c_int64), ("src_type", ctypes.c_int32),
+                ("dst_type", ctypes.c_int32)]
+
+
+class Clipped(NamedTuple):
+    norm: torch.Tensor    # fp32, 0-dim: the norm before clipping
+    scale: torch.Tensor   # fp32, 0-dim
+    norms: torch.Tensor   # fp32 [n]: every tensor's own norm
+
+
+class GradClip:
+    """A plan over a fixed list of CUDA tensors; ``clip`` is one call on their current values.
+
+    grads: contiguous tensors of one device. dst: where the clipped values go, one tensor of the
+    same size each (any of the three types), or None for in place. The plan keeps references to
+    both. A dst tensor must not overlap any gradient but its own.
+    """
+
+    def __init__(self, grads, dst=None, stream=None):
+        self.grads = list(grads)
+        self.dst = self.grads if dst is None else list(dst)
+        if not self.grads:
+            raise ValueError("GradClip needs at least one tensor")
+        if len(self.dst) != len(self.grads):
+            raise ValueError(f"{len(self.grads)} gradients, {len(self.dst)} destinations")
+        dev = self.grads[0].device
+        for name, ts in (("grads", self.grads), ("dst", self.dst)):
+            for i, t in enumerate(ts):
+                if not (t.is_cuda and t.dtype in TYPES and t.is_contiguous() and t.device == dev and t.numel() == self.grads[i].numel()):
+                    raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor on {dev} in bfloat16, float16 or float32, "
+                                     "of its gradient's size")
+        self.device = dev
+        n = len(self.grads)
+        rows = (GradTensor * n)(*[GradTensor(g.data_ptr(), d.data_ptr(), g.numel(), TYPES[g.dtype], TYPES[d.dtype])
+                                  for g, d in zip(self.grads, self.dst)])
+        size = _lib().zero_grads_workspace(n)
+        with _on(stream):
+            self.workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        plan = ctypes.c_void_p()
+        _check(_lib().zero_grads_init(ctypes.byref(plan), ctypes.cast(rows, ctypes.c_void_p), n, self.workspace.data_ptr(),
+                                      size, _handle(stream, dev)), "zero_grads_init")
+        self._plan = plan
+
+    @classmethod
+    def into(cls, opt, grads, buf, stream=None):
+        """Clip into `buf`, a padded bf16 gradient buffer of the optimizer `opt` (one of
+        ``new_grad_buffers``), tensor i into its place; the padding lanes are not touched."""
+        if len(grads) != len(opt.numel):
+            raise ValueError(f"the optimizer has {len(opt.numel)} tensors, got {len(grads)}")
+        return cls(grads, [opt.tensor_view(buf, i) for i in range(len(opt.numel))], stream=stream)
+
+    def clip(self, max_norm: float, stream=None) -> Clipped:
+        """Measure, and write gradient * min(1, max_norm / norm). A norm that is not finite leaves
+        the values as they are (scale 1). max_norm may be infinite."""
+        with _on(stream):
+            r = torch.empty(2 + len(self.grads), dtype=torch.float32, device=self.device)
+        base = r.data_ptr()
+        _check(_lib().zero_grads_clip(self._plan, max_norm, base, base + 4, base + 8, _handle(stream, self.device)),
+               "zero_grads_clip")
+        return Clipped(r[0], r[1], r[2:])
+
+    def close(self):
+        if getattr(self, "_plan", None) is not None and self._plan.value:
+            _lib().zero_grads_destroy(self._plan)
+            self._plan = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
