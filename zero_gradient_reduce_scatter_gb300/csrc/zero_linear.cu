@@ -16,10 +16,14 @@
 namespace zg {
 namespace {
 
-constexpr int kRowsTile = 128;    // tokens of a tile: the lanes of TMEM
+constexpr int kRowsTile = 128;    // tokens of a CTA's tile: the lanes of TMEM
 constexpr int kDepth = 64;         // elements of the inner dimension per stage: 128 bytes
 constexpr int kEpilogueWarps = 8;  // two for each quarter of the lanes
-constexpr int kLinearThreads = 64 + 32 * kEpilogueWarps;
+constexpr int kLinearThreads = 128 + 32 * kEpilogueWarps;
+// 384 threads launch with 168 registers each, 64,512 in all: the first warpgroup gives back what
+// the two of the epilogue take (128 (56 + 2 x 224) = 64,512).
+constexpr int kFewRegisters = 56, kManyRegisters = 224;
+static_assert(128 * (kFewRegisters + 2 * kManyRegisters) <= kLinearThreads * 168, "the register split fits the launch");
 
 struct LinearArgs {
     const int64_t* targets;
@@ -27,8 +31,9 @@ struct LinearArgs {
     float* zy;         // [rows] the target's logit
     int32_t* tiles;    // [0]: how many row tiles hold a target, [1]: set when a wait gave up, [4...]: those tiles
     int64_t rows, vocab, dim;
-    int32_t row_tiles, col_tiles, group;
-    float c, inv_t;  // log2(e) / temperature, 1 / temperature
+    int32_t tile_rows, row_tiles, col_tiles, group;
+    Scale k;       // log2(e) / temperature
+    double inv_t;  // 1 / temperature
 };
 
 // Row tiles with at least one target, in order. One CTA.
@@ -42,8 +47,8 @@ __global__ void __launch_bounds__(1024) k_linear_tiles(const LinearArgs a) {
         const int32_t t = t0 + warp;
         bool any = false;
         if (t < a.row_tiles)
-            for (int i = lane; i < kRowsTile; i += 32) {
-                const int64_t r = (int64_t)t * kRowsTile + i;
+            for (int i = lane; i < a.tile_rows; i += 32) {
+                const int64_t r = (int64_t)t * a.tile_rows + i;
                 any |= r < a.rows && a.targets[r] >= 0;
             }
         any = __any_sync(~0u, any);
@@ -76,34 +81,43 @@ __device__ __forceinline__ void tile_of(const LinearArgs& a, int32_t live, int64
     *row = a.tiles[4 + first + (int32_t)(in % size)];
 }
 
-// 32 logits of one row into its sums.
-__device__ __forceinline__ void add32(RowStat& st, const float (&v)[32], float c) {
+// N logits of one row: their sums, in four chains.
+template <int N>
+__device__ __forceinline__ RowStat sum_of(const float (&v)[N], Scale k) {
     float m = v[0];
 #pragma unroll
-    for (int j = 1; j < 32; ++j) m = fmaxf(m, v[j]);
-    m = fmaxf(m, st.m);
+    for (int j = 1; j < N; ++j) m = fmaxf(m, v[j]);
     const float base = base_of(m);
-    rebase<true>(st, base, c);
-    st.m = m;
+    RowStat part[4];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) add_term<true>(st, v[j], c, base);
+    for (int i = 0; i < 4; ++i) part[i] = {m, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < N; ++j) add_term<true>(part[j & 3], v[j], k, base);
+    return {m, (part[0].s + part[1].s) + (part[2].s + part[3].s), (part[0].q + part[1].q) + (part[2].q + part[3].q)};
 }
 
-// One CTA per SM walks over tiles of 128 tokens by BN columns of the vocabulary. Warp 0 keeps
-// kStages pairs of operand tiles on their way by TMA, one thread of warp 1 issues the MMAs into
-// one of two accumulators in TMEM, and eight warps take the other's logits through the softmax
-// sums meanwhile, one row per thread, half of the columns per warpgroup.
-template <int BN>
+// One CTA per SM walks over tiles of 128 tokens by BN columns of the vocabulary, or (CG = 2) a
+// pair of CTAs over tiles of 256 by BN, each CTA loading its own tokens and half of the columns.
+// Warp 0 keeps kStages pairs of operand tiles on their way by TMA, one thread of warp 1 (of the
+// pair's first CTA) issues the MMAs into one of two accumulators in TMEM, and eight warps read the
+// other, one row per thread, half of the columns per warpgroup. The tensor core drops the low
+// bits of each sum it forms, always towards zero, so an accumulator takes kChunk stages (512
+// products) only; the epilogue adds the accumulators of a tile in registers, rounded to nearest,
+// and then forms the softmax sums while the next tile's products run.
+constexpr int kChunk = 8;
+
+template <int CG, int BN>
 struct LinearShape {
-    static constexpr int kA = kRowsTile * 128, kB = BN * 128, kStage = kA + kB;
+    static constexpr int kBRows = BN / CG;
+    static constexpr int kA = kRowsTile * 128, kB = kBRows * 128, kStage = kA + kB;
     static constexpr int kStages = 196608 / kStage;
     static constexpr int kSmem = kStages * kStage + 1024;
 };
 
-template <int TYPE, int BN>
+template <int TYPE, int CG, int BN>
 __global__ void __launch_bounds__(kLinearThreads, 1)
     k_linear_mma(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const LinearArgs a) {
-    using S = LinearShape<BN>;
+    using S = LinearShape<CG, BN>;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t bars[2 * S::kStages + 5];
     __shared__ uint32_t tmem_slot;
@@ -111,6 +125,7 @@ __global__ void __launch_bounds__(kLinearThreads, 1)
     const uint32_t tiles = (smem_addr(raw) + 1023) & ~1023u;
     const uint32_t full = smem_addr(bars), empty = full + 8 * S::kStages, acc_full = empty + 8 * S::kStages,
                    acc_empty = acc_full + 16, drained = acc_empty + 16;
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         gave_up = 0;
@@ -120,99 +135,126 @@ __global__ void __launch_bounds__(kLinearThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
-            mbar_init(acc_empty + 8 * i, kEpilogueWarps);
+            mbar_init(acc_empty + 8 * i, CG * kEpilogueWarps);
         }
         mbar_init(drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), 2 * BN);
+    if (warp == 1) tmem_alloc<CG>(smem_addr(&tmem_slot), 2 * BN);
     tcgen05_before_sync();
     __syncthreads();
+    if (CG == 2) cluster_sync();
     tcgen05_after_sync();
     const uint32_t tmem = tmem_slot;
     const int32_t live = a.tiles[0];
     const int64_t total = (int64_t)live * a.col_tiles;
     const int steps = (int)((a.dim + kDepth - 1) / kDepth);
 
-    if (warp == 0) {
-        if (lane == 0) {
-            int64_t n = 0;  // stages filled so far
+    if (warp < 4) {
+        fewer_registers<kFewRegisters>();
+        if (warp == 0 && lane == 0) {
+            Ring<S::kStages> ring;
+            int filled = 0;  // stages in use, up to all of them
             bool ok = true;
-            for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
+            for (int64_t i = blockIdx.x / CG; i < total && ok; i += gridDim.x / CG) {
                 int32_t row, col;
                 tile_of(a, live, i, &row, &col);
-                for (int k = 0; k < steps; ++k, ++n) {
-                    const int st = (int)(n % S::kStages);
-                    const uint32_t turn = (uint32_t)(n / S::kStages);
-                    if (!(ok = mbar_wait(empty + 8 * st, (turn & 1) ^ 1, &gave_up))) break;
-                    const uint32_t at = tiles + st * S::kStage;
-                    mbar_expect(full + 8 * st, S::kStage);
-                    tma_load(at, &map_a, full + 8 * st, k * kDepth, row * kRowsTile);
-                    tma_load(at + S::kA, &map_b, full + 8 * st, k * kDepth, col * BN);
+                for (int k = 0; k < steps; ++k) {
+                    if (!(ok = mbar_wait(empty + 8 * ring.at, ring.phase ^ 1, &gave_up))) break;
+                    const uint32_t at = tiles + ring.at * S::kStage;
+                    // both CTAs' bytes count on the first one's barrier
+                    if (rank == 0) mbar_expect(full + 8 * ring.at, CG * S::kStage);
+                    const uint32_t bar = CG == 2 ? smem_of(full + 8 * ring.at, 0) : full + 8 * ring.at;
+                    tma_load<CG>(at, &map_a, bar, k * kDepth, (row * CG + (int)rank) * kRowsTile);
+                    tma_load<CG>(at + S::kA, &map_b, bar, k * kDepth, col * BN + (int)rank * S::kBRows);
+                    ring.next();
+                    filled += filled < S::kStages;
                 }
             }
-            if (!ok)  // leave no copy in flight behind
-                for (int64_t k = n > S::kStages ? n - S::kStages : 0; k < n; ++k)
-                    for (int j = 0; j < kWaitLimit && !mbar_try(full + 8 * (int)(k % S::kStages), (uint32_t)(k / S::kStages) & 1); ++j) {}
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = instr_desc(kRowsTile, BN, TYPE == ZERO_T_BF16 ? 1 : 0);
-            int64_t n = 0, it = 0;
+            // the last stages' releases have arrived before the barriers go away
+            for (int k = 0; k < filled && ok; ++k) {
+                // back over the ring: stage at - 1 - k, in the phase it was filled in
+                const int st = ring.at - 1 - k < 0 ? ring.at - 1 - k + S::kStages : ring.at - 1 - k;
+                ok = mbar_wait(empty + 8 * st, ring.at - 1 - k < 0 ? ring.phase ^ 1 : ring.phase, &gave_up);
+            }
+            if (!ok) {  // leave no copy in flight behind: they take microseconds, this a millisecond
+                for (int j = 0; j < 1000; ++j) __nanosleep(1000);
+            }
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = instr_desc(CG * kRowsTile, BN, TYPE == ZERO_T_BF16 ? 1 : 0);
+            const uint64_t desc_a = smem_desc(tiles), desc_b = smem_desc(tiles + S::kA);
+            Ring<S::kStages> ring;
+            Ring<2> acc;
             bool ok = true;
-            for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x, ++it) {
-                const int acc = (int)(it & 1);
-                if (!(ok = mbar_wait(acc_empty + 8 * acc, ((uint32_t)(it >> 1) & 1) ^ 1, &gave_up))) break;
-                tcgen05_after_sync();
-                for (int k = 0; k < steps; ++k, ++n) {
-                    const int st = (int)(n % S::kStages);
-                    if (!(ok = mbar_wait(full + 8 * st, (uint32_t)(n / S::kStages) & 1, &gave_up))) break;
+            for (int64_t i = blockIdx.x / CG; i < total && ok; i += gridDim.x / CG) {
+                for (int k0 = 0; k0 < steps && ok; k0 += kChunk) {
+                    if (!(ok = mbar_wait(acc_empty + 8 * acc.at, acc.phase ^ 1, &gave_up))) break;
                     tcgen05_after_sync();
-                    const uint64_t da = smem_desc(tiles + st * S::kStage), db = smem_desc(tiles + st * S::kStage + S::kA);
+                    const uint32_t d = tmem + acc.at * BN;
+                    const int n = min(kChunk, steps - k0);
+                    for (int k = 0; k < n; ++k) {
+                        if (!(ok = mbar_wait(full + 8 * ring.at, ring.phase, &gave_up))) break;
+                        tcgen05_after_sync();
+                        const uint64_t at = (uint64_t)(ring.at * (S::kStage >> 4));
 #pragma unroll
-                    for (int j = 0; j < kDepth / 16; ++j)  // 16 elements: 32 bytes further in the swizzled rows
-                        mma_f16(tmem + acc * BN, da + 2 * j, db + 2 * j, idesc, k > 0 || j > 0);
-                    mma_commit(empty + 8 * st);
+                        for (int j = 0; j < kDepth / 16; ++j)  // 16 elements: 32 bytes further in the swizzled rows
+                            mma_f16<CG>(d, desc_a + at + 2 * j, desc_b + at + 2 * j, idesc, k > 0 || j > 0);
+                        mma_commit<CG>(empty + 8 * ring.at);
+                        ring.next();
+                    }
+                    if (ok) mma_commit<CG>(acc_full + 8 * acc.at);
+                    acc.next();
                 }
-                if (ok) mma_commit(acc_full + 8 * acc);
             }
             if (!ok) {
-                mma_commit(drained);
+                mma_commit<CG>(drained);
                 for (int j = 0; j < kWaitLimit && !mbar_try(drained, 0); ++j) {}
             }
         }
     } else {
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
-        int64_t it = 0;
-        for (int64_t i = blockIdx.x; i < total; i += gridDim.x, ++it) {
+        more_registers<kManyRegisters>();
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + half * (BN / 2);
+        Ring<2> acc;
+        bool ok = true;
+        for (int64_t i = blockIdx.x / CG; i < total && ok; i += gridDim.x / CG) {
             int32_t row, col;
             tile_of(a, live, i, &row, &col);
-            const int acc = (int)(it & 1);
-            const int64_t r = (int64_t)row * kRowsTile + quarter * 32 + lane;
+            const int64_t r = ((int64_t)row * CG + rank) * kRowsTile + quarter * 32 + lane;
             const int64_t col0 = (int64_t)col * BN + half * (BN / 2);
             const int64_t y = r < a.rows ? a.targets[r] - col0 : -1;
-            if (!__all_sync(~0u, mbar_wait(acc_full + 8 * acc, (uint32_t)(it >> 1) & 1, &gave_up))) break;
-            tcgen05_after_sync();
-            RowStat st = empty_stat();
-#pragma unroll 1
-            for (int j = 0; j < BN / 2; j += 32) {
-                float v[32];
-                tmem_load32(tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN + half * (BN / 2) + j, v);
-                if (col0 + j + 32 > a.vocab) {
+            float v[BN / 2];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (col0 + j + k >= a.vocab) v[k] = -INFINITY;
-                }
-                if (__any_sync(~0u, y >= j && y < j + 32)) {
+            for (int j = 0; j < BN / 2; ++j) v[j] = 0.0f;
+            for (int k = 0; k < steps; k += kChunk, acc.next()) {
+                if (!(ok = __all_sync(~0u, mbar_wait(acc_full + 8 * acc.at, acc.phase, &gave_up)))) break;
+                tcgen05_after_sync();
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (y == j + k && col0 + y < a.vocab) a.zy[r] = v[k];
+                for (int j = 0; j < BN / 2; j += 64) {
+                    float u[64];
+                    tmem_load64(mine + acc.at * BN + j, u);
+#pragma unroll
+                    for (int n = 0; n < 64; ++n) v[j + n] += u[n];
                 }
-                add32(st, v, a.c);
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 2) mbar_arrive_at(smem_of(acc_empty + 8 * acc.at, 0));
+                    else mbar_arrive(acc_empty + 8 * acc.at);
+                }
             }
-            tcgen05_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty + 8 * acc);
+            if (!ok) break;
+            if (col0 + BN / 2 > a.vocab) {
+#pragma unroll
+                for (int j = 0; j < BN / 2; ++j)
+                    if (col0 + j >= a.vocab) v[j] = -INFINITY;
+            }
+            if (__any_sync(~0u, y >= 0 && y < BN / 2)) {
+#pragma unroll
+                for (int j = 0; j < BN / 2; ++j)
+                    if (y == j && col0 + y < a.vocab) a.zy[r] = v[j];
+            }
+            const RowStat st = sum_of(v, a.k);
             if (r < a.rows) {
                 const int64_t o = ((int64_t)col * 2 + half) * a.rows + r;
                 a.m[o] = st.m;
@@ -221,10 +263,12 @@ __global__ void __launch_bounds__(kLinearThreads, 1)
             }
         }
     }
+    __syncwarp();
     __syncthreads();
+    if (CG == 2) cluster_sync();  // neither CTA leaves while the other's MMAs or arrivals use its memory
     if (warp == 1) {
         tcgen05_after_sync();
-        tmem_free(tmem, 2 * BN);
+        tmem_free<CG>(tmem, 2 * BN);
     }
     if (threadIdx.x == 0 && gave_up) a.tiles[1] = 1;
 }
@@ -239,12 +283,12 @@ __global__ void __launch_bounds__(1024) k_linear_join(const LinearArgs a, int64_
     if (y >= 0)  // parts of rows without a target may not have been written
         for (int64_t p = warp; p < parts; p += 32) {
             const RowStat b = {a.m[p * a.rows + t], a.s[p * a.rows + t], a.q[p * a.rows + t]};
-            s = join<true>(s, b, a.c);
+            s = join<true>(s, b, a.k);
         }
     sm[warp][lane] = s;
     __syncthreads();
     if (warp != 0 || t >= a.rows) return;
-    for (int w = 1; w < 32; ++w) s = join<true>(s, sm[w][lane], a.c);
+    for (int w = 1; w < 32; ++w) s = join<true>(s, sm[w][lane], a.k);
     RowResult r = {0.0f, 0.0f, 0.0f};
     if (y >= 0) {
         r = finish_row(s, y < a.vocab ? a.zy[t] : NAN, a.inv_t);
@@ -256,15 +300,16 @@ __global__ void __launch_bounds__(1024) k_linear_join(const LinearArgs a, int64_
     if (entropy) entropy[t] = r.entropy;
 }
 
-constexpr int kMaxBN = 256;
+// Pairs of CTAs once there are tokens for more than one CTA's tile.
+bool linear_pairs(int64_t rows) { return rows > kRowsTile; }
 
 // Where the parts, the targets' logits and the list of row tiles lie in the workspace.
 struct LinearLayout {
     int64_t row_tiles, parts, parts_bytes, bytes;
 };
-LinearLayout linear_layout(int64_t rows, int64_t vocab, int bn) {
+LinearLayout linear_layout(int64_t rows, int64_t vocab, int tile_rows, int bn) {
     LinearLayout l;
-    l.row_tiles = (rows + kRowsTile - 1) / kRowsTile;
+    l.row_tiles = (rows + tile_rows - 1) / tile_rows;
     l.parts = (vocab + bn - 1) / bn * 2;
     l.parts_bytes = (12 * l.parts * rows + 4 * rows + 15) / 16 * 16;
     l.bytes = l.parts_bytes + 4 * (4 + l.row_tiles);
@@ -301,17 +346,36 @@ bool encode(CUtensorMap* map, int32_t type, const void* p, int64_t rows, int64_t
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int TYPE, int BN>
-int launch_linear(const zero_linear* x, LinearArgs a, int sms, cudaStream_t s) {
+template <int TYPE, int CG, int BN>
+int launch_linear(const zero_linear* x, const LinearArgs& a, int sms, cudaStream_t s) {
+    using S = LinearShape<CG, BN>;
     CUtensorMap ma, mb;
     if (!encode(&ma, x->type, x->hidden, x->rows, x->dim, x->ld_hidden, kRowsTile) ||
-        !encode(&mb, x->type, x->weight, x->vocab, x->dim, x->ld_weight, BN))
+        !encode(&mb, x->type, x->weight, x->vocab, x->dim, x->ld_weight, S::kBRows))
         return record_cuda_error(cudaErrorInvalidValue);
-    const cudaError_t e = cudaFuncSetAttribute(k_linear_mma<TYPE, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, LinearShape<BN>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(k_linear_mma<TYPE, CG, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return record_cuda_error(e);
-    const int64_t tiles = (int64_t)a.row_tiles * a.col_tiles;
-    k_linear_mma<TYPE, BN><<<(unsigned)std::min<int64_t>(tiles, sms), kLinearThreads, LinearShape<BN>::kSmem, s>>>(ma, mb, a);
-    return launched();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CG;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(std::min<int64_t>((int64_t)a.row_tiles * a.col_tiles, sms / CG) * CG));
+    cfg.blockDim = dim3(kLinearThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = CG == 2 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, k_linear_mma<TYPE, CG, BN>, ma, mb, a);
+    return e == cudaSuccess ? ZERO_OK : record_cuda_error(e);
+}
+
+template <int CG, int BN>
+int run_linear(const zero_linear* x, const LinearArgs& a, int sms, cudaStream_t s) {
+    k_linear_tiles<<<1, 1024, 0, s>>>(a);
+    const int rc = launched();
+    if (rc) return rc;
+    return x->type == ZERO_T_BF16 ? launch_linear<ZERO_T_BF16, CG, BN>(x, a, sms, s) : launch_linear<ZERO_T_FP16, CG, BN>(x, a, sms, s);
 }
 
 }  // namespace
@@ -321,7 +385,7 @@ using namespace zg;
 
 extern "C" int64_t zero_linear_logp_workspace(int64_t rows, int64_t vocab) {
     if (rows < 0 || vocab < 1 || vocab > INT32_MAX || rows > INT32_MAX) return -1;
-    return linear_layout(rows, vocab, kMaxBN).bytes;
+    return linear_layout(rows, vocab, linear_pairs(rows) ? 2 * kRowsTile : kRowsTile, 256).bytes;
 }
 
 extern "C" int zero_linear_logp(const zero_linear* x, float* logp, float* lse, float* entropy, void* workspace,
@@ -345,7 +409,8 @@ extern "C" int zero_linear_logp(const zero_linear* x, float* logp, float* lse, f
     if (d.rc) return d.rc;
     if (!encoder()) return record_cuda_error(cudaErrorNotSupported);
     cudaStream_t s = (cudaStream_t)stream;
-    const LinearLayout l = linear_layout(x->rows, x->vocab, kMaxBN);
+    const bool pairs = linear_pairs(x->rows);
+    const LinearLayout l = linear_layout(x->rows, x->vocab, pairs ? 2 * kRowsTile : kRowsTile, 256);
     LinearArgs a;
     a.targets = x->targets;
     a.m = (float*)workspace;
@@ -356,16 +421,14 @@ extern "C" int zero_linear_logp(const zero_linear* x, float* logp, float* lse, f
     a.rows = x->rows;
     a.vocab = x->vocab;
     a.dim = x->dim;
+    a.tile_rows = (int32_t)(pairs ? 2 * kRowsTile : kRowsTile);
     a.row_tiles = (int32_t)l.row_tiles;
     a.col_tiles = (int32_t)(l.parts / 2);
-    a.group = (int32_t)std::max<int64_t>(1, std::min<int64_t>(64, (INT64_C(32) << 20) / (kRowsTile * 2 * x->dim)));
-    a.c = (float)(1.4426950408889634 / x->temperature);
-    a.inv_t = (float)(1.0 / x->temperature);
-    k_linear_tiles<<<1, 1024, 0, s>>>(a);
-    int rc = launched();
-    if (rc) return rc;
+    a.group = (int32_t)std::max<int64_t>(1, std::min<int64_t>(8192 / a.tile_rows, (INT64_C(32) << 20) / (a.tile_rows * 2 * x->dim)));
+    a.k = make_scale(x->temperature);
+    a.inv_t = 1.0 / x->temperature;
     const int sms = d.sm_count();
-    rc = x->type == ZERO_T_BF16 ? launch_linear<ZERO_T_BF16, 256>(x, a, sms, s) : launch_linear<ZERO_T_FP16, 256>(x, a, sms, s);
+    int rc = pairs ? run_linear<2, 256>(x, a, sms, s) : run_linear<1, 256>(x, a, sms, s);
     if (rc) return rc;
     k_linear_join<<<(unsigned)((x->rows + 31) / 32), 1024, 0, s>>>(a, l.parts, logp, lse, entropy);
     return launched();

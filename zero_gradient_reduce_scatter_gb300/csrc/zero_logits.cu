@@ -23,7 +23,9 @@ struct Rows {
     const int64_t* targets;
     const float* weight;  // nullptr, or 0 for rows that carry no loss
     int64_t rows, vocab, stride;
-    float c, inv_t;       // log2(e) / temperature, 1 / temperature
+    Scale k;              // log2(e) / temperature
+    float c;              // the same in one number, for gradients
+    double inv_t;         // 1 / temperature
 };
 
 template <class T>
@@ -33,13 +35,13 @@ __device__ __forceinline__ int64_t live_target(const Rows<T>& a, int64_t t) {
 
 // The sums of one row, read by a whole CTA.
 template <class T, bool ENTROPY>
-__device__ __forceinline__ RowStat read_row(const T* x, int64_t n, float c) {
+__device__ __forceinline__ RowStat read_row(const T* x, int64_t n, Scale k) {
     RowStat a = empty_stat();
     for (int64_t j = threadIdx.x; j < n; j += kRowThreads) {
         const float v = widen(x[j]), m = fmaxf(a.m, v), base = base_of(m);
-        rebase<ENTROPY>(a, base, c);
+        rebase<ENTROPY>(a, base, k);
         a.m = m;
-        add_term<ENTROPY>(a, v, c, base);
+        add_term<ENTROPY>(a, v, k, base);
     }
     return a;
 }
@@ -52,9 +54,11 @@ __global__ void __launch_bounds__(kRowThreads) k_token_logp(const Rows<T> a, flo
         RowResult r = {0.0f, 0.0f, 0.0f};
         if (y >= 0) {
             const T* x = a.x + t * a.stride;
-            const RowStat s = cta_join<ENTROPY, kRowThreads>(read_row<T, ENTROPY>(x, a.vocab, a.c), a.c, sm);
-            r = finish_row(s, y < a.vocab ? widen(x[y]) : NAN, a.inv_t);
-            if (y >= a.vocab) r.logp = NAN;
+            const RowStat s = cta_join<ENTROPY, kRowThreads>(read_row<T, ENTROPY>(x, a.vocab, a.k), a.k, sm);
+            if (threadIdx.x == 0) {
+                r = finish_row(s, y < a.vocab ? widen(x[y]) : NAN, a.inv_t);
+                if (y >= a.vocab) r.logp = NAN;
+            }
         }
         if (threadIdx.x == 0) {
             logp[t] = r.logp;
@@ -71,14 +75,15 @@ struct GradRow {
     float g, ka, kb, base, off;
 };
 
-__device__ __forceinline__ GradRow grad_row(float g, float h, float x_y, float logp, float lse, float entropy, float inv_t) {
+__device__ __forceinline__ GradRow grad_row(float g, float h, float x_y, float logp, float lse, float entropy, double inv_t_d) {
     GradRow r;
+    const float inv_t = (float)inv_t_d;
     if (fabsf(logp) <= fabsf(lse)) {
         r.base = x_y;
         r.off = -logp * kLog2e;
     } else {
         r.base = lse / inv_t;
-        r.off = (float)(((double)lse - (double)r.base * (double)inv_t) * 1.4426950408889634);
+        r.off = (float)(((double)lse - (double)r.base * inv_t_d) * 1.4426950408889634);
     }
     r.g = g * inv_t;
     r.ka = inv_t * (h == 0.0f ? g : fmaf(h, entropy, g));
@@ -387,8 +392,9 @@ Rows<T> rows_of(const zero_logits* x, const float* weight) {
     a.rows = x->rows;
     a.vocab = x->vocab;
     a.stride = x->stride;
+    a.k = make_scale(x->temperature);
     a.c = (float)(1.4426950408889634 / x->temperature);
-    a.inv_t = (float)(1.0 / x->temperature);
+    a.inv_t = 1.0 / x->temperature;
     return a;
 }
 
