@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <utility>
 
 #include "zero_host.h"
 #include "zero_softmax.cuh"
@@ -29,45 +30,45 @@ struct LinearArgs {
     const int64_t* targets;
     float *m, *s, *q;  // [parts, rows]
     float* zy;         // [rows] the target's logit
-    int32_t* tiles;    // [0]: how many row tiles hold a target, [1]: set when a wait gave up, [4...]: those tiles
+    int32_t* status;   // [grid of the product] set where a wait gave up
+    int32_t* tiles;    // [0]: how many row tiles hold a target, [4...]: those tiles; nullptr: one tile, taken as it is
     int64_t rows, vocab, dim;
-    int32_t tile_rows, row_tiles, col_tiles, group;
+    int32_t tile_rows, row_tiles, tile_cols, col_tiles, group, grid;
     Scale k;       // log2(e) / temperature
     double inv_t;  // 1 / temperature
 };
 
-// Row tiles with at least one target, in order. One CTA.
+// All three kernels may be launched while the kernel before them is still running: each waits
+// for it (griddepcontrol.wait) before its first access to memory.
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Row tiles with at least one target, in order. One CTA, a warp per tile.
 __global__ void __launch_bounds__(1024) k_linear_tiles(const LinearArgs a) {
-    __shared__ int32_t base, sums[32];
+    __shared__ int32_t any[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (threadIdx.x == 0) base = 0;
-    __syncthreads();
+    let_next_kernel_start();
+    wait_for_kernel_before();
+    int32_t n = 0;  // kept by warp 0
     for (int32_t t0 = 0; t0 < a.row_tiles; t0 += 32) {
-        // a warp per tile looks at its rows
         const int32_t t = t0 + warp;
-        bool any = false;
+        bool mine = false;
         if (t < a.row_tiles)
             for (int i = lane; i < a.tile_rows; i += 32) {
                 const int64_t r = (int64_t)t * a.tile_rows + i;
-                any |= r < a.rows && a.targets[r] >= 0;
+                mine |= r < a.rows && a.targets[r] >= 0;
             }
-        any = __any_sync(~0u, any);
-        if (lane == 0) sums[warp] = any;
+        mine = __any_sync(~0u, mine);
+        if (lane == 0) any[warp] = mine;
         __syncthreads();
         if (warp == 0) {
-            const bool mine = sums[lane] != 0;
-            const unsigned ballot = __ballot_sync(~0u, mine);
-            const int32_t at = base;
-            if (mine) a.tiles[4 + at + __popc(ballot & ((1u << lane) - 1))] = t0 + lane;
-            __syncwarp();
-            if (lane == 0) base = at + __popc(ballot);
+            const unsigned ballot = __ballot_sync(~0u, any[lane] != 0);
+            if (any[lane]) a.tiles[4 + n + __popc(ballot & ((1u << lane) - 1))] = t0 + lane;
+            n += __popc(ballot);
         }
         __syncthreads();
     }
-    if (threadIdx.x == 0) {
-        a.tiles[0] = base;
-        a.tiles[1] = 0;
-    }
+    if (threadIdx.x == 0) a.tiles[0] = n;
 }
 
 // Tile `i` of the run: groups of row tiles that stay in L2 while the vocabulary passes by, and
@@ -78,11 +79,11 @@ __device__ __forceinline__ void tile_of(const LinearArgs& a, int32_t live, int64
     const int32_t size = min(a.group, live - first);
     const int64_t in = i - (int64_t)g * per;
     *col = (int32_t)(in / size);
-    *row = a.tiles[4 + first + (int32_t)(in % size)];
+    *row = a.tiles ? a.tiles[4 + first + (int32_t)(in % size)] : 0;
 }
 
 // N logits of one row: their sums, in four chains.
-template <int N>
+template <bool ENTROPY, int N>
 __device__ __forceinline__ RowStat sum_of(const float (&v)[N], Scale k) {
     float m = v[0];
 #pragma unroll
@@ -92,12 +93,13 @@ __device__ __forceinline__ RowStat sum_of(const float (&v)[N], Scale k) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) part[i] = {m, 0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < N; ++j) add_term<true>(part[j & 3], v[j], k, base);
+    for (int j = 0; j < N; ++j) add_term<ENTROPY>(part[j & 3], v[j], k, base);
     return {m, (part[0].s + part[1].s) + (part[2].s + part[3].s), (part[0].q + part[1].q) + (part[2].q + part[3].q)};
 }
 
-// One CTA per SM walks over tiles of 128 tokens by BN columns of the vocabulary, or (CG = 2) a
-// pair of CTAs over tiles of 256 by BN, each CTA loading its own tokens and half of the columns.
+// One CTA per SM walks over tiles of 128 tokens by tile_cols (at most BN) columns of the
+// vocabulary, or (CG = 2) a pair of CTAs over tiles of 256 by tile_cols, each CTA loading its own
+// tokens and half of the columns.
 // Warp 0 keeps kStages pairs of operand tiles on their way by TMA, one thread of warp 1 (of the
 // pair's first CTA) issues the MMAs into one of two accumulators in TMEM, and eight warps read the
 // other, one row per thread, half of the columns per warpgroup. The tensor core drops the low
@@ -114,7 +116,7 @@ struct LinearShape {
     static constexpr int kSmem = kStages * kStage + 1024;
 };
 
-template <int TYPE, int CG, int BN>
+template <int TYPE, int CG, int BN, bool ENTROPY>
 __global__ void __launch_bounds__(kLinearThreads, 1)
     k_linear_mma(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const LinearArgs a) {
     using S = LinearShape<CG, BN>;
@@ -146,7 +148,9 @@ __global__ void __launch_bounds__(kLinearThreads, 1)
     if (CG == 2) cluster_sync();
     tcgen05_after_sync();
     const uint32_t tmem = tmem_slot;
-    const int32_t live = a.tiles[0];
+    let_next_kernel_start();
+    wait_for_kernel_before();
+    const int32_t live = a.tiles ? a.tiles[0] : 1;
     const int64_t total = (int64_t)live * a.col_tiles;
     const int steps = (int)((a.dim + kDepth - 1) / kDepth);
 
@@ -163,10 +167,10 @@ __global__ void __launch_bounds__(kLinearThreads, 1)
                     if (!(ok = mbar_wait(empty + 8 * ring.at, ring.phase ^ 1, &gave_up))) break;
                     const uint32_t at = tiles + ring.at * S::kStage;
                     // both CTAs' bytes count on the first one's barrier
-                    if (rank == 0) mbar_expect(full + 8 * ring.at, CG * S::kStage);
+                    if (rank == 0) mbar_expect(full + 8 * ring.at, CG * S::kA + a.tile_cols * 128);
                     const uint32_t bar = CG == 2 ? smem_of(full + 8 * ring.at, 0) : full + 8 * ring.at;
                     tma_load<CG>(at, &map_a, bar, k * kDepth, (row * CG + (int)rank) * kRowsTile);
-                    tma_load<CG>(at + S::kA, &map_b, bar, k * kDepth, col * BN + (int)rank * S::kBRows);
+                    tma_load<CG>(at + S::kA, &map_b, bar, k * kDepth, col * a.tile_cols + (int)rank * (a.tile_cols / CG));
                     ring.next();
                     filled += filled < S::kStages;
                 }
@@ -181,7 +185,7 @@ __global__ void __launch_bounds__(kLinearThreads, 1)
                 for (int j = 0; j < 1000; ++j) __nanosleep(1000);
             }
         } else if (warp == 1 && lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = instr_desc(CG * kRowsTile, BN, TYPE == ZERO_T_BF16 ? 1 : 0);
+            const uint32_t idesc = instr_desc(CG * kRowsTile, a.tile_cols, TYPE == ZERO_T_BF16 ? 1 : 0);
             const uint64_t desc_a = smem_desc(tiles), desc_b = smem_desc(tiles + S::kA);
             Ring<S::kStages> ring;
             Ring<2> acc;
@@ -214,14 +218,16 @@ __global__ void __launch_bounds__(kLinearThreads, 1)
     } else {
         more_registers<kManyRegisters>();
         const int quarter = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + half * (BN / 2);
+        const int cols = a.tile_cols / 2;  // of this thread's part of a row
+        const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16) + half * cols;
         Ring<2> acc;
         bool ok = true;
         for (int64_t i = blockIdx.x / CG; i < total && ok; i += gridDim.x / CG) {
             int32_t row, col;
             tile_of(a, live, i, &row, &col);
             const int64_t r = ((int64_t)row * CG + rank) * kRowsTile + quarter * 32 + lane;
-            const int64_t col0 = (int64_t)col * BN + half * (BN / 2);
+            const int64_t col0 = (int64_t)col * a.tile_cols + half * cols;
+            const int n = (int)min((int64_t)cols, a.vocab - col0);  // may be 0 or less
             const int64_t y = r < a.rows ? a.targets[r] - col0 : -1;
             float v[BN / 2];
 #pragma unroll
@@ -244,22 +250,22 @@ __global__ void __launch_bounds__(kLinearThreads, 1)
                 }
             }
             if (!ok) break;
-            if (col0 + BN / 2 > a.vocab) {
+            if (n < BN / 2) {
 #pragma unroll
                 for (int j = 0; j < BN / 2; ++j)
-                    if (col0 + j >= a.vocab) v[j] = -INFINITY;
+                    if (j >= n) v[j] = -INFINITY;
             }
-            if (__any_sync(~0u, y >= 0 && y < BN / 2)) {
+            if (__any_sync(~0u, y >= 0 && y < n)) {
 #pragma unroll
                 for (int j = 0; j < BN / 2; ++j)
-                    if (y == j && col0 + y < a.vocab) a.zy[r] = v[j];
+                    if (y == j && j < n) a.zy[r] = v[j];
             }
-            const RowStat st = sum_of(v, a.k);
+            const RowStat st = sum_of<ENTROPY>(v, a.k);
             if (r < a.rows) {
                 const int64_t o = ((int64_t)col * 2 + half) * a.rows + r;
                 a.m[o] = st.m;
                 a.s[o] = st.s;
-                a.q[o] = st.q;
+                if (ENTROPY) a.q[o] = st.q;
             }
         }
     }
@@ -270,49 +276,83 @@ __global__ void __launch_bounds__(kLinearThreads, 1)
         tcgen05_after_sync();
         tmem_free<CG>(tmem, 2 * BN);
     }
-    if (threadIdx.x == 0 && gave_up) a.tiles[1] = 1;
+    if (threadIdx.x == 0) a.status[blockIdx.x] = gave_up;
 }
 
-// 32 rows by 32 slices of their parts; the slices are joined in order.
-__global__ void __launch_bounds__(1024) k_linear_join(const LinearArgs a, int64_t parts, float* logp, float* lse, float* entropy) {
-    __shared__ RowStat sm[32][33];
+// 32 rows by 16 slices of their parts, four parts on their way at a time; the slices are joined
+// in order.
+constexpr int kJoinSlices = 16;
+
+template <bool ENTROPY>
+__global__ void __launch_bounds__(32 * kJoinSlices) k_linear_join(const LinearArgs a, int64_t parts, float* logp, float* lse, float* entropy) {
+    __shared__ RowStat sm[kJoinSlices][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    wait_for_kernel_before();
     const int64_t t = (int64_t)blockIdx.x * 32 + lane;
     RowStat s = empty_stat();
     const int64_t y = t < a.rows ? a.targets[t] : -1;
     if (y >= 0)  // parts of rows without a target may not have been written
-        for (int64_t p = warp; p < parts; p += 32) {
-            const RowStat b = {a.m[p * a.rows + t], a.s[p * a.rows + t], a.q[p * a.rows + t]};
-            s = join<true>(s, b, a.k);
+        for (int64_t p0 = warp; p0 < parts; p0 += 4 * kJoinSlices) {
+            RowStat b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t p = p0 + i * kJoinSlices;
+                b[i] = empty_stat();
+                if (p < parts) b[i] = {a.m[p * a.rows + t], a.s[p * a.rows + t], ENTROPY ? a.q[p * a.rows + t] : 0.0f};
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s = join<ENTROPY>(s, b[i], a.k);
         }
     sm[warp][lane] = s;
-    __syncthreads();
+    bool gave_up = false;
+    for (int i = threadIdx.x; i < a.grid; i += 32 * kJoinSlices) gave_up |= a.status[i] != 0;
+    gave_up = __syncthreads_or(gave_up);
     if (warp != 0 || t >= a.rows) return;
-    for (int w = 1; w < 32; ++w) s = join<true>(s, sm[w][lane], a.k);
+    for (int w = 1; w < kJoinSlices; ++w) s = join<ENTROPY>(s, sm[w][lane], a.k);
     RowResult r = {0.0f, 0.0f, 0.0f};
     if (y >= 0) {
         r = finish_row(s, y < a.vocab ? a.zy[t] : NAN, a.inv_t);
         if (y >= a.vocab) r.logp = NAN;
     }
-    if (a.tiles[1]) r.logp = r.lse = r.entropy = NAN;  // a wait of the product gave up: no result
+    if (gave_up) r.logp = r.lse = r.entropy = NAN;  // no result
     logp[t] = r.logp;
     lse[t] = r.lse;
-    if (entropy) entropy[t] = r.entropy;
+    if (ENTROPY) entropy[t] = r.entropy;
 }
 
-// Pairs of CTAs once there are tokens for more than one CTA's tile.
-bool linear_pairs(int64_t rows) { return rows > kRowsTile; }
+constexpr int kMaxGrid = 1024;
 
-// Where the parts, the targets' logits and the list of row tiles lie in the workspace.
-struct LinearLayout {
-    int64_t row_tiles, parts, parts_bytes, bytes;
+// How a call is cut up, and where things lie in its workspace.
+struct LinearPlan {
+    bool pairs;
+    int32_t tile_rows, row_tiles, tile_cols, col_tiles;
+    int64_t parts, parts_bytes, bytes;
 };
-LinearLayout linear_layout(int64_t rows, int64_t vocab, int tile_rows, int bn) {
-    LinearLayout l;
-    l.row_tiles = (rows + tile_rows - 1) / tile_rows;
-    l.parts = (vocab + bn - 1) / bn * 2;
+
+// Pairs of CTAs once there are tokens for more than one CTA's tile. The width of a tile is the
+// one (of the multiples of 16, for pairs of 32, that an MMA takes) for which the busiest CTA has the fewest columns to go
+// through: few tokens are bound by reading the vocabulary matrix, and 50257 columns over 152 CTAs
+// are three tiles of 112 each rather than one or two of 256. Pairs keep to wide tiles, which
+// their MMAs need to run at full rate.
+LinearPlan linear_plan(int64_t rows, int64_t vocab, int sms) {
+    LinearPlan l;
+    l.pairs = rows > kRowsTile;
+    l.tile_rows = l.pairs ? 2 * kRowsTile : kRowsTile;
+    l.row_tiles = (int32_t)((rows + l.tile_rows - 1) / l.tile_rows);
+    const int workers = std::max(1, l.pairs ? sms / 2 : sms), widest = l.pairs ? 256 : 128;
+    int64_t least = INT64_MAX;
+    l.tile_cols = widest;
+    for (int cols = widest; cols >= (l.pairs ? 224 : 64); cols -= l.pairs ? 32 : 16) {
+        const int64_t tiles = (vocab + cols - 1) / cols * l.row_tiles, most = (tiles + workers - 1) / workers * cols;
+        if (most < least) {
+            least = most;
+            l.tile_cols = cols;
+        }
+    }
+    l.col_tiles = (int32_t)((vocab + l.tile_cols - 1) / l.tile_cols);
+    l.parts = 2 * (int64_t)l.col_tiles;
     l.parts_bytes = (12 * l.parts * rows + 4 * rows + 15) / 16 * 16;
-    l.bytes = l.parts_bytes + 4 * (4 + l.row_tiles);
+    l.bytes = l.parts_bytes + 4 * (kMaxGrid + 4 + (int64_t)l.row_tiles);
     return l;
 }
 
@@ -346,36 +386,53 @@ bool encode(CUtensorMap* map, int32_t type, const void* p, int64_t rows, int64_t
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int TYPE, int CG, int BN>
-int launch_linear(const zero_linear* x, const LinearArgs& a, int sms, cudaStream_t s) {
-    using S = LinearShape<CG, BN>;
-    CUtensorMap ma, mb;
-    if (!encode(&ma, x->type, x->hidden, x->rows, x->dim, x->ld_hidden, kRowsTile) ||
-        !encode(&mb, x->type, x->weight, x->vocab, x->dim, x->ld_weight, S::kBRows))
-        return record_cuda_error(cudaErrorInvalidValue);
-    cudaError_t e = cudaFuncSetAttribute(k_linear_mma<TYPE, CG, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-    if (e != cudaSuccess) return record_cuda_error(e);
+// A launch that may begin while the kernel before it ends, in clusters of `cluster` CTAs.
+template <class... P, class... A>
+int launch_linked(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, int cluster, cudaStream_t s, A&&... args) {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = CG;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(std::min<int64_t>((int64_t)a.row_tiles * a.col_tiles, sms / CG) * CG));
-    cfg.blockDim = dim3(kLinearThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = at;
-    cfg.numAttrs = CG == 2 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, k_linear_mma<TYPE, CG, BN>, ma, mb, a);
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
     return e == cudaSuccess ? ZERO_OK : record_cuda_error(e);
 }
 
-template <int CG, int BN>
-int run_linear(const zero_linear* x, const LinearArgs& a, int sms, cudaStream_t s) {
-    k_linear_tiles<<<1, 1024, 0, s>>>(a);
-    const int rc = launched();
+template <int TYPE, int CG, int BN, bool ENTROPY>
+int launch_product(const zero_linear* x, const LinearArgs& a, cudaStream_t s) {
+    using S = LinearShape<CG, BN>;
+    CUtensorMap ma, mb;
+    if (!encode(&ma, x->type, x->hidden, x->rows, x->dim, x->ld_hidden, kRowsTile) ||
+        !encode(&mb, x->type, x->weight, x->vocab, x->dim, x->ld_weight, a.tile_cols / CG))
+        return record_cuda_error(cudaErrorInvalidValue);
+    const cudaError_t e = cudaFuncSetAttribute(k_linear_mma<TYPE, CG, BN, ENTROPY>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return record_cuda_error(e);
+    return launch_linked(k_linear_mma<TYPE, CG, BN, ENTROPY>, a.grid, kLinearThreads, S::kSmem, CG, s, ma, mb, a);
+}
+
+template <bool ENTROPY>
+int run_linear(const zero_linear* x, const LinearArgs& a, const LinearPlan& l, float* logp, float* lse, float* entropy, cudaStream_t s) {
+    int rc = a.tiles ? launch_linked(k_linear_tiles, 1, 1024, 0, 1, s, a) : ZERO_OK;
     if (rc) return rc;
-    return x->type == ZERO_T_BF16 ? launch_linear<ZERO_T_BF16, CG, BN>(x, a, sms, s) : launch_linear<ZERO_T_FP16, CG, BN>(x, a, sms, s);
+    const bool bf16 = x->type == ZERO_T_BF16;
+    if (l.pairs) rc = bf16 ? launch_product<ZERO_T_BF16, 2, 256, ENTROPY>(x, a, s) : launch_product<ZERO_T_FP16, 2, 256, ENTROPY>(x, a, s);
+    else rc = bf16 ? launch_product<ZERO_T_BF16, 1, 128, ENTROPY>(x, a, s) : launch_product<ZERO_T_FP16, 1, 128, ENTROPY>(x, a, s);
+    if (rc) return rc;
+    return launch_linked(k_linear_join<ENTROPY>, (unsigned)((x->rows + 31) / 32), 32 * kJoinSlices, 0, 1, s, a, l.parts, logp, lse, entropy);
+}
+
+// The workspace of any number of SMs.
+int64_t most_bytes(int64_t rows, int64_t vocab) {
+    const int64_t narrowest = rows > kRowsTile ? 224 : 64;
+    return 12 * 2 * ((vocab + narrowest - 1) / narrowest) * rows + 4 * rows + 16 + 4 * (kMaxGrid + 4 + rows / kRowsTile + 1);
 }
 
 }  // namespace
@@ -385,7 +442,7 @@ using namespace zg;
 
 extern "C" int64_t zero_linear_logp_workspace(int64_t rows, int64_t vocab) {
     if (rows < 0 || vocab < 1 || vocab > INT32_MAX || rows > INT32_MAX) return -1;
-    return linear_layout(rows, vocab, linear_pairs(rows) ? 2 * kRowsTile : kRowsTile, 256).bytes;
+    return most_bytes(rows, vocab);
 }
 
 extern "C" int zero_linear_logp(const zero_linear* x, float* logp, float* lse, float* entropy, void* workspace,
@@ -409,27 +466,28 @@ extern "C" int zero_linear_logp(const zero_linear* x, float* logp, float* lse, f
     if (d.rc) return d.rc;
     if (!encoder()) return record_cuda_error(cudaErrorNotSupported);
     cudaStream_t s = (cudaStream_t)stream;
-    const bool pairs = linear_pairs(x->rows);
-    const LinearLayout l = linear_layout(x->rows, x->vocab, pairs ? 2 * kRowsTile : kRowsTile, 256);
+    const int sms = d.sm_count();
+    const LinearPlan l = linear_plan(x->rows, x->vocab, sms);
     LinearArgs a;
     a.targets = x->targets;
     a.m = (float*)workspace;
     a.s = a.m + l.parts * x->rows;
     a.q = a.s + l.parts * x->rows;
     a.zy = a.q + l.parts * x->rows;
-    a.tiles = (int32_t*)((char*)workspace + l.parts_bytes);
+    a.status = (int32_t*)((char*)workspace + l.parts_bytes);
+    a.tiles = l.row_tiles > 1 ? a.status + kMaxGrid : nullptr;
     a.rows = x->rows;
     a.vocab = x->vocab;
     a.dim = x->dim;
-    a.tile_rows = (int32_t)(pairs ? 2 * kRowsTile : kRowsTile);
-    a.row_tiles = (int32_t)l.row_tiles;
-    a.col_tiles = (int32_t)(l.parts / 2);
+    a.tile_rows = l.tile_rows;
+    a.row_tiles = l.row_tiles;
+    a.tile_cols = l.tile_cols;
+    a.col_tiles = l.col_tiles;
+    // row tiles of 32 MB of hidden states at most stay in L2 together
     a.group = (int32_t)std::max<int64_t>(1, std::min<int64_t>(8192 / a.tile_rows, (INT64_C(32) << 20) / (a.tile_rows * 2 * x->dim)));
+    const int width = l.pairs ? 2 : 1;
+    a.grid = (int32_t)(std::min<int64_t>((int64_t)l.row_tiles * l.col_tiles, std::min(sms, kMaxGrid) / width) * width);
     a.k = make_scale(x->temperature);
     a.inv_t = 1.0 / x->temperature;
-    const int sms = d.sm_count();
-    int rc = pairs ? run_linear<2, 256>(x, a, sms, s) : run_linear<1, 256>(x, a, sms, s);
-    if (rc) return rc;
-    k_linear_join<<<(unsigned)((x->rows + 31) / 32), 1024, 0, s>>>(a, l.parts, logp, lse, entropy);
-    return launched();
+    return entropy ? run_linear<true>(x, a, l, logp, lse, entropy, s) : run_linear<false>(x, a, l, logp, lse, entropy, s);
 }
