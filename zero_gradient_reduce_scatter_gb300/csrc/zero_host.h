@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <utility>
 
 #include <cuda_runtime.h>
 
@@ -90,6 +91,28 @@ private:
     bool restore_ = false;
     cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;  // then the caller's own
 };
+
+// A launch that may begin while the kernel before it on the stream is still running, in clusters
+// of `cluster` CTAs: the kernel waits for its predecessor (griddepcontrol.wait) before it touches
+// memory that the predecessor may write or still read.
+template <class... P, class... A>
+int launch_linked(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, int cluster, cudaStream_t s, A&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+    return e == cudaSuccess ? ZERO_OK : record_cuda_error(e);
+}
 
 inline int launched() {
     const cudaError_t e = cudaGetLastError();

@@ -8,7 +8,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <utility>
 
 #include "zero_host.h"
 #include "zero_softmax.cuh"
@@ -37,11 +36,6 @@ struct LinearArgs {
     Scale k;       // log2(e) / temperature
     double inv_t;  // 1 / temperature
 };
-
-// All three kernels may be launched while the kernel before them is still running: each waits
-// for it (griddepcontrol.wait) before its first access to memory.
-__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Row tiles with at least one target, in order. One CTA, a warp per tile.
 __global__ void __launch_bounds__(1024) k_linear_tiles(const LinearArgs a) {
@@ -384,26 +378,6 @@ bool encode(CUtensorMap* map, int32_t type, const void* p, int64_t rows, int64_t
     return encoder()(map, type == ZERO_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, (void*)p, dims,
                      strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// A launch that may begin while the kernel before it ends, in clusters of `cluster` CTAs.
-template <class... P, class... A>
-int launch_linked(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, int cluster, cudaStream_t s, A&&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)cluster;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
-    return e == cudaSuccess ? ZERO_OK : record_cuda_error(e);
 }
 
 template <int TYPE, int CG, int BN, bool ENTROPY>

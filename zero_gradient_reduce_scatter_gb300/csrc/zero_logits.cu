@@ -8,13 +8,18 @@
 #include <cmath>
 #include <cstdint>
 
+#include <cooperative_groups.h>
+
 #include "zero_host.h"
 #include "zero_softmax.cuh"
 
 namespace zg {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kRowThreads = 256;
+constexpr int kUnroll = 4;  // 16-byte loads of a thread on their way at a time
 
 // Logits as the kernels take them.
 template <class T>
@@ -33,88 +38,222 @@ __device__ __forceinline__ int64_t live_target(const Rows<T>& a, int64_t t) {
     return a.weight && a.weight[t] == 0.0f ? -1 : a.targets[t];
 }
 
-// The sums of one row, read by a whole CTA.
-template <class T, bool ENTROPY>
-__device__ __forceinline__ RowStat read_row(const T* x, int64_t n, Scale k) {
-    RowStat a = empty_stat();
-    for (int64_t j = threadIdx.x; j < n; j += kRowThreads) {
-        const float v = widen(x[j]), m = fmaxf(a.m, v), base = base_of(m);
-        rebase<ENTROPY>(a, base, k);
-        a.m = m;
-        add_term<ENTROPY>(a, v, k, base);
-    }
+// A row as the CTAs of a cluster share it: up to 7 elements before the first 16-byte boundary
+// (the first CTA's), whole vectors [lo, hi) of each CTA, and up to 7 behind the last (the last
+// CTA's). A row of an odd vocabulary starts at any even address.
+struct Slice {
+    int64_t head, lo, hi, tail;  // elements before, this CTA's vectors, elements behind
+    int64_t tail_at;             // first element behind
+};
+template <class T>
+__device__ __forceinline__ Slice slice_of(const T* x, int64_t n, int rank, int size) {
+    Slice s;
+    const int64_t to = (int64_t)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int64_t)sizeof(T);
+    s.head = to < n ? to : n;
+    const int64_t vecs = (n - s.head) / kVec<T>, per = (vecs + size - 1) / size;
+    s.lo = per * rank < vecs ? per * rank : vecs;
+    s.hi = s.lo + per < vecs ? s.lo + per : vecs;
+    s.tail_at = s.head + vecs * kVec<T>;
+    s.tail = rank == size - 1 ? n - s.tail_at : 0;
+    if (rank != 0) s.head = 0;
+    return s;
+}
+// The vectors' base address: that of the row's first 16-byte boundary.
+template <class T>
+__device__ __forceinline__ const uint4* vectors(const T* x) {
+    return reinterpret_cast<const uint4*>((reinterpret_cast<uintptr_t>(x) + 15) & ~(uintptr_t)15);
+}
+
+// The sums of all CTAs of a cluster, in the order of their ranks; valid everywhere. `mine` is
+// shared memory of this CTA; `after` runs before any CTA may leave or overwrite what was read.
+template <bool ENTROPY>
+__device__ __forceinline__ RowStat cluster_join(RowStat a, int size, Scale k, RowStat* mine) {
+    if (size == 1) return a;
+    cg::cluster_group cl = cg::this_cluster();
+    if (threadIdx.x == 0) *mine = a;
+    cl.sync();
+    a = *cl.map_shared_rank(mine, 0);
+    for (int r = 1; r < size; ++r) a = join<ENTROPY>(a, *cl.map_shared_rank(mine, r), k);
     return a;
 }
 
+// Forward, bound by reading the logits once: `size` CTAs per row (a cluster; several where there
+// are few rows), each thread kUnroll vectors at a time.
 template <class T, bool ENTROPY>
-__global__ void __launch_bounds__(kRowThreads) k_token_logp(const Rows<T> a, float* logp, float* lse, float* entropy) {
-    __shared__ RowStat sm[kRowThreads / 32];
-    for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
-        const int64_t y = live_target(a, t);
-        RowResult r = {0.0f, 0.0f, 0.0f};
-        if (y >= 0) {
-            const T* x = a.x + t * a.stride;
-            const RowStat s = cta_join<ENTROPY, kRowThreads>(read_row<T, ENTROPY>(x, a.vocab, a.k), a.k, sm);
-            if (threadIdx.x == 0) {
-                r = finish_row(s, y < a.vocab ? widen(x[y]) : NAN, a.inv_t);
-                if (y >= a.vocab) r.logp = NAN;
-            }
+__global__ void __launch_bounds__(kRowThreads)
+    k_token_logp(const Rows<T> a, int size, float* logp, float* lse, float* entropy, float* cleared) {
+    __shared__ RowStat sm[kRowThreads / 32], mine;
+    let_next_kernel_start();
+    wait_for_kernel_before();
+    const int64_t t = blockIdx.x / size;
+    const int rank = (int)(blockIdx.x % size);
+    const int64_t y = live_target(a, t);
+    RowResult r = {0.0f, 0.0f, 0.0f};
+    if (y >= 0) {
+        const T* x = a.x + t * a.stride;
+        const Slice s = slice_of(x, a.vocab, rank, size);
+        const uint4* v = vectors(x);
+        RunningStat<T, ENTROPY> run(a.k);
+        for (int64_t i = s.lo + threadIdx.x; i < s.hi; i += kUnroll * kRowThreads) {
+            uint4 q[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (i + u * kRowThreads < s.hi) q[u] = __ldg(v + i + u * kRowThreads);
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (i + u * kRowThreads < s.hi) run.add(q[u]);
         }
-        if (threadIdx.x == 0) {
-            logp[t] = r.logp;
-            if (lse) lse[t] = r.lse;
-            if (ENTROPY) entropy[t] = r.entropy;
+        if (threadIdx.x < s.head) run.add_one(widen(x[threadIdx.x]));
+        if (threadIdx.x < s.tail) run.add_one(widen(x[s.tail_at + threadIdx.x]));
+        RowStat st = cta_join<ENTROPY, kRowThreads>(run.stat(), a.k, sm);
+        st = cluster_join<ENTROPY>(st, size, a.k, &mine);
+        if (threadIdx.x == 0 && rank == 0) {
+            r = finish_row(st, y < a.vocab ? widen(x[y]) : NAN, a.inv_t);
+            if (y >= a.vocab) r.logp = NAN;
         }
     }
+    if (threadIdx.x == 0 && rank == 0) {
+        logp[t] = r.logp;
+        lse[t] = r.lse;
+        if (ENTROPY) entropy[t] = r.entropy;
+        if (cleared) cleared[t] = 0.0f;
+    }
+    if (size > 1 && y >= 0) cg::this_cluster().sync();  // no CTA leaves while another reads its sums
 }
 
-// dx_j = g [j = y] - 2^d_j (ka + kb d_j), d_j = log2 p_j = (x_j - base) c - off.
-// log p is rebuilt from whichever is the smaller number and so the more exact in fp32: the
-// target's log-probability (base = its logit) or lse.
+// dx_j = g [j = y] - 2^d_j (ka + kb d_j) with d_j = (x_j - base) c - off, so that 2^d_j is p_j or
+// a multiple of it that ka and kb make up for.
 struct GradRow {
     float g, ka, kb, base, off;
 };
 
-__device__ __forceinline__ GradRow grad_row(float g, float h, float x_y, float logp, float lse, float entropy, double inv_t_d) {
+// From what zero_token_logp gave. log p is rebuilt from whichever is the smaller number and so
+// the more exact in fp32: the target's log-probability (base = its logit) or lse.
+__device__ __forceinline__ GradRow grad_row(float g, float h, float x_y, float logp, float lse, float entropy, double inv_t) {
     GradRow r;
-    const float inv_t = (float)inv_t_d;
+    const float i = (float)inv_t;
     if (fabsf(logp) <= fabsf(lse)) {
         r.base = x_y;
         r.off = -logp * kLog2e;
     } else {
-        r.base = lse / inv_t;
-        r.off = (float)(((double)lse - (double)r.base * inv_t_d) * 1.4426950408889634);
+        r.base = lse / i;
+        r.off = (float)(((double)lse - (double)r.base * inv_t) * 1.4426950408889634);
     }
-    r.g = g * inv_t;
-    r.ka = inv_t * (h == 0.0f ? g : fmaf(h, entropy, g));
-    r.kb = inv_t * h * kLn2;
+    r.g = g * i;
+    r.ka = i * (h == 0.0f ? g : fmaf(h, entropy, g));
+    r.kb = i * h * kLn2;
     return r;
 }
 
-__device__ __forceinline__ float grad_term(const GradRow& r, float x, float c) {
+// From a row's sums: 2^d_j = s p_j, and log p_j = (d_j - log2 s) ln 2.
+__device__ __forceinline__ GradRow grad_row(float g, float h, const RowStat& a, float entropy, double inv_t) {
+    const float i = (float)inv_t, f = i / a.s;
+    return {g * i, f * (h == 0.0f ? g : fmaf(h, entropy - log2f(a.s) * kLn2, g)), f * h * kLn2, base_of(a.m), 0.0f};
+}
+
+// One element, in the very operations of grad_vector: the bits do not depend on alignment.
+template <bool H>
+__device__ __forceinline__ float grad_term(const GradRow& r, float x, float c, bool target) {
     const float d = fmaf(x - r.base, c, -r.off);
-    return -pow2(d) * fmaf(r.kb, fmaxf(d, kFar), r.ka);
+    const float f = __fmul_rn(pow2(d), H ? fmaf(-r.kb, fmaxf(d, kFar), -r.ka) : -r.ka);
+    return target ? __fadd_rn(f, r.g) : f;
+}
+
+// 16 bytes of a row; dy is the target's place in them (outside 0 .. kVec - 1: elsewhere).
+template <class T, bool H>
+__device__ __forceinline__ uint4 grad_vector(const GradRow& r, const uint4& x, float c, int64_t dy) {
+    const uint64_t base = pack2(-r.base, -r.base), c2 = pack2(c, c), off = pack2(-r.off, -r.off);
+    const uint64_t ka = pack2(-r.ka, -r.ka), kb = pack2(-r.kb, -r.kb);
+    uint64_t f[kVec<T> / 2];
+#pragma unroll
+    for (int i = 0; i < kVec<T> / 2; ++i) {
+        const uint64_t d = fma2(add2(widen2<T>(x, i), base), c2, off);
+        const float2 df = unpack2(d);
+        const uint64_t e = pack2(pow2(df.x), pow2(df.y));
+        f[i] = mul2(e, H ? fma2(kb, pack2(fmaxf(df.x, kFar), fmaxf(df.y, kFar)), ka) : ka);
+    }
+    uint4 out;
+    if (dy >= 0 && dy < kVec<T>) {
+#pragma unroll
+        for (int i = 0; i < kVec<T> / 2; ++i) {
+            float2 u = unpack2(f[i]);
+            if (dy == 2 * i) u.x += r.g;
+            if (dy == 2 * i + 1) u.y += r.g;
+            f[i] = pack2(u.x, u.y);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kVec<T> / 2; ++i) narrow2<T>(out, i, unpack2(f[i]));
+    return out;
+}
+
+// Zeros into this CTA's share of a row of another alignment than its own.
+template <class T, int THREADS>
+__device__ __forceinline__ void zero_row(T* out, int64_t n, int rank, int size) {
+    const Slice s = slice_of(out, n, rank, size);
+    uint4* v = const_cast<uint4*>(vectors(out));
+    for (int64_t i = s.lo + threadIdx.x; i < s.hi; i += THREADS) __stcs(v + i, make_uint4(0, 0, 0, 0));
+    if (threadIdx.x < s.head) out[threadIdx.x] = narrow<T>(0.0f);
+    if (threadIdx.x < s.tail) out[s.tail_at + threadIdx.x] = narrow<T>(0.0f);
 }
 
 template <class T>
-__global__ void __launch_bounds__(kRowThreads)
-    k_token_grad(const Rows<T> a, const float* logp, const float* lse, const float* entropy, const float* dlogp,
-                 const float* dentropy, T* dx, int64_t dstride) {
-    for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
-        const int64_t y = live_target(a, t);
-        const float g = y < 0 ? 0.0f : dlogp[t], h = y < 0 || !dentropy ? 0.0f : dentropy[t];
-        T* out = dx + t * dstride;
-        if ((g == 0.0f && h == 0.0f) || lse[t] == -INFINITY) {
-            for (int64_t j = threadIdx.x; j < a.vocab; j += kRowThreads) out[j] = narrow<T>(0.0f);
-            continue;
+__device__ __forceinline__ bool same_alignment(const T* a, const T* b) {
+    return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0;
+}
+
+// Backward, bound by reading and writing the logits once. Where the gradient's rows have another
+// alignment than the logits', elements are taken one at a time.
+template <class T, bool H>
+__device__ __forceinline__ void write_grad(const Rows<T>& a, const GradRow& r, const T* x, T* out, int64_t y, int rank, int size) {
+    const Slice s = slice_of(x, a.vocab, rank, size);
+    const int64_t head = (reinterpret_cast<uintptr_t>(vectors(x)) - reinterpret_cast<uintptr_t>(x)) / sizeof(T);
+    const uint4* v = vectors(x);
+    if (same_alignment(x, out)) {
+        uint4* w = const_cast<uint4*>(vectors(out));
+        for (int64_t i = s.lo + threadIdx.x; i < s.hi; i += kUnroll * kRowThreads) {
+            uint4 q[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (i + u * kRowThreads < s.hi) q[u] = __ldcs(v + i + u * kRowThreads);
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int64_t k = i + u * kRowThreads;
+                if (k < s.hi) __stcs(w + k, grad_vector<T, H>(r, q[u], a.c, y - head - k * kVec<T>));
+            }
         }
-        const T* x = a.x + t * a.stride;
-        const GradRow r = grad_row(y < a.vocab ? g : NAN, h, y < a.vocab ? widen(x[y]) : NAN, logp[t], lse[t],
-                                   h != 0.0f ? entropy[t] : 0.0f, a.inv_t);
-        if (out == x) __syncthreads();  // the target's logit is read before any thread writes it
-        for (int64_t j = threadIdx.x; j < a.vocab; j += kRowThreads)
-            out[j] = narrow<T>(grad_term(r, widen(x[j]), a.c) + (j == y ? r.g : 0.0f));
+    } else {
+        for (int64_t j = head + s.lo * kVec<T> + threadIdx.x; j < head + s.hi * kVec<T>; j += kRowThreads)
+            out[j] = narrow<T>(grad_term<H>(r, widen(x[j]), a.c, j == y));
     }
+    if (threadIdx.x < s.head) out[threadIdx.x] = narrow<T>(grad_term<H>(r, widen(x[threadIdx.x]), a.c, threadIdx.x == y));
+    const int64_t j = s.tail_at + threadIdx.x;
+    if (threadIdx.x < s.tail) out[j] = narrow<T>(grad_term<H>(r, widen(x[j]), a.c, j == y));
+}
+
+template <class T, bool H>
+__global__ void __launch_bounds__(kRowThreads)
+    k_token_grad(const Rows<T> a, int size, const float* logp, const float* lse, const float* entropy, const float* dlogp,
+                 const float* dentropy, T* dx, int64_t dstride) {
+    let_next_kernel_start();
+    wait_for_kernel_before();
+    const int64_t t = blockIdx.x / size;
+    const int rank = (int)(blockIdx.x % size);
+    const int64_t y = live_target(a, t);
+    const float g = y < 0 ? 0.0f : dlogp[t], h = y < 0 || !H ? 0.0f : dentropy[t];
+    T* out = dx + t * dstride;
+    if ((g == 0.0f && h == 0.0f) || lse[t] == -INFINITY) {
+        zero_row<T, kRowThreads>(out, a.vocab, rank, size);
+        return;
+    }
+    const T* x = a.x + t * a.stride;
+    const GradRow r = grad_row(y < a.vocab ? g : NAN, h, y < a.vocab ? widen(x[y]) : NAN, logp[t], lse[t],
+                               h != 0.0f ? entropy[t] : 0.0f, a.inv_t);
+    if (out == x) {  // the target's logit is read before any thread writes it
+        if (size > 1) cg::this_cluster().sync();
+        else __syncthreads();
+    }
+    write_grad<T, H>(a, r, x, out, y, rank, size);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -210,10 +349,6 @@ __global__ void __launch_bounds__(1024) k_mean(const float* x, int64_t n, float*
     for (int64_t i = threadIdx.x; i < n; i += 1024) s += (double)x[i];
     s = cta_sum<1024>(s, sm);
     if (threadIdx.x == 0) *out = (float)(s / (double)n);
-}
-
-__global__ void __launch_bounds__(kRowThreads) k_zero(float* x, int64_t n) {
-    for (int64_t i = blockIdx.x * (int64_t)kRowThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kRowThreads) x[i] = 0.0f;
 }
 
 // ---------------------------------------------------------------------------------------
@@ -372,7 +507,7 @@ __global__ void __launch_bounds__(kSetupThreads) k_policy_finish(const PolicyTok
 // Host side.
 // ---------------------------------------------------------------------------------------
 int check_logits(const zero_logits* x) {
-    if (!x || x->rows < 0 || x->vocab < 1 || x->vocab > INT32_MAX || x->stride < x->vocab || !type_ok(x->type)) return ZERO_ERR_INVALID_ARG;
+    if (!x || x->rows < 0 || x->rows > INT32_MAX || x->vocab < 1 || x->vocab > INT32_MAX || x->stride < x->vocab || !type_ok(x->type)) return ZERO_ERR_INVALID_ARG;
     if (!(x->temperature > 0.0) || !std::isfinite(x->temperature)) return ZERO_ERR_INVALID_ARG;
     if (x->rows > 0 && x->stride > INT64_MAX / 8 / x->rows) return ZERO_ERR_INVALID_ARG;
     return ZERO_OK;
@@ -405,27 +540,37 @@ int by_type(int32_t type, F f) {
     return f(float());
 }
 
-int row_grid(int64_t rows) { return (int)(rows < (1 << 20) ? rows : (1 << 20)); }
+// CTAs per row: 1 where the rows fill the GPU, else the row is cut (into at most 8, of 4 KB at
+// least), until every SM has two.
+int ctas_per_row(const zero_logits* x, int sms) {
+    int size = 1;
+    while (size < 8 && 2 * size * x->rows <= 2 * (int64_t)sms && x->vocab * type_size(x->type) / (2 * size) >= 4096) size *= 2;
+    return size;
+}
 
-int launch_token_logp(const zero_logits* x, const float* weight, float* logp, float* lse, float* entropy, cudaStream_t s) {
+int launch_token_logp(const zero_logits* x, const float* weight, float* logp, float* lse, float* entropy, float* cleared, int sms,
+                      cudaStream_t s) {
     if (x->rows == 0) return ZERO_OK;
     return by_type(x->type, [&](auto tag) {
         using T = decltype(tag);
         const Rows<T> a = rows_of<T>(x, weight);
-        if (entropy) k_token_logp<T, true><<<row_grid(x->rows), kRowThreads, 0, s>>>(a, logp, lse, entropy);
-        else k_token_logp<T, false><<<row_grid(x->rows), kRowThreads, 0, s>>>(a, logp, lse, entropy);
-        return launched();
+        const int size = ctas_per_row(x, sms);
+        const unsigned grid = (unsigned)(x->rows * size);
+        return launch_linked(entropy ? k_token_logp<T, true> : k_token_logp<T, false>, grid, kRowThreads, 0, size, s, a, size, logp, lse,
+                             entropy, cleared);
     });
 }
 
 int launch_token_grad(const zero_logits* x, const float* weight, const float* logp, const float* lse, const float* entropy,
-                      const float* g, const float* h, void* dx, int64_t dstride, cudaStream_t s) {
+                      const float* g, const float* h, void* dx, int64_t dstride, int sms, cudaStream_t s) {
     if (x->rows == 0) return ZERO_OK;
     return by_type(x->type, [&](auto tag) {
         using T = decltype(tag);
-        k_token_grad<T><<<row_grid(x->rows), kRowThreads, 0, s>>>(rows_of<T>(x, weight), logp, lse, entropy, g, h,
-                                                                  (T*)dx, dstride);
-        return launched();
+        const Rows<T> a = rows_of<T>(x, weight);
+        const int size = ctas_per_row(x, sms);
+        const unsigned grid = (unsigned)(x->rows * size);
+        return launch_linked(h ? k_token_grad<T, true> : k_token_grad<T, false>, grid, kRowThreads, 0, size, s, a, size, logp, lse,
+                             entropy, g, h, (T*)dx, dstride);
     });
 }
 
@@ -451,7 +596,7 @@ extern "C" int zero_token_logp(const zero_logits* x, float* logp, float* lse, fl
     d.need(lse, 4);
     d.optional(entropy, 4);
     if (d.rc) return d.rc;
-    return launch_token_logp(x, nullptr, logp, lse, entropy, (cudaStream_t)stream);
+    return launch_token_logp(x, nullptr, logp, lse, entropy, nullptr, d.sm_count(), (cudaStream_t)stream);
 }
 
 extern "C" int zero_token_logp_backward(const zero_logits* x, const float* logp, const float* lse, const float* entropy,
@@ -469,7 +614,7 @@ extern "C" int zero_token_logp_backward(const zero_logits* x, const float* logp,
     d.optional(dentropy, 4);
     d.need(dlogits, type_size(x->type));
     if (d.rc) return d.rc;
-    return launch_token_grad(x, nullptr, logp, lse, entropy, dlogp, dentropy, dlogits, dstride, (cudaStream_t)stream);
+    return launch_token_grad(x, nullptr, logp, lse, entropy, dlogp, dentropy, dlogits, dstride, d.sm_count(), (cudaStream_t)stream);
 }
 
 extern "C" int64_t zero_preference_workspace(int64_t rows) {
@@ -504,18 +649,15 @@ extern "C" int zero_preference_loss(const zero_logits* x, const zero_preference*
     cudaStream_t s = (cudaStream_t)stream;
     float* lse = (float*)workspace;
     float* g = lse + round_up(x->rows, 4);
-    if (x->rows > 0) {
-        k_zero<<<(int)std::min<int64_t>((x->rows + kRowThreads - 1) / kRowThreads, 1024), kRowThreads, 0, s>>>(g, x->rows);
-        if ((rc = launched())) return rc;
-    }
-    if ((rc = launch_token_logp(x, nullptr, p->logp, lse, nullptr, s))) return rc;
+    const int sms = d.sm_count();
+    if ((rc = launch_token_logp(x, nullptr, p->logp, lse, nullptr, g, sms, s))) return rc;
     const PairArgs a = {x->targets, p->offsets, p->logp, p->ref_logp, g, p->pair_loss, p->chosen_reward, p->rejected_reward,
                         x->rows, p->pairs, p->beta, p->kind == ZERO_PREF_SIGMOID ? p->label_smoothing : 0.0, p->kind, p->average};
     k_pairs<<<(int)std::min<int64_t>(p->pairs, 1 << 20), kRowThreads, 0, s>>>(a);
     if ((rc = launched())) return rc;
     k_mean<<<1, 1024, 0, s>>>(p->pair_loss, p->pairs, p->loss);
     if ((rc = launched())) return rc;
-    return launch_token_grad(x, nullptr, p->logp, lse, nullptr, g, nullptr, p->dlogits, p->dstride, s);
+    return launch_token_grad(x, nullptr, p->logp, lse, nullptr, g, nullptr, p->dlogits, p->dstride, sms, s);
 }
 
 extern "C" int64_t zero_policy_workspace(int64_t rows) {
@@ -581,13 +723,14 @@ extern "C" int zero_policy_loss(const zero_logits* x, const zero_policy* p, void
     a.kl_kind = p->kl;
     a.reduce = p->reduce;
     a.per_sequence = p->per_sequence;
+    const int sms = d.sm_count();
     if (x->rows > 0) {
         k_policy_setup<<<1, kSetupThreads, 0, s>>>(a);
         if ((rc = launched())) return rc;
-        if ((rc = launch_token_logp(x, a.w, p->logp, a.lse, p->entropy, s))) return rc;
+        if ((rc = launch_token_logp(x, a.w, p->logp, a.lse, p->entropy, nullptr, sms, s))) return rc;
         k_policy_tokens<<<(int)std::min<int64_t>((x->rows + kRowThreads - 1) / kRowThreads, 1024), kRowThreads, 0, s>>>(a, p->logp, p->entropy);
         if ((rc = launched())) return rc;
-        rc = launch_token_grad(x, a.w, p->logp, a.lse, p->entropy, a.g, a.entropy_coef != 0.0f ? a.h : nullptr, p->dlogits, p->dstride, s);
+        rc = launch_token_grad(x, a.w, p->logp, a.lse, p->entropy, a.g, a.entropy_coef != 0.0f ? a.h : nullptr, p->dlogits, p->dstride, sms, s);
         if (rc) return rc;
     }
     k_policy_finish<<<1, kSetupThreads, 0, s>>>(a);

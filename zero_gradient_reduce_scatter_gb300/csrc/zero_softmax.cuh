@@ -17,6 +17,10 @@
 
 namespace zg {
 
+// For kernels launched with launch_linked.
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -92,6 +96,154 @@ __device__ __forceinline__ void add_term(RowStat& a, float x, Scale k, float m) 
     a.s += e;
     if (ENTROPY) a.q = fmaf(e, fmaxf(d, kFar), a.q);
 }
+
+// ---- two fp32 numbers in one instruction -------------------------------------------------
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// ---- 16 bytes of a row ---------------------------------------------------------------------
+template <class T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+// Elements 2i and 2i + 1 as fp32.
+template <class T>
+__device__ __forceinline__ uint64_t widen2(const uint4& v, int i);
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+template <>
+__device__ __forceinline__ uint64_t widen2<__nv_bfloat16>(const uint4& v, int i) {
+    const uint32_t w = word(v, i);
+    return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <>
+__device__ __forceinline__ uint64_t widen2<__half>(const uint4& v, int i) {
+    const uint32_t w = word(v, i);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return pack2(f.x, f.y);
+}
+template <>
+__device__ __forceinline__ uint64_t widen2<float>(const uint4& v, int i) {
+    return pack2(__uint_as_float(word(v, 2 * i)), __uint_as_float(word(v, 2 * i + 1)));
+}
+// The largest element; a NaN beside numbers is passed over (its term makes the sum NaN).
+template <class T>
+__device__ __forceinline__ float max_of(const uint4& v);
+template <>
+__device__ __forceinline__ float max_of<__nv_bfloat16>(const uint4& v) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+template <>
+__device__ __forceinline__ float max_of<__half>(const uint4& v) {
+    const __half2* h = reinterpret_cast<const __half2*>(&v);
+    const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+template <>
+__device__ __forceinline__ float max_of<float>(const uint4& v) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+// Two fp32 numbers rounded to the row's type, for word i of 16 bytes.
+template <class T>
+__device__ __forceinline__ void narrow2(uint4& v, int i, float2 f);
+__device__ __forceinline__ void set_word(uint4& v, int i, uint32_t w) {
+    if (i == 0) v.x = w;
+    else if (i == 1) v.y = w;
+    else if (i == 2) v.z = w;
+    else v.w = w;
+}
+template <>
+__device__ __forceinline__ void narrow2<__nv_bfloat16>(uint4& v, int i, float2 f) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+    set_word(v, i, *reinterpret_cast<const uint32_t*>(&h));
+}
+template <>
+__device__ __forceinline__ void narrow2<__half>(uint4& v, int i, float2 f) {
+    const __half2 h = __floats2half2_rn(f.x, f.y);
+    set_word(v, i, *reinterpret_cast<const uint32_t*>(&h));
+}
+template <>
+__device__ __forceinline__ void narrow2<float>(uint4& v, int i, float2 f) {
+    set_word(v, 2 * i, __float_as_uint(f.x));
+    set_word(v, 2 * i + 1, __float_as_uint(f.y));
+}
+
+// One thread's running sums. The base follows the maximum only when a value exceeds it by a
+// factor 2^40: the sums are floating-point, so any base near the maximum is as exact, and
+// comparing costs a fraction of rescaling at every new maximum.
+template <class T, bool ENTROPY>
+struct RunningStat {
+    float m, limit;  // base, and the largest value that is taken over it
+    uint64_t s[2], q[2];
+    Scale k;
+    float margin;
+
+    __device__ __forceinline__ explicit RunningStat(Scale k) : k(k), margin(40.0f / k.c) {
+        m = limit = -INFINITY;
+        s[0] = s[1] = q[0] = q[1] = pack2(0.0f, 0.0f);
+    }
+    __device__ __forceinline__ void raise(float top) {
+        const float to = base_of(top), shift = scaled(m - to, k), f = pow2(shift);
+        const uint64_t f2 = pack2(f, f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (ENTROPY) {
+                const float d = fmaxf(shift, kFar);
+                q[i] = mul2(f2, fma2(s[i], pack2(d, d), q[i]));
+            }
+            s[i] = mul2(s[i], f2);
+        }
+        m = top;
+        limit = top + margin;
+    }
+    __device__ __forceinline__ void term(int i, uint64_t x, uint64_t base, uint64_t c, uint64_t lo) {
+        const uint64_t t = add2(x, base), d = fma2(t, lo, mul2(t, c));
+        const float2 df = unpack2(d);
+        const uint64_t e = pack2(pow2(df.x), pow2(df.y));
+        s[i] = add2(s[i], e);
+        if (ENTROPY) q[i] = fma2(e, pack2(fmaxf(df.x, kFar), fmaxf(df.y, kFar)), q[i]);
+    }
+    __device__ __forceinline__ void add(const uint4& v) {
+        const float top = max_of<T>(v);
+        if (top > limit) raise(top);
+        const float b = -base_of(m);
+        const uint64_t base = pack2(b, b), c = pack2(k.c, k.c), lo = pack2(k.lo, k.lo);
+#pragma unroll
+        for (int i = 0; i < kVec<T> / 2; ++i) term(i & 1, widen2<T>(v, i), base, c, lo);
+    }
+    __device__ __forceinline__ void add_one(float x) {
+        if (x > limit) raise(x);
+        const float b = -base_of(m);
+        term(0, pack2(x, -INFINITY), pack2(b, b), pack2(k.c, k.c), pack2(k.lo, k.lo));
+    }
+    __device__ __forceinline__ RowStat stat() const {
+        const float2 a = unpack2(add2(s[0], s[1])), b = unpack2(add2(q[0], q[1]));
+        return {m, a.x + a.y, ENTROPY ? b.x + b.y : 0.0f};
+    }
+};
 
 // Joins the parts of all threads of a CTA, in a fixed order; the result is valid everywhere.
 template <bool ENTROPY, int THREADS>

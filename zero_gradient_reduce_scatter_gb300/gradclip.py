@@ -13,7 +13,7 @@ from typing import NamedTuple
 import torch
 
 from . import _check, _lib
-from .losses import TYPES, _handle, _on
+from .losses import TYPES, _floats, _handle, _on
 
 
 class GradTensor(ctypes.Structure):
@@ -74,11 +74,10 @@ class GradClip:
         """Measure, and write gradient * min(1, max_norm / norm). A norm that is not finite leaves
         the values as they are (scale 1). max_norm may be infinite."""
         with _on(stream):
-            r = torch.empty(2 + len(self.grads), dtype=torch.float32, device=self.device)
-        base = r.data_ptr()
-        _check(_lib().zero_grads_clip(self._plan, max_norm, base, base + 4, base + 8, _handle(stream, self.device)),
-               "zero_grads_clip")
-        return Clipped(r[0], r[1], r[2:])
+            norm, scale, norms = _floats(self.device), _floats(self.device), _floats(self.device, len(self.grads))
+        _check(_lib().zero_grads_clip(self._plan, max_norm, norm.data_ptr(), scale.data_ptr(), norms.data_ptr(),
+                                      _handle(stream, self.device)), "zero_grads_clip")
+        return Clipped(norm, scale, norms)
 
     def close(self):
         if getattr(self, "_plan", None) is not None and self._plan.value:

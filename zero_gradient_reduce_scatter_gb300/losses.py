@@ -90,8 +90,19 @@ class PolicyLoss(NamedTuple):
     dlogits: torch.Tensor              # [T, V] of the logits' type
 
 
+_NOTHING = contextlib.nullcontext()
+
+
 def _on(stream):
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _NOTHING if stream is None else torch.cuda.stream(stream)
+
+
+def _floats(device, *shape):
+    return torch.empty(shape, dtype=torch.float32, device=device)
+
+
+def _bytes(device, size):
+    return torch.empty(size, dtype=torch.uint8, device=device)
 
 
 def _handle(stream, device) -> int:
@@ -144,12 +155,13 @@ def _gradient(logits, a, out):
 def token_logp(logits, targets, *, temperature: float = 1.0, entropy: bool = False, stream=None) -> TokenLogp:
     """Log-probabilities of targets [T] (int64) under logits [T, V] / temperature."""
     a = _logits(logits, targets, temperature)
-    with _on(stream):
-        r = torch.empty((3 if entropy else 2, a.rows), dtype=torch.float32, device=logits.device)
-    out = r.unbind(0)
-    _check(_lib().zero_token_logp(ctypes.byref(a), out[0].data_ptr(), out[1].data_ptr(),
-                                  out[2].data_ptr() if entropy else None, _handle(stream, logits.device)), "zero_token_logp")
-    return TokenLogp(out[0], out[1], out[2] if entropy else None)
+    dev = logits.device
+    with _on(stream):  # a tensor each: views of one allocation cost more host time than the allocations
+        logp, lse = _floats(dev, a.rows), _floats(dev, a.rows)
+        ent = _floats(dev, a.rows) if entropy else None
+    _check(_lib().zero_token_logp(ctypes.byref(a), logp.data_ptr(), lse.data_ptr(), ent.data_ptr() if entropy else None,
+                                  _handle(stream, dev)), "zero_token_logp")
+    return TokenLogp(logp, lse, ent)
 
 
 def token_logp_backward(logits, targets, forward: TokenLogp, dlogp, dentropy=None, *, temperature: float = 1.0, out=None,
@@ -187,12 +199,11 @@ def linear_logp(hidden, weight, targets, *, temperature: float = 1.0, entropy: b
                ld_h, ld_w, TYPES[hidden.dtype], temperature)
     size = _lib().zero_linear_logp_workspace(rows, vocab)
     with _on(stream):
-        r = torch.empty((3 if entropy else 2, rows), dtype=torch.float32, device=dev)
-        ws = torch.empty(max(size, 0), dtype=torch.uint8, device=dev)
-    out = r.unbind(0)
-    _check(_lib().zero_linear_logp(ctypes.byref(a), out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr() if entropy else None,
+        logp, lse, ws = _floats(dev, rows), _floats(dev, rows), _bytes(dev, max(size, 0))
+        ent = _floats(dev, rows) if entropy else None
+    _check(_lib().zero_linear_logp(ctypes.byref(a), logp.data_ptr(), lse.data_ptr(), ent.data_ptr() if entropy else None,
                                    ws.data_ptr(), size, _handle(stream, dev)), "zero_linear_logp")
-    return TokenLogp(out[0], out[1], out[2] if entropy else None)
+    return TokenLogp(logp, lse, ent)
 
 
 def preference_loss(logits, targets, offsets, ref_logp=None, *, beta: float = 0.1, kind: str = "sigmoid",
@@ -210,14 +221,13 @@ def preference_loss(logits, targets, offsets, ref_logp=None, *, beta: float = 0.
     size = _lib().zero_preference_workspace(a.rows)
     with _on(stream):
         out, dstride = _gradient(logits, a, out)
-        r = torch.empty(1 + 3 * pairs + a.rows, dtype=f32, device=dev)
-        ws = torch.empty(size, dtype=torch.uint8, device=dev)
-    loss, pair_loss, chosen, rejected, logp = r.split((1, pairs, pairs, pairs, a.rows))
+        loss, logp, ws = _floats(dev), _floats(dev, a.rows), _bytes(dev, size)
+        pair_loss, chosen, rejected = _floats(dev, pairs), _floats(dev, pairs), _floats(dev, pairs)
     p = Preference(off, ref, pairs, beta, label_smoothing, PREFERENCE[kind], 1 if average else 0, loss.data_ptr(),
                    pair_loss.data_ptr(), chosen.data_ptr(), rejected.data_ptr(), logp.data_ptr(), out.data_ptr(), dstride)
     _check(_lib().zero_preference_loss(ctypes.byref(a), ctypes.byref(p), ws.data_ptr(), size, _handle(stream, dev)),
            "zero_preference_loss")
-    return PreferenceLoss(loss[0], pair_loss, chosen, rejected, logp, out)
+    return PreferenceLoss(loss, pair_loss, chosen, rejected, logp, out)
 
 
 def policy_loss(logits, targets, advantages, old_logp=None, ref_logp=None, *, offsets=None, clip_low: float = 0.2,
@@ -248,14 +258,12 @@ def policy_loss(logits, targets, advantages, old_logp=None, ref_logp=None, *, of
     size = _lib().zero_policy_workspace(a.rows)
     with _on(stream):
         out, dstride = _gradient(logits, a, out)
-        r = torch.empty(3 + (2 if with_entropy else 1) * a.rows, dtype=f32, device=dev)
-        ws = torch.empty(size, dtype=torch.uint8, device=dev)
-    logp = r[3:3 + a.rows]
-    entropy = r[3 + a.rows:] if with_entropy else None
-    base = r.data_ptr()
+        loss, clip_fraction, kl_mean, ws = _floats(dev), _floats(dev), _floats(dev), _bytes(dev, size)
+        logp = _floats(dev, a.rows)
+        entropy = _floats(dev, a.rows) if with_entropy else None
     p = Policy(adv, old, ref, off, seqs, clip_low, clip_high, dual_clip, kl_coef, entropy_coef, KL[kl], REDUCE[reduce],
-               1 if per_sequence else 0, base, base + 4, base + 8, logp.data_ptr(), entropy.data_ptr() if with_entropy else None,
+               1 if per_sequence else 0, loss.data_ptr(), clip_fraction.data_ptr(), kl_mean.data_ptr(), logp.data_ptr(), entropy.data_ptr() if with_entropy else None,
                out.data_ptr(), dstride)
     _check(_lib().zero_policy_loss(ctypes.byref(a), ctypes.byref(p), ws.data_ptr(), size, _handle(stream, dev)),
            "zero_policy_loss")
-    return PolicyLoss(r[0], r[1], r[2], logp, entropy, out)
+    return PolicyLoss(loss, clip_fraction, kl_mean, logp, entropy, out)
