@@ -358,6 +358,10 @@ POLICY = [  # lens, reduce, advantages per, old, ref, kl, kl_coef, entropy_coef,
     ([64, 64, 64], "sum", "token", False, True, "k3", 0.02, 0.0, 0.0, 1.3, 513, "fp32"),
     (None, "token", "token", True, True, "k3", 0.1, 0.02, 0.0, 1.0, 50257, "bf16"),
     (None, "sum", "token", False, False, "k3", 0.0, 0.0, 0.0, 1.0, 130, "fp16"),
+    # rows cut over a cluster, and rows too long for one
+    ([3, 2], "token", "token", True, True, "k3", 0.1, 0.02, 0.0, 1.0, 131073, "bf16"),
+    ([3, 2], "sequence", "sequence", True, True, "k3", 0.1, 0.02, 3.0, 1.0, 300001, "fp32"),
+    ([310], "token", "token", True, False, "k3", 0.0, 0.01, 0.0, 1.0, 60001, "bf16"),
 ]
 
 

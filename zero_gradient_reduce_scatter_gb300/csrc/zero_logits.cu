@@ -12,6 +12,7 @@
 
 #include "zero_host.h"
 #include "zero_softmax.cuh"
+#include "zero_tcgen05.cuh"
 
 namespace zg {
 namespace {
@@ -381,6 +382,7 @@ __device__ __forceinline__ int64_t warp_sum(int64_t x) {
 __global__ void __launch_bounds__(kSetupThreads) k_policy_setup(const PolicyTokens a) {
     __shared__ unsigned long long total, nonempty;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = kSetupThreads / 32;
+    let_next_kernel_start();
     if (threadIdx.x == 0) total = nonempty = 0;
     __syncthreads();
     for (int64_t t = threadIdx.x; t < a.rows; t += kSetupThreads) a.w[t] = 0.0f;
@@ -470,6 +472,110 @@ __device__ __forceinline__ TokenLoss policy_token(const PolicyTokens& a, int64_t
     return r;
 }
 
+// Forward and backward of a row in one pass over it: its slice is brought to shared memory by
+// bulk copies, read once for the sums as it arrives, joined over the cluster, and read again for
+// the gradient. So the logits cross HBM once each way, where a second pass over them would read
+// them again. Two CTAs of 512 threads per SM: one waits for its copies or its sums while the
+// other computes.
+constexpr int kFusedThreads = 512, kChunks = 8;
+constexpr int64_t kFusedBytes = 110 * 1024;  // of a slice: two fit an SM
+
+template <class T, bool H>
+__global__ void __launch_bounds__(kFusedThreads, 2)
+    k_policy_rows(const Rows<T> a, const PolicyTokens p, int size, float* logp, float* entropy, T* dx, int64_t dstride) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ RowStat sm[kFusedThreads / 32], mine;
+    __shared__ GradRow shared_row;
+    __shared__ bool shared_zero;
+    __shared__ uint64_t bars[kChunks];
+    __shared__ int gave_up;
+    const int64_t t = blockIdx.x / size;
+    const int rank = (int)(blockIdx.x % size);
+    // The kernel before this one sets up the weights and was itself launched behind the logits'
+    // producer, so logits and targets may be read at once.
+    const int64_t y = a.targets[t];
+    T* out = dx + t * dstride;
+    if (y < 0) {
+        wait_for_kernel_before();
+        zero_row<T, kFusedThreads>(out, a.vocab, rank, size);
+        if (threadIdx.x == 0 && rank == 0) {
+            logp[t] = p.loss[t] = p.kl[t] = p.clipped[t] = 0.0f;
+            if (entropy) entropy[t] = 0.0f;
+        }
+        return;
+    }
+    const T* x = a.x + t * a.stride;
+    const Slice s = slice_of(x, a.vocab, rank, size);
+    const int n = (int)(s.hi - s.lo), per = (n + kChunks - 1) / kChunks;  // vectors, and of one copy
+    const uint4* v = reinterpret_cast<const uint4*>(smem);
+    if (threadIdx.x == 0) {
+        gave_up = 0;
+        for (int i = 0; i < kChunks; ++i) mbar_init(smem_addr(bars + i), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        for (int i = 0; i < kChunks; ++i) {
+            const int at = min(n, i * per), bytes = 16 * (min(n, at + per) - at);
+            mbar_expect(smem_addr(bars + i), bytes);
+            if (bytes) bulk_load(smem_addr(smem) + 16 * at, vectors(x) + s.lo + at, bytes, smem_addr(bars + i));
+        }
+    }
+    __syncthreads();
+    RunningStat<T, H> run(a.k);
+    if (threadIdx.x < s.head) run.add_one(widen(x[threadIdx.x]));
+    if (threadIdx.x < s.tail) run.add_one(widen(x[s.tail_at + threadIdx.x]));
+    bool ok = true;
+    for (int i = 0; i < kChunks; ++i) {
+        ok = ok && mbar_wait(smem_addr(bars + i), 0, &gave_up);
+        const int end = min(n, (i + 1) * per);
+        for (int j = i * per + threadIdx.x; j < end; j += kFusedThreads) run.add(v[j]);
+    }
+    const float x_y = threadIdx.x == 0 && y < a.vocab ? widen(x[y]) : NAN;  // before any CTA writes
+    RowStat st = run.stat();
+    if (!ok) st.s = NAN;  // a copy did not come: no result
+    st = cta_join<H, kFusedThreads>(st, a.k, sm);
+    st = cluster_join<H>(st, size, a.k, &mine);
+    wait_for_kernel_before();
+    if (threadIdx.x == 0) {
+        const float w = p.w[t];
+        RowResult r = {0.0f, 0.0f, 0.0f};
+        TokenLoss l = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (w != 0.0f) {
+            r = finish_row(st, x_y, a.inv_t);
+            if (y >= a.vocab) r.logp = NAN;
+            l = policy_token(p, t, w, r.logp, r.entropy);
+        }
+        shared_zero = (l.g == 0.0f && l.h == 0.0f) || st.s == 0.0f;
+        shared_row = grad_row(l.g, l.h, st, r.entropy, a.inv_t);
+        if (rank == 0) {
+            logp[t] = r.logp;
+            if (entropy) entropy[t] = r.entropy;
+            p.loss[t] = l.loss;
+            p.kl[t] = l.kl;
+            p.clipped[t] = l.clipped;
+        }
+    }
+    __syncthreads();
+    if (shared_zero) {
+        zero_row<T, kFusedThreads>(out, a.vocab, rank, size);
+    } else {
+        const GradRow r = shared_row;
+        const int64_t head = (reinterpret_cast<uintptr_t>(vectors(x)) - reinterpret_cast<uintptr_t>(x)) / sizeof(T);
+        const int64_t first = head + s.lo * kVec<T>;  // element of the slice's first vector
+        if (same_alignment(x, out)) {
+            uint4* to = const_cast<uint4*>(vectors(out)) + s.lo;
+            for (int j = threadIdx.x; j < n; j += kFusedThreads)
+                __stcs(to + j, grad_vector<T, H>(r, v[j], a.c, y - first - (int64_t)j * kVec<T>));
+        } else {
+            const T* e = reinterpret_cast<const T*>(smem);
+            for (int j = threadIdx.x; j < n * kVec<T>; j += kFusedThreads)
+                out[first + j] = narrow<T>(grad_term<H>(r, widen(e[j]), a.c, first + j == y));
+        }
+        if (threadIdx.x < s.head) out[threadIdx.x] = narrow<T>(grad_term<H>(r, widen(x[threadIdx.x]), a.c, threadIdx.x == y));
+        const int64_t j = s.tail_at + threadIdx.x;
+        if (threadIdx.x < s.tail) out[j] = narrow<T>(grad_term<H>(r, widen(x[j]), a.c, j == y));
+    }
+    if (size > 1) cg::this_cluster().sync();  // no CTA leaves while another reads its sums
+}
+
 __global__ void __launch_bounds__(kRowThreads) k_policy_tokens(const PolicyTokens a, const float* logp, const float* entropy) {
     for (int64_t t = blockIdx.x * (int64_t)kRowThreads + threadIdx.x; t < a.rows; t += (int64_t)gridDim.x * kRowThreads) {
         const float w = a.w[t];
@@ -485,6 +591,7 @@ __global__ void __launch_bounds__(kRowThreads) k_policy_tokens(const PolicyToken
 
 __global__ void __launch_bounds__(kSetupThreads) k_policy_finish(const PolicyTokens a) {
     __shared__ double sm[kSetupThreads];
+    wait_for_kernel_before();
     double loss = 0.0, kl = 0.0, clipped = 0.0, n = 0.0;
     for (int64_t t = threadIdx.x; t < a.rows; t += kSetupThreads) {
         loss += (double)a.loss[t];
@@ -548,6 +655,12 @@ int ctas_per_row(const zero_logits* x, int sms) {
     return size;
 }
 
+// Shared memory for one CTA's share of a row.
+int64_t fused_bytes(const zero_logits* x, int size) {
+    const int64_t vecs = x->vocab * type_size(x->type) / 16;
+    return 16 * ((vecs + size - 1) / size);
+}
+
 int launch_token_logp(const zero_logits* x, const float* weight, float* logp, float* lse, float* entropy, float* cleared, int sms,
                       cudaStream_t s) {
     if (x->rows == 0) return ZERO_OK;
@@ -572,6 +685,28 @@ int launch_token_grad(const zero_logits* x, const float* weight, const float* lo
         return launch_linked(h ? k_token_grad<T, true> : k_token_grad<T, false>, grid, kRowThreads, 0, size, s, a, size, logp, lse,
                              entropy, g, h, (T*)dx, dstride);
     });
+}
+
+// CTAs per row of the one-pass kernel: enough that a slice fits, then as ctas_per_row. 0: the row
+// is too long for eight CTAs (over 450,000 16-bit logits), and takes two passes.
+int fused_size(const zero_logits* x, int sms) {
+    int size = ctas_per_row(x, sms);
+    while (size <= 8 && fused_bytes(x, size) > kFusedBytes) size *= 2;
+    return size <= 8 ? size : 0;
+}
+
+int launch_policy_rows(const zero_logits* x, const PolicyTokens& p, const zero_policy* q, int sms, cudaStream_t s) {
+    const int size = fused_size(x, sms);
+    const int rc = by_type(x->type, [&](auto tag) {
+        using T = decltype(tag);
+        auto* kernel = q->entropy_coef != 0.0 ? k_policy_rows<T, true> : k_policy_rows<T, false>;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFusedBytes);
+        if (e != cudaSuccess) return record_cuda_error(e);
+        return launch_linked(kernel, (unsigned)(x->rows * size), kFusedThreads, (size_t)fused_bytes(x, size), size, s,
+                             rows_of<T>(x, nullptr), p, size, q->logp, q->entropy, (T*)q->dlogits, q->dstride);
+    });
+    if (rc) return rc;
+    return launch_linked(k_policy_finish, 1, kSetupThreads, 0, 1, s, p);
 }
 
 int check_dlogits(const zero_logits* x, const void* dx, int64_t dstride) {
@@ -727,6 +862,7 @@ extern "C" int zero_policy_loss(const zero_logits* x, const zero_policy* p, void
     if (x->rows > 0) {
         k_policy_setup<<<1, kSetupThreads, 0, s>>>(a);
         if ((rc = launched())) return rc;
+        if (fused_size(x, sms)) return launch_policy_rows(x, a, p, sms, s);
         if ((rc = launch_token_logp(x, a.w, p->logp, a.lse, p->entropy, nullptr, sms, s))) return rc;
         k_policy_tokens<<<(int)std::min<int64_t>((x->rows + kRowThreads - 1) / kRowThreads, 1024), kRowThreads, 0, s>>>(a, p->logp, p->entropy);
         if ((rc = launched())) return rc;

@@ -1,5 +1,4 @@
-// Inline PTX of the tensor-core kernels: mbarriers, tiled TMA loads, tcgen05 with accumulators
-// in TMEM. Every wait has an iteration limit.
+// Inline PTX: mbarriers, bulk and tiled TMA loads, tcgen05 with accumulators in TMEM. Every wait has an iteration limit.
 #pragma once
 
 #include <cstdint>
@@ -75,6 +74,13 @@ __device__ __forceinline__ void cluster_sync() {
 // says that TMEM has been read, and no memory write has to be seen with it.
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
+                 "r"(bar)
+                 : "memory");
 }
 
 // A tile of a 2-D tensor map into shared memory; x (elements, innermost) starts 16-byte aligned.
