@@ -655,7 +655,7 @@ typedef struct {
     const void* logits;      /* device [rows, vocab] of `type`, aligned to the element size   */
     const int64_t* targets;  /* device [rows]                                                 */
     int64_t rows;            /* 0 .. 2^31 - 1; 0 rows is a valid, empty call                  */
-    int64_t vocab;           /* 1 .. 2^31 - 1                                                 */
+    int64_t vocab;           /* 1 .. 2^30                                                     */
     int64_t stride;          /* elements from one row to the next, >= vocab                   */
     int32_t type;            /* ZERO_T_*                                                      */
     double temperature;      /* > 0, finite                                                   */

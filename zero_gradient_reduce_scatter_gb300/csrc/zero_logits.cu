@@ -40,29 +40,46 @@ __device__ __forceinline__ int64_t live_target(const Rows<T>& a, int64_t t) {
 }
 
 // A row as the CTAs of a cluster share it: up to 7 elements before the first 16-byte boundary
-// (the first CTA's), whole vectors [lo, hi) of each CTA, and up to 7 behind the last (the last
-// CTA's). A row of an odd vocabulary starts at any even address.
+// (the first CTA's), `n` whole vectors of each CTA from element `first` on, and up to 7 elements
+// behind the last (the last CTA's). A row of an odd vocabulary starts at any even address.
+template <class T>
 struct Slice {
-    int64_t head, lo, hi, tail;  // elements before, this CTA's vectors, elements behind
-    int64_t tail_at;             // first element behind
+    int head, n, first, tail_at, tail;
+    const uint4* v;  // this CTA's vectors
+
+    __device__ __forceinline__ Slice(const T* x, int64_t vocab, int rank, int size) {
+        const int len = (int)vocab, to = (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T);
+        const int before = min(to, len), vecs = (len - before) / kVec<T>, per = (vecs + size - 1) / size;
+        const int lo = min(per * rank, vecs);
+        n = min(per, vecs - lo);
+        first = before + lo * kVec<T>;
+        tail_at = before + vecs * kVec<T>;
+        head = rank == 0 ? before : 0;
+        tail = rank == size - 1 ? len - tail_at : 0;
+        v = reinterpret_cast<const uint4*>(x + first);
+    }
 };
-template <class T>
-__device__ __forceinline__ Slice slice_of(const T* x, int64_t n, int rank, int size) {
-    Slice s;
-    const int64_t to = (int64_t)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int64_t)sizeof(T);
-    s.head = to < n ? to : n;
-    const int64_t vecs = (n - s.head) / kVec<T>, per = (vecs + size - 1) / size;
-    s.lo = per * rank < vecs ? per * rank : vecs;
-    s.hi = s.lo + per < vecs ? s.lo + per : vecs;
-    s.tail_at = s.head + vecs * kVec<T>;
-    s.tail = rank == size - 1 ? n - s.tail_at : 0;
-    if (rank != 0) s.head = 0;
-    return s;
-}
-// The vectors' base address: that of the row's first 16-byte boundary.
-template <class T>
-__device__ __forceinline__ const uint4* vectors(const T* x) {
-    return reinterpret_cast<const uint4*>((reinterpret_cast<uintptr_t>(x) + 15) & ~(uintptr_t)15);
+
+// f(i) for this thread's vectors of n, kUnroll at a time: `load` first for all of them, then `use`.
+template <int THREADS, class L, class U>
+__device__ __forceinline__ void for_vectors(int n, L load, U use) {
+    int i = threadIdx.x;
+    for (; i + (kUnroll - 1) * THREADS < n; i += kUnroll * THREADS) {
+        uint4 q[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) q[u] = load(i + u * THREADS);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) use(i + u * THREADS, q[u]);
+    }
+    if (i < n) {
+        uint4 q[kUnroll - 1];
+#pragma unroll
+        for (int u = 0; u < kUnroll - 1; ++u)
+            if (i + u * THREADS < n) q[u] = load(i + u * THREADS);
+#pragma unroll
+        for (int u = 0; u < kUnroll - 1; ++u)
+            if (i + u * THREADS < n) use(i + u * THREADS, q[u]);
+    }
 }
 
 // The sums of all CTAs of a cluster, in the order of their ranks; valid everywhere. `mine` is
@@ -92,18 +109,9 @@ __global__ void __launch_bounds__(kRowThreads)
     RowResult r = {0.0f, 0.0f, 0.0f};
     if (y >= 0) {
         const T* x = a.x + t * a.stride;
-        const Slice s = slice_of(x, a.vocab, rank, size);
-        const uint4* v = vectors(x);
+        const Slice<T> s(x, a.vocab, rank, size);
         RunningStat<T, ENTROPY> run(a.k);
-        for (int64_t i = s.lo + threadIdx.x; i < s.hi; i += kUnroll * kRowThreads) {
-            uint4 q[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-                if (i + u * kRowThreads < s.hi) q[u] = __ldg(v + i + u * kRowThreads);
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-                if (i + u * kRowThreads < s.hi) run.add(q[u]);
-        }
+        for_vectors<kRowThreads>(s.n, [&](int i) { return __ldg(s.v + i); }, [&](int, const uint4& q) { run.add(q); });
         if (threadIdx.x < s.head) run.add_one(widen(x[threadIdx.x]));
         if (threadIdx.x < s.tail) run.add_one(widen(x[s.tail_at + threadIdx.x]));
         RowStat st = cta_join<ENTROPY, kRowThreads>(run.stat(), a.k, sm);
@@ -160,40 +168,50 @@ __device__ __forceinline__ float grad_term(const GradRow& r, float x, float c, b
     return target ? __fadd_rn(f, r.g) : f;
 }
 
-// 16 bytes of a row; dy is the target's place in them (outside 0 .. kVec - 1: elsewhere).
+// The same for 16 bytes of a row. dy is the target's place in them (outside 0 .. kVec - 1:
+// elsewhere).
 template <class T, bool H>
-__device__ __forceinline__ uint4 grad_vector(const GradRow& r, const uint4& x, float c, int64_t dy) {
-    const uint64_t base = pack2(-r.base, -r.base), c2 = pack2(c, c), off = pack2(-r.off, -r.off);
-    const uint64_t ka = pack2(-r.ka, -r.ka), kb = pack2(-r.kb, -r.kb);
-    uint64_t f[kVec<T> / 2];
-#pragma unroll
-    for (int i = 0; i < kVec<T> / 2; ++i) {
-        const uint64_t d = fma2(add2(widen2<T>(x, i), base), c2, off);
-        const float2 df = unpack2(d);
-        const uint64_t e = pack2(pow2(df.x), pow2(df.y));
-        f[i] = mul2(e, H ? fma2(kb, pack2(fmaxf(df.x, kFar), fmaxf(df.y, kFar)), ka) : ka);
-    }
-    uint4 out;
-    if (dy >= 0 && dy < kVec<T>) {
+struct GradVector {
+    const uint64_t base, c, off, ka, kb;  // twice each
+    const float g;
+
+    __device__ __forceinline__ GradVector(const GradRow& r, float c)
+        : base(pack2(-r.base, -r.base)), c(pack2(c, c)), off(pack2(-r.off, -r.off)), ka(pack2(-r.ka, -r.ka)), kb(pack2(-r.kb, -r.kb)), g(r.g) {}
+
+    __device__ __forceinline__ uint4 operator()(const uint4& x, int dy) const {
+        uint64_t f[kVec<T> / 2];
 #pragma unroll
         for (int i = 0; i < kVec<T> / 2; ++i) {
-            float2 u = unpack2(f[i]);
-            if (dy == 2 * i) u.x += r.g;
-            if (dy == 2 * i + 1) u.y += r.g;
-            f[i] = pack2(u.x, u.y);
+            const uint64_t d = fma2(add2(widen2<T>(x, i), base), c, off);
+            const float2 df = unpack2(d);
+            const uint64_t e = pack2(pow2(df.x), pow2(df.y));
+            f[i] = mul2(e, H ? fma2(kb, pack2(fmaxf(df.x, kFar), fmaxf(df.y, kFar)), ka) : ka);
         }
-    }
+        if ((unsigned)dy < (unsigned)kVec<T>) {
 #pragma unroll
-    for (int i = 0; i < kVec<T> / 2; ++i) narrow2<T>(out, i, unpack2(f[i]));
-    return out;
-}
+            for (int i = 0; i < kVec<T> / 2; ++i) {
+                float2 u = unpack2(f[i]);
+                if (dy == 2 * i) u.x += g;
+                if (dy == 2 * i + 1) u.y += g;
+                f[i] = pack2(u.x, u.y);
+            }
+        }
+        uint4 out;
+#pragma unroll
+        for (int i = 0; i < kVec<T> / 2; ++i) narrow2<T>(out, i, unpack2(f[i]));
+        return out;
+    }
+};
 
-// Zeros into this CTA's share of a row of another alignment than its own.
+// The target's place in a row that has it, or a place that no vector reaches.
+__device__ __forceinline__ int place_of(int64_t y, int64_t vocab) { return y < vocab ? (int)y : INT32_MIN / 2; }
+
+// Zeros into this CTA's share of a row.
 template <class T, int THREADS>
-__device__ __forceinline__ void zero_row(T* out, int64_t n, int rank, int size) {
-    const Slice s = slice_of(out, n, rank, size);
-    uint4* v = const_cast<uint4*>(vectors(out));
-    for (int64_t i = s.lo + threadIdx.x; i < s.hi; i += THREADS) __stcs(v + i, make_uint4(0, 0, 0, 0));
+__device__ __forceinline__ void zero_row(T* out, int64_t vocab, int rank, int size) {
+    const Slice<T> s(out, vocab, rank, size);
+    uint4* v = const_cast<uint4*>(s.v);
+    for (int i = threadIdx.x; i < s.n; i += THREADS) __stcs(v + i, make_uint4(0, 0, 0, 0));
     if (threadIdx.x < s.head) out[threadIdx.x] = narrow<T>(0.0f);
     if (threadIdx.x < s.tail) out[s.tail_at + threadIdx.x] = narrow<T>(0.0f);
 }
@@ -203,33 +221,30 @@ __device__ __forceinline__ bool same_alignment(const T* a, const T* b) {
     return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0;
 }
 
+// The elements of a row that no vector holds.
+template <class T, bool H>
+__device__ __forceinline__ void write_ends(const Slice<T>& s, const GradRow& r, const T* x, T* out, float c, int y) {
+    const int i = threadIdx.x;
+    if (i < s.head) out[i] = narrow<T>(grad_term<H>(r, widen(x[i]), c, i == y));
+    if (i < s.tail) out[s.tail_at + i] = narrow<T>(grad_term<H>(r, widen(x[s.tail_at + i]), c, s.tail_at + i == y));
+}
+
 // Backward, bound by reading and writing the logits once. Where the gradient's rows have another
 // alignment than the logits', elements are taken one at a time.
 template <class T, bool H>
-__device__ __forceinline__ void write_grad(const Rows<T>& a, const GradRow& r, const T* x, T* out, int64_t y, int rank, int size) {
-    const Slice s = slice_of(x, a.vocab, rank, size);
-    const int64_t head = (reinterpret_cast<uintptr_t>(vectors(x)) - reinterpret_cast<uintptr_t>(x)) / sizeof(T);
-    const uint4* v = vectors(x);
+__device__ __forceinline__ void write_grad(const Rows<T>& a, const GradRow& r, const T* x, T* out, int y, int rank, int size) {
+    const Slice<T> s(x, a.vocab, rank, size);
     if (same_alignment(x, out)) {
-        uint4* w = const_cast<uint4*>(vectors(out));
-        for (int64_t i = s.lo + threadIdx.x; i < s.hi; i += kUnroll * kRowThreads) {
-            uint4 q[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-                if (i + u * kRowThreads < s.hi) q[u] = __ldcs(v + i + u * kRowThreads);
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int64_t k = i + u * kRowThreads;
-                if (k < s.hi) __stcs(w + k, grad_vector<T, H>(r, q[u], a.c, y - head - k * kVec<T>));
-            }
-        }
+        const GradVector<T, H> grad(r, a.c);
+        uint4* to = reinterpret_cast<uint4*>(out + s.first);
+        const int dy = y - s.first;
+        for_vectors<kRowThreads>(s.n, [&](int i) { return __ldcs(s.v + i); },
+                                 [&](int i, const uint4& q) { __stcs(to + i, grad(q, dy - i * kVec<T>)); });
     } else {
-        for (int64_t j = head + s.lo * kVec<T> + threadIdx.x; j < head + s.hi * kVec<T>; j += kRowThreads)
+        for (int j = s.first + threadIdx.x; j < s.first + s.n * kVec<T>; j += kRowThreads)
             out[j] = narrow<T>(grad_term<H>(r, widen(x[j]), a.c, j == y));
     }
-    if (threadIdx.x < s.head) out[threadIdx.x] = narrow<T>(grad_term<H>(r, widen(x[threadIdx.x]), a.c, threadIdx.x == y));
-    const int64_t j = s.tail_at + threadIdx.x;
-    if (threadIdx.x < s.tail) out[j] = narrow<T>(grad_term<H>(r, widen(x[j]), a.c, j == y));
+    write_ends<T, H>(s, r, x, out, a.c, y);
 }
 
 template <class T, bool H>
@@ -254,7 +269,7 @@ __global__ void __launch_bounds__(kRowThreads)
         if (size > 1) cg::this_cluster().sync();
         else __syncthreads();
     }
-    write_grad<T, H>(a, r, x, out, y, rank, size);
+    write_grad<T, H>(a, r, x, out, place_of(y, a.vocab), rank, size);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -505,17 +520,17 @@ __global__ void __launch_bounds__(kFusedThreads, 2)
         return;
     }
     const T* x = a.x + t * a.stride;
-    const Slice s = slice_of(x, a.vocab, rank, size);
-    const int n = (int)(s.hi - s.lo), per = (n + kChunks - 1) / kChunks;  // vectors, and of one copy
+    const Slice<T> s(x, a.vocab, rank, size);
+    const int per = (s.n + kChunks - 1) / kChunks;  // vectors of one copy
     const uint4* v = reinterpret_cast<const uint4*>(smem);
     if (threadIdx.x == 0) {
         gave_up = 0;
         for (int i = 0; i < kChunks; ++i) mbar_init(smem_addr(bars + i), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         for (int i = 0; i < kChunks; ++i) {
-            const int at = min(n, i * per), bytes = 16 * (min(n, at + per) - at);
+            const int at = min(s.n, i * per), bytes = 16 * (min(s.n, at + per) - at);
             mbar_expect(smem_addr(bars + i), bytes);
-            if (bytes) bulk_load(smem_addr(smem) + 16 * at, vectors(x) + s.lo + at, bytes, smem_addr(bars + i));
+            if (bytes) bulk_load(smem_addr(smem) + 16 * at, s.v + at, bytes, smem_addr(bars + i));
         }
     }
     __syncthreads();
@@ -525,8 +540,8 @@ __global__ void __launch_bounds__(kFusedThreads, 2)
     bool ok = true;
     for (int i = 0; i < kChunks; ++i) {
         ok = ok && mbar_wait(smem_addr(bars + i), 0, &gave_up);
-        const int end = min(n, (i + 1) * per);
-        for (int j = i * per + threadIdx.x; j < end; j += kFusedThreads) run.add(v[j]);
+        const int at = min(s.n, i * per);
+        for_vectors<kFusedThreads>(min(s.n, at + per) - at, [&](int j) { return v[at + j]; }, [&](int, const uint4& q) { run.add(q); });
     }
     const float x_y = threadIdx.x == 0 && y < a.vocab ? widen(x[y]) : NAN;  // before any CTA writes
     RowStat st = run.stat();
@@ -558,20 +573,19 @@ __global__ void __launch_bounds__(kFusedThreads, 2)
         zero_row<T, kFusedThreads>(out, a.vocab, rank, size);
     } else {
         const GradRow r = shared_row;
-        const int64_t head = (reinterpret_cast<uintptr_t>(vectors(x)) - reinterpret_cast<uintptr_t>(x)) / sizeof(T);
-        const int64_t first = head + s.lo * kVec<T>;  // element of the slice's first vector
+        const int at = place_of(y, a.vocab);
         if (same_alignment(x, out)) {
-            uint4* to = const_cast<uint4*>(vectors(out)) + s.lo;
-            for (int j = threadIdx.x; j < n; j += kFusedThreads)
-                __stcs(to + j, grad_vector<T, H>(r, v[j], a.c, y - first - (int64_t)j * kVec<T>));
+            const GradVector<T, H> grad(r, a.c);
+            uint4* to = reinterpret_cast<uint4*>(out + s.first);
+            const int dy = at - s.first;
+            for_vectors<kFusedThreads>(s.n, [&](int j) { return v[j]; },
+                                       [&](int j, const uint4& q) { __stcs(to + j, grad(q, dy - j * kVec<T>)); });
         } else {
             const T* e = reinterpret_cast<const T*>(smem);
-            for (int j = threadIdx.x; j < n * kVec<T>; j += kFusedThreads)
-                out[first + j] = narrow<T>(grad_term<H>(r, widen(e[j]), a.c, first + j == y));
+            for (int j = threadIdx.x; j < s.n * kVec<T>; j += kFusedThreads)
+                out[s.first + j] = narrow<T>(grad_term<H>(r, widen(e[j]), a.c, s.first + j == at));
         }
-        if (threadIdx.x < s.head) out[threadIdx.x] = narrow<T>(grad_term<H>(r, widen(x[threadIdx.x]), a.c, threadIdx.x == y));
-        const int64_t j = s.tail_at + threadIdx.x;
-        if (threadIdx.x < s.tail) out[j] = narrow<T>(grad_term<H>(r, widen(x[j]), a.c, j == y));
+        write_ends<T, H>(s, r, x, out, a.c, at);
     }
     if (size > 1) cg::this_cluster().sync();  // no CTA leaves while another reads its sums
 }
@@ -614,7 +628,7 @@ __global__ void __launch_bounds__(kSetupThreads) k_policy_finish(const PolicyTok
 // Host side.
 // ---------------------------------------------------------------------------------------
 int check_logits(const zero_logits* x) {
-    if (!x || x->rows < 0 || x->rows > INT32_MAX || x->vocab < 1 || x->vocab > INT32_MAX || x->stride < x->vocab || !type_ok(x->type)) return ZERO_ERR_INVALID_ARG;
+    if (!x || x->rows < 0 || x->rows > INT32_MAX || x->vocab < 1 || x->vocab > (1 << 30) || x->stride < x->vocab || !type_ok(x->type)) return ZERO_ERR_INVALID_ARG;
     if (!(x->temperature > 0.0) || !std::isfinite(x->temperature)) return ZERO_ERR_INVALID_ARG;
     if (x->rows > 0 && x->stride > INT64_MAX / 8 / x->rows) return ZERO_ERR_INVALID_ARG;
     return ZERO_OK;

@@ -196,14 +196,15 @@ __device__ __forceinline__ void narrow2<float>(uint4& v, int i, float2 f) {
 // comparing costs a fraction of rescaling at every new maximum.
 template <class T, bool ENTROPY>
 struct RunningStat {
-    float m, limit;  // base, and the largest value that is taken over it
+    float m, limit;     // base, and the largest value that is taken over it
+    uint64_t base;      // -base_of(m), twice
     uint64_t s[2], q[2];
-    Scale k;
-    float margin;
+    const uint64_t c, lo;  // the scale's parts, twice each
+    const Scale k;
 
-    __device__ __forceinline__ explicit RunningStat(Scale k) : k(k), margin(40.0f / k.c) {
+    __device__ __forceinline__ explicit RunningStat(Scale k) : c(pack2(k.c, k.c)), lo(pack2(k.lo, k.lo)), k(k) {
         m = limit = -INFINITY;
-        s[0] = s[1] = q[0] = q[1] = pack2(0.0f, 0.0f);
+        base = s[0] = s[1] = q[0] = q[1] = pack2(0.0f, 0.0f);
     }
     __device__ __forceinline__ void raise(float top) {
         const float to = base_of(top), shift = scaled(m - to, k), f = pow2(shift);
@@ -217,9 +218,10 @@ struct RunningStat {
             s[i] = mul2(s[i], f2);
         }
         m = top;
-        limit = top + margin;
+        base = pack2(-to, -to);
+        limit = top + 40.0f / k.c;
     }
-    __device__ __forceinline__ void term(int i, uint64_t x, uint64_t base, uint64_t c, uint64_t lo) {
+    __device__ __forceinline__ void term(int i, uint64_t x) {
         const uint64_t t = add2(x, base), d = fma2(t, lo, mul2(t, c));
         const float2 df = unpack2(d);
         const uint64_t e = pack2(pow2(df.x), pow2(df.y));
@@ -229,15 +231,12 @@ struct RunningStat {
     __device__ __forceinline__ void add(const uint4& v) {
         const float top = max_of<T>(v);
         if (top > limit) raise(top);
-        const float b = -base_of(m);
-        const uint64_t base = pack2(b, b), c = pack2(k.c, k.c), lo = pack2(k.lo, k.lo);
 #pragma unroll
-        for (int i = 0; i < kVec<T> / 2; ++i) term(i & 1, widen2<T>(v, i), base, c, lo);
+        for (int i = 0; i < kVec<T> / 2; ++i) term(i & 1, widen2<T>(v, i));
     }
     __device__ __forceinline__ void add_one(float x) {
         if (x > limit) raise(x);
-        const float b = -base_of(m);
-        term(0, pack2(x, -INFINITY), pack2(b, b), pack2(k.c, k.c), pack2(k.lo, k.lo));
+        term(0, pack2(x, -INFINITY));
     }
     __device__ __forceinline__ RowStat stat() const {
         const float2 a = unpack2(add2(s[0], s[1])), b = unpack2(add2(q[0], q[1]));
