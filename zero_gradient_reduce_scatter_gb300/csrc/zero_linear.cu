@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(32 * kJoinSlices) k_linear_join(const LinearAr
     for (int w = 1; w < kJoinSlices; ++w) s = join<ENTROPY>(s, sm[w][lane], a.k);
     RowResult r = {0.0f, 0.0f, 0.0f};
     if (y >= 0) {
-        r = finish_row(s, y < a.vocab ? a.zy[t] : NAN, a.inv_t);
+        r = finish_row<ENTROPY>(s, y < a.vocab ? a.zy[t] : NAN, a.k, a.inv_t);
         if (y >= a.vocab) r.logp = NAN;
     }
     if (gave_up) r.logp = r.lse = r.entropy = NAN;  // no result

@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 
@@ -83,7 +84,7 @@ __device__ __forceinline__ void for_vectors(int n, L load, U use) {
 }
 
 // The sums of all CTAs of a cluster, in the order of their ranks; valid everywhere. `mine` is
-// shared memory of this CTA; `after` runs before any CTA may leave or overwrite what was read.
+// shared memory of this CTA, which stays as it is until the cluster's next barrier.
 template <bool ENTROPY>
 __device__ __forceinline__ RowStat cluster_join(RowStat a, int size, Scale k, RowStat* mine) {
     if (size == 1) return a;
@@ -93,6 +94,14 @@ __device__ __forceinline__ RowStat cluster_join(RowStat a, int size, Scale k, Ro
     a = *cl.map_shared_rank(mine, 0);
     for (int r = 1; r < size; ++r) a = join<ENTROPY>(a, *cl.map_shared_rank(mine, r), k);
     return a;
+}
+
+// Whether a row is taken without CHECKED (Sums) first: its target's logit is a base, and a
+// vocabulary padded with -inf, at its end or start, does not make an entropy's sum fail anyway.
+// A function of the row alone, so that its bits are too.
+template <bool ENTROPY, class T>
+__device__ __forceinline__ bool fast_row(const T* x, int64_t vocab, float x_y) {
+    return fabsf(x_y) < INFINITY && !(ENTROPY && (widen(x[0]) == -INFINITY || widen(x[vocab - 1]) == -INFINITY));
 }
 
 // Forward, bound by reading the logits once: `size` CTAs per row (a cluster; several where there
@@ -109,15 +118,27 @@ __global__ void __launch_bounds__(kRowThreads)
     RowResult r = {0.0f, 0.0f, 0.0f};
     if (y >= 0) {
         const T* x = a.x + t * a.stride;
+        const float x_y = y < a.vocab ? widen(x[y]) : NAN;
         const Slice<T> s(x, a.vocab, rank, size);
-        RunningStat<T, ENTROPY> run(a.k);
-        for_vectors<kRowThreads>(s.n, [&](int i) { return __ldg(s.v + i); }, [&](int, const uint4& q) { run.add(q); });
-        if (threadIdx.x < s.head) run.add_one(widen(x[threadIdx.x]));
-        if (threadIdx.x < s.tail) run.add_one(widen(x[s.tail_at + threadIdx.x]));
-        RowStat st = cta_join<ENTROPY, kRowThreads>(run.stat(), a.k, sm);
+        auto sums = [&](auto checked) {
+            constexpr bool kChecked = decltype(checked)::value;
+            Sums<T, ENTROPY, kChecked> run(a.k, x_y);
+            for_vectors<kRowThreads>(s.n, [&](int i) { return __ldg(s.v + i); }, [&](int, const uint4& q) { run.add(q); });
+            if (threadIdx.x < s.head) run.add_one(widen(x[threadIdx.x]));
+            if (threadIdx.x < s.tail) run.add_one(widen(x[s.tail_at + threadIdx.x]));
+            return group_join<ENTROPY, kChecked, kRowThreads / 32>(run.stat(), a.k, sm, 0);
+        };
+        RowStat st;
+        bool good = false;
+        if (fast_row<ENTROPY>(x, a.vocab, x_y)) {
+            st = sums(std::false_type());
+            good = good_sums<ENTROPY>(st);
+            if (!good) __syncthreads();
+        }
+        if (!good) st = sums(std::true_type());
         st = cluster_join<ENTROPY>(st, size, a.k, &mine);
         if (threadIdx.x == 0 && rank == 0) {
-            r = finish_row(st, y < a.vocab ? widen(x[y]) : NAN, a.inv_t);
+            r = finish_row<ENTROPY>(st, x_y, a.k, a.inv_t);
             if (y >= a.vocab) r.logp = NAN;
         }
     }
@@ -160,51 +181,39 @@ __device__ __forceinline__ GradRow grad_row(float g, float h, const RowStat& a, 
     return {g * i, f * (h == 0.0f ? g : fmaf(h, entropy - log2f(a.s) * kLn2, g)), f * h * kLn2, base_of(a.m), 0.0f};
 }
 
-// One element, in the very operations of grad_vector: the bits do not depend on alignment.
-template <bool H>
+// One element, in the very operations of GradVector: the bits do not depend on alignment. CLAMP:
+// the row may hold -inf, whose term 2^d (ka + kb d) is 0 times -inf.
+template <bool H, bool CLAMP = H>
 __device__ __forceinline__ float grad_term(const GradRow& r, float x, float c, bool target) {
     const float d = fmaf(x - r.base, c, -r.off);
-    const float f = __fmul_rn(pow2(d), H ? fmaf(-r.kb, fmaxf(d, kFar), -r.ka) : -r.ka);
+    const float f = __fmul_rn(pow2(d), H ? fmaf(-r.kb, CLAMP ? fmaxf(d, kFar) : d, -r.ka) : -r.ka);
     return target ? __fadd_rn(f, r.g) : f;
 }
 
-// The same for 16 bytes of a row. dy is the target's place in them (outside 0 .. kVec - 1:
-// elsewhere).
-template <class T, bool H>
+// The same for 16 bytes of a row that do not hold the target, or before it is set right.
+template <class T, bool H, bool CLAMP = H>
 struct GradVector {
     const uint64_t base, c, off, ka, kb;  // twice each
-    const float g;
 
     __device__ __forceinline__ GradVector(const GradRow& r, float c)
-        : base(pack2(-r.base, -r.base)), c(pack2(c, c)), off(pack2(-r.off, -r.off)), ka(pack2(-r.ka, -r.ka)), kb(pack2(-r.kb, -r.kb)), g(r.g) {}
+        : base(pack2(-r.base, -r.base)), c(pack2(c, c)), off(pack2(-r.off, -r.off)), ka(pack2(-r.ka, -r.ka)), kb(pack2(-r.kb, -r.kb)) {}
 
-    __device__ __forceinline__ uint4 operator()(const uint4& x, int dy) const {
-        uint64_t f[kVec<T> / 2];
+    __device__ __forceinline__ uint4 operator()(const uint4& x) const {
+        uint4 out;
 #pragma unroll
         for (int i = 0; i < kVec<T> / 2; ++i) {
             const uint64_t d = fma2(add2(widen2<T>(x, i), base), c, off);
             const float2 df = unpack2(d);
             const uint64_t e = pack2(pow2(df.x), pow2(df.y));
-            f[i] = mul2(e, H ? fma2(kb, pack2(fmaxf(df.x, kFar), fmaxf(df.y, kFar)), ka) : ka);
+            const uint64_t b = CLAMP ? pack2(fmaxf(df.x, kFar), fmaxf(df.y, kFar)) : d;
+            narrow2<T>(out, i, unpack2(mul2(e, H ? fma2(kb, b, ka) : ka)));
         }
-        if ((unsigned)dy < (unsigned)kVec<T>) {
-#pragma unroll
-            for (int i = 0; i < kVec<T> / 2; ++i) {
-                float2 u = unpack2(f[i]);
-                if (dy == 2 * i) u.x += g;
-                if (dy == 2 * i + 1) u.y += g;
-                f[i] = pack2(u.x, u.y);
-            }
-        }
-        uint4 out;
-#pragma unroll
-        for (int i = 0; i < kVec<T> / 2; ++i) narrow2<T>(out, i, unpack2(f[i]));
         return out;
     }
 };
 
-// The target's place in a row that has it, or a place that no vector reaches.
-__device__ __forceinline__ int place_of(int64_t y, int64_t vocab) { return y < vocab ? (int)y : INT32_MIN / 2; }
+// The target's place in a row that has it, or a place that no slice reaches.
+__device__ __forceinline__ int place_of(int64_t y, int64_t vocab) { return y < vocab ? (int)y : -1; }
 
 // Zeros into this CTA's share of a row.
 template <class T, int THREADS>
@@ -222,24 +231,25 @@ __device__ __forceinline__ bool same_alignment(const T* a, const T* b) {
 }
 
 // The elements of a row that no vector holds.
-template <class T, bool H>
+template <class T, bool H, bool CLAMP = H>
 __device__ __forceinline__ void write_ends(const Slice<T>& s, const GradRow& r, const T* x, T* out, float c, int y) {
     const int i = threadIdx.x;
-    if (i < s.head) out[i] = narrow<T>(grad_term<H>(r, widen(x[i]), c, i == y));
-    if (i < s.tail) out[s.tail_at + i] = narrow<T>(grad_term<H>(r, widen(x[s.tail_at + i]), c, s.tail_at + i == y));
+    if (i < s.head) out[i] = narrow<T>(grad_term<H, CLAMP>(r, widen(x[i]), c, i == y));
+    if (i < s.tail) out[s.tail_at + i] = narrow<T>(grad_term<H, CLAMP>(r, widen(x[s.tail_at + i]), c, s.tail_at + i == y));
 }
 
 // Backward, bound by reading and writing the logits once. Where the gradient's rows have another
 // alignment than the logits', elements are taken one at a time.
 template <class T, bool H>
-__device__ __forceinline__ void write_grad(const Rows<T>& a, const GradRow& r, const T* x, T* out, int y, int rank, int size) {
+__device__ __forceinline__ void write_grad(const Rows<T>& a, const GradRow& r, const T* x, T* out, int y, float x_y, int rank, int size) {
     const Slice<T> s(x, a.vocab, rank, size);
     if (same_alignment(x, out)) {
         const GradVector<T, H> grad(r, a.c);
         uint4* to = reinterpret_cast<uint4*>(out + s.first);
-        const int dy = y - s.first;
-        for_vectors<kRowThreads>(s.n, [&](int i) { return __ldcs(s.v + i); },
-                                 [&](int i, const uint4& q) { __stcs(to + i, grad(q, dy - i * kVec<T>)); });
+        for_vectors<kRowThreads>(s.n, [&](int i) { return __ldcs(s.v + i); }, [&](int i, const uint4& q) { __stcs(to + i, grad(q)); });
+        // the thread that wrote the target's vector sets the target right
+        const int at = y - s.first;
+        if (at >= 0 && at < s.n * kVec<T> && at / kVec<T> % kRowThreads == threadIdx.x) out[y] = narrow<T>(grad_term<H>(r, x_y, a.c, true));
     } else {
         for (int j = s.first + threadIdx.x; j < s.first + s.n * kVec<T>; j += kRowThreads)
             out[j] = narrow<T>(grad_term<H>(r, widen(x[j]), a.c, j == y));
@@ -263,13 +273,14 @@ __global__ void __launch_bounds__(kRowThreads)
         return;
     }
     const T* x = a.x + t * a.stride;
-    const GradRow r = grad_row(y < a.vocab ? g : NAN, h, y < a.vocab ? widen(x[y]) : NAN, logp[t], lse[t],
+    const float x_y = y < a.vocab ? widen(x[y]) : NAN;
+    const GradRow r = grad_row(y < a.vocab ? g : NAN, h, x_y, logp[t], lse[t],
                                h != 0.0f ? entropy[t] : 0.0f, a.inv_t);
     if (out == x) {  // the target's logit is read before any thread writes it
         if (size > 1) cg::this_cluster().sync();
         else __syncthreads();
     }
-    write_grad<T, H>(a, r, x, out, place_of(y, a.vocab), rank, size);
+    write_grad<T, H>(a, r, x, out, place_of(y, a.vocab), x_y, rank, size);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -380,6 +391,7 @@ struct PolicyTokens {
     float *lse, *g, *h;          // [rows]
     float *loss, *kl, *clipped;  // [rows]
     float *out_loss, *out_clip, *out_kl;
+    uint32_t* ticket;            // the next row of the one-pass kernel
     int64_t rows, seqs;
     float lo, hi, dual, kl_coef, entropy_coef;
     int32_t kl_kind, reduce, per_sequence;
@@ -398,9 +410,15 @@ __global__ void __launch_bounds__(kSetupThreads) k_policy_setup(const PolicyToke
     __shared__ unsigned long long total, nonempty;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = kSetupThreads / 32;
     let_next_kernel_start();
-    if (threadIdx.x == 0) total = nonempty = 0;
+    if (threadIdx.x == 0) {
+        total = nonempty = 0;
+        *a.ticket = 0;
+    }
     __syncthreads();
-    for (int64_t t = threadIdx.x; t < a.rows; t += kSetupThreads) a.w[t] = 0.0f;
+    for (int64_t t = threadIdx.x; t < a.rows; t += kSetupThreads) {
+        a.w[t] = 0.0f;
+        a.loss[t] = NAN;  // until its row is done
+    }
     if (a.offsets) {
         for (int64_t s = warp; s < a.seqs; s += warps) {
             const int64_t b = clamp_offset(a.offsets[s], 0, a.rows), e = clamp_offset(a.offsets[s + 1], b, a.rows);
@@ -487,107 +505,195 @@ __device__ __forceinline__ TokenLoss policy_token(const PolicyTokens& a, int64_t
     return r;
 }
 
-// Forward and backward of a row in one pass over it: its slice is brought to shared memory by
-// bulk copies, read once for the sums as it arrives, joined over the cluster, and read again for
-// the gradient. So the logits cross HBM once each way, where a second pass over them would read
-// them again. Two CTAs of 512 threads per SM: one waits for its copies or its sums while the
-// other computes.
-constexpr int kFusedThreads = 512, kChunks = 8;
+// Forward and backward in one pass over each row: its slice is brought to shared memory by bulk
+// copies, read for the sums as it arrives, joined over the cluster, and read again for the
+// gradient. So the logits cross HBM once each way, where a second pass over them would read them
+// again. Two CTAs per SM, each with one slice: a producer warp refills a part of it with the next
+// row as soon as the gradient of this one has been taken from it, so that copies run beside
+// everything else. Rows are handed out one by one (some carry no loss and cost half).
+constexpr int kFusedWarps = 10, kFusedThreads = 32 * kFusedWarps;
+constexpr int kChunks = 4;
 constexpr int64_t kFusedBytes = 110 * 1024;  // of a slice: two fit an SM
 
+template <int THREADS>
+__device__ __forceinline__ void consumers_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+
 template <class T, bool H>
-__global__ void __launch_bounds__(kFusedThreads, 2)
-    k_policy_rows(const Rows<T> a, const PolicyTokens p, int size, float* logp, float* entropy, T* dx, int64_t dstride) {
+__global__ void __launch_bounds__(kFusedThreads + 32, 2)
+    k_policy_rows(const Rows<T> a, const PolicyTokens p, int size, int per, float* logp, float* entropy, T* dx, int64_t dstride) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ RowStat sm[kFusedThreads / 32], mine;
+    __shared__ RowStat sm[kFusedWarps], mine[2];
     __shared__ GradRow shared_row;
     __shared__ bool shared_zero;
-    __shared__ uint64_t bars[kChunks];
+    __shared__ int64_t row_at[2], row_y[2];
+    __shared__ float row_x[2];  // the target's logit
+    __shared__ bool row_fast[2];
+    __shared__ uint64_t bars[2 * kChunks + 4];
     __shared__ int gave_up;
-    const int64_t t = blockIdx.x / size;
-    const int rank = (int)(blockIdx.x % size);
-    // The kernel before this one sets up the weights and was itself launched behind the logits'
-    // producer, so logits and targets may be read at once.
-    const int64_t y = a.targets[t];
-    T* out = dx + t * dstride;
-    if (y < 0) {
-        wait_for_kernel_before();
-        zero_row<T, kFusedThreads>(out, a.vocab, rank, size);
-        if (threadIdx.x == 0 && rank == 0) {
-            logp[t] = p.loss[t] = p.kl[t] = p.clipped[t] = 0.0f;
-            if (entropy) entropy[t] = 0.0f;
-        }
-        return;
-    }
-    const T* x = a.x + t * a.stride;
-    const Slice<T> s(x, a.vocab, rank, size);
-    const int per = (s.n + kChunks - 1) / kChunks;  // vectors of one copy
-    const uint4* v = reinterpret_cast<const uint4*>(smem);
+    const uint32_t full = smem_addr(bars), empty = full + 8 * kChunks, row_full = empty + 8 * kChunks, row_empty = row_full + 16;
+    const int rank = (int)(blockIdx.x % size), lane = threadIdx.x & 31;
+    const int64_t first = blockIdx.x / size, clusters = gridDim.x / size;
     if (threadIdx.x == 0) {
         gave_up = 0;
-        for (int i = 0; i < kChunks; ++i) mbar_init(smem_addr(bars + i), 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         for (int i = 0; i < kChunks; ++i) {
-            const int at = min(s.n, i * per), bytes = 16 * (min(s.n, at + per) - at);
-            mbar_expect(smem_addr(bars + i), bytes);
-            if (bytes) bulk_load(smem_addr(smem) + 16 * at, s.v + at, bytes, smem_addr(bars + i));
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, kFusedWarps);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(row_full + 8 * i, 1);
+            mbar_init(row_empty + 8 * i, kFusedWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
-    RunningStat<T, H> run(a.k);
-    if (threadIdx.x < s.head) run.add_one(widen(x[threadIdx.x]));
-    if (threadIdx.x < s.tail) run.add_one(widen(x[s.tail_at + threadIdx.x]));
-    bool ok = true;
-    for (int i = 0; i < kChunks; ++i) {
-        ok = ok && mbar_wait(smem_addr(bars + i), 0, &gave_up);
-        const int at = min(s.n, i * per);
-        for_vectors<kFusedThreads>(min(s.n, at + per) - at, [&](int j) { return v[at + j]; }, [&](int, const uint4& q) { run.add(q); });
-    }
-    const float x_y = threadIdx.x == 0 && y < a.vocab ? widen(x[y]) : NAN;  // before any CTA writes
-    RowStat st = run.stat();
-    if (!ok) st.s = NAN;  // a copy did not come: no result
-    st = cta_join<H, kFusedThreads>(st, a.k, sm);
-    st = cluster_join<H>(st, size, a.k, &mine);
-    wait_for_kernel_before();
-    if (threadIdx.x == 0) {
-        const float w = p.w[t];
-        RowResult r = {0.0f, 0.0f, 0.0f};
-        TokenLoss l = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        if (w != 0.0f) {
-            r = finish_row(st, x_y, a.inv_t);
-            if (y >= a.vocab) r.logp = NAN;
-            l = policy_token(p, t, w, r.logp, r.entropy);
+
+    // The kernel before this one sets up the weights; it was itself launched behind the logits'
+    // producer, so logits and targets may be read at once, and the rest after it.
+    if (threadIdx.x >= kFusedThreads) {
+        uint32_t filled = 0;  // rows brought in
+        bool ok = true;
+        for (int64_t n = 0;; ++n) {
+            int64_t t = first + n * clusters;
+            if (size == 1 && n > 0) {
+                if (n == 1) wait_for_kernel_before();
+                if (lane == 0) t = (int64_t)gridDim.x + (int64_t)atomicAdd(p.ticket, 1u);
+                t = __shfl_sync(~0u, t, 0);
+            }
+            if (t >= a.rows) t = -1;
+            ok = ok && mbar_wait(row_empty + 8 * (n & 1), ((uint32_t)(n >> 1) & 1) ^ 1, &gave_up);
+            ok = __all_sync(~0u, ok);
+            if (!ok) t = -1;
+            const int64_t y = t >= 0 ? a.targets[t] : -1;
+            const T* x = a.x + t * a.stride;
+            if (lane == 0) {
+                row_at[n & 1] = t;
+                row_y[n & 1] = y;
+                const float x_y = y >= 0 && y < a.vocab ? widen(x[y]) : NAN;
+                row_x[n & 1] = x_y;
+                row_fast[n & 1] = y >= 0 && fast_row<H>(x, a.vocab, x_y);
+                mbar_arrive(row_full + 8 * (n & 1));
+            }
+            if (t < 0) break;
+            if (y < 0) continue;
+            if (lane == 0) {
+                const Slice<T> s(x, a.vocab, rank, size);
+                for (int i = 0; i < kChunks; ++i) {
+                    ok = ok && mbar_wait(empty + 8 * i, (filled & 1) ^ 1, &gave_up);
+                    const int at = min(s.n, i * per), bytes = 16 * (min(s.n, at + per) - at);
+                    mbar_expect(full + 8 * i, ok ? bytes : 0);
+                    if (ok && bytes) bulk_load(smem_addr(smem) + 16 * at, s.v + at, bytes, full + 8 * i);
+                }
+            }
+            ++filled;
+            if (size > 1) cg::this_cluster().sync();  // the consumers' cluster_join
         }
-        shared_zero = (l.g == 0.0f && l.h == 0.0f) || st.s == 0.0f;
-        shared_row = grad_row(l.g, l.h, st, r.entropy, a.inv_t);
-        if (rank == 0) {
-            logp[t] = r.logp;
-            if (entropy) entropy[t] = r.entropy;
-            p.loss[t] = l.loss;
-            p.kl[t] = l.kl;
-            p.clipped[t] = l.clipped;
-        }
-    }
-    __syncthreads();
-    if (shared_zero) {
-        zero_row<T, kFusedThreads>(out, a.vocab, rank, size);
     } else {
-        const GradRow r = shared_row;
-        const int at = place_of(y, a.vocab);
-        if (same_alignment(x, out)) {
-            const GradVector<T, H> grad(r, a.c);
-            uint4* to = reinterpret_cast<uint4*>(out + s.first);
-            const int dy = at - s.first;
-            for_vectors<kFusedThreads>(s.n, [&](int j) { return v[j]; },
-                                       [&](int j, const uint4& q) { __stcs(to + j, grad(q, dy - j * kVec<T>)); });
-        } else {
-            const T* e = reinterpret_cast<const T*>(smem);
-            for (int j = threadIdx.x; j < s.n * kVec<T>; j += kFusedThreads)
-                out[s.first + j] = narrow<T>(grad_term<H>(r, widen(e[j]), a.c, s.first + j == at));
+        uint32_t taken = 0;
+        const uint4* v = reinterpret_cast<const uint4*>(smem);
+        for (int64_t n = 0;; ++n) {
+            const bool got = mbar_wait(row_full + 8 * (n & 1), (uint32_t)(n >> 1) & 1, &gave_up);
+            const int64_t t = got ? row_at[n & 1] : -1, y = row_y[n & 1];
+            const float x_y = row_x[n & 1];
+            const bool try_fast = row_fast[n & 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(row_empty + 8 * (n & 1));
+            if (t < 0) break;
+            T* out = dx + t * dstride;
+            if (y < 0) {
+                if (n == 0) wait_for_kernel_before();
+                zero_row<T, kFusedThreads>(out, a.vocab, rank, size);
+                if (threadIdx.x == 0 && rank == 0) {
+                    logp[t] = p.loss[t] = p.kl[t] = p.clipped[t] = 0.0f;
+                    if (entropy) entropy[t] = 0.0f;
+                }
+                continue;
+            }
+            const T* x = a.x + t * a.stride;
+            const Slice<T> s(x, a.vocab, rank, size);
+            bool ok = true;
+            auto sums = [&](auto checked) {
+                constexpr bool kChecked = decltype(checked)::value;
+                Sums<T, H, kChecked> run(a.k, x_y);
+                if (threadIdx.x < s.head) run.add_one(widen(x[threadIdx.x]));
+                if (threadIdx.x < s.tail) run.add_one(widen(x[s.tail_at + threadIdx.x]));
+                for (int i = 0; i < kChunks; ++i) {
+                    ok = ok && mbar_wait(full + 8 * i, taken & 1, &gave_up);
+                    const int at = min(s.n, i * per);
+                    for_vectors<kFusedThreads>(min(s.n, at + per) - at, [&](int j) { return v[at + j]; }, [&](int, const uint4& q) { run.add(q); });
+                }
+                return group_join<H, kChecked, kFusedWarps>(run.stat(), a.k, sm, 1);
+            };
+            RowStat st;
+            bool good = false;
+            if (try_fast) {
+                st = sums(std::false_type());
+                good = good_sums<H>(st);
+                if (!good) consumers_sync<kFusedThreads>();
+            }
+            if (!good) st = sums(std::true_type());
+            if (!ok || *(volatile int*)&gave_up) st.s = NAN;  // a copy did not come: no result
+            st = cluster_join<H>(st, size, a.k, mine + (taken & 1));
+            if (n == 0) wait_for_kernel_before();
+            if (threadIdx.x == 0) {
+                const float w = p.w[t];
+                RowResult r = {0.0f, 0.0f, 0.0f};
+                TokenLoss l = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                if (w != 0.0f) {
+                    r = finish_row<H>(st, x_y, a.k, a.inv_t);
+                    if (y >= a.vocab) r.logp = NAN;
+                    l = policy_token(p, t, w, r.logp, r.entropy);
+                }
+                shared_zero = (l.g == 0.0f && l.h == 0.0f) || st.s == 0.0f;
+                shared_row = grad_row(l.g, l.h, st, r.entropy, a.inv_t);
+                if (rank == 0) {
+                    logp[t] = r.logp;
+                    if (entropy) entropy[t] = r.entropy;
+                    p.loss[t] = l.loss;
+                    p.kl[t] = l.kl;
+                    p.clipped[t] = l.clipped;
+                }
+            }
+            consumers_sync<kFusedThreads>();
+            const GradRow r = shared_row;
+            const bool zero = shared_zero;
+            const int place = place_of(y, a.vocab);
+            const bool fast = same_alignment(x, out);
+            const float c = H ? a.k.c : a.c;  // as in the sums
+            auto write = [&](auto clamp) {
+                constexpr bool kClamp = decltype(clamp)::value;
+                const GradVector<T, H, kClamp> grad(r, c);
+                if (zero) zero_row<T, kFusedThreads>(out, a.vocab, rank, size);
+                else write_ends<T, H, kClamp>(s, r, x, out, c, place);
+                for (int i = 0; i < kChunks; ++i) {
+                    const int at = min(s.n, i * per), m = min(s.n, at + per) - at;
+                    const int from = s.first + at * kVec<T>;  // the chunk's first element
+                    if (!zero && fast) {
+                        uint4* to = reinterpret_cast<uint4*>(out + from);
+                        for_vectors<kFusedThreads>(m, [&](int j) { return v[at + j]; }, [&](int j, const uint4& q) { __stcs(to + j, grad(q)); });
+                        // the thread that wrote the target's vector sets the target right
+                        const int dy = place - from;
+                        if (dy >= 0 && dy < m * kVec<T> && dy / kVec<T> % kFusedThreads == threadIdx.x)
+                            out[place] = narrow<T>(grad_term<H, kClamp>(r, x_y, c, true));
+                    } else if (!zero) {
+                        const T* e = reinterpret_cast<const T*>(v + at);
+                        for (int j = threadIdx.x; j < m * kVec<T>; j += kFusedThreads)
+                            out[from + j] = narrow<T>(grad_term<H, kClamp>(r, widen(e[j]), c, from + j == place));
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(empty + 8 * i);  // this warp has done with the chunk
+                }
+            };
+            if (H && !good) write(std::true_type());  // this slice may hold -inf
+            else write(std::false_type());
+            ++taken;
         }
-        write_ends<T, H>(s, r, x, out, a.c, at);
     }
-    if (size > 1) cg::this_cluster().sync();  // no CTA leaves while another reads its sums
+    if (size > 1) {  // no CTA leaves while another reads its sums
+        __syncwarp();
+        cg::this_cluster().sync();
+    }
 }
 
 __global__ void __launch_bounds__(kRowThreads) k_policy_tokens(const PolicyTokens a, const float* logp, const float* entropy) {
@@ -669,11 +775,12 @@ int ctas_per_row(const zero_logits* x, int sms) {
     return size;
 }
 
-// Shared memory for one CTA's share of a row.
-int64_t fused_bytes(const zero_logits* x, int size) {
+// Vectors of one part of a CTA's share of a row, and the shared memory for all its parts.
+int64_t fused_part(const zero_logits* x, int size) {
     const int64_t vecs = x->vocab * type_size(x->type) / 16;
-    return 16 * ((vecs + size - 1) / size);
+    return ((vecs + size - 1) / size + kChunks - 1) / kChunks;
 }
+int64_t fused_bytes(const zero_logits* x, int size) { return 16 * kChunks * fused_part(x, size); }
 
 int launch_token_logp(const zero_logits* x, const float* weight, float* logp, float* lse, float* entropy, float* cleared, int sms,
                       cudaStream_t s) {
@@ -716,8 +823,9 @@ int launch_policy_rows(const zero_logits* x, const PolicyTokens& p, const zero_p
         auto* kernel = q->entropy_coef != 0.0 ? k_policy_rows<T, true> : k_policy_rows<T, false>;
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFusedBytes);
         if (e != cudaSuccess) return record_cuda_error(e);
-        return launch_linked(kernel, (unsigned)(x->rows * size), kFusedThreads, (size_t)fused_bytes(x, size), size, s,
-                             rows_of<T>(x, nullptr), p, size, q->logp, q->entropy, (T*)q->dlogits, q->dstride);
+        const int64_t clusters = std::min<int64_t>(x->rows, 2 * sms / size);
+        return launch_linked(kernel, (unsigned)(clusters * size), kFusedThreads + 32, (size_t)fused_bytes(x, size), size, s,
+                             rows_of<T>(x, nullptr), p, size, (int)fused_part(x, size), q->logp, q->entropy, (T*)q->dlogits, q->dstride);
     });
     if (rc) return rc;
     return launch_linked(k_policy_finish, 1, kSetupThreads, 0, 1, s, p);
@@ -859,6 +967,7 @@ extern "C" int zero_policy_loss(const zero_logits* x, const zero_policy* p, void
     a.loss = f + 5 * n;
     a.kl = f + 6 * n;
     a.clipped = f + 7 * n;
+    a.ticket = (uint32_t*)(f + 8 * n);
     a.out_loss = p->loss;
     a.out_clip = p->clip_fraction;
     a.out_kl = p->kl_mean;

@@ -42,10 +42,11 @@ __device__ __forceinline__ float pow2(float x) {
     return y;
 }
 
-// C in two parts, c a little below it and lo > 0 the rest. C rounded to one fp32 number would
-// shift every d_j the same way, and the log-probabilities of a sequence with it: 6e-8 each at
-// temperature 1, which outgrows their own roundings once a few dozen are added up. With both
-// parts positive a difference of -inf stays -inf.
+// C in two parts, c and the rest lo. C rounded to one fp32 number would shift every d_j the same
+// way, and the log-probabilities of a sequence with it: 6e-8 each at temperature 1, which outgrows
+// their own roundings once a few dozen are added up. Where q is formed, it gives the shift back at
+// the end (log2 s moves by lo / c times q / s); elsewhere every d_j is formed with both parts,
+// which are both positive, so that a difference of -inf stays -inf.
 struct Scale {
     float c, lo;
 };
@@ -57,7 +58,8 @@ inline Scale make_scale(double temperature) {
     k.lo = fmaxf((float)(C - (double)k.c), 1e-30f);
     return k;
 }
-__device__ __forceinline__ float scaled(float x, Scale k) { return fmaf(x, k.lo, x * k.c); }
+template <bool ENTROPY>
+__device__ __forceinline__ float scaled(float x, Scale k) { return ENTROPY ? x * k.c : fmaf(x, k.lo, x * k.c); }
 
 // A maximum as it is subtracted: 0 for a part that has no value above -inf, so that its terms
 // are 2^-inf = 0 and not 2^(inf - inf).
@@ -76,7 +78,7 @@ __device__ __forceinline__ RowStat empty_stat() { return {-INFINITY, 0.0f, 0.0f}
 // The sums of `a` taken to the base `m` (base_of a maximum that is at least a.m).
 template <bool ENTROPY>
 __device__ __forceinline__ void rebase(RowStat& a, float m, Scale k) {
-    const float shift = scaled(a.m - m, k), f = pow2(shift);
+    const float shift = scaled<ENTROPY>(a.m - m, k), f = pow2(shift);
     if (ENTROPY) a.q = f * fmaf(a.s, fmaxf(shift, kFar), a.q);
     a.s *= f;
 }
@@ -92,7 +94,7 @@ __device__ __forceinline__ RowStat join(RowStat a, RowStat b, Scale k) {
 // One term over the base m.
 template <bool ENTROPY>
 __device__ __forceinline__ void add_term(RowStat& a, float x, Scale k, float m) {
-    const float d = scaled(x - m, k), e = pow2(d);
+    const float d = scaled<ENTROPY>(x - m, k), e = pow2(d);
     a.s += e;
     if (ENTROPY) a.q = fmaf(e, fmaxf(d, kFar), a.q);
 }
@@ -191,23 +193,29 @@ __device__ __forceinline__ void narrow2<float>(uint4& v, int i, float2 f) {
     set_word(v, 2 * i + 1, __float_as_uint(f.y));
 }
 
-// One thread's running sums. The base follows the maximum only when a value exceeds it by a
-// factor 2^40: the sums are floating-point, so any base near the maximum is as exact, and
-// comparing costs a fraction of rescaling at every new maximum.
-template <class T, bool ENTROPY>
-struct RunningStat {
-    float m, limit;     // base, and the largest value that is taken over it
-    uint64_t base;      // -base_of(m), twice
+// One thread's sums over a row.
+// Not CHECKED: over a base that is given and stays, usually the target's logit: no comparing, no
+// rescaling, and the parts of a row are plain sums. The sums are floating-point, so a base well
+// below the maximum is as good, until 2^60; and an entropy's sum meets 0 times -inf at a logit of
+// -inf. Both show in the result, and the row is then taken again, CHECKED: the base follows the
+// maximum (only once a value exceeds it by 2^40: comparing costs less than rescaling) and
+// differences are kept finite.
+template <class T, bool ENTROPY, bool CHECKED>
+struct Sums {
+    float m, limit;  // base, and the largest value that is taken over it
+    uint64_t base;   // -m, twice
     uint64_t s[2], q[2];
     const uint64_t c, lo;  // the scale's parts, twice each
     const Scale k;
 
-    __device__ __forceinline__ explicit RunningStat(Scale k) : c(pack2(k.c, k.c)), lo(pack2(k.lo, k.lo)), k(k) {
-        m = limit = -INFINITY;
-        base = s[0] = s[1] = q[0] = q[1] = pack2(0.0f, 0.0f);
+    __device__ __forceinline__ Sums(Scale k, float from) : c(pack2(k.c, k.c)), lo(pack2(k.lo, k.lo)), k(k) {
+        m = CHECKED ? -INFINITY : base_of(from);
+        limit = -INFINITY;
+        base = CHECKED ? pack2(0.0f, 0.0f) : pack2(-m, -m);
+        s[0] = s[1] = q[0] = q[1] = pack2(0.0f, 0.0f);
     }
     __device__ __forceinline__ void raise(float top) {
-        const float to = base_of(top), shift = scaled(m - to, k), f = pow2(shift);
+        const float to = base_of(top), shift = scaled<ENTROPY>(m - to, k), f = pow2(shift);
         const uint64_t f2 = pack2(f, f);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -222,21 +230,25 @@ struct RunningStat {
         limit = top + 40.0f / k.c;
     }
     __device__ __forceinline__ void term(int i, uint64_t x) {
-        const uint64_t t = add2(x, base), d = fma2(t, lo, mul2(t, c));
+        const uint64_t t = add2(x, base), d = ENTROPY ? mul2(t, c) : fma2(t, lo, mul2(t, c));
         const float2 df = unpack2(d);
         const uint64_t e = pack2(pow2(df.x), pow2(df.y));
         s[i] = add2(s[i], e);
-        if (ENTROPY) q[i] = fma2(e, pack2(fmaxf(df.x, kFar), fmaxf(df.y, kFar)), q[i]);
+        if (ENTROPY) q[i] = fma2(e, CHECKED ? pack2(fmaxf(df.x, kFar), fmaxf(df.y, kFar)) : d, q[i]);
     }
     __device__ __forceinline__ void add(const uint4& v) {
-        const float top = max_of<T>(v);
-        if (top > limit) raise(top);
+        if (CHECKED) {
+            const float top = max_of<T>(v);
+            if (top > limit) raise(top);
+        }
 #pragma unroll
         for (int i = 0; i < kVec<T> / 2; ++i) term(i & 1, widen2<T>(v, i));
     }
     __device__ __forceinline__ void add_one(float x) {
-        if (x > limit) raise(x);
-        term(0, pack2(x, -INFINITY));
+        if (CHECKED && x > limit) raise(x);
+        const float d = scaled<ENTROPY>(x - base_of(m), k), e = pow2(d);
+        s[0] = add2(s[0], pack2(e, 0.0f));
+        if (ENTROPY) q[0] = fma2(pack2(e, 0.0f), pack2(CHECKED ? fmaxf(d, kFar) : d, 0.0f), q[0]);
     }
     __device__ __forceinline__ RowStat stat() const {
         const float2 a = unpack2(add2(s[0], s[1])), b = unpack2(add2(q[0], q[1]));
@@ -244,24 +256,46 @@ struct RunningStat {
     }
 };
 
-// Joins the parts of all threads of a CTA, in a fixed order; the result is valid everywhere.
-template <bool ENTROPY, int THREADS>
-__device__ __forceinline__ RowStat cta_join(RowStat a, Scale k, RowStat* sm) {
+// Whether sums that were not CHECKED are good.
+template <bool ENTROPY>
+__device__ __forceinline__ bool good_sums(const RowStat& a) {
+    return a.s < 0x1p60f && (!ENTROPY || a.q == a.q);
+}
+
+// Joins the parts of a warp's lanes (the first N of them) in a fixed order; valid in every lane.
+// One rescaling each: the common base first, then plain sums.
+// CHECKED as in Sums: else all bases are equal.
+template <bool ENTROPY, bool CHECKED, int N = 32>
+__device__ __forceinline__ RowStat warp_join(RowStat a, Scale k) {
+    if (CHECKED) {
+        float m = a.m;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            if (o < N) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        rebase<ENTROPY>(a, base_of(m), k);
+        a.m = m;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        RowStat b;
-        b.m = __shfl_xor_sync(~0u, a.m, o);
-        b.s = __shfl_xor_sync(~0u, a.s, o);
-        b.q = ENTROPY ? __shfl_xor_sync(~0u, a.q, o) : 0.0f;
-        a = join<ENTROPY>(a, b, k);
+        if (o >= N) continue;
+        a.s += __shfl_xor_sync(~0u, a.s, o);
+        if (ENTROPY) a.q += __shfl_xor_sync(~0u, a.q, o);
     }
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = a;
-    __syncthreads();
-    a = sm[0];
-#pragma unroll
-    for (int w = 1; w < THREADS / 32; ++w) a = join<ENTROPY>(a, sm[w], k);
-    __syncthreads();
     return a;
+}
+
+// Joins the parts of all threads of a group of WARPS warps (at most 16) that meet at the named
+// barrier `id`; valid in all of them. sm[0 .. WARPS) may be written again after the group's next
+// barrier.
+template <bool ENTROPY, bool CHECKED, int WARPS>
+__device__ __forceinline__ RowStat group_join(RowStat a, Scale k, RowStat* sm, int id) {
+    a = warp_join<ENTROPY, CHECKED>(a, k);
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) sm[threadIdx.x >> 5] = a;
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(32 * WARPS) : "memory");
+    const RowStat none = {CHECKED ? -INFINITY : a.m, 0.0f, 0.0f};
+    a = (lane & 15) < WARPS ? sm[lane & 15] : none;
+    return warp_join<ENTROPY, CHECKED, 16>(a, k);
 }
 
 struct RowResult {
@@ -269,22 +303,26 @@ struct RowResult {
 };
 
 // pow2 errs low by this share on average (measured over 2^24 arguments), and so does a sum of many
-// terms, all but its largest, which is 2^0 = 1 exactly. A log-probability's own rounding hides it,
-// a sequence's sum of them would not.
+// terms, all but the base's own, which is 2^0 = 1 exactly. A log-probability's own rounding hides
+// it, a sequence's sum of them would not.
 constexpr double kPow2Low = 4.9e-8;
 
-// A row's results from its sums, rounded once; x_y is the target's logit.
-__device__ __forceinline__ RowResult finish_row(const RowStat& a, float x_y, double inv_t) {
+// A row's results from its sums, rounded once; x_y is the target's logit. ENTROPY says how the
+// sums were formed.
+template <bool ENTROPY>
+__device__ __forceinline__ RowResult finish_row(const RowStat& a, float x_y, Scale k, double inv_t) {
     RowResult r;
     if (a.s == 0.0f) {  // nothing but -inf
         r.logp = r.lse = -INFINITY;
         r.entropy = 0.0f;
         return r;
     }
-    const double s = (double)a.s, l = log(s) + kPow2Low * (1.0 - 1.0 / s);
-    r.logp = (float)(((double)x_y - (double)a.m) * inv_t - l);
-    r.lse = (float)((double)a.m * inv_t + l);
-    r.entropy = (float)(l - (double)a.q / s * 0.69314718055994530942);
+    const double s = (double)a.s, mean = ENTROPY ? (double)a.q / s * 0.69314718055994530942 : 0.0;
+    const double low = (double)(k.lo / k.c);
+    const double l = log(s) + kPow2Low * (1.0 - 1.0 / s) + low * mean;
+    r.logp = (float)(((double)x_y - (double)base_of(a.m)) * inv_t - l);
+    r.lse = (float)((double)base_of(a.m) * inv_t + l);
+    r.entropy = (float)(l - mean * (1.0 + low));
     return r;
 }
 
