@@ -34,7 +34,7 @@ struct LinearArgs {
     int64_t rows, vocab, dim;
     int32_t tile_rows, row_tiles, tile_cols, col_tiles, group, grid;
     Scale k;       // log2(e) / temperature
-    double inv_t;  // 1 / temperature
+    float inv_t;   // 1 / temperature
 };
 
 // Row tiles with at least one target, in order. One CTA, a warp per tile.
@@ -462,6 +462,6 @@ extern "C" int zero_linear_logp(const zero_linear* x, float* logp, float* lse, f
     const int width = l.pairs ? 2 : 1;
     a.grid = (int32_t)(std::min<int64_t>((int64_t)l.row_tiles * l.col_tiles, std::min(sms, kMaxGrid) / width) * width);
     a.k = make_scale(x->temperature);
-    a.inv_t = 1.0 / x->temperature;
+    a.inv_t = (float)(1.0 / x->temperature);
     return entropy ? run_linear<true>(x, a, l, logp, lse, entropy, s) : run_linear<false>(x, a, l, logp, lse, entropy, s);
 }

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kRowThreads)
         if (!good) st = sums(std::true_type());
         st = cluster_join<ENTROPY>(st, size, a.k, &mine);
         if (threadIdx.x == 0 && rank == 0) {
-            r = finish_row<ENTROPY>(st, x_y, a.k, a.inv_t);
+            r = finish_row<ENTROPY>(st, x_y, a.k, (float)a.inv_t);
             if (y >= a.vocab) r.logp = NAN;
         }
     }
@@ -232,10 +232,10 @@ __device__ __forceinline__ bool same_alignment(const T* a, const T* b) {
 
 // The elements of a row that no vector holds.
 template <class T, bool H, bool CLAMP = H>
-__device__ __forceinline__ void write_ends(const Slice<T>& s, const GradRow& r, const T* x, T* out, float c, int y) {
+__device__ __forceinline__ void write_ends(const Slice<T>& s, const GradRow& r, float x_head, float x_tail, T* out, float c, int y) {
     const int i = threadIdx.x;
-    if (i < s.head) out[i] = narrow<T>(grad_term<H, CLAMP>(r, widen(x[i]), c, i == y));
-    if (i < s.tail) out[s.tail_at + i] = narrow<T>(grad_term<H, CLAMP>(r, widen(x[s.tail_at + i]), c, s.tail_at + i == y));
+    if (i < s.head) out[i] = narrow<T>(grad_term<H, CLAMP>(r, x_head, c, i == y));
+    if (i < s.tail) out[s.tail_at + i] = narrow<T>(grad_term<H, CLAMP>(r, x_tail, c, s.tail_at + i == y));
 }
 
 // Backward, bound by reading and writing the logits once. Where the gradient's rows have another
@@ -243,6 +243,8 @@ __device__ __forceinline__ void write_ends(const Slice<T>& s, const GradRow& r, 
 template <class T, bool H>
 __device__ __forceinline__ void write_grad(const Rows<T>& a, const GradRow& r, const T* x, T* out, int y, float x_y, int rank, int size) {
     const Slice<T> s(x, a.vocab, rank, size);
+    const float x_head = threadIdx.x < s.head ? widen(x[threadIdx.x]) : 0.0f;
+    const float x_tail = threadIdx.x < s.tail ? widen(x[s.tail_at + threadIdx.x]) : 0.0f;
     if (same_alignment(x, out)) {
         const GradVector<T, H> grad(r, a.c);
         uint4* to = reinterpret_cast<uint4*>(out + s.first);
@@ -254,7 +256,7 @@ __device__ __forceinline__ void write_grad(const Rows<T>& a, const GradRow& r, c
         for (int j = s.first + threadIdx.x; j < s.first + s.n * kVec<T>; j += kRowThreads)
             out[j] = narrow<T>(grad_term<H>(r, widen(x[j]), a.c, j == y));
     }
-    write_ends<T, H>(s, r, x, out, a.c, y);
+    write_ends<T, H>(s, r, x_head, x_tail, out, a.c, y);
 }
 
 template <class T, bool H>
@@ -284,19 +286,52 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 // ---------------------------------------------------------------------------------------
-// Sums over a CTA in fp64, in a fixed order; valid in thread 0.
+// Sums over tokens: a number and the rounding errors of its additions, which is as good as fp64
+// here. An SM adds two fp64 numbers a cycle: a thousand threads that reduce four of them took
+// 14 us, these take one.
 // ---------------------------------------------------------------------------------------
-template <int THREADS>
-__device__ __forceinline__ double cta_sum(double x, double* sm) {
-    sm[threadIdx.x] = x;
-    __syncthreads();
-    for (int h = THREADS / 2; h > 0; h >>= 1) {
-        if (threadIdx.x < h) sm[threadIdx.x] += sm[threadIdx.x + h];
-        __syncthreads();
+struct Sum {
+    float hi = 0.0f, lo = 0.0f;
+    __device__ __forceinline__ void add(float x) {
+        const float t = __fadd_rn(hi, x), z = __fsub_rn(t, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, z)), __fsub_rn(x, z)));
+        hi = t;
     }
-    const double r = sm[0];
+    __device__ __forceinline__ void add(const Sum& o) {
+        add(o.hi);
+        lo = __fadd_rn(lo, o.lo);
+    }
+    // Infinities and NaN are kept; their error terms are not numbers.
+    __device__ __forceinline__ double value() const { return isfinite(hi) ? (double)hi + (double)lo : (double)hi; }
+};
+
+__device__ __forceinline__ Sum warp_sum(Sum x) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        // the lower lane's sum first on both sides: equal everywhere, in a fixed order
+        Sum y;
+        y.hi = __shfl_xor_sync(~0u, x.hi, o);
+        y.lo = __shfl_xor_sync(~0u, x.lo, o);
+        if ((threadIdx.x & o) != 0) {
+            y.add(x);
+            x = y;
+        } else {
+            x.add(y);
+        }
+    }
+    return x;
+}
+
+// Over a CTA of THREADS, in a fixed order; valid in every thread.
+template <int THREADS>
+__device__ __forceinline__ Sum cta_sum(Sum x, Sum* sm) {
+    const int lane = threadIdx.x & 31;
+    x = warp_sum(x);
+    if (lane == 0) sm[threadIdx.x >> 5] = x;
     __syncthreads();
-    return r;
+    x = lane < THREADS / 32 ? sm[lane] : Sum();
+    __syncthreads();
+    return warp_sum(x);
 }
 
 __device__ __forceinline__ int64_t clamp_offset(int64_t o, int64_t lo, int64_t hi) {
@@ -323,7 +358,7 @@ struct PairArgs {
 __device__ __forceinline__ double softplus(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
 
 __global__ void __launch_bounds__(kRowThreads) k_pairs(const PairArgs a) {
-    __shared__ double sm[kRowThreads];
+    __shared__ Sum sm[kRowThreads / 32];
     __shared__ float g_side[2];
     for (int64_t i = blockIdx.x; i < a.pairs; i += gridDim.x) {
         int64_t lo[2], hi[2];
@@ -331,14 +366,25 @@ __global__ void __launch_bounds__(kRowThreads) k_pairs(const PairArgs a) {
         for (int k = 0; k < 2; ++k) {
             lo[k] = clamp_offset(a.offsets[2 * i + k], 0, a.rows);
             hi[k] = clamp_offset(a.offsets[2 * i + k + 1], lo[k], a.rows);
-            double sum = 0.0, count = 0.0;
+            Sum sum;
+            int count = 0;
             for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kRowThreads) {
                 if (a.targets[t] < 0) continue;
-                sum += (double)a.logp[t] - (a.ref ? (double)a.ref[t] : 0.0);
-                count += 1.0;
+                sum.add(a.logp[t]);
+                if (a.ref) sum.add(-a.ref[t]);
+                ++count;
             }
-            d[k] = cta_sum<kRowThreads>(sum, sm);
-            n[k] = a.average ? fmax(cta_sum<kRowThreads>(count, sm), 1.0) : 1.0;
+            d[k] = cta_sum<kRowThreads>(sum, sm).value();
+            n[k] = 1.0;
+            if (a.average) {
+                __shared__ unsigned long long total;
+                if (threadIdx.x == 0) total = 0;
+                __syncthreads();
+                atomicAdd(&total, (unsigned long long)count);
+                __syncthreads();
+                n[k] = total ? (double)total : 1.0;
+                __syncthreads();
+            }
             d[k] /= n[k];
         }
         if (threadIdx.x == 0) {
@@ -371,11 +417,11 @@ __global__ void __launch_bounds__(kRowThreads) k_pairs(const PairArgs a) {
 }
 
 __global__ void __launch_bounds__(1024) k_mean(const float* x, int64_t n, float* out) {
-    __shared__ double sm[1024];
-    double s = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += 1024) s += (double)x[i];
+    __shared__ Sum sm[32];
+    Sum s;
+    for (int64_t i = threadIdx.x; i < n; i += 1024) s.add(x[i]);
     s = cta_sum<1024>(s, sm);
-    if (threadIdx.x == 0) *out = (float)(s / (double)n);
+    if (threadIdx.x == 0) *out = (float)(s.value() / (double)n);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -415,10 +461,11 @@ __global__ void __launch_bounds__(kSetupThreads) k_policy_setup(const PolicyToke
         *a.ticket = 0;
     }
     __syncthreads();
-    for (int64_t t = threadIdx.x; t < a.rows; t += kSetupThreads) {
-        a.w[t] = 0.0f;
-        a.loss[t] = NAN;  // until its row is done
-    }
+    // sequences leave no gaps: what lies before the first and behind the last carries no loss
+    const int64_t begin = a.offsets ? clamp_offset(a.offsets[0], 0, a.rows) : 0;
+    const int64_t end = a.offsets ? clamp_offset(a.offsets[a.seqs], begin, a.rows) : a.rows;
+    for (int64_t t = threadIdx.x; t < begin; t += kSetupThreads) a.w[t] = 0.0f;
+    for (int64_t t = end + threadIdx.x; t < a.rows; t += kSetupThreads) a.w[t] = 0.0f;
     if (a.offsets) {
         for (int64_t s = warp; s < a.seqs; s += warps) {
             const int64_t b = clamp_offset(a.offsets[s], 0, a.rows), e = clamp_offset(a.offsets[s + 1], b, a.rows);
@@ -443,6 +490,7 @@ __global__ void __launch_bounds__(kSetupThreads) k_policy_setup(const PolicyToke
         for (int64_t t = threadIdx.x; t < a.rows; t += kSetupThreads) {
             a.w[t] = a.targets[t] >= 0 ? w : 0.0f;
             a.adv[t] = a.advantages[t];
+            a.loss[t] = NAN;  // until its row is done
         }
         return;
     }
@@ -458,17 +506,25 @@ __global__ void __launch_bounds__(kSetupThreads) k_policy_setup(const PolicyToke
         for (int64_t t = b + lane; t < e; t += 32) {
             a.w[t] = a.targets[t] >= 0 ? w : 0.0f;
             a.adv[t] = a.advantages[a.per_sequence ? s : t];
+            a.loss[t] = NAN;
         }
     }
 }
+
+// What a token's loss takes, read ahead of its row's sums.
+struct TokenIn {
+    float w, adv, old, ref;
+    __device__ __forceinline__ TokenIn(const PolicyTokens& a, int64_t t)
+        : w(a.w[t]), adv(a.adv[t]), old(a.old_logp ? a.old_logp[t] : 0.0f), ref(a.ref_logp ? a.ref_logp[t] : 0.0f) {}
+};
 
 struct TokenLoss {
     float loss, kl, clipped, g, h;  // loss and the gradients on logp and entropy, weighted
 };
 
-__device__ __forceinline__ TokenLoss policy_token(const PolicyTokens& a, int64_t t, float w, float logp, float entropy) {
+__device__ __forceinline__ TokenLoss policy_token(const PolicyTokens& a, const TokenIn& in, float logp, float entropy) {
     TokenLoss r;
-    const float A = a.adv[t], ratio = a.old_logp ? expf(logp - a.old_logp[t]) : expf(logp - logp);
+    const float w = in.w, A = in.adv, ratio = expf(logp - (a.old_logp ? in.old : logp));
     const float plain = -ratio * A, clip = -fminf(fmaxf(ratio, a.lo), a.hi) * A;
     float loss = !(plain < clip) ? plain : clip;  // a NaN stays
     bool off = (A > 0.0f && ratio > a.hi) || (A < 0.0f && ratio < a.lo);
@@ -479,7 +535,7 @@ __device__ __forceinline__ TokenLoss policy_token(const PolicyTokens& a, int64_t
     float g = off ? 0.0f : plain;
     r.kl = 0.0f;
     if (a.ref_logp) {
-        const float d = a.ref_logp[t] - logp;
+        const float d = in.ref - logp;
         float dkl;
         if (a.kl_kind == ZERO_KL_K1) {
             r.kl = -d;
@@ -601,8 +657,8 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
             if (lane == 0) mbar_arrive(row_empty + 8 * (n & 1));
             if (t < 0) break;
             T* out = dx + t * dstride;
+            if (n == 0) wait_for_kernel_before();
             if (y < 0) {
-                if (n == 0) wait_for_kernel_before();
                 zero_row<T, kFusedThreads>(out, a.vocab, rank, size);
                 if (threadIdx.x == 0 && rank == 0) {
                     logp[t] = p.loss[t] = p.kl[t] = p.clipped[t] = 0.0f;
@@ -612,17 +668,21 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
             }
             const T* x = a.x + t * a.stride;
             const Slice<T> s(x, a.vocab, rank, size);
+            // read ahead: the token's numbers and the elements that no vector holds
+            const TokenIn in(p, t);
+            const float x_head = threadIdx.x < s.head ? widen(x[threadIdx.x]) : 0.0f;
+            const float x_tail = threadIdx.x < s.tail ? widen(x[s.tail_at + threadIdx.x]) : 0.0f;
             bool ok = true;
             auto sums = [&](auto checked) {
                 constexpr bool kChecked = decltype(checked)::value;
                 Sums<T, H, kChecked> run(a.k, x_y);
-                if (threadIdx.x < s.head) run.add_one(widen(x[threadIdx.x]));
-                if (threadIdx.x < s.tail) run.add_one(widen(x[s.tail_at + threadIdx.x]));
                 for (int i = 0; i < kChunks; ++i) {
                     ok = ok && mbar_wait(full + 8 * i, taken & 1, &gave_up);
                     const int at = min(s.n, i * per);
                     for_vectors<kFusedThreads>(min(s.n, at + per) - at, [&](int j) { return v[at + j]; }, [&](int, const uint4& q) { run.add(q); });
                 }
+                if (threadIdx.x < s.head) run.add_one(x_head);
+                if (threadIdx.x < s.tail) run.add_one(x_tail);
                 return group_join<H, kChecked, kFusedWarps>(run.stat(), a.k, sm, 1);
             };
             RowStat st;
@@ -635,15 +695,13 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
             if (!good) st = sums(std::true_type());
             if (!ok || *(volatile int*)&gave_up) st.s = NAN;  // a copy did not come: no result
             st = cluster_join<H>(st, size, a.k, mine + (taken & 1));
-            if (n == 0) wait_for_kernel_before();
             if (threadIdx.x == 0) {
-                const float w = p.w[t];
                 RowResult r = {0.0f, 0.0f, 0.0f};
                 TokenLoss l = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-                if (w != 0.0f) {
-                    r = finish_row<H>(st, x_y, a.k, a.inv_t);
+                if (in.w != 0.0f) {
+                    r = finish_row<H>(st, x_y, a.k, (float)a.inv_t);
                     if (y >= a.vocab) r.logp = NAN;
-                    l = policy_token(p, t, w, r.logp, r.entropy);
+                    l = policy_token(p, in, r.logp, r.entropy);
                 }
                 shared_zero = (l.g == 0.0f && l.h == 0.0f) || st.s == 0.0f;
                 shared_row = grad_row(l.g, l.h, st, r.entropy, a.inv_t);
@@ -665,7 +723,7 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
                 constexpr bool kClamp = decltype(clamp)::value;
                 const GradVector<T, H, kClamp> grad(r, c);
                 if (zero) zero_row<T, kFusedThreads>(out, a.vocab, rank, size);
-                else write_ends<T, H, kClamp>(s, r, x, out, c, place);
+                else write_ends<T, H, kClamp>(s, r, x_head, x_tail, out, c, place);
                 for (int i = 0; i < kChunks; ++i) {
                     const int at = min(s.n, i * per), m = min(s.n, at + per) - at;
                     const int from = s.first + at * kVec<T>;  // the chunk's first element
@@ -698,9 +756,9 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
 
 __global__ void __launch_bounds__(kRowThreads) k_policy_tokens(const PolicyTokens a, const float* logp, const float* entropy) {
     for (int64_t t = blockIdx.x * (int64_t)kRowThreads + threadIdx.x; t < a.rows; t += (int64_t)gridDim.x * kRowThreads) {
-        const float w = a.w[t];
+        const TokenIn in(a, t);
         TokenLoss r = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        if (w != 0.0f) r = policy_token(a, t, w, logp[t], entropy ? entropy[t] : 0.0f);
+        if (in.w != 0.0f) r = policy_token(a, in, logp[t], entropy ? entropy[t] : 0.0f);
         a.loss[t] = r.loss;
         a.kl[t] = r.kl;
         a.clipped[t] = r.clipped;
@@ -710,23 +768,34 @@ __global__ void __launch_bounds__(kRowThreads) k_policy_tokens(const PolicyToken
 }
 
 __global__ void __launch_bounds__(kSetupThreads) k_policy_finish(const PolicyTokens a) {
-    __shared__ double sm[kSetupThreads];
+    __shared__ Sum sm[kSetupThreads / 32];
     wait_for_kernel_before();
-    double loss = 0.0, kl = 0.0, clipped = 0.0, n = 0.0;
+    Sum loss, kl;
+    int clipped = 0, n = 0;
+#pragma unroll 4
     for (int64_t t = threadIdx.x; t < a.rows; t += kSetupThreads) {
-        loss += (double)a.loss[t];
-        kl += (double)a.kl[t];
-        clipped += (double)a.clipped[t];
-        n += a.w[t] != 0.0f ? 1.0 : 0.0;
+        loss.add(a.w[t] != 0.0f ? a.loss[t] : 0.0f);
+        kl.add(a.kl[t]);
+        clipped += a.clipped[t] != 0.0f;
+        n += a.w[t] != 0.0f;
     }
     loss = cta_sum<kSetupThreads>(loss, sm);
     kl = cta_sum<kSetupThreads>(kl, sm);
-    clipped = cta_sum<kSetupThreads>(clipped, sm);
-    n = fmax(cta_sum<kSetupThreads>(n, sm), 1.0);
+    __shared__ unsigned long long total, all_clipped;
+    if (threadIdx.x == 0) total = all_clipped = 0;
+    __syncthreads();
+    clipped = __reduce_add_sync(~0u, clipped);
+    n = __reduce_add_sync(~0u, n);
+    if ((threadIdx.x & 31) == 0) {
+        atomicAdd(&total, (unsigned long long)n);
+        atomicAdd(&all_clipped, (unsigned long long)clipped);
+    }
+    __syncthreads();
     if (threadIdx.x == 0) {
-        *a.out_loss = (float)loss;
-        *a.out_kl = (float)(kl / n);
-        *a.out_clip = (float)(clipped / n);
+        const double tokens = total ? (double)total : 1.0;
+        *a.out_loss = (float)loss.value();
+        *a.out_kl = (float)(kl.value() / tokens);
+        *a.out_clip = (float)((double)all_clipped / tokens);
     }
 }
 
