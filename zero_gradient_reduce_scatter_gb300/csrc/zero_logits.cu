@@ -464,12 +464,15 @@ __global__ void __launch_bounds__(kSetupThreads) k_policy_setup(const PolicyToke
     // sequences leave no gaps: what lies before the first and behind the last carries no loss
     const int64_t begin = a.offsets ? clamp_offset(a.offsets[0], 0, a.rows) : 0;
     const int64_t end = a.offsets ? clamp_offset(a.offsets[a.seqs], begin, a.rows) : a.rows;
+#pragma unroll 4
     for (int64_t t = threadIdx.x; t < begin; t += kSetupThreads) a.w[t] = 0.0f;
+#pragma unroll 4
     for (int64_t t = end + threadIdx.x; t < a.rows; t += kSetupThreads) a.w[t] = 0.0f;
     if (a.offsets) {
         for (int64_t s = warp; s < a.seqs; s += warps) {
             const int64_t b = clamp_offset(a.offsets[s], 0, a.rows), e = clamp_offset(a.offsets[s + 1], b, a.rows);
             int64_t n = 0;
+#pragma unroll 4
             for (int64_t t = b + lane; t < e; t += 32) n += a.targets[t] >= 0;
             n = warp_sum(n);
             if (lane == 0 && n) {
@@ -479,6 +482,7 @@ __global__ void __launch_bounds__(kSetupThreads) k_policy_setup(const PolicyToke
         }
     } else {
         int64_t n = 0;
+#pragma unroll 4
         for (int64_t t = threadIdx.x; t < a.rows; t += kSetupThreads) n += a.targets[t] >= 0;
         n = warp_sum(n);
         if (lane == 0) atomicAdd(&total, (unsigned long long)n);
@@ -487,6 +491,7 @@ __global__ void __launch_bounds__(kSetupThreads) k_policy_setup(const PolicyToke
     const float tokens = (float)(total ? total : 1), filled = (float)(nonempty ? nonempty : 1);
     if (!a.offsets) {
         const float w = a.reduce == ZERO_REDUCE_TOKEN ? 1.0f / tokens : 1.0f;
+#pragma unroll 4
         for (int64_t t = threadIdx.x; t < a.rows; t += kSetupThreads) {
             a.w[t] = a.targets[t] >= 0 ? w : 0.0f;
             a.adv[t] = a.advantages[t];
@@ -499,10 +504,12 @@ __global__ void __launch_bounds__(kSetupThreads) k_policy_setup(const PolicyToke
         float w = a.reduce == ZERO_REDUCE_TOKEN ? 1.0f / tokens : 1.0f;
         if (a.reduce == ZERO_REDUCE_SEQUENCE) {
             int64_t n = 0;
+#pragma unroll 4
             for (int64_t t = b + lane; t < e; t += 32) n += a.targets[t] >= 0;
             n = warp_sum(n);
             w = 1.0f / (float)(n ? n : 1) / filled;
         }
+#pragma unroll 4
         for (int64_t t = b + lane; t < e; t += 32) {
             a.w[t] = a.targets[t] >= 0 ? w : 0.0f;
             a.adv[t] = a.advantages[a.per_sequence ? s : t];
@@ -567,8 +574,8 @@ __device__ __forceinline__ TokenLoss policy_token(const PolicyTokens& a, const T
 // again. Two CTAs per SM, each with one slice: a producer warp refills a part of it with the next
 // row as soon as the gradient of this one has been taken from it, so that copies run beside
 // everything else. Rows are handed out one by one (some carry no loss and cost half).
-constexpr int kFusedWarps = 10, kFusedThreads = 32 * kFusedWarps;
-constexpr int kChunks = 4;
+constexpr int kFusedWarps = 7, kFusedThreads = 32 * kFusedWarps;
+constexpr int kChunks = 2;
 constexpr int64_t kFusedBytes = 110 * 1024;  // of a slice: two fit an SM
 
 template <int THREADS>
@@ -607,6 +614,7 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
 
     // The kernel before this one sets up the weights; it was itself launched behind the logits'
     // producer, so logits and targets may be read at once, and the rest after it.
+    let_next_kernel_start();
     if (threadIdx.x >= kFusedThreads) {
         uint32_t filled = 0;  // rows brought in
         bool ok = true;
