@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 CHECKED_LIB_PATH = os.path.join(BUILD_DIR, "libzero_gb300_checked.so")
 
 SOURCES = ["zero_kernels.cu", "zero_api.cpp", "zero_noalloc.cu", "zero_logits.cu", "zero_linear.cu", "zero_grads.cu"]
-HEADERS = ["zero_internal.h", "zero_host.h", "zero_softmax.cuh", "zero_tcgen05.cuh"]
+HEADERS = ["zero_internal.h", "zero_host.h", "zero_softmax.cuh", "zero_sum.cuh", "zero_tcgen05.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

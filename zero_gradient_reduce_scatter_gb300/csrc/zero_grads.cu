@@ -4,7 +4,8 @@
 // 128 bytes of that line, and the line is cut into one range per CTA, so that every CTA reads
 // the same number of bytes whatever the tensors' sizes and types. A CTA's part of a tensor has
 // a slot of its own (CTA index + tensor index: along the line one of the two always grows), and
-// the slots of a tensor are added in order: the sums do not depend on which CTA ends first.
+// slots and totals are added in a fixed order: the sums do not depend on which CTA ends first.
+// Two launches: the sums of squares, and the scaled copy, each CTA over the same range.
 
 #include <algorithm>
 #include <cmath>
@@ -16,22 +17,22 @@
 
 #include "zero_host.h"
 #include "zero_softmax.cuh"
+#include "zero_sum.cuh"
 
 struct zero_grads {
-    int device;
-    int64_t n;
-    int64_t units;
+    int64_t n, units, per;  // tensors; 2-byte units of the line, and of one CTA
     int grid;
-    bool has_dst;
     char* workspace;
 };
 
 namespace zg {
 namespace {
 
-constexpr int kGradThreads = 512;
+constexpr int kGradThreads = 512, kGradWarps = kGradThreads / 32;
 constexpr int kGradMaxGrid = 1024;
 constexpr int64_t kGradAlign = 64;  // units: 128 bytes of source
+constexpr int kBatch = 64;          // tensors whose rows a CTA holds at a time
+constexpr int kSmallSpan = 4096;    // elements of a tensor up to which one warp takes it alone
 
 // One tensor of the line.
 struct GradRow {
@@ -45,17 +46,13 @@ static_assert(sizeof(GradRow) == 40, "table row is 40 bytes");
 
 struct GradArgs {
     const GradRow* rows;
-    double* slots;   // [n + grid]
-    int64_t n, units;
+    double* slots;     // [n + grid] one per CTA's part of a tensor
+    double* totals;    // [grid] of a CTA's whole range
+    int64_t n, units, per;  // units of a CTA
+    int32_t grid;      // CTAs of the line
     float *norm, *scale, *norms;
     double max_norm;
 };
-
-__host__ __device__ __forceinline__ int64_t range_start(int64_t units, int grid, int b) {
-    const int64_t per = (units / kGradAlign + grid - 1) / grid * kGradAlign;
-    const int64_t u = per * b;
-    return u < units ? u : units;
-}
 
 // The tensor that holds unit u: the last one that starts at or before it.
 __device__ __forceinline__ int64_t tensor_of(const GradRow* rows, int64_t n, int64_t u) {
@@ -77,87 +74,274 @@ __device__ __forceinline__ Span span_of(const GradRow& r, int64_t u0, int64_t u1
     int64_t b = (u0 - r.start) >> w, e = (u1 - r.start) >> w;
     b = b < 0 ? 0 : b;
     e = e > r.numel ? r.numel : e;
-    return {b, e};
+    return {b, e < b ? b : e};
 }
 
-__device__ __forceinline__ float load_any(const void* p, int32_t type, int64_t i) {
-    if (type == ZERO_T_BF16) return widen(((const __nv_bfloat16*)p)[i]);
-    if (type == ZERO_T_FP16) return widen(((const __half*)p)[i]);
-    return ((const float*)p)[i];
-}
-__device__ __forceinline__ void store_any(void* p, int32_t type, int64_t i, float x) {
-    if (type == ZERO_T_BF16) ((__nv_bfloat16*)p)[i] = narrow<__nv_bfloat16>(x);
-    else if (type == ZERO_T_FP16) ((__half*)p)[i] = narrow<__half>(x);
-    else ((float*)p)[i] = x;
-}
-
-__device__ __forceinline__ double block_sum(double x, double* sm) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = x;
-    __syncthreads();
-    double t = 0.0;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) t += sm[w];
-    __syncthreads();
-    return t;
-}
-
-__global__ void __launch_bounds__(kGradThreads) k_grads_sumsq(const GradArgs a) {
-    __shared__ double sm[kGradThreads / 32];
-    const int64_t u0 = range_start(a.units, gridDim.x, blockIdx.x), u1 = range_start(a.units, gridDim.x, blockIdx.x + 1);
+// Calls `whole(i, row, span)` with all threads for this CTA's part of each large tensor and
+// `alone(i, row, span)` with one warp for each small one; i is the tensor. The rows of up to kBatch
+// tensors are fetched at once: thousands of small tensors would wait for each other's otherwise.
+template <class W, class A>
+__device__ __forceinline__ void for_tensors(const GradArgs& a, int64_t u0, int64_t u1, GradRow* batch, W whole, A alone) {
     if (u0 >= u1) return;
-    for (int64_t t = tensor_of(a.rows, a.n, u0); t < a.n && a.rows[t].start < u1; ++t) {
-        const GradRow r = a.rows[t];
-        const Span sp = span_of(r, u0, u1);
-        double s = 0.0;
-        for (int64_t i = sp.b + threadIdx.x; i < sp.e; i += kGradThreads) {
-            const double x = load_any(r.src, r.src_type, i);
-            s += x * x;
+    const int warp = threadIdx.x >> 5;
+    for (int64_t t0 = tensor_of(a.rows, a.n, u0);; t0 += kBatch) {
+        const int64_t t = t0 + threadIdx.x;
+        if (threadIdx.x < kBatch) {
+            batch[threadIdx.x].start = INT64_MAX;
+            if (t < a.n) batch[threadIdx.x] = a.rows[t];
         }
-        s = block_sum(s, sm);
-        if (threadIdx.x == 0) a.slots[blockIdx.x + t] = s;
+        __syncthreads();
+        for (int i = 0; i < kBatch && batch[i].start < u1; ++i) {
+            const Span sp = span_of(batch[i], u0, u1);
+            if (sp.e - sp.b > kSmallSpan) whole(t0 + i, batch[i], sp);
+        }
+        for (int i = warp; i < kBatch && batch[i].start < u1; i += kGradWarps) {
+            const Span sp = span_of(batch[i], u0, u1);
+            if (sp.e - sp.b <= kSmallSpan) alone(t0 + i, batch[i], sp);
+        }
+        const bool more = batch[kBatch - 1].start < u1;
+        __syncthreads();
+        if (!more) return;
     }
 }
 
-// One warp per tensor adds its slots; then the tensors' sums are added in order.
-__global__ void __launch_bounds__(1024) k_grads_finish(const GradArgs a, int grid) {
-    __shared__ double sm[32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t per = (a.units / kGradAlign + grid - 1) / grid * kGradAlign;
-    double total = 0.0;
-    for (int64_t t = warp; t < a.n; t += 32) {
-        const GradRow r = a.rows[t];
-        const int64_t len = r.src_type == ZERO_T_FP32 ? 2 * r.numel : r.numel;
-        double s = 0.0;
-        if (len > 0) {
-            const int64_t b0 = r.start / per, b1 = (r.start + len - 1) / per;
-            for (int64_t b = b0 + lane; b <= b1; b += 32) s += a.slots[b + t];
+// A sum of squares whose terms may leave fp32 either way. The squares of up to 32 values are added
+// in fp32; where that sum is no usable number (over 2^126, or under 2^-100: values of 2^-50 and
+// less, or none but zeros), each value goes into the sum of its own size, scaled into range.
+struct Squares {
+    Sum mid, big, small;  // big: times 2^-132, small: times 2^150
+    __device__ __forceinline__ void one_by_one(float x) {
+        const float y = fabsf(x);
+        if (y > 0x1p60f) big.add((x * 0x1p-66f) * (x * 0x1p-66f));
+        else if (y < 0x1p-60f) small.add((x * 0x1p75f) * (x * 0x1p75f));
+        else mid.add(x * x);
+    }
+    template <int N>
+    __device__ __forceinline__ void add(const float (&x)[N]) {
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i & 3] = fmaf(x[i], x[i], s[i & 3]);
+        const float p = (s[0] + s[1]) + (s[2] + s[3]);
+        if (p >= 0x1p-100f && p < 0x1p126f) {
+            mid.add(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) one_by_one(x[i]);
         }
+    }
+    __device__ __forceinline__ void over_warp() {
+        mid = warp_sum(mid);
+        if (__any_sync(~0u, big.hi != 0.0f)) big = warp_sum(big);
+        if (__any_sync(~0u, small.hi != 0.0f)) small = warp_sum(small);
+    }
+    __device__ __forceinline__ double value() const { return mid.value() + big.value() * 0x1p132 + small.value() * 0x1p-150; }
+};
+
+// Eight elements of type T from p (aligned for 16-byte loads where ALIGNED). LAST: nothing reads
+// them again; they may be written by this kernel, so not through the read-only path.
+template <class T, bool ALIGNED, bool LAST>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+    if constexpr (!ALIGNED) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = widen(p[i]);
+    } else {
+        constexpr int kVecs = 8 / kVec<T>;
+        uint4 v[kVecs];
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const uint4* q = reinterpret_cast<const uint4*>(p) + i;
+            v[i] = LAST ? __ldcs(q) : __ldg(q);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack2(widen2<T>(v[i / (kVec<T> / 2)], i % (kVec<T> / 2)));
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    }
+}
+template <class T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
+    constexpr int kVecs = 8 / kVec<T>;
+    uint4 v[kVecs];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) narrow2<T>(v[i / (kVec<T> / 2)], i % (kVec<T> / 2), make_float2(x[2 * i], x[2 * i + 1]));
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) __stcs(reinterpret_cast<uint4*>(p) + i, v[i]);
+}
+
+// Elements before the first 16-byte boundary of p.
+template <class T>
+__device__ __forceinline__ int64_t to_boundary(const T* p) {
+    return (int64_t)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int64_t)sizeof(T);
+}
+
+// Squares of src[b, e) as threads `id` of `count` take them, 32 elements at a time.
+template <class T>
+__device__ __forceinline__ void sum_span(const T* src, Span sp, int id, int count, Squares& sq) {
+    const T* p = src + sp.b;
+    const int64_t n = sp.e - sp.b;
+    int64_t head = to_boundary(p);
+    head = head < n ? head : n;
+    const int64_t groups = (n - head) / 8, tail = head + groups * 8;
+    p += head;
+    int64_t i = id;
+    for (; i + 3 * (int64_t)count < groups; i += 4 * (int64_t)count) {
+        float x[4][8];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) load8<T, true, false>(p + (i + u * (int64_t)count) * 8, x[u]);
+        sq.add(reinterpret_cast<float(&)[32]>(x));
+    }
+    for (; i < groups; i += count) {
+        float x[8];
+        load8<T, true, false>(p + i * 8, x);
+        sq.add(x);
+    }
+    p -= head;
+    if (id < head) sq.one_by_one(widen(p[id]));
+    if (id < n - tail) sq.one_by_one(widen(p[tail + id]));
+}
+__device__ __forceinline__ void sum_any(const GradRow& r, Span sp, int id, int count, Squares& sq) {
+    if (r.src_type == ZERO_T_BF16) sum_span((const __nv_bfloat16*)r.src, sp, id, count, sq);
+    else if (r.src_type == ZERO_T_FP16) sum_span((const __half*)r.src, sp, id, count, sq);
+    else sum_span((const float*)r.src, sp, id, count, sq);
+}
+
+// Bound by reading the gradients once.
+__global__ void __launch_bounds__(kGradThreads, 2) k_grads_sumsq(const GradArgs a) {
+    __shared__ GradRow batch[kBatch];
+    __shared__ double sm[kGradWarps], small_totals[kGradWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    let_next_kernel_start();
+    wait_for_kernel_before();
+    const int64_t u0 = min(a.units, a.per * blockIdx.x), u1 = min(a.units, u0 + a.per);
+    double total = 0.0, alone_total = 0.0;  // in thread 0; in lane 0 of each warp
+    for_tensors(
+        a, u0, u1, batch,
+        [&](int64_t t, const GradRow& r, Span sp) {
+            Squares sq;
+            sum_any(r, sp, threadIdx.x, kGradThreads, sq);
+            sq.over_warp();
+            if (lane == 0) sm[warp] = sq.value();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                double s = 0.0;
+                for (int w = 0; w < kGradWarps; ++w) s += sm[w];
+                a.slots[blockIdx.x + t] = s;
+                total += s;
+            }
+            __syncthreads();
+        },
+        [&](int64_t t, const GradRow& r, Span sp) {
+            Squares sq;
+            sum_any(r, sp, lane, 32, sq);
+            sq.over_warp();
+            if (lane == 0) {
+                const double s = sq.value();
+                a.slots[blockIdx.x + t] = s;
+                alone_total += s;
+            }
+        });
+    if (lane == 0) small_totals[warp] = alone_total;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 0; w < kGradWarps; ++w) total += small_totals[w];
+        a.totals[blockIdx.x] = total;
+    }
+}
+
+// dst[b, e) = src[b, e) * f as threads `id` of `count` take them, from the end: what the sum of
+// squares read last may still be in L2. Groups of eight lie at dst's 16-byte boundaries; src's are
+// loaded one by one (through L1) where its alignment differs.
+template <class S, class D, bool ALIGNED>
+__device__ __forceinline__ void scale_groups(const S* s, D* d, int64_t groups, int id, int count, float f) {
+    const int64_t last = (groups - 1 - id) / count;  // this thread's last round; negative rounds to 0
+    if (id >= groups) return;
+    int64_t k = last;
+    for (; k >= 3; k -= 4) {
+        float x[4][8];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) load8<S, ALIGNED, true>(s + (id + (k - u) * count) * 8, x[u]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[u][j] *= f;
+            store8(d + (id + (k - u) * count) * 8, x[u]);
+        }
+    }
+    for (; k >= 0; --k) {
+        float x[8];
+        load8<S, ALIGNED, true>(s + (id + k * count) * 8, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] *= f;
+        store8(d + (id + k * count) * 8, x);
+    }
+}
+template <class S, class D>
+__device__ __forceinline__ void scale_span(const S* src, D* dst, Span sp, int id, int count, float f) {
+    const S* s = src + sp.b;
+    D* d = dst + sp.b;
+    const int64_t n = sp.e - sp.b;
+    int64_t head = to_boundary(d);
+    head = head < n ? head : n;
+    const int64_t groups = (n - head) / 8, tail = head + groups * 8;
+    if (to_boundary(s + head) == 0) scale_groups<S, D, true>(s + head, d + head, groups, id, count, f);
+    else scale_groups<S, D, false>(s + head, d + head, groups, id, count, f);
+    if (id < head) d[id] = narrow<D>(widen(s[id]) * f);
+    if (id < n - tail) d[tail + id] = narrow<D>(widen(s[tail + id]) * f);
+}
+template <class S>
+__device__ __forceinline__ void scale_to(const GradRow& r, Span sp, int id, int count, float f) {
+    if (r.dst_type == ZERO_T_BF16) scale_span((const S*)r.src, (__nv_bfloat16*)r.dst, sp, id, count, f);
+    else if (r.dst_type == ZERO_T_FP16) scale_span((const S*)r.src, (__half*)r.dst, sp, id, count, f);
+    else scale_span((const S*)r.src, (float*)r.dst, sp, id, count, f);
+}
+__device__ __forceinline__ void scale_any(const GradRow& r, Span sp, int id, int count, float f) {
+    if (!r.dst || (r.dst == r.src && f == 1.0f)) return;
+    if (r.src_type == ZERO_T_BF16) scale_to<__nv_bfloat16>(r, sp, id, count, f);
+    else if (r.src_type == ZERO_T_FP16) scale_to<__half>(r, sp, id, count, f);
+    else scale_to<float>(r, sp, id, count, f);
+}
+
+// Bound by reading the gradients again and writing them. Every CTA adds the totals of all in the
+// same order (a warp, a few hundred numbers from L2), which is cheaper than a kernel between.
+__global__ void __launch_bounds__(kGradThreads, 2) k_grads_scale(const GradArgs a) {
+    __shared__ GradRow batch[kBatch];
+    __shared__ float factor;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    wait_for_kernel_before();
+    if (warp == 0) {
+        double s = 0.0;
+        for (int i = lane; i < a.grid; i += 32) s += a.totals[i];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
         if (lane == 0) {
-            total += s;
-            if (a.norms) a.norms[t] = (float)sqrt(s);
+            const double norm = sqrt(s);
+            factor = isfinite(norm) && norm > a.max_norm ? (float)(a.max_norm / norm) : 1.0f;
+            if (blockIdx.x == 0) {
+                *a.norm = (float)norm;
+                *a.scale = factor;
+            }
         }
     }
-    const double norm = sqrt(block_sum(total, sm));
-    if (threadIdx.x == 0) {
-        *a.norm = (float)norm;
-        *a.scale = isfinite(norm) && norm > a.max_norm ? (float)(a.max_norm / norm) : 1.0f;
-    }
-}
-
-__global__ void __launch_bounds__(kGradThreads) k_grads_scale(const GradArgs a) {
-    const float f = *a.scale;
-    const int64_t u0 = range_start(a.units, gridDim.x, blockIdx.x), u1 = range_start(a.units, gridDim.x, blockIdx.x + 1);
-    if (u0 >= u1) return;
-    for (int64_t t = tensor_of(a.rows, a.n, u0); t < a.n && a.rows[t].start < u1; ++t) {
-        const GradRow r = a.rows[t];
-        if (!r.dst || (r.dst == r.src && f == 1.0f)) continue;
-        const Span sp = span_of(r, u0, u1);
-        for (int64_t i = sp.b + threadIdx.x; i < sp.e; i += kGradThreads)
-            store_any(r.dst, r.dst_type, i, load_any(r.src, r.src_type, i) * f);
-    }
+    __syncthreads();
+    // every tensor's own norm, a warp each
+    if (a.norms)
+        for (int64_t t = (int64_t)blockIdx.x * kGradWarps + warp; t < a.n; t += (int64_t)gridDim.x * kGradWarps) {
+            const GradRow r = a.rows[t];
+            const int64_t len = r.src_type == ZERO_T_FP32 ? 2 * r.numel : r.numel;
+            double s = 0.0;
+            if (len > 0)
+                for (int64_t b = r.start / a.per + lane; b <= (r.start + len - 1) / a.per; b += 32) s += a.slots[b + t];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+            if (lane == 0) a.norms[t] = (float)sqrt(s);
+        }
+    const float f = factor;
+    const int64_t u0 = min(a.units, a.per * blockIdx.x), u1 = min(a.units, u0 + a.per);
+    for_tensors(
+        a, u0, u1, batch, [&](int64_t, const GradRow& r, Span sp) { scale_any(r, sp, threadIdx.x, kGradThreads, f); },
+        [&](int64_t, const GradRow& r, Span sp) { scale_any(r, sp, lane, 32, f); });
 }
 
 std::mutex g_plans_mu;
@@ -172,7 +356,7 @@ using namespace zg;
 
 extern "C" int64_t zero_grads_workspace(int64_t n) {
     if (n < 1 || n > INT32_MAX) return -1;
-    return table_bytes(n) + (n + kGradMaxGrid) * 8;
+    return table_bytes(n) + (n + 2 * kGradMaxGrid) * 8;
 }
 
 extern "C" int zero_grads_init(zero_grads** out, const zero_grad_tensor* tensors, int64_t n, void* workspace,
@@ -189,7 +373,6 @@ extern "C" int zero_grads_init(zero_grads** out, const zero_grad_tensor* tensors
         return ZERO_ERR_INVALID_ARG;
     }
     int64_t at = 0;
-    bool has_dst = false;
     for (int64_t i = 0; i < n && !d.rc; ++i) {
         const zero_grad_tensor& t = tensors[i];
         if (t.numel < 0 || t.numel > (INT64_C(1) << 44) || !type_ok(t.src_type) || (t.dst && !type_ok(t.dst_type))) return ZERO_ERR_INVALID_ARG;
@@ -197,7 +380,6 @@ extern "C" int zero_grads_init(zero_grads** out, const zero_grad_tensor* tensors
         if (t.numel > 0) {
             d.need(t.src, type_size(t.src_type));
             if (t.dst) d.need(t.dst, type_size(t.dst_type));
-            has_dst |= t.dst != nullptr;
         }
         rows[(size_t)i] = GradRow{t.src, t.numel > 0 ? t.dst : nullptr, t.numel, at, t.src_type, t.dst_type};
         const int64_t units = t.numel * (type_size(t.src_type) / 2);
@@ -205,13 +387,15 @@ extern "C" int zero_grads_init(zero_grads** out, const zero_grad_tensor* tensors
         if (at > (INT64_C(1) << 46)) return ZERO_ERR_INVALID_ARG;
     }
     if (d.rc) return d.rc;
-    const int64_t want = at / (16 * kGradAlign) + 1;  // at least 2 KB of source a CTA
-    const int grid = (int)std::min<int64_t>(std::min<int64_t>(want, 4 * d.sm_count()), kGradMaxGrid);
+    const int64_t want = at / (32 * kGradAlign) + 1;  // at least 4 KB of source a CTA
+    const int64_t most = std::min<int64_t>(std::min<int64_t>(want, 2 * d.sm_count()), kGradMaxGrid);
+    const int64_t per = std::max<int64_t>(1, (at / kGradAlign + most - 1) / most) * kGradAlign;
+    const int grid = (int)std::max<int64_t>(1, (at + per - 1) / per);
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e = cudaMemcpyAsync(workspace, rows.data(), (size_t)n * sizeof(GradRow), cudaMemcpyHostToDevice, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return record_cuda_error(e);
-    zero_grads* p = new (std::nothrow) zero_grads{d.device(), n, at, grid, has_dst, (char*)workspace};
+    zero_grads* p = new (std::nothrow) zero_grads{n, at, per, grid, (char*)workspace};
     if (!p) return ZERO_ERR_INVALID_ARG;
     try {
         std::lock_guard<std::mutex> lk(g_plans_mu);
@@ -239,24 +423,17 @@ extern "C" int zero_grads_clip(zero_grads* p, double max_norm, float* norm, floa
     GradArgs a;
     a.rows = (const GradRow*)p->workspace;
     a.slots = (double*)(p->workspace + table_bytes(p->n));
+    a.totals = a.slots + p->n + kGradMaxGrid;
     a.n = p->n;
     a.units = p->units;
+    a.per = p->per;
+    a.grid = p->grid;
     a.norm = norm;
     a.scale = scale;
     a.norms = tensor_norms;
     a.max_norm = max_norm;
-    int rc = ZERO_OK;
-    if (p->units > 0) {
-        k_grads_sumsq<<<p->grid, kGradThreads, 0, s>>>(a);
-        if ((rc = launched())) return rc;
-    }
-    k_grads_finish<<<1, 1024, 0, s>>>(a, p->grid);
-    if ((rc = launched())) return rc;
-    if (p->units > 0 && p->has_dst) {
-        k_grads_scale<<<p->grid, kGradThreads, 0, s>>>(a);
-        rc = launched();
-    }
-    return rc;
+    const int rc = launch_linked(k_grads_sumsq, (unsigned)p->grid, kGradThreads, 0, 1, s, a);
+    return rc ? rc : launch_linked(k_grads_scale, (unsigned)p->grid, kGradThreads, 0, 1, s, a);
 }
 
 extern "C" int zero_grads_destroy(zero_grads* p) {
