@@ -273,12 +273,34 @@ __global__ void __launch_bounds__(kLinearThreads, 1)
     if (threadIdx.x == 0) a.status[blockIdx.x] = gave_up;
 }
 
-// 32 rows by 16 slices of their parts, four parts on their way at a time; the slices are joined
-// in order.
+// A row's results from its joined sums, by one thread.
+template <bool ENTROPY>
+__device__ __forceinline__ void finish(const LinearArgs& a, int64_t t, int64_t y, const RowStat& s, bool gave_up, float* logp, float* lse,
+                                       float* entropy) {
+    RowResult r = {0.0f, 0.0f, 0.0f};
+    if (y >= 0) {
+        r = finish_row<ENTROPY>(s, y < a.vocab ? a.zy[t] : NAN, a.k, a.inv_t);
+        if (y >= a.vocab) r.logp = NAN;
+    }
+    if (gave_up) r.logp = r.lse = r.entropy = NAN;  // no result
+    logp[t] = r.logp;
+    lse[t] = r.lse;
+    if (ENTROPY) entropy[t] = r.entropy;
+}
+
+// Whether a wait of the product gave up, seen by all threads.
+__device__ __forceinline__ bool any_gave_up(const LinearArgs& a) {
+    bool gave_up = false;
+    for (int i = threadIdx.x; i < a.grid; i += blockDim.x) gave_up |= a.status[i] != 0;
+    return __syncthreads_or(gave_up);
+}
+
+// Many rows: 32 rows (lanes, so that loads are whole lines) by 16 slices of their parts, four
+// parts on their way at a time; the slices are joined in order.
 constexpr int kJoinSlices = 16;
 
 template <bool ENTROPY>
-__global__ void __launch_bounds__(32 * kJoinSlices) k_linear_join(const LinearArgs a, int64_t parts, float* logp, float* lse, float* entropy) {
+__global__ void __launch_bounds__(32 * kJoinSlices) k_linear_join(const LinearArgs a, int parts, float* logp, float* lse, float* entropy) {
     __shared__ RowStat sm[kJoinSlices][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     wait_for_kernel_before();
@@ -286,7 +308,7 @@ __global__ void __launch_bounds__(32 * kJoinSlices) k_linear_join(const LinearAr
     RowStat s = empty_stat();
     const int64_t y = t < a.rows ? a.targets[t] : -1;
     if (y >= 0)  // parts of rows without a target may not have been written
-        for (int64_t p0 = warp; p0 < parts; p0 += 4 * kJoinSlices) {
+        for (int p0 = warp; p0 < parts; p0 += 4 * kJoinSlices) {
             RowStat b[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -298,20 +320,31 @@ __global__ void __launch_bounds__(32 * kJoinSlices) k_linear_join(const LinearAr
             for (int i = 0; i < 4; ++i) s = join<ENTROPY>(s, b[i], a.k);
         }
     sm[warp][lane] = s;
-    bool gave_up = false;
-    for (int i = threadIdx.x; i < a.grid; i += 32 * kJoinSlices) gave_up |= a.status[i] != 0;
-    gave_up = __syncthreads_or(gave_up);
+    const bool gave_up = any_gave_up(a);
     if (warp != 0 || t >= a.rows) return;
     for (int w = 1; w < kJoinSlices; ++w) s = join<ENTROPY>(s, sm[w][lane], a.k);
-    RowResult r = {0.0f, 0.0f, 0.0f};
-    if (y >= 0) {
-        r = finish_row<ENTROPY>(s, y < a.vocab ? a.zy[t] : NAN, a.k, a.inv_t);
-        if (y >= a.vocab) r.logp = NAN;
-    }
-    if (gave_up) r.logp = r.lse = r.entropy = NAN;  // no result
-    logp[t] = r.logp;
-    lse[t] = r.lse;
-    if (ENTROPY) entropy[t] = r.entropy;
+    finish<ENTROPY>(a, t, y, s, gave_up, logp, lse, entropy);
+}
+
+// Few rows: a CTA each, a thread per part. The other form would have one CTA go through all parts
+// of 32 rows, one latency after the other (14 us for 16 rows of 898 parts).
+constexpr int kJoinThreads = 256;
+constexpr int64_t kJoinFewRows = 1024;
+
+template <bool ENTROPY>
+__global__ void __launch_bounds__(kJoinThreads) k_linear_join_few(const LinearArgs a, int parts, float* logp, float* lse, float* entropy) {
+    __shared__ RowStat sm[kJoinThreads / 32];
+    wait_for_kernel_before();
+    const int64_t t = blockIdx.x, y = a.targets[t];
+    RowStat s = empty_stat();
+    if (y >= 0)
+        for (int64_t p = threadIdx.x; p < parts; p += kJoinThreads) {
+            const RowStat b = {a.m[p * a.rows + t], a.s[p * a.rows + t], ENTROPY ? a.q[p * a.rows + t] : 0.0f};
+            s = join<ENTROPY>(s, b, a.k);
+        }
+    s = group_join<ENTROPY, true, kJoinThreads / 32>(s, a.k, sm, 0);
+    const bool gave_up = any_gave_up(a);
+    if (threadIdx.x == 0) finish<ENTROPY>(a, t, y, s, gave_up, logp, lse, entropy);
 }
 
 constexpr int kMaxGrid = 1024;
@@ -400,7 +433,9 @@ int run_linear(const zero_linear* x, const LinearArgs& a, const LinearPlan& l, f
     if (l.pairs) rc = bf16 ? launch_product<ZERO_T_BF16, 2, 256, ENTROPY>(x, a, s) : launch_product<ZERO_T_FP16, 2, 256, ENTROPY>(x, a, s);
     else rc = bf16 ? launch_product<ZERO_T_BF16, 1, 128, ENTROPY>(x, a, s) : launch_product<ZERO_T_FP16, 1, 128, ENTROPY>(x, a, s);
     if (rc) return rc;
-    return launch_linked(k_linear_join<ENTROPY>, (unsigned)((x->rows + 31) / 32), 32 * kJoinSlices, 0, 1, s, a, l.parts, logp, lse, entropy);
+    if (x->rows <= kJoinFewRows)
+        return launch_linked(k_linear_join_few<ENTROPY>, (unsigned)x->rows, kJoinThreads, 0, 1, s, a, (int)l.parts, logp, lse, entropy);
+    return launch_linked(k_linear_join<ENTROPY>, (unsigned)((x->rows + 31) / 32), 32 * kJoinSlices, 0, 1, s, a, (int)l.parts, logp, lse, entropy);
 }
 
 // The workspace of any number of SMs.
