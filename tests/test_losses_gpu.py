@@ -245,7 +245,7 @@ def make_offsets(lens):
     return torch.tensor(off, dtype=torch.int64, device=DEV)
 
 
-PAIRS = [[1, 1], [5, 0], [0, 0], [3, 9, 1, 2], [40, 17, 0, 5, 64, 64, 2, 1], [300, 211]]
+PAIRS = [[1, 1], [5, 0], [0, 0], [3, 9, 1, 2], [40, 17, 0, 5, 64, 64, 2, 1], [300, 211], [7, 1, 0, 0, 130, 95, 211, 60, 0, 0, 1, 88]]
 
 
 @pytest.mark.parametrize("lens", PAIRS)

@@ -109,7 +109,7 @@ __device__ __forceinline__ bool fast_row(const T* x, int64_t vocab, float x_y) {
 // are few rows), each thread kUnroll vectors at a time.
 template <class T, bool ENTROPY>
 __global__ void __launch_bounds__(kRowThreads)
-    k_token_logp(const Rows<T> a, int size, float* logp, float* lse, float* entropy, float* cleared) {
+    k_token_logp(const Rows<T> a, int size, float* logp, float* lse, float* entropy, float* cleared, uint32_t* counter) {
     __shared__ RowStat sm[kRowThreads / 32], mine;
     let_next_kernel_start();
     wait_for_kernel_before();
@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(kRowThreads)
         lse[t] = r.lse;
         if (ENTROPY) entropy[t] = r.entropy;
         if (cleared) cleared[t] = 0.0f;
+        if (counter && t == 0) *counter = 0;
     }
     if (size > 1 && y >= 0) cg::this_cluster().sync();  // no CTA leaves while another reads its sums
 }
@@ -303,18 +304,22 @@ struct PairArgs {
     const float* logp;
     const float* ref;
     float* g;
-    float *pair_loss, *chosen, *rejected;
+    float *pair_loss, *chosen, *rejected, *loss;
+    uint32_t* done;  // CTAs that have ended; 0 before
     int64_t rows, pairs;
     double beta, smoothing;
     int32_t kind, average;
 };
 
-// log(1 + e^x) without overflow
-__device__ __forceinline__ double softplus(double x) { return fmax(x, 0.0) + log1p(exp(-fabs(x))); }
+// log(1 + e^x) without overflow; a NaN stays
+__device__ __forceinline__ float softplus(float x) { return (x < 0.0f ? 0.0f : x) + log1pf(expf(-fabsf(x))); }
 
 __global__ void __launch_bounds__(kRowThreads) k_pairs(const PairArgs a) {
     __shared__ Sum sm[kRowThreads / 32];
+    __shared__ unsigned long long count;
     __shared__ float g_side[2];
+    let_next_kernel_start();
+    wait_for_kernel_before();
     for (int64_t i = blockIdx.x; i < a.pairs; i += gridDim.x) {
         int64_t lo[2], hi[2];
         double d[2], n[2];
@@ -322,61 +327,67 @@ __global__ void __launch_bounds__(kRowThreads) k_pairs(const PairArgs a) {
             lo[k] = clamp_offset(a.offsets[2 * i + k], 0, a.rows);
             hi[k] = clamp_offset(a.offsets[2 * i + k + 1], lo[k], a.rows);
             Sum sum;
-            int count = 0;
+            unsigned targets = 0;
+#pragma unroll 4
             for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kRowThreads) {
                 if (a.targets[t] < 0) continue;
                 sum.add(a.logp[t]);
                 if (a.ref) sum.add(-a.ref[t]);
-                ++count;
+                ++targets;
             }
-            d[k] = cta_sum<kRowThreads>(sum, sm).value();
+            if (threadIdx.x == 0) count = 0;
+            sum = cta_sum<kRowThreads>(sum, sm);
             n[k] = 1.0;
             if (a.average) {
-                __shared__ unsigned long long total;
-                if (threadIdx.x == 0) total = 0;
+                atomicAdd(&count, (unsigned long long)targets);
                 __syncthreads();
-                atomicAdd(&total, (unsigned long long)count);
-                __syncthreads();
-                n[k] = total ? (double)total : 1.0;
+                n[k] = count ? (double)count : 1.0;
                 __syncthreads();
             }
-            d[k] /= n[k];
+            d[k] = sum.value() / n[k];
         }
         if (threadIdx.x == 0) {
-            const double m = d[0] - d[1], b = a.beta, e = a.smoothing;
-            double loss, dm;
+            // the margin in fp64 (it may cancel), what follows from it in fp32
+            const double m = d[0] - d[1];
+            const float b = (float)a.beta, e = (float)a.smoothing, s = (float)(a.beta * m);
+            float loss, dm;
             if (a.kind == ZERO_PREF_SIGMOID) {
-                loss = (1.0 - e) * softplus(-b * m) + e * softplus(b * m);
+                loss = (1.0f - e) * softplus(-s) + e * softplus(s);
                 // sigmoid(s) - (1 - e), each half formed without cancellation
-                dm = b * (e / (1.0 + exp(-b * m)) - (1.0 - e) / (1.0 + exp(b * m)));
+                dm = b * (e / (1.0f + expf(-s)) - (1.0f - e) / (1.0f + expf(s)));
             } else if (a.kind == ZERO_PREF_HINGE) {
-                const double gap = 1.0 - b * m;
-                loss = gap > 0.0 || gap != gap ? gap : 0.0;
-                dm = gap > 0.0 ? -b : gap * 0.0;
+                const float gap = (float)(1.0 - a.beta * m);
+                loss = gap > 0.0f || gap != gap ? gap : 0.0f;
+                dm = gap > 0.0f ? -b : gap * 0.0f;
             } else {
-                const double gap = m - 0.5 / b;
+                const float gap = (float)(m - 0.5 / a.beta);
                 loss = gap * gap;
-                dm = 2.0 * gap;
+                dm = 2.0f * gap;
             }
-            a.pair_loss[i] = (float)loss;
-            a.chosen[i] = (float)(b * d[0]);
-            a.rejected[i] = (float)(b * d[1]);
-            g_side[0] = (float)(dm / n[0] / (double)a.pairs);
-            g_side[1] = (float)(-dm / n[1] / (double)a.pairs);
+            a.pair_loss[i] = loss;
+            a.chosen[i] = (float)(a.beta * d[0]);
+            a.rejected[i] = (float)(a.beta * d[1]);
+            g_side[0] = dm / ((float)n[0] * (float)a.pairs);
+            g_side[1] = -dm / ((float)n[1] * (float)a.pairs);
         }
         __syncthreads();
         for (int k = 0; k < 2; ++k)
             for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kRowThreads) a.g[t] = g_side[k];
         __syncthreads();
     }
-}
-
-__global__ void __launch_bounds__(1024) k_mean(const float* x, int64_t n, float* out) {
-    __shared__ Sum sm[32];
+    // the CTA that ends last takes the mean, in the pairs' order
+    __shared__ bool last;
+    if (threadIdx.x == 0) {
+        __threadfence();
+        last = atomicAdd(a.done, 1u) == gridDim.x - 1;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!last) return;
     Sum s;
-    for (int64_t i = threadIdx.x; i < n; i += 1024) s.add(x[i]);
-    s = cta_sum<1024>(s, sm);
-    if (threadIdx.x == 0) *out = (float)(s.value() / (double)n);
+    for (int64_t i = threadIdx.x; i < a.pairs; i += kRowThreads) s.add(__ldcg(a.pair_loss + i));
+    s = cta_sum<kRowThreads>(s, sm);
+    if (threadIdx.x == 0) *a.loss = (float)(s.value() / (double)a.pairs);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -814,8 +825,8 @@ int64_t fused_part(const zero_logits* x, int size) {
 }
 int64_t fused_bytes(const zero_logits* x, int size) { return 16 * kChunks * fused_part(x, size); }
 
-int launch_token_logp(const zero_logits* x, const float* weight, float* logp, float* lse, float* entropy, float* cleared, int sms,
-                      cudaStream_t s) {
+int launch_token_logp(const zero_logits* x, const float* weight, float* logp, float* lse, float* entropy, float* cleared,
+                      uint32_t* counter, int sms, cudaStream_t s) {
     if (x->rows == 0) return ZERO_OK;
     return by_type(x->type, [&](auto tag) {
         using T = decltype(tag);
@@ -823,7 +834,7 @@ int launch_token_logp(const zero_logits* x, const float* weight, float* logp, fl
         const int size = ctas_per_row(x, sms);
         const unsigned grid = (unsigned)(x->rows * size);
         return launch_linked(entropy ? k_token_logp<T, true> : k_token_logp<T, false>, grid, kRowThreads, 0, size, s, a, size, logp, lse,
-                             entropy, cleared);
+                             entropy, cleared, counter);
     });
 }
 
@@ -885,7 +896,7 @@ extern "C" int zero_token_logp(const zero_logits* x, float* logp, float* lse, fl
     d.need(lse, 4);
     d.optional(entropy, 4);
     if (d.rc) return d.rc;
-    return launch_token_logp(x, nullptr, logp, lse, entropy, nullptr, d.sm_count(), (cudaStream_t)stream);
+    return launch_token_logp(x, nullptr, logp, lse, entropy, nullptr, nullptr, d.sm_count(), (cudaStream_t)stream);
 }
 
 extern "C" int zero_token_logp_backward(const zero_logits* x, const float* logp, const float* lse, const float* entropy,
@@ -938,14 +949,16 @@ extern "C" int zero_preference_loss(const zero_logits* x, const zero_preference*
     cudaStream_t s = (cudaStream_t)stream;
     float* lse = (float*)workspace;
     float* g = lse + round_up(x->rows, 4);
+    uint32_t* done = (uint32_t*)(g + round_up(x->rows, 4));
     const int sms = d.sm_count();
-    if ((rc = launch_token_logp(x, nullptr, p->logp, lse, nullptr, g, sms, s))) return rc;
-    const PairArgs a = {x->targets, p->offsets, p->logp, p->ref_logp, g, p->pair_loss, p->chosen_reward, p->rejected_reward,
+    const PairArgs a = {x->targets, p->offsets, p->logp, p->ref_logp, g, p->pair_loss, p->chosen_reward, p->rejected_reward, p->loss, done,
                         x->rows, p->pairs, p->beta, p->kind == ZERO_PREF_SIGMOID ? p->label_smoothing : 0.0, p->kind, p->average};
-    k_pairs<<<(int)std::min<int64_t>(p->pairs, 1 << 20), kRowThreads, 0, s>>>(a);
-    if ((rc = launched())) return rc;
-    k_mean<<<1, 1024, 0, s>>>(p->pair_loss, p->pairs, p->loss);
-    if ((rc = launched())) return rc;
+    if (x->rows == 0) {  // no forward kernel that clears the counter
+        const cudaError_t e = cudaMemsetAsync(done, 0, 4, s);
+        if (e != cudaSuccess) return record_cuda_error(e);
+    }
+    if ((rc = launch_token_logp(x, nullptr, p->logp, lse, nullptr, g, done, sms, s))) return rc;
+    if ((rc = launch_linked(k_pairs, (unsigned)std::min<int64_t>(p->pairs, 1 << 20), kRowThreads, 0, 1, s, a))) return rc;
     return launch_token_grad(x, nullptr, p->logp, lse, nullptr, g, nullptr, p->dlogits, p->dstride, sms, s);
 }
 
@@ -1018,7 +1031,7 @@ extern "C" int zero_policy_loss(const zero_logits* x, const zero_policy* p, void
         k_policy_setup<<<1, kSetupThreads, 0, s>>>(a);
         if ((rc = launched())) return rc;
         if (fused_size(x, sms)) return launch_policy_rows(x, a, p, sms, s);
-        if ((rc = launch_token_logp(x, a.w, p->logp, a.lse, p->entropy, nullptr, sms, s))) return rc;
+        if ((rc = launch_token_logp(x, a.w, p->logp, a.lse, p->entropy, nullptr, nullptr, sms, s))) return rc;
         k_policy_tokens<<<(int)std::min<int64_t>((x->rows + kRowThreads - 1) / kRowThreads, 1024), kRowThreads, 0, s>>>(a, p->logp, p->entropy);
         if ((rc = launched())) return rc;
         rc = launch_token_grad(x, a.w, p->logp, a.lse, p->entropy, a.g, a.entropy_coef != 0.0f ? a.h : nullptr, p->dlogits, p->dstride, sms, s);
