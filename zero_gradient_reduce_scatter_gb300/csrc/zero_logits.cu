@@ -267,7 +267,8 @@ __global__ void __launch_bounds__(kRowThreads)
                  const float* dentropy, T* dx, int64_t dstride) {
     let_next_kernel_start();
     wait_for_kernel_before();
-    const int64_t t = blockIdx.x / size;
+    // From the last row: what a forward pass read last may still be in L2.
+    const int64_t t = a.rows - 1 - blockIdx.x / size;
     const int rank = (int)(blockIdx.x % size);
     const int64_t y = live_target(a, t);
     const float g = y < 0 ? 0.0f : dlogp[t], h = y < 0 || !H ? 0.0f : dentropy[t];
