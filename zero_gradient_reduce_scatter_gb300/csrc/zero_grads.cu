@@ -46,6 +46,7 @@ static_assert(sizeof(GradRow) == 40, "table row is 40 bytes");
 
 struct GradArgs {
     const GradRow* rows;
+    const int32_t* first;  // [grid] the tensor that holds a CTA's first unit
     double* slots;     // [n + grid] one per CTA's part of a tensor
     double* totals;    // [grid] of a CTA's whole range
     int64_t n, units, per;  // units of a CTA
@@ -53,17 +54,6 @@ struct GradArgs {
     float *norm, *scale, *norms;
     double max_norm;
 };
-
-// The tensor that holds unit u: the last one that starts at or before it.
-__device__ __forceinline__ int64_t tensor_of(const GradRow* rows, int64_t n, int64_t u) {
-    int64_t lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi + 1) >> 1;
-        if (rows[mid].start <= u) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
-}
 
 // Elements of tensor r that lie in units [u0, u1).
 struct Span {
@@ -84,7 +74,7 @@ template <class W, class A>
 __device__ __forceinline__ void for_tensors(const GradArgs& a, int64_t u0, int64_t u1, GradRow* batch, W whole, A alone) {
     if (u0 >= u1) return;
     const int warp = threadIdx.x >> 5;
-    for (int64_t t0 = tensor_of(a.rows, a.n, u0);; t0 += kBatch) {
+    for (int64_t t0 = a.first[blockIdx.x];; t0 += kBatch) {
         const int64_t t = t0 + threadIdx.x;
         if (threadIdx.x < kBatch) {
             batch[threadIdx.x].start = INT64_MAX;
@@ -349,6 +339,10 @@ std::unordered_set<const zero_grads*> g_plans;  // plans not yet destroyed
 
 int64_t table_bytes(int64_t n) { return (n * (int64_t)sizeof(GradRow) + 255) / 256 * 256; }
 
+// A plan's workspace: the table, slots, totals, and the CTAs' first tensors.
+double* slots_of(void* workspace, int64_t n) { return (double*)((char*)workspace + table_bytes(n)); }
+int32_t* first_of(void* workspace, int64_t n) { return (int32_t*)(slots_of(workspace, n) + n + 2 * kGradMaxGrid); }
+
 }  // namespace
 }  // namespace zg
 
@@ -356,7 +350,7 @@ using namespace zg;
 
 extern "C" int64_t zero_grads_workspace(int64_t n) {
     if (n < 1 || n > INT32_MAX) return -1;
-    return table_bytes(n) + (n + 2 * kGradMaxGrid) * 8;
+    return table_bytes(n) + (n + 2 * kGradMaxGrid) * 8 + kGradMaxGrid * 4;
 }
 
 extern "C" int zero_grads_init(zero_grads** out, const zero_grad_tensor* tensors, int64_t n, void* workspace,
@@ -391,8 +385,14 @@ extern "C" int zero_grads_init(zero_grads** out, const zero_grad_tensor* tensors
     const int64_t most = std::min<int64_t>(std::min<int64_t>(want, 2 * d.sm_count()), kGradMaxGrid);
     const int64_t per = std::max<int64_t>(1, (at / kGradAlign + most - 1) / most) * kGradAlign;
     const int grid = (int)std::max<int64_t>(1, (at + per - 1) / per);
+    int32_t first[kGradMaxGrid] = {};
+    for (int64_t b = 0, t = 0; b < grid; ++b) {  // the last tensor that starts at or before the CTA's range
+        while (t + 1 < n && rows[(size_t)t + 1].start <= b * per) ++t;
+        first[b] = (int32_t)t;
+    }
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e = cudaMemcpyAsync(workspace, rows.data(), (size_t)n * sizeof(GradRow), cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(first_of(workspace, n), first, sizeof first, cudaMemcpyHostToDevice, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return record_cuda_error(e);
     zero_grads* p = new (std::nothrow) zero_grads{n, at, per, grid, (char*)workspace};
@@ -422,7 +422,8 @@ extern "C" int zero_grads_clip(zero_grads* p, double max_norm, float* norm, floa
     cudaStream_t s = (cudaStream_t)stream;
     GradArgs a;
     a.rows = (const GradRow*)p->workspace;
-    a.slots = (double*)(p->workspace + table_bytes(p->n));
+    a.first = first_of(p->workspace, p->n);
+    a.slots = slots_of(p->workspace, p->n);
     a.totals = a.slots + p->n + kGradMaxGrid;
     a.n = p->n;
     a.units = p->units;

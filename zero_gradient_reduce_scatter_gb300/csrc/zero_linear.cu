@@ -33,6 +33,7 @@ struct LinearArgs {
     int32_t* tiles;    // [0]: how many row tiles hold a target, [4...]: those tiles; nullptr: one tile, taken as it is
     int64_t rows, vocab, dim;
     int32_t tile_rows, row_tiles, tile_cols, col_tiles, group, grid;
+    int32_t load_rows;  // tokens of a CTA's tile that are loaded: all, or the multiple of 8 that holds the few there are
     Scale k;       // log2(e) / temperature
     float inv_t;   // 1 / temperature
 };
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kLinearThreads, 1)
                     if (!(ok = mbar_wait(empty + 8 * ring.at, ring.phase ^ 1, &gave_up))) break;
                     const uint32_t at = tiles + ring.at * S::kStage;
                     // both CTAs' bytes count on the first one's barrier
-                    if (rank == 0) mbar_expect(full + 8 * ring.at, CG * S::kA + a.tile_cols * 128);
+                    if (rank == 0) mbar_expect(full + 8 * ring.at, CG * a.load_rows * 128 + a.tile_cols * 128);
                     const uint32_t bar = CG == 2 ? smem_of(full + 8 * ring.at, 0) : full + 8 * ring.at;
                     tma_load<CG>(at, &map_a, bar, k * kDepth, (row * CG + (int)rank) * kRowsTile);
                     tma_load<CG>(at + S::kA, &map_b, bar, k * kDepth, col * a.tile_cols + (int)rank * (a.tile_cols / CG));
@@ -417,7 +418,7 @@ template <int TYPE, int CG, int BN, bool ENTROPY>
 int launch_product(const zero_linear* x, const LinearArgs& a, cudaStream_t s) {
     using S = LinearShape<CG, BN>;
     CUtensorMap ma, mb;
-    if (!encode(&ma, x->type, x->hidden, x->rows, x->dim, x->ld_hidden, kRowsTile) ||
+    if (!encode(&ma, x->type, x->hidden, x->rows, x->dim, x->ld_hidden, a.load_rows) ||
         !encode(&mb, x->type, x->weight, x->vocab, x->dim, x->ld_weight, a.tile_cols / CG))
         return record_cuda_error(cudaErrorInvalidValue);
     const cudaError_t e = cudaFuncSetAttribute(k_linear_mma<TYPE, CG, BN, ENTROPY>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
@@ -490,6 +491,8 @@ extern "C" int zero_linear_logp(const zero_linear* x, float* logp, float* lse, f
     a.dim = x->dim;
     a.tile_rows = l.tile_rows;
     a.row_tiles = l.row_tiles;
+    // the MMA's other rows then hold whatever the stage held: no row of a product sees another
+    a.load_rows = (int32_t)std::min<int64_t>(kRowsTile, (x->rows + 7) / 8 * 8);
     a.tile_cols = l.tile_cols;
     a.col_tiles = l.col_tiles;
     // row tiles of 32 MB of hidden states at most stay in L2 together

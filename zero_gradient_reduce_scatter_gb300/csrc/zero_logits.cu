@@ -22,6 +22,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kRowThreads = 256;
+constexpr int kRowCtas = 12;  // CTAs of an SM up to which short batches cut their rows
 constexpr int kUnroll = 4;  // 16-byte loads of a thread on their way at a time
 
 // Logits as the kernels take them.
@@ -308,7 +309,7 @@ struct PairArgs {
     float *pair_loss, *chosen, *rejected, *loss;
     uint32_t* done;  // CTAs that have ended; 0 before
     int64_t rows, pairs;
-    double beta, smoothing;
+    double beta, half_over_beta, smoothing;
     int32_t kind, average;
 };
 
@@ -316,38 +317,46 @@ struct PairArgs {
 __device__ __forceinline__ float softplus(float x) { return (x < 0.0f ? 0.0f : x) + log1pf(expf(-fabsf(x))); }
 
 __global__ void __launch_bounds__(kRowThreads) k_pairs(const PairArgs a) {
-    __shared__ Sum sm[kRowThreads / 32];
-    __shared__ unsigned long long count;
+    constexpr int kWarps = kRowThreads / 32, kHalf = kRowThreads / 2;  // half of the CTA per sequence
+    __shared__ Sum sm[kWarps];
+    __shared__ int counts[kWarps];
     __shared__ float g_side[2];
     let_next_kernel_start();
     wait_for_kernel_before();
+    const int warp = threadIdx.x >> 5, side = threadIdx.x / kHalf, id = threadIdx.x % kHalf;
     for (int64_t i = blockIdx.x; i < a.pairs; i += gridDim.x) {
-        int64_t lo[2], hi[2];
-        double d[2], n[2];
-        for (int k = 0; k < 2; ++k) {
-            lo[k] = clamp_offset(a.offsets[2 * i + k], 0, a.rows);
-            hi[k] = clamp_offset(a.offsets[2 * i + k + 1], lo[k], a.rows);
-            Sum sum;
-            unsigned targets = 0;
+        const int64_t lo = clamp_offset(a.offsets[2 * i + side], 0, a.rows), hi = clamp_offset(a.offsets[2 * i + side + 1], lo, a.rows);
+        Sum sum;
+        int targets = 0;
 #pragma unroll 4
-            for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kRowThreads) {
-                if (a.targets[t] < 0) continue;
-                sum.add(a.logp[t]);
-                if (a.ref) sum.add(-a.ref[t]);
-                ++targets;
-            }
-            if (threadIdx.x == 0) count = 0;
-            sum = cta_sum<kRowThreads>(sum, sm);
-            n[k] = 1.0;
-            if (a.average) {
-                atomicAdd(&count, (unsigned long long)targets);
-                __syncthreads();
-                n[k] = count ? (double)count : 1.0;
-                __syncthreads();
-            }
-            d[k] = sum.value() / n[k];
+        for (int64_t t = lo + id; t < hi; t += kHalf) {
+            const float lp = a.logp[t], ref = a.ref ? a.ref[t] : 0.0f;
+            if (a.targets[t] < 0) continue;
+            sum.add(lp);
+            if (a.ref) sum.add(-ref);
+            ++targets;
         }
+        sum = warp_sum(sum);
+        targets = __reduce_add_sync(~0u, targets);
+        if ((threadIdx.x & 31) == 0) {
+            sm[warp] = sum;
+            counts[warp] = targets;
+        }
+        __syncthreads();
         if (threadIdx.x == 0) {
+            double d[2];
+            float n[2];
+            for (int k = 0; k < 2; ++k) {
+                Sum all = sm[k * kWarps / 2];
+                int count = counts[k * kWarps / 2];
+                for (int w = 1; w < kWarps / 2; ++w) {
+                    all.add(sm[k * kWarps / 2 + w]);
+                    count += counts[k * kWarps / 2 + w];
+                }
+                n[k] = a.average && count ? (float)count : 1.0f;
+                d[k] = all.value();
+                if (a.average && count) d[k] /= (double)count;
+            }
             // the margin in fp64 (it may cancel), what follows from it in fp32
             const double m = d[0] - d[1];
             const float b = (float)a.beta, e = (float)a.smoothing, s = (float)(a.beta * m);
@@ -361,19 +370,18 @@ __global__ void __launch_bounds__(kRowThreads) k_pairs(const PairArgs a) {
                 loss = gap > 0.0f || gap != gap ? gap : 0.0f;
                 dm = gap > 0.0f ? -b : gap * 0.0f;
             } else {
-                const float gap = (float)(m - 0.5 / a.beta);
+                const float gap = (float)(m - a.half_over_beta);
                 loss = gap * gap;
                 dm = 2.0f * gap;
             }
             a.pair_loss[i] = loss;
             a.chosen[i] = (float)(a.beta * d[0]);
             a.rejected[i] = (float)(a.beta * d[1]);
-            g_side[0] = dm / ((float)n[0] * (float)a.pairs);
-            g_side[1] = -dm / ((float)n[1] * (float)a.pairs);
+            g_side[0] = dm / (n[0] * (float)a.pairs);
+            g_side[1] = -dm / (n[1] * (float)a.pairs);
         }
         __syncthreads();
-        for (int k = 0; k < 2; ++k)
-            for (int64_t t = lo[k] + threadIdx.x; t < hi[k]; t += kRowThreads) a.g[t] = g_side[k];
+        for (int64_t t = lo + id; t < hi; t += kHalf) a.g[t] = g_side[side];
         __syncthreads();
     }
     // the CTA that ends last takes the mean, in the pairs' order
@@ -812,10 +820,10 @@ int by_type(int32_t type, F f) {
 }
 
 // CTAs per row: 1 where the rows fill the GPU, else the row is cut (into at most 8, of 4 KB at
-// least), until every SM has two.
-int ctas_per_row(const zero_logits* x, int sms) {
+// least), while every SM has at most `per_sm`.
+int ctas_per_row(const zero_logits* x, int sms, int per_sm = kRowCtas) {
     int size = 1;
-    while (size < 8 && 2 * size * x->rows <= 2 * (int64_t)sms && x->vocab * type_size(x->type) / (2 * size) >= 4096) size *= 2;
+    while (size < 8 && 2 * size * x->rows <= per_sm * (int64_t)sms && x->vocab * type_size(x->type) / (2 * size) >= 4096) size *= 2;
     return size;
 }
 
@@ -855,7 +863,7 @@ int launch_token_grad(const zero_logits* x, const float* weight, const float* lo
 // CTAs per row of the one-pass kernel: enough that a slice fits, then as ctas_per_row. 0: the row
 // is too long for eight CTAs (over 450,000 16-bit logits), and takes two passes.
 int fused_size(const zero_logits* x, int sms) {
-    int size = ctas_per_row(x, sms);
+    int size = ctas_per_row(x, sms, 2);
     while (size <= 8 && fused_bytes(x, size) > kFusedBytes) size *= 2;
     return size <= 8 ? size : 0;
 }
@@ -953,7 +961,7 @@ extern "C" int zero_preference_loss(const zero_logits* x, const zero_preference*
     uint32_t* done = (uint32_t*)(g + round_up(x->rows, 4));
     const int sms = d.sm_count();
     const PairArgs a = {x->targets, p->offsets, p->logp, p->ref_logp, g, p->pair_loss, p->chosen_reward, p->rejected_reward, p->loss, done,
-                        x->rows, p->pairs, p->beta, p->kind == ZERO_PREF_SIGMOID ? p->label_smoothing : 0.0, p->kind, p->average};
+                        x->rows, p->pairs, p->beta, 0.5 / p->beta, p->kind == ZERO_PREF_SIGMOID ? p->label_smoothing : 0.0, p->kind, p->average};
     if (x->rows == 0) {  // no forward kernel that clears the counter
         const cudaError_t e = cudaMemsetAsync(done, 0, 4, s);
         if (e != cudaSuccess) return record_cuda_error(e);
