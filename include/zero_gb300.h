@@ -658,7 +658,7 @@ typedef struct {
     int64_t vocab;           /* 1 .. 2^30                                                     */
     int64_t stride;          /* elements from one row to the next, >= vocab                   */
     int32_t type;            /* ZERO_T_*                                                      */
-    double temperature;      /* > 0, finite                                                   */
+    double temperature;      /* 2^-64 .. 2^64                                                 */
 } zero_logits;
 
 /* logp[t] = z_t[y] - lse_t, lse_t = log sum_j exp(z_t[j]) and, where `entropy` is not NULL,
@@ -767,7 +767,7 @@ typedef struct {
     const int64_t* targets;  /* device [rows]                                                 */
     int64_t rows, vocab, dim, ld_hidden, ld_weight;
     int32_t type;
-    double temperature;
+    double temperature;      /* 2^-64 .. 2^64                                                 */
 } zero_linear;
 int64_t zero_linear_logp_workspace(int64_t rows, int64_t vocab);
 int zero_linear_logp(const zero_linear* x, float* logp, float* lse, float* entropy, void* workspace,

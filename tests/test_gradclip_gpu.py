@@ -115,6 +115,32 @@ def test_values_whose_squares_leave_fp32():
     assert abs(float(r.norm) - norm) <= NORM * norm and abs(float(r.norms[0]) - norms[0]) <= NORM * norms[0]
 
 
+def test_many_values_at_the_ends_of_fp32():
+    """Sums of squares that pass fp32 by their number: 2^20 values of 2^58, and of 2^-62. A norm that
+    is no fp32 number counts as not finite."""
+    for x in (2.0 ** 58, 2.0 ** -62, 2.0 ** 39):
+        grads = [torch.full((1 << 20,), x, device=DEV), torch.full((3,), x, device=DEV, dtype=B)]
+        r = zg.GradClip(grads).clip(math.inf)
+        want = x * math.sqrt((1 << 20) + 3)
+        assert abs(float(r.norm) - want) <= NORM * want and abs(float(r.norms[0]) - x * 1024) <= NORM * x * 1024
+    grads = [torch.full((4096,), 3e38, device=DEV)]
+    r = zg.GradClip(grads).clip(1.0)
+    assert float(r.norm) == math.inf and float(r.scale) == 1.0 and bool((grads[0] == 3e38).all())
+
+
+def test_more_values_than_32_bits_count():
+    n = 2 ** 31 + 12345
+    x = torch.zeros(n, dtype=B, device=DEV)
+    x[-3:] = 4.0
+    x[:2] = 2.0
+    r = zg.GradClip([x]).clip(1.0)
+    want = math.sqrt(3 * 16 + 2 * 4)
+    assert abs(float(r.norm) - want) <= NORM * want
+    s = float(r.scale)
+    assert bool((x[-3:] == torch.tensor(4.0 * s, device=DEV).to(B)).all()) and bool((x[:2] == torch.tensor(2.0 * s, device=DEV).to(B)).all())
+    assert int((x != 0).sum()) == 5
+
+
 @pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
 def test_a_norm_that_is_not_finite_leaves_the_values(value):
     grads = make([100, 3000], [F, B], 4)

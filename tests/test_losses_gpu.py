@@ -309,6 +309,20 @@ def test_preference_loss(lens, kind, smoothing, average):
     assert torch.equal(x, r.dlogits) and torch.equal(inplace.loss, r.loss)
 
 
+def test_infinite_margins():
+    """A target that the model gives no probability (its logit masked by -inf) in one side of a pair:
+    the margin is infinite, the loss its limit, and no gradient is NaN."""
+    x, _ = make_logits(8, 64, "bf16", 4)
+    y = torch.randint(0, 32, (8,), device=DEV, generator=gen(2))
+    off = make_offsets([2, 2, 2, 2])
+    x[3, y[3]] = -math.inf        # rejected of pair 0: margin +inf
+    x[4, y[4]] = -math.inf        # chosen of pair 1: margin -inf
+    for kind, limits in (("sigmoid", (0.0, math.inf)), ("hinge", (0.0, math.inf))):
+        r = zg.preference_loss(x, y, off, beta=0.1, kind=kind)
+        assert (float(r.pair_loss[0]), float(r.pair_loss[1])) == limits
+        assert bool(r.dlogits.isfinite().all()) and bool((r.dlogits[:4] == 0).all()) and bool((r.dlogits[4:] != 0).any())
+
+
 def policy_reference(x, y, adv, old, ref, off, lo, hi, dual, kl, kc, ec, reduce, temperature):
     logq, lp, lse, ent = reference(x, y, temperature)
     T = lp.shape[0]
@@ -522,7 +536,7 @@ def test_side_stream_and_graph():
 
 
 LINEAR = [  # T, V, D, ld_hidden, ld_weight
-    (1, 1, 8, 8, 8), (1, 50257, 768, 768, 768), (3, 127, 64, 64, 64), (5, 129, 72, 80, 88), (16, 1000, 8, 8, 16),
+    (1, 1, 8, 8, 8), (1, 9, 3, 8, 8), (1, 50257, 768, 768, 768), (3, 127, 64, 64, 64), (5, 129, 72, 80, 88), (16, 1000, 8, 8, 16),
     (130, 300, 200, 200, 200), (257, 2049, 136, 136, 136), (64, 4096, 1024, 1024, 1024), (300, 777, 1000, 1000, 1008),
 ]
 

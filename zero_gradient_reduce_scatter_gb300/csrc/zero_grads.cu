@@ -96,13 +96,14 @@ __device__ __forceinline__ void for_tensors(const GradArgs& a, int64_t u0, int64
 }
 
 // A sum of squares whose terms may leave fp32 either way. The squares of up to 32 values are added
-// in fp32; where that sum is no usable number (over 2^126, or under 2^-100: values of 2^-50 and
-// less, or none but zeros), each value goes into the sum of its own size, scaled into range.
+// in fp32; where that sum is no usable number (over 2^80, or under 2^-100: values of 2^-50 and
+// less, or none but zeros), each value goes into the sum of its own size, scaled so that 2^31 of
+// the largest still fit.
 struct Squares {
-    Sum mid, big, small;  // big: times 2^-132, small: times 2^150
+    Sum mid, big, small;  // big: times 2^-180, small: times 2^150
     __device__ __forceinline__ void one_by_one(float x) {
         const float y = fabsf(x);
-        if (y > 0x1p60f) big.add((x * 0x1p-66f) * (x * 0x1p-66f));
+        if (y > 0x1p40f) big.add((x * 0x1p-90f) * (x * 0x1p-90f));
         else if (y < 0x1p-60f) small.add((x * 0x1p75f) * (x * 0x1p75f));
         else mid.add(x * x);
     }
@@ -112,7 +113,7 @@ struct Squares {
 #pragma unroll
         for (int i = 0; i < N; ++i) s[i & 3] = fmaf(x[i], x[i], s[i & 3]);
         const float p = (s[0] + s[1]) + (s[2] + s[3]);
-        if (p >= 0x1p-100f && p < 0x1p126f) {
+        if (p >= 0x1p-100f && p < 0x1p80f) {
             mid.add(p);
         } else {
 #pragma unroll
@@ -124,7 +125,7 @@ struct Squares {
         if (__any_sync(~0u, big.hi != 0.0f)) big = warp_sum(big);
         if (__any_sync(~0u, small.hi != 0.0f)) small = warp_sum(small);
     }
-    __device__ __forceinline__ double value() const { return mid.value() + big.value() * 0x1p132 + small.value() * 0x1p-150; }
+    __device__ __forceinline__ double value() const { return mid.value() + big.value() * 0x1p180 + small.value() * 0x1p-150; }
 };
 
 // Eight elements of type T from p (aligned for 16-byte loads where ALIGNED). LAST: nothing reads
@@ -307,9 +308,10 @@ __global__ void __launch_bounds__(kGradThreads, 2) k_grads_scale(const GradArgs 
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
         if (lane == 0) {
             const double norm = sqrt(s);
-            factor = isfinite(norm) && norm > a.max_norm ? (float)(a.max_norm / norm) : 1.0f;
+            const float rounded = (float)norm;
+            factor = isfinite(rounded) && norm > a.max_norm ? (float)(a.max_norm / norm) : 1.0f;
             if (blockIdx.x == 0) {
-                *a.norm = (float)norm;
+                *a.norm = rounded;
                 *a.scale = factor;
             }
         }

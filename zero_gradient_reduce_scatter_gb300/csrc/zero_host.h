@@ -13,6 +13,8 @@
 namespace zg {
 
 constexpr int64_t type_size(int32_t type) { return type == ZERO_T_FP32 ? 4 : 2; }
+// A temperature whose scale and inverse are ordinary fp32 numbers (false for NaN).
+constexpr bool temperature_ok(double t) { return t >= 0x1p-64 && t <= 0x1p64; }
 constexpr bool type_ok(int32_t type) { return type >= ZERO_T_BF16 && type <= ZERO_T_FP32; }
 inline bool aligned(const void* p, int64_t to) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(to - 1)) == 0; }
 

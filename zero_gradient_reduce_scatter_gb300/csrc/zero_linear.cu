@@ -459,7 +459,7 @@ extern "C" int zero_linear_logp(const zero_linear* x, float* logp, float* lse, f
                                 int64_t workspace_bytes, void* stream) {
     if (!x || x->rows < 0 || x->rows > INT32_MAX || x->vocab < 1 || x->vocab > INT32_MAX || x->dim < 1 || x->dim > INT32_MAX ||
         x->ld_hidden < x->dim || x->ld_weight < x->dim || (x->type != ZERO_T_BF16 && x->type != ZERO_T_FP16) ||
-        !(x->temperature > 0.0) || !std::isfinite(x->temperature))
+        !temperature_ok(x->temperature))
         return ZERO_ERR_INVALID_ARG;
     if (x->ld_hidden > (INT64_C(1) << 36) || x->ld_weight > (INT64_C(1) << 36)) return ZERO_ERR_INVALID_ARG;
     if (x->ld_hidden % 8 || x->ld_weight % 8) return ZERO_ERR_MISALIGNED;

@@ -362,13 +362,14 @@ __global__ void __launch_bounds__(kRowThreads) k_pairs(const PairArgs a) {
             const float b = (float)a.beta, e = (float)a.smoothing, s = (float)(a.beta * m);
             float loss, dm;
             if (a.kind == ZERO_PREF_SIGMOID) {
-                loss = (1.0f - e) * softplus(-s) + e * softplus(s);
+                loss = (1.0f - e) * softplus(-s);
+                if (e != 0.0f) loss += e * softplus(s);  // not 0 times an infinite margin
                 // sigmoid(s) - (1 - e), each half formed without cancellation
                 dm = b * (e / (1.0f + expf(-s)) - (1.0f - e) / (1.0f + expf(s)));
             } else if (a.kind == ZERO_PREF_HINGE) {
                 const float gap = (float)(1.0 - a.beta * m);
                 loss = gap > 0.0f || gap != gap ? gap : 0.0f;
-                dm = gap > 0.0f ? -b : gap * 0.0f;
+                dm = gap > 0.0f ? -b : gap == gap ? 0.0f : gap;
             } else {
                 const float gap = (float)(m - a.half_over_beta);
                 loss = gap * gap;
@@ -787,7 +788,7 @@ __global__ void __launch_bounds__(kSetupThreads) k_policy_finish(const PolicyTok
 // ---------------------------------------------------------------------------------------
 int check_logits(const zero_logits* x) {
     if (!x || x->rows < 0 || x->rows > INT32_MAX || x->vocab < 1 || x->vocab > (1 << 30) || x->stride < x->vocab || !type_ok(x->type)) return ZERO_ERR_INVALID_ARG;
-    if (!(x->temperature > 0.0) || !std::isfinite(x->temperature)) return ZERO_ERR_INVALID_ARG;
+    if (!temperature_ok(x->temperature)) return ZERO_ERR_INVALID_ARG;
     if (x->rows > 0 && x->stride > INT64_MAX / 8 / x->rows) return ZERO_ERR_INVALID_ARG;
     return ZERO_OK;
 }

@@ -75,6 +75,8 @@ class GradClip:
         the values as they are (scale 1). max_norm may be infinite."""
         with _on(stream):
             norm, scale, norms = _floats(self.device), _floats(self.device), _floats(self.device, len(self.grads))
+        if stream is not None:
+            self.workspace.record_stream(stream)  # not handed out again before this call is done
         _check(_lib().zero_grads_clip(self._plan, max_norm, norm.data_ptr(), scale.data_ptr(), norms.data_ptr(),
                                       _handle(stream, self.device)), "zero_grads_clip")
         return Clipped(norm, scale, norms)

@@ -195,6 +195,8 @@ def linear_logp(hidden, weight, targets, *, temperature: float = 1.0, entropy: b
     if weight.dtype != hidden.dtype or weight.device != hidden.device or wdim != dim:
         raise ValueError("hidden and weight must have the same type, device and last dimension")
     dev = hidden.device
+    ld_h = ld_h if rows > 1 else -(-dim // 8) * 8  # of a single row: no stride is used
+    ld_w = ld_w if vocab > 1 else -(-dim // 8) * 8
     a = Linear(hidden.data_ptr(), weight.data_ptr(), _vector(targets, "targets", rows, torch.int64, dev), rows, vocab, dim,
                ld_h, ld_w, TYPES[hidden.dtype], temperature)
     size = _lib().zero_linear_logp_workspace(rows, vocab)
