@@ -141,7 +141,7 @@ __device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             const uint4* q = reinterpret_cast<const uint4*>(p) + i;
-            v[i] = LAST ? __ldcs(q) : __ldg(q);
+            v[i] = LAST ? __ldcs(q) : load_once(q);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kRowThreads)
         auto sums = [&](auto checked) {
             constexpr bool kChecked = decltype(checked)::value;
             Sums<T, ENTROPY, kChecked> run(a.k, x_y);
-            for_vectors<kRowThreads>(s.n, [&](int i) { return __ldg(s.v + i); }, [&](int, const uint4& q) { run.add(q); });
+            for_vectors<kRowThreads>(s.n, [&](int i) { return load_once(s.v + i); }, [&](int, const uint4& q) { run.add(q); });
             if (threadIdx.x < s.head) run.add_one(widen(x[threadIdx.x]));
             if (threadIdx.x < s.tail) run.add_one(widen(x[s.tail_at + threadIdx.x]));
             return group_join<ENTROPY, kChecked, kRowThreads / 32>(run.stat(), a.k, sm, 0);

@@ -126,6 +126,13 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return r;
 }
 
+// 16 bytes that this kernel reads once and does not write, past L1.
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
 // ---- 16 bytes of a row ---------------------------------------------------------------------
 template <class T>
 constexpr int kVec = 16 / (int)sizeof(T);
