@@ -15,6 +15,10 @@ Typical use (one GPU, M emulated ranks)::
     opt.step(grads, zg.Hyper(lr=1e-3, clip=True, max_grad_norm=1.0))
     params = opt.params()                       # bf16 [n], unpadded, tensor order
 
+Before the step, when a language model is trained on preferences or rewards (``losses.py``,
+``gradclip.py``): ``token_logp``, ``linear_logp``, ``preference_loss``, ``policy_loss`` and
+``GradClip``.
+
 The method follows "CS336 2026 Lecture 8" notes, Slides 8 and 17-26, and
 "并行训练优化、MoE扩展与系统瓶颈" 1.2.2 and 2.2.1-2.2.6: reduce-scatter the gradients,
 update each owner's shard with its own optimizer state, all-gather the parameters.

@@ -100,7 +100,13 @@ __device__ __forceinline__ RowStat sum_of(const float (&v)[N], Scale k) {
 // other, one row per thread, half of the columns per warpgroup. The tensor core drops the low
 // bits of each sum it forms, always towards zero, so an accumulator takes kChunk stages (512
 // products) only; the epilogue adds the accumulators of a tile in registers, rounded to nearest,
-// and then forms the softmax sums while the next tile's products run.
+// and then forms the softmax sums while the next tile's products run. In whole sums of 2048
+// products log-probabilities were off by 1.7e-6 of themselves, in these by 3.8e-7, as the fp32
+// product is; it costs 3%.
+// 8192 tokens x 50257 x 2048, a quarter masked: 672 us for 1.26e12 operations, 1.88 PFLOP/s, the
+// rate of the library's bf16 product (750 us under the power cap of a long run); bound by the tensor
+// cores, 83% busy beside the loads. 16 tokens x 50257 x 768: 22 us, half of the rate of reading the
+// matrix (77 MB), the rest a first load's latency, the last tile's sums and the join.
 constexpr int kChunk = 8;
 
 template <int CG, int BN>

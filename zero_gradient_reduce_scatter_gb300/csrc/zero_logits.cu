@@ -2,7 +2,10 @@
 // preference and policy losses on them, for sm_103a.
 //
 // All of it is bound by reading and writing [rows, vocab] logits; the arithmetic on them is a
-// softmax, so every row is read with its maximum and sums carried along (zero_softmax.cuh).
+// softmax, so every row is read with its sums carried along (zero_softmax.cuh). An element costs
+// about six instructions forward and six back, the most of them two to an instruction, which
+// leaves an SM's issue slots half free at HBM's rate. Figures below: one GB300, HBM copy peak
+// 6,673 GB/s, a vocabulary of 50257 (rows at any even address), calls replayed from a graph.
 
 #include <algorithm>
 #include <cmath>
@@ -107,7 +110,9 @@ __device__ __forceinline__ bool fast_row(const T* x, int64_t vocab, float x_y) {
 }
 
 // Forward, bound by reading the logits once: `size` CTAs per row (a cluster; several where there
-// are few rows), each thread kUnroll vectors at a time.
+// are few rows), each thread kUnroll vectors at a time. 4096 fp16 tokens, a quarter of them masked:
+// 53.9 us, 309 MB, 86% of the copy peak (128 or 512 threads and 2 or 6 vectors lie within 5%); one
+// token 4.4 us, over eight CTAs.
 template <class T, bool ENTROPY>
 __global__ void __launch_bounds__(kRowThreads)
     k_token_logp(const Rows<T> a, int size, float* logp, float* lse, float* entropy, float* cleared, uint32_t* counter) {
@@ -241,8 +246,9 @@ __device__ __forceinline__ void write_ends(const Slice<T>& s, const GradRow& r, 
     if (i < s.tail) out[s.tail_at + i] = narrow<T>(grad_term<H, CLAMP>(r, x_tail, c, s.tail_at + i == y));
 }
 
-// Backward, bound by reading and writing the logits once. Where the gradient's rows have another
-// alignment than the logits', elements are taken one at a time.
+// Backward, bound by reading the logits and writing their gradient: 2048 bf16 rows in 62.9 us, 412
+// MB, 98% of the copy peak. Where the gradient's rows have another alignment than the logits',
+// elements are taken one at a time.
 template <class T, bool H>
 __device__ __forceinline__ void write_grad(const Rows<T>& a, const GradRow& r, const T* x, T* out, int y, float x_y, int rank, int size) {
     const Slice<T> s(x, a.vocab, rank, size);
@@ -297,8 +303,12 @@ __device__ __forceinline__ int64_t clamp_offset(int64_t o, int64_t lo, int64_t h
 }
 
 // ---------------------------------------------------------------------------------------
-// Preference loss: one CTA per pair sums its two sequences and spreads the gradient over their
-// tokens. g holds 0 for the tokens of no pair (written before).
+// Preference loss, between the forward kernel and the gradient's: a CTA per pair sums its two
+// sequences and spreads the gradient over their tokens. g holds 0 for the tokens of no pair
+// (written before). The loss of a pair needs all of its rows, so the logits are read twice: 8192
+// tokens in 16 pairs, a quarter masked, take 326 us, 94% of the copy peak on their 2.06 GB. One
+// kernel that follows each pair's forward rows with its gradient rows, to read them from L2, took
+// 450 us and more: the L2 gave back 6%, handing out rows cost 20%.
 // ---------------------------------------------------------------------------------------
 struct PairArgs {
     const int64_t* targets;
@@ -549,7 +559,10 @@ __device__ __forceinline__ TokenLoss policy_token(const PolicyTokens& a, const T
 // gradient. So the logits cross HBM once each way, where a second pass over them would read them
 // again. Two CTAs per SM, each with one slice: a producer warp refills a part of it with the next
 // row as soon as the gradient of this one has been taken from it, so that copies run beside
-// everything else. Rows are handed out one by one (some carry no loss and cost half).
+// everything else. Rows are handed out one by one (some carry no loss and cost half). 8192 bf16
+// tokens, a quarter masked, with entropy bonus: 235 us the whole call, 1.44 GB, 92% of the copy
+// peak (two passes over the logits: 383 us). Seven warps compute: with ten, and four parts to a
+// slice, 252 us, since registers then spill; with fifteen 325.
 constexpr int kFusedWarps = 7, kFusedThreads = 32 * kFusedWarps;
 constexpr int kChunks = 2;
 constexpr int64_t kFusedBytes = 110 * 1024;  // of a slice: two fit an SM
