@@ -207,6 +207,12 @@ __device__ __forceinline__ void narrow2<float>(uint4& v, int i, float2 f) {
 // -inf. Both show in the result, and the row is then taken again, CHECKED: the base follows the
 // maximum (only once a value exceeds it by 2^40: comparing costs less than rescaling) and
 // differences are kept finite.
+// pow2 errs low below 0 and high above it, by 5e-8 and 3e-8 on average: over a base that is not the
+// maximum the errors of a row's terms would depend on where its mass lies. So without CHECKED the
+// terms are 2^(d_j - kDown), below 1 for all but rows whose target is 2^kDown times less likely
+// than another token, and the sums are taken back up in the end; the base's own term stays exact.
+constexpr float kDown = 20.0f;
+
 template <class T, bool ENTROPY, bool CHECKED>
 struct Sums {
     float m, limit;  // base, and the largest value that is taken over it
@@ -237,7 +243,8 @@ struct Sums {
         limit = top + 40.0f / k.c;
     }
     __device__ __forceinline__ void term(int i, uint64_t x) {
-        const uint64_t t = add2(x, base), d = ENTROPY ? mul2(t, c) : fma2(t, lo, mul2(t, c));
+        const uint64_t t = add2(x, base), p = CHECKED ? mul2(t, c) : fma2(t, c, pack2(-kDown, -kDown));
+        const uint64_t d = ENTROPY ? p : fma2(t, lo, p);
         const float2 df = unpack2(d);
         const uint64_t e = pack2(pow2(df.x), pow2(df.y));
         s[i] = add2(s[i], e);
@@ -253,13 +260,15 @@ struct Sums {
     }
     __device__ __forceinline__ void add_one(float x) {
         if (CHECKED && x > limit) raise(x);
-        const float d = scaled<ENTROPY>(x - base_of(m), k), e = pow2(d);
+        const float t = x - base_of(m), p = CHECKED ? t * k.c : fmaf(t, k.c, -kDown), d = ENTROPY ? p : fmaf(t, k.lo, p), e = pow2(d);
         s[0] = add2(s[0], pack2(e, 0.0f));
         if (ENTROPY) q[0] = fma2(pack2(e, 0.0f), pack2(CHECKED ? fmaxf(d, kFar) : d, 0.0f), q[0]);
     }
     __device__ __forceinline__ RowStat stat() const {
         const float2 a = unpack2(add2(s[0], s[1])), b = unpack2(add2(q[0], q[1]));
-        return {m, a.x + a.y, ENTROPY ? b.x + b.y : 0.0f};
+        const float up = CHECKED ? 1.0f : 0x1p20f, sum = a.x + a.y;
+        static_assert(kDown == 20.0f, "2^kDown");
+        return {m, sum * up, ENTROPY ? (CHECKED ? b.x + b.y : fmaf(kDown, sum, b.x + b.y) * up) : 0.0f};
     }
 };
 
@@ -309,10 +318,10 @@ struct RowResult {
     float logp, lse, entropy;
 };
 
-// pow2 errs low by this share on average (measured over 2^24 arguments), and so does a sum of many
-// terms, all but the base's own, which is 2^0 = 1 exactly. A log-probability's own rounding hides
-// it, a sequence's sum of them would not.
-constexpr float kPow2Low = 4.9e-8f;
+// pow2 errs low by this share on average (measured over 2^24 arguments below 0), and so does a sum
+// of many terms, all but the base's own, whose argument is an integer. A log-probability's own
+// rounding hides it, a sequence's sum of them would not.
+constexpr float kPow2Low = 5.0e-8f;
 
 // A row's results from its sums; x_y is the target's logit. ENTROPY says how the sums were formed.
 // log s and what is added to it is held in two fp32 numbers until the last sum: with s = 2^n f,
