@@ -117,8 +117,8 @@ template <class T, bool ENTROPY>
 __global__ void __launch_bounds__(kRowThreads)
     k_token_logp(const Rows<T> a, int size, float* logp, float* lse, float* entropy, float* cleared, uint32_t* counter) {
     __shared__ RowStat sm[kRowThreads / 32], mine;
-    let_next_kernel_start();
     wait_for_kernel_before();
+    let_next_kernel_start();
     const int64_t t = blockIdx.x / size;
     const int rank = (int)(blockIdx.x % size);
     const int64_t y = live_target(a, t);
@@ -272,8 +272,8 @@ template <class T, bool H>
 __global__ void __launch_bounds__(kRowThreads)
     k_token_grad(const Rows<T> a, int size, const float* logp, const float* lse, const float* entropy, const float* dlogp,
                  const float* dentropy, T* dx, int64_t dstride) {
-    let_next_kernel_start();
     wait_for_kernel_before();
+    let_next_kernel_start();
     // From the last row: what a forward pass read last may still be in L2.
     const int64_t t = a.rows - 1 - blockIdx.x / size;
     const int rank = (int)(blockIdx.x % size);

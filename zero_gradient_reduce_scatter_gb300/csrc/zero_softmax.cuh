@@ -17,7 +17,9 @@
 
 namespace zg {
 
-// For kernels launched with launch_linked.
+// For kernels launched with launch_linked. A call's last kernel lets the next one start only after
+// its own wait, or not at all: what follows the call may be a kernel that does not wait itself
+// (ZERO_OVERLAP_BUCKETS), and must not start before all that preceded the call is complete.
 __device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
