@@ -77,19 +77,27 @@ __device__ __forceinline__ void tile_of(const LinearArgs& a, int32_t live, int64
     *row = a.tiles ? a.tiles[4 + first + (int32_t)(in % size)] : 0;
 }
 
-// N logits of one row: their sums, in four chains.
+// N logits of one row: their sums, in four chains of two numbers to an instruction.
 template <bool ENTROPY, int N>
 __device__ __forceinline__ RowStat sum_of(const float (&v)[N], Scale k) {
-    float m = v[0];
+    float top[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-    for (int j = 1; j < N; ++j) m = fmaxf(m, v[j]);
-    const float base = base_of(m);
-    RowStat part[4];
+    for (int j = 4; j < N; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
+    const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    const uint64_t base = pack2(-base_of(m), -base_of(m)), c = pack2(k.c, k.c), lo = pack2(k.lo, k.lo);
+    uint64_t s[4], q[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) part[i] = {m, 0.0f, 0.0f};
+    for (int i = 0; i < 4; ++i) s[i] = q[i] = pack2(0.0f, 0.0f);
 #pragma unroll
-    for (int j = 0; j < N; ++j) add_term<ENTROPY>(part[j & 3], v[j], k, base);
-    return {m, (part[0].s + part[1].s) + (part[2].s + part[3].s), (part[0].q + part[1].q) + (part[2].q + part[3].q)};
+    for (int j = 0; j < N / 2; ++j) {
+        const uint64_t t = add2(pack2(v[2 * j], v[2 * j + 1]), base), p = mul2(t, c);
+        const float2 d = unpack2(ENTROPY ? p : fma2(t, lo, p));
+        const uint64_t e = pack2(pow2(d.x), pow2(d.y));
+        s[j & 3] = add2(s[j & 3], e);
+        if (ENTROPY) q[j & 3] = fma2(e, pack2(fmaxf(d.x, kFar), fmaxf(d.y, kFar)), q[j & 3]);
+    }
+    const float2 a = unpack2(add2(add2(s[0], s[1]), add2(s[2], s[3]))), b = unpack2(add2(add2(q[0], q[1]), add2(q[2], q[3])));
+    return {m, a.x + a.y, b.x + b.y};
 }
 
 // One CTA per SM walks over tiles of 128 tokens by tile_cols (at most BN) columns of the

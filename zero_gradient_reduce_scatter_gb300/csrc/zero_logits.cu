@@ -88,17 +88,18 @@ __device__ __forceinline__ void for_vectors(int n, L load, U use) {
     }
 }
 
-// The sums of all CTAs of a cluster, in the order of their ranks; valid everywhere. `mine` is
-// shared memory of this CTA, which stays as it is until the cluster's next barrier.
+// The sums of all CTAs of a cluster (at most 8), joined in a fixed order; valid everywhere. `mine` is
+// shared memory of this CTA, which stays as it is until the cluster's next barrier. A lane reads a
+// CTA's sums, so that their latencies are one.
 template <bool ENTROPY>
 __device__ __forceinline__ RowStat cluster_join(RowStat a, int size, Scale k, RowStat* mine) {
     if (size == 1) return a;
     cg::cluster_group cl = cg::this_cluster();
     if (threadIdx.x == 0) *mine = a;
     cl.sync();
-    a = *cl.map_shared_rank(mine, 0);
-    for (int r = 1; r < size; ++r) a = join<ENTROPY>(a, *cl.map_shared_rank(mine, r), k);
-    return a;
+    const int lane = threadIdx.x & 7;
+    a = lane < size ? *cl.map_shared_rank(mine, lane) : empty_stat();
+    return warp_join<ENTROPY, true, 8>(a, k);
 }
 
 // Whether a row is taken without CHECKED (Sums) first: its target's logit is a base, and a
