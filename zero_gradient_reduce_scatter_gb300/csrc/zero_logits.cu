@@ -565,17 +565,29 @@ __device__ __forceinline__ TokenLoss policy_token(const PolicyTokens& a, const T
 // peak (two passes over the logits: 383 us). Seven warps compute: with ten, and four parts to a
 // slice, 252 us, since registers then spill; with fifteen 325.
 constexpr int kFusedWarps = 7, kFusedThreads = 32 * kFusedWarps;
-constexpr int kChunks = 2;
-constexpr int64_t kFusedBytes = 110 * 1024;  // of a slice: two fit an SM
+constexpr int kChunks = 2, kSlots = 8;  // parts of a slice; most parts that shared memory holds
+constexpr int64_t kFusedBytes = 110 * 1024;  // of a CTA's parts: two CTAs fit an SM
 
 template <int THREADS>
 __device__ __forceinline__ void consumers_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
+// Place and phase in a ring of a number of slots.
+struct Slot {
+    int at = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int slots) {
+        if (++at == slots) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+};
+
 template <class T, bool H>
 __global__ void __launch_bounds__(kFusedThreads + 32, 2)
-    k_policy_rows(const Rows<T> a, const PolicyTokens p, int size, int per, float* logp, float* entropy, T* dx, int64_t dstride) {
+    k_policy_rows(const Rows<T> a, const PolicyTokens p, int size, int per, int slots, float* logp, float* entropy, T* dx, int64_t dstride) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ RowStat sm[kFusedWarps], mine[2];
     __shared__ GradRow shared_row;
@@ -583,14 +595,14 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
     __shared__ int64_t row_at[2], row_y[2];
     __shared__ float row_x[2];  // the target's logit
     __shared__ bool row_fast[2];
-    __shared__ uint64_t bars[2 * kChunks + 4];
+    __shared__ uint64_t bars[2 * kSlots + 4];
     __shared__ int gave_up;
-    const uint32_t full = smem_addr(bars), empty = full + 8 * kChunks, row_full = empty + 8 * kChunks, row_empty = row_full + 16;
+    const uint32_t full = smem_addr(bars), empty = full + 8 * kSlots, row_full = empty + 8 * kSlots, row_empty = row_full + 16;
     const int rank = (int)(blockIdx.x % size), lane = threadIdx.x & 31;
     const int64_t first = blockIdx.x / size, clusters = gridDim.x / size;
     if (threadIdx.x == 0) {
         gave_up = 0;
-        for (int i = 0; i < kChunks; ++i) {
+        for (int i = 0; i < slots; ++i) {
             mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, kFusedWarps);
         }
@@ -606,7 +618,7 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
     // producer, so logits and targets may be read at once, and the rest after it.
     let_next_kernel_start();
     if (threadIdx.x >= kFusedThreads) {
-        uint32_t filled = 0;  // rows brought in
+        Slot slot;
         bool ok = true;
         for (int64_t n = 0;; ++n) {
             int64_t t = first + n * clusters;
@@ -634,18 +646,19 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
             if (lane == 0) {
                 const Slice<T> s(x, a.vocab, rank, size);
                 for (int i = 0; i < kChunks; ++i) {
-                    ok = ok && mbar_wait(empty + 8 * i, (filled & 1) ^ 1, &gave_up);
+                    ok = ok && mbar_wait(empty + 8 * slot.at, slot.phase ^ 1, &gave_up);
                     const int at = min(s.n, i * per), bytes = 16 * (min(s.n, at + per) - at);
-                    mbar_expect(full + 8 * i, ok ? bytes : 0);
-                    if (ok && bytes) bulk_load(smem_addr(smem) + 16 * at, s.v + at, bytes, full + 8 * i);
+                    mbar_expect(full + 8 * slot.at, ok ? bytes : 0);
+                    if (ok && bytes) bulk_load(smem_addr(smem) + 16 * slot.at * per, s.v + at, bytes, full + 8 * slot.at);
+                    slot.next(slots);
                 }
             }
-            ++filled;
             if (size > 1) cg::this_cluster().sync();  // the consumers' cluster_join
         }
     } else {
         uint32_t taken = 0;
-        const uint4* v = reinterpret_cast<const uint4*>(smem);
+        Slot begin;  // of the row at hand
+        const uint4* parts = reinterpret_cast<const uint4*>(smem);
         for (int64_t n = 0;; ++n) {
             const bool got = mbar_wait(row_full + 8 * (n & 1), (uint32_t)(n >> 1) & 1, &gave_up);
             const int64_t t = got ? row_at[n & 1] : -1, y = row_y[n & 1];
@@ -674,10 +687,12 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
             auto sums = [&](auto checked) {
                 constexpr bool kChecked = decltype(checked)::value;
                 Sums<T, H, kChecked> run(a.k, x_y);
-                for (int i = 0; i < kChunks; ++i) {
-                    ok = ok && mbar_wait(full + 8 * i, taken & 1, &gave_up);
+                Slot slot = begin;
+                for (int i = 0; i < kChunks; ++i, slot.next(slots)) {
+                    ok = ok && mbar_wait(full + 8 * slot.at, slot.phase, &gave_up);
                     const int at = min(s.n, i * per);
-                    for_vectors<kFusedThreads>(min(s.n, at + per) - at, [&](int j) { return v[at + j]; }, [&](int, const uint4& q) { run.add(q); });
+                    const uint4* v = parts + slot.at * per;
+                    for_vectors<kFusedThreads>(min(s.n, at + per) - at, [&](int j) { return v[j]; }, [&](int, const uint4& q) { run.add(q); });
                 }
                 if (threadIdx.x < s.head) run.add_one(x_head);
                 if (threadIdx.x < s.tail) run.add_one(x_tail);
@@ -722,23 +737,24 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
                 const GradVector<T, H, kClamp> grad(r, c);
                 if (zero) zero_row<T, kFusedThreads>(out, a.vocab, rank, size);
                 else write_ends<T, H, kClamp>(s, r, x_head, x_tail, out, c, place);
-                for (int i = 0; i < kChunks; ++i) {
+                for (int i = 0; i < kChunks; ++i, begin.next(slots)) {
                     const int at = min(s.n, i * per), m = min(s.n, at + per) - at;
+                    const uint4* v = parts + begin.at * per;
                     const int from = s.first + at * kVec<T>;  // the chunk's first element
                     if (!zero && fast) {
                         uint4* to = reinterpret_cast<uint4*>(out + from);
-                        for_vectors<kFusedThreads>(m, [&](int j) { return v[at + j]; }, [&](int j, const uint4& q) { __stcs(to + j, grad(q)); });
+                        for_vectors<kFusedThreads>(m, [&](int j) { return v[j]; }, [&](int j, const uint4& q) { __stcs(to + j, grad(q)); });
                         // the thread that wrote the target's vector sets the target right
                         const int dy = place - from;
                         if (dy >= 0 && dy < m * kVec<T> && dy / kVec<T> % kFusedThreads == threadIdx.x)
                             out[place] = narrow<T>(grad_term<H, kClamp>(r, x_y, c, true));
                     } else if (!zero) {
-                        const T* e = reinterpret_cast<const T*>(v + at);
+                        const T* e = reinterpret_cast<const T*>(v);
                         for (int j = threadIdx.x; j < m * kVec<T>; j += kFusedThreads)
                             out[from + j] = narrow<T>(grad_term<H, kClamp>(r, widen(e[j]), c, from + j == place));
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(empty + 8 * i);  // this warp has done with the chunk
+                    if (lane == 0) mbar_arrive(empty + 8 * begin.at);  // this warp has done with the part
                 }
             };
             if (H && !good) write(std::true_type());  // this slice may hold -inf
@@ -848,6 +864,10 @@ int64_t fused_part(const zero_logits* x, int size) {
     return ((vecs + size - 1) / size + kChunks - 1) / kChunks;
 }
 int64_t fused_bytes(const zero_logits* x, int size) { return 16 * kChunks * fused_part(x, size); }
+// Parts that fit: with more than a row's, the next row's copies begin before this one is done.
+int fused_slots(const zero_logits* x, int size) {
+    return (int)std::max<int64_t>(kChunks, std::min<int64_t>(kSlots, kFusedBytes / std::max<int64_t>(16, 16 * fused_part(x, size))));
+}
 
 int launch_token_logp(const zero_logits* x, const float* weight, float* logp, float* lse, float* entropy, float* cleared,
                       uint32_t* counter, int sms, cudaStream_t s) {
@@ -891,8 +911,8 @@ int launch_policy_rows(const zero_logits* x, const PolicyTokens& p, const zero_p
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFusedBytes);
         if (e != cudaSuccess) return record_cuda_error(e);
         const int64_t clusters = std::min<int64_t>(x->rows, 2 * sms / size);
-        return launch_linked(kernel, (unsigned)(clusters * size), kFusedThreads + 32, (size_t)fused_bytes(x, size), size, s,
-                             rows_of<T>(x, nullptr), p, size, (int)fused_part(x, size), q->logp, q->entropy, (T*)q->dlogits, q->dstride);
+        return launch_linked(kernel, (unsigned)(clusters * size), kFusedThreads + 32, (size_t)(16 * fused_slots(x, size) * fused_part(x, size)), size, s,
+                             rows_of<T>(x, nullptr), p, size, (int)fused_part(x, size), fused_slots(x, size), q->logp, q->entropy, (T*)q->dlogits, q->dstride);
     });
     if (rc) return rc;
     return launch_linked(k_policy_finish, 1, kSetupThreads, 0, 1, s, p);
