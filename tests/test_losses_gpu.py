@@ -6,8 +6,9 @@ of a number of at most R = max |z - max z| that matters (terms below 2^-40 of th
 lost in the sum anyway, so R is cut at 28) plus log V, the exponential 2^-22, and a sum of n/256
 terms in a row at most n/256 roundings. So log p and the entropy are within
     E = 2^-22 (8 + R) + 2^-24 n / 256,
-times 1 + |value| for the final roundings; a gradient entry p (|g| + |h| (|log p| + H)) / temperature
-is within 2 E of itself and is then rounded once to its type (half its spacing: 2^-8, 2^-11, 2^-24), with half the
+times 1 + |value| for the final roundings. A gradient entry p (g + h (log p + H)) / temperature takes
+the relative error of p, E, and in the bracket the absolute ones of log p and H, E (1 + |log p|) and
+E (1 + H): in all 2 E p (|g| + |h| (1 + |log p| + H)) / temperature. It is then rounded once to its type (half its spacing: 2^-8, 2^-11, 2^-24), with half the
 smallest fp16 number, 2^-25, where that type underflows. Losses are sums of such terms: their
 bound is the sum of the terms' bounds.
 """
@@ -93,7 +94,7 @@ def check_grad(got, want, logq, y, g, h, ent, E, dtype, temperature):
     q = torch.exp(logq)
     size = g.abs()[:, None].expand_as(q)
     if h is not None:
-        size = size + h.abs()[:, None] * (torch.where(q > 0, logq.abs(), torch.zeros_like(q)) + ent[:, None])
+        size = size + h.abs()[:, None] * (1 + torch.where(q > 0, logq.abs(), torch.zeros_like(q)) + ent[:, None])
     # the target's entry g (1 - p) cancels: its error is that of p and of g
     hot = torch.zeros_like(q).scatter_(1, y.clamp(min=0)[:, None], 1.0)
     tol = (2 * E[:, None] * q * size + hot * g.abs()[:, None] * 2.0 ** -22) / temperature + UNIT[dtype] * want.abs() + 2.0 ** -100
@@ -112,6 +113,7 @@ def check(got, want, E, what):
 SHAPES = [  # T, V, stride, offset
     (1, 1, None, 0), (1, 50257, None, 0), (3, 7, None, 1), (5, 8, None, 0), (4, 9, 17, 3), (17, 1000, 1008, 0),
     (33, 4099, None, 5), (2, 8192, None, 8), (64, 257, 264, 0), (700, 130, 131, 2), (3, 131072, None, 1),
+    (1300, 515, 518, 1), (1217, 3, None, 0), (1251, 4099, None, 0),  # a warp per row
 ]
 
 
@@ -245,7 +247,7 @@ def make_offsets(lens):
     return torch.tensor(off, dtype=torch.int64, device=DEV)
 
 
-PAIRS = [[1, 1], [5, 0], [0, 0], [3, 9, 1, 2], [40, 17, 0, 5, 64, 64, 2, 1], [300, 211], [7, 1, 0, 0, 130, 95, 211, 60, 0, 0, 1, 88]]
+PAIRS = [[700, 0, 311, 260], [1, 1], [5, 0], [0, 0], [3, 9, 1, 2], [40, 17, 0, 5, 64, 64, 2, 1], [300, 211], [7, 1, 0, 0, 130, 95, 211, 60, 0, 0, 1, 88]]
 
 
 @pytest.mark.parametrize("lens", PAIRS)
@@ -276,8 +278,10 @@ def test_preference_loss(lens, kind, smoothing, average):
         m = d[0] - d[1]
         s = beta * m
         if kind == "sigmoid":
-            loss = (1 - smoothing) * math.log1p(math.exp(-s)) + smoothing * math.log1p(math.exp(s))
-            dm = beta * (1 / (1 + math.exp(-s)) - (1 - smoothing))
+            tail = math.log1p(math.exp(-abs(s)))       # log(1 + e^x) = max(x, 0) + this, at any margin
+            loss = (1 - smoothing) * (max(-s, 0) + tail) + smoothing * (max(s, 0) + tail)
+            sig = 1 / (1 + math.exp(-s)) if s > 0 else math.exp(s) / (1 + math.exp(s))
+            dm = beta * (sig - (1 - smoothing))
             slope, curve = beta, beta * beta / 4
         elif kind == "hinge":
             loss, dm, slope, curve = max(0.0, 1 - s), -beta if s < 1 else 0.0, beta, 0.0
@@ -372,6 +376,8 @@ POLICY = [  # lens, reduce, advantages per, old, ref, kl, kl_coef, entropy_coef,
     ([64, 64, 64], "sum", "token", False, True, "k3", 0.02, 0.0, 0.0, 1.3, 513, "fp32"),
     (None, "token", "token", True, True, "k3", 0.1, 0.02, 0.0, 1.0, 50257, "bf16"),
     (None, "sum", "token", False, False, "k3", 0.0, 0.0, 0.0, 1.0, 130, "fp16"),
+    ([700, 0, 640], "sequence", "sequence", True, True, "k3", 0.1, 0.02, 3.0, 0.9, 517, "bf16"),  # a warp per row
+    ([700, 640], "token", "token", True, True, "k2", 0.1, 0.0, 0.0, 1.0, 1001, "fp32"),
     # rows cut over a cluster, and rows too long for one
     ([3, 2], "token", "token", True, True, "k3", 0.1, 0.02, 0.0, 1.0, 131073, "bf16"),
     ([3, 2], "sequence", "sequence", True, True, "k3", 0.1, 0.02, 3.0, 1.0, 300001, "fp32"),

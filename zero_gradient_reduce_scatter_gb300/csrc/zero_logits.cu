@@ -66,10 +66,14 @@ struct Slice {
     }
 };
 
-// f(i) for this thread's vectors of n, kUnroll at a time: `load` first for all of them, then `use`.
+// A thread's place among the THREADS that share a row: those of a CTA, or of a warp.
+template <int THREADS>
+__device__ __forceinline__ int place_in_group() { return THREADS == 32 ? threadIdx.x & 31 : threadIdx.x; }
+
+// This thread's vectors of n, kUnroll at a time: `load` first for all of them, then `use`.
 template <int THREADS, class L, class U>
 __device__ __forceinline__ void for_vectors(int n, L load, U use) {
-    int i = threadIdx.x;
+    int i = place_in_group<THREADS>();
     for (; i + (kUnroll - 1) * THREADS < n; i += kUnroll * THREADS) {
         uint4 q[kUnroll];
 #pragma unroll
@@ -110,54 +114,72 @@ __device__ __forceinline__ bool fast_row(const T* x, int64_t vocab, float x_y) {
     return fabsf(x_y) < INFINITY && !(ENTROPY && (widen(x[0]) == -INFINITY || widen(x[vocab - 1]) == -INFINITY));
 }
 
+// The sums of a row, or of a CTA's share of it, by the THREADS that take it: a CTA's (joined through
+// sm, THREADS / 32 entries), or one warp's, which takes the whole row and needs no sm.
+template <int THREADS, bool ENTROPY, class T>
+__device__ __forceinline__ RowStat row_sums(const T* x, int64_t vocab, float x_y, Scale k, int rank, int size, RowStat* sm) {
+    const Slice<T> s(x, vocab, rank, size);
+    const int id = place_in_group<THREADS>();
+    auto sums = [&](auto checked) {
+        constexpr bool kChecked = decltype(checked)::value;
+        Sums<T, ENTROPY, kChecked> run(k, x_y);
+        for_vectors<THREADS>(s.n, [&](int i) { return THREADS == 32 ? __ldg(s.v + i) : load_once(s.v + i); },
+                             [&](int, const uint4& q) { run.add(q); });
+        if (id < s.head) run.add_one(widen(x[id]));
+        if (id < s.tail) run.add_one(widen(x[s.tail_at + id]));
+        if constexpr (THREADS == 32) return warp_join<ENTROPY, kChecked>(run.stat(), k);
+        else return group_join<ENTROPY, kChecked, THREADS / 32>(run.stat(), k, sm, 0);
+    };
+    if (fast_row<ENTROPY>(x, vocab, x_y)) {
+        const RowStat st = sums(std::false_type());
+        if (good_sums<ENTROPY>(st)) return st;
+        if (THREADS > 32) __syncthreads();
+    }
+    return sums(std::true_type());
+}
+
+// The row and the part of it that this thread works on: `size` CTAs per row, or (THREADS = 32) a
+// warp each.
+template <int THREADS>
+__device__ __forceinline__ int64_t row_of(int size) {
+    return THREADS == 32 ? (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5) : blockIdx.x / size;
+}
+
 // Forward, bound by reading the logits once: `size` CTAs per row (a cluster; several where there
 // are few rows), each thread kUnroll vectors at a time. 4096 fp16 tokens, a quarter of them masked:
 // 53.9 us, 309 MB, 86% of the copy peak (128 or 512 threads and 2 or 6 vectors lie within 5%); one
-// token 4.4 us, over eight CTAs.
-template <class T, bool ENTROPY>
-__global__ void __launch_bounds__(kRowThreads)
+// token 4.4 us, over eight CTAs. Rows of up to kShortRow bytes go to a warp each: a CTA's joining
+// would take longer than their reading.
+template <class T, bool ENTROPY, int THREADS>
+__global__ void __launch_bounds__(kRowThreads, 5)
     k_token_logp(const Rows<T> a, int size, float* logp, float* lse, float* entropy, float* cleared, uint32_t* counter) {
     __shared__ RowStat sm[kRowThreads / 32], mine;
     wait_for_kernel_before();
     let_next_kernel_start();
-    const int64_t t = blockIdx.x / size;
-    const int rank = (int)(blockIdx.x % size);
+    const int64_t t = row_of<THREADS>(size);
+    if (THREADS == 32 && t >= a.rows) return;
+    const int rank = THREADS == 32 ? 0 : (int)(blockIdx.x % size);
     const int64_t y = live_target(a, t);
     RowResult r = {0.0f, 0.0f, 0.0f};
+    const bool first = place_in_group<THREADS>() == 0 && rank == 0;
     if (y >= 0) {
         const T* x = a.x + t * a.stride;
         const float x_y = y < a.vocab ? widen(x[y]) : NAN;
-        const Slice<T> s(x, a.vocab, rank, size);
-        auto sums = [&](auto checked) {
-            constexpr bool kChecked = decltype(checked)::value;
-            Sums<T, ENTROPY, kChecked> run(a.k, x_y);
-            for_vectors<kRowThreads>(s.n, [&](int i) { return load_once(s.v + i); }, [&](int, const uint4& q) { run.add(q); });
-            if (threadIdx.x < s.head) run.add_one(widen(x[threadIdx.x]));
-            if (threadIdx.x < s.tail) run.add_one(widen(x[s.tail_at + threadIdx.x]));
-            return group_join<ENTROPY, kChecked, kRowThreads / 32>(run.stat(), a.k, sm, 0);
-        };
-        RowStat st;
-        bool good = false;
-        if (fast_row<ENTROPY>(x, a.vocab, x_y)) {
-            st = sums(std::false_type());
-            good = good_sums<ENTROPY>(st);
-            if (!good) __syncthreads();
-        }
-        if (!good) st = sums(std::true_type());
-        st = cluster_join<ENTROPY>(st, size, a.k, &mine);
-        if (threadIdx.x == 0 && rank == 0) {
+        RowStat st = row_sums<THREADS, ENTROPY>(x, a.vocab, x_y, a.k, rank, size, sm);
+        if (THREADS != 32) st = cluster_join<ENTROPY>(st, size, a.k, &mine);
+        if (first) {
             r = finish_row<ENTROPY>(st, x_y, a.k, (float)a.inv_t);
             if (y >= a.vocab) r.logp = NAN;
         }
     }
-    if (threadIdx.x == 0 && rank == 0) {
+    if (first) {
         logp[t] = r.logp;
         lse[t] = r.lse;
         if (ENTROPY) entropy[t] = r.entropy;
         if (cleared) cleared[t] = 0.0f;
         if (counter && t == 0) *counter = 0;
     }
-    if (size > 1 && y >= 0) cg::this_cluster().sync();  // no CTA leaves while another reads its sums
+    if (THREADS != 32 && size > 1 && y >= 0) cg::this_cluster().sync();  // no CTA leaves while another reads its sums
 }
 
 // dx_j = g [j = y] - 2^d_j (ka + kb d_j) with d_j = (x_j - base) c - off, so that 2^d_j is p_j or
@@ -228,10 +250,11 @@ __device__ __forceinline__ int place_of(int64_t y, int64_t vocab) { return y < v
 template <class T, int THREADS>
 __device__ __forceinline__ void zero_row(T* out, int64_t vocab, int rank, int size) {
     const Slice<T> s(out, vocab, rank, size);
+    const int id = place_in_group<THREADS>();
     uint4* v = const_cast<uint4*>(s.v);
-    for (int i = threadIdx.x; i < s.n; i += THREADS) __stcs(v + i, make_uint4(0, 0, 0, 0));
-    if (threadIdx.x < s.head) out[threadIdx.x] = narrow<T>(0.0f);
-    if (threadIdx.x < s.tail) out[s.tail_at + threadIdx.x] = narrow<T>(0.0f);
+    for (int i = id; i < s.n; i += THREADS) __stcs(v + i, make_uint4(0, 0, 0, 0));
+    if (id < s.head) out[id] = narrow<T>(0.0f);
+    if (id < s.tail) out[s.tail_at + id] = narrow<T>(0.0f);
 }
 
 template <class T>
@@ -241,8 +264,7 @@ __device__ __forceinline__ bool same_alignment(const T* a, const T* b) {
 
 // The elements of a row that no vector holds.
 template <class T, bool H, bool CLAMP = H>
-__device__ __forceinline__ void write_ends(const Slice<T>& s, const GradRow& r, float x_head, float x_tail, T* out, float c, int y) {
-    const int i = threadIdx.x;
+__device__ __forceinline__ void write_ends(const Slice<T>& s, const GradRow& r, int i, float x_head, float x_tail, T* out, float c, int y) {
     if (i < s.head) out[i] = narrow<T>(grad_term<H, CLAMP>(r, x_head, c, i == y));
     if (i < s.tail) out[s.tail_at + i] = narrow<T>(grad_term<H, CLAMP>(r, x_tail, c, s.tail_at + i == y));
 }
@@ -250,50 +272,52 @@ __device__ __forceinline__ void write_ends(const Slice<T>& s, const GradRow& r, 
 // Backward, bound by reading the logits and writing their gradient: 2048 bf16 rows in 62.9 us, 412
 // MB, 98% of the copy peak. Where the gradient's rows have another alignment than the logits',
 // elements are taken one at a time.
-template <class T, bool H>
-__device__ __forceinline__ void write_grad(const Rows<T>& a, const GradRow& r, const T* x, T* out, int y, float x_y, int rank, int size) {
-    const Slice<T> s(x, a.vocab, rank, size);
-    const float x_head = threadIdx.x < s.head ? widen(x[threadIdx.x]) : 0.0f;
-    const float x_tail = threadIdx.x < s.tail ? widen(x[s.tail_at + threadIdx.x]) : 0.0f;
+template <int THREADS, bool H, class T>
+__device__ __forceinline__ void write_grad(float c, const GradRow& r, const T* x, T* out, int64_t vocab, int y, float x_y, int rank, int size) {
+    const Slice<T> s(x, vocab, rank, size);
+    const int id = place_in_group<THREADS>();
+    const float x_head = id < s.head ? widen(x[id]) : 0.0f;
+    const float x_tail = id < s.tail ? widen(x[s.tail_at + id]) : 0.0f;
     if (same_alignment(x, out)) {
-        const GradVector<T, H> grad(r, a.c);
+        const GradVector<T, H> grad(r, c);
         uint4* to = reinterpret_cast<uint4*>(out + s.first);
-        for_vectors<kRowThreads>(s.n, [&](int i) { return __ldcs(s.v + i); }, [&](int i, const uint4& q) { __stcs(to + i, grad(q)); });
+        for_vectors<THREADS>(s.n, [&](int i) { return __ldcs(s.v + i); }, [&](int i, const uint4& q) { __stcs(to + i, grad(q)); });
         // the thread that wrote the target's vector sets the target right
         const int at = y - s.first;
-        if (at >= 0 && at < s.n * kVec<T> && at / kVec<T> % kRowThreads == threadIdx.x) out[y] = narrow<T>(grad_term<H>(r, x_y, a.c, true));
+        if (at >= 0 && at < s.n * kVec<T> && at / kVec<T> % THREADS == id) out[y] = narrow<T>(grad_term<H>(r, x_y, c, true));
     } else {
-        for (int j = s.first + threadIdx.x; j < s.first + s.n * kVec<T>; j += kRowThreads)
-            out[j] = narrow<T>(grad_term<H>(r, widen(x[j]), a.c, j == y));
+        for (int j = s.first + id; j < s.first + s.n * kVec<T>; j += THREADS)
+            out[j] = narrow<T>(grad_term<H>(r, widen(x[j]), c, j == y));
     }
-    write_ends<T, H>(s, r, x_head, x_tail, out, a.c, y);
+    write_ends<T, H>(s, r, id, x_head, x_tail, out, c, y);
 }
 
-template <class T, bool H>
+template <class T, bool H, int THREADS>
 __global__ void __launch_bounds__(kRowThreads)
     k_token_grad(const Rows<T> a, int size, const float* logp, const float* lse, const float* entropy, const float* dlogp,
                  const float* dentropy, T* dx, int64_t dstride) {
     wait_for_kernel_before();
     let_next_kernel_start();
     // From the last row: what a forward pass read last may still be in L2.
-    const int64_t t = a.rows - 1 - blockIdx.x / size;
-    const int rank = (int)(blockIdx.x % size);
+    const int64_t t = a.rows - 1 - row_of<THREADS>(size);
+    if (THREADS == 32 && t < 0) return;
+    const int rank = THREADS == 32 ? 0 : (int)(blockIdx.x % size);
     const int64_t y = live_target(a, t);
     const float g = y < 0 ? 0.0f : dlogp[t], h = y < 0 || !H ? 0.0f : dentropy[t];
     T* out = dx + t * dstride;
     if ((g == 0.0f && h == 0.0f) || lse[t] == -INFINITY) {
-        zero_row<T, kRowThreads>(out, a.vocab, rank, size);
+        zero_row<T, THREADS>(out, a.vocab, rank, size);
         return;
     }
     const T* x = a.x + t * a.stride;
     const float x_y = y < a.vocab ? widen(x[y]) : NAN;
-    const GradRow r = grad_row(y < a.vocab ? g : NAN, h, x_y, logp[t], lse[t],
-                               h != 0.0f ? entropy[t] : 0.0f, a.inv_t);
+    const GradRow r = grad_row(y < a.vocab ? g : NAN, h, x_y, logp[t], lse[t], h != 0.0f ? entropy[t] : 0.0f, a.inv_t);
     if (out == x) {  // the target's logit is read before any thread writes it
-        if (size > 1) cg::this_cluster().sync();
+        if (THREADS == 32) __syncwarp();
+        else if (size > 1) cg::this_cluster().sync();
         else __syncthreads();
     }
-    write_grad<T, H>(a, r, x, out, place_of(y, a.vocab), x_y, rank, size);
+    write_grad<THREADS, H>(a.c, r, x, out, a.vocab, place_of(y, a.vocab), x_y, rank, size);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -736,7 +760,7 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
                 constexpr bool kClamp = decltype(clamp)::value;
                 const GradVector<T, H, kClamp> grad(r, c);
                 if (zero) zero_row<T, kFusedThreads>(out, a.vocab, rank, size);
-                else write_ends<T, H, kClamp>(s, r, x_head, x_tail, out, c, place);
+                else write_ends<T, H, kClamp>(s, r, threadIdx.x, x_head, x_tail, out, c, place);
                 for (int i = 0; i < kChunks; ++i, begin.next(slots)) {
                     const int at = min(s.n, i * per), m = min(s.n, at + per) - at;
                     const uint4* v = parts + begin.at * per;
@@ -766,6 +790,47 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
         __syncwarp();
         cg::this_cluster().sync();
     }
+}
+
+// The same for rows of up to kShortRow bytes, a warp each, which reads its row twice, the second
+// time from L1 or L2.
+template <class T, bool H>
+__global__ void __launch_bounds__(kRowThreads)
+    k_policy_short(const Rows<T> a, const PolicyTokens p, float* logp, float* entropy, T* dx, int64_t dstride) {
+    let_next_kernel_start();
+    const int64_t t = row_of<32>(1);
+    wait_for_kernel_before();
+    if (t >= a.rows) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t y = live_target(a, t);
+    T* out = dx + t * dstride;
+    const T* x = a.x + t * a.stride;
+    RowResult r = {0.0f, 0.0f, 0.0f};
+    TokenLoss l = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    RowStat st = empty_stat();
+    float x_y = NAN;
+    if (y >= 0) {
+        const TokenIn in(p, t);
+        x_y = y < a.vocab ? widen(x[y]) : NAN;
+        st = row_sums<32, H>(x, a.vocab, x_y, a.k, 0, 1, nullptr);
+        r = finish_row<H>(st, x_y, a.k, (float)a.inv_t);
+        if (y >= a.vocab) r.logp = NAN;
+        l = policy_token(p, in, r.logp, r.entropy);
+    }
+    if (lane == 0) {
+        logp[t] = r.logp;
+        if (entropy) entropy[t] = r.entropy;
+        p.loss[t] = l.loss;
+        p.kl[t] = l.kl;
+        p.clipped[t] = l.clipped;
+    }
+    if ((l.g == 0.0f && l.h == 0.0f) || st.s == 0.0f) {
+        zero_row<T, 32>(out, a.vocab, 0, 1);
+        return;
+    }
+    const GradRow grad = grad_row(l.g, l.h, st, r.entropy, a.inv_t);
+    __syncwarp();  // the row's ends and its target are read before any lane writes
+    write_grad<32, H>(H ? a.k.c : a.c, grad, x, out, a.vocab, place_of(y, a.vocab), x_y, 0, 1);
 }
 
 __global__ void __launch_bounds__(kRowThreads) k_policy_tokens(const PolicyTokens a, const float* logp, const float* entropy) {
@@ -858,6 +923,13 @@ int ctas_per_row(const zero_logits* x, int sms, int per_sm = kRowCtas) {
     return size;
 }
 
+// Whether each row goes to a warp: short rows, enough of them for every SM. At 16 KB a warp is the
+// faster (8192 rows, forward: 31 us against 42; policy loss 71 against 92), at 32 KB a CTA (policy
+// loss 114 us against 126).
+constexpr int64_t kShortRow = 16384;
+bool short_rows(const zero_logits* x, int sms) { return x->vocab * type_size(x->type) <= kShortRow && x->rows >= 8 * (int64_t)sms; }
+unsigned short_grid(const zero_logits* x) { return (unsigned)((x->rows + kRowThreads / 32 - 1) / (kRowThreads / 32)); }
+
 // Vectors of one part of a CTA's share of a row, and the shared memory for all its parts.
 int64_t fused_part(const zero_logits* x, int size) {
     const int64_t vecs = x->vocab * type_size(x->type) / 16;
@@ -875,10 +947,12 @@ int launch_token_logp(const zero_logits* x, const float* weight, float* logp, fl
     return by_type(x->type, [&](auto tag) {
         using T = decltype(tag);
         const Rows<T> a = rows_of<T>(x, weight);
+        if (short_rows(x, sms))
+            return launch_linked(entropy ? k_token_logp<T, true, 32> : k_token_logp<T, false, 32>, short_grid(x), kRowThreads, 0, 1, s, a, 1,
+                                 logp, lse, entropy, cleared, counter);
         const int size = ctas_per_row(x, sms);
-        const unsigned grid = (unsigned)(x->rows * size);
-        return launch_linked(entropy ? k_token_logp<T, true> : k_token_logp<T, false>, grid, kRowThreads, 0, size, s, a, size, logp, lse,
-                             entropy, cleared, counter);
+        return launch_linked(entropy ? k_token_logp<T, true, kRowThreads> : k_token_logp<T, false, kRowThreads>, (unsigned)(x->rows * size),
+                             kRowThreads, 0, size, s, a, size, logp, lse, entropy, cleared, counter);
     });
 }
 
@@ -888,25 +962,32 @@ int launch_token_grad(const zero_logits* x, const float* weight, const float* lo
     return by_type(x->type, [&](auto tag) {
         using T = decltype(tag);
         const Rows<T> a = rows_of<T>(x, weight);
+        if (short_rows(x, sms))
+            return launch_linked(h ? k_token_grad<T, true, 32> : k_token_grad<T, false, 32>, short_grid(x), kRowThreads, 0, 1, s, a, 1, logp,
+                                 lse, entropy, g, h, (T*)dx, dstride);
         const int size = ctas_per_row(x, sms);
-        const unsigned grid = (unsigned)(x->rows * size);
-        return launch_linked(h ? k_token_grad<T, true> : k_token_grad<T, false>, grid, kRowThreads, 0, size, s, a, size, logp, lse,
-                             entropy, g, h, (T*)dx, dstride);
+        return launch_linked(h ? k_token_grad<T, true, kRowThreads> : k_token_grad<T, false, kRowThreads>, (unsigned)(x->rows * size),
+                             kRowThreads, 0, size, s, a, size, logp, lse, entropy, g, h, (T*)dx, dstride);
     });
 }
 
-// CTAs per row of the one-pass kernel: enough that a slice fits, then as ctas_per_row. 0: the row
-// is too long for eight CTAs (over 450,000 16-bit logits), and takes two passes.
+// CTAs per row of the one-pass kernel: as ctas_per_row for few rows, else one, or two where a slice
+// would not fit. 0: the row takes two passes. Four CTAs per row wait for each other longer than the
+// second pass takes (2709 rows of 151936 bf16: 414 us against 330).
 int fused_size(const zero_logits* x, int sms) {
-    int size = ctas_per_row(x, sms, 2);
-    while (size <= 8 && fused_bytes(x, size) > kFusedBytes) size *= 2;
-    return size <= 8 ? size : 0;
+    const int few = ctas_per_row(x, sms, 2);
+    for (int size = few; size <= std::max(few, 2); size *= 2)
+        if (fused_bytes(x, size) <= kFusedBytes) return size;
+    return 0;
 }
 
 int launch_policy_rows(const zero_logits* x, const PolicyTokens& p, const zero_policy* q, int sms, cudaStream_t s) {
     const int size = fused_size(x, sms);
     const int rc = by_type(x->type, [&](auto tag) {
         using T = decltype(tag);
+        if (short_rows(x, sms))
+            return launch_linked(q->entropy_coef != 0.0 ? k_policy_short<T, true> : k_policy_short<T, false>, short_grid(x), kRowThreads, 0, 1, s,
+                                 rows_of<T>(x, p.w), p, q->logp, q->entropy, (T*)q->dlogits, q->dstride);
         auto* kernel = q->entropy_coef != 0.0 ? k_policy_rows<T, true> : k_policy_rows<T, false>;
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFusedBytes);
         if (e != cudaSuccess) return record_cuda_error(e);

@@ -245,12 +245,13 @@ struct Sums {
         limit = top + 40.0f / k.c;
     }
     __device__ __forceinline__ void term(int i, uint64_t x) {
-        const uint64_t t = add2(x, base), p = CHECKED ? mul2(t, c) : fma2(t, c, pack2(-kDown, -kDown));
-        const uint64_t d = ENTROPY ? p : fma2(t, lo, p);
-        const float2 df = unpack2(d);
-        const uint64_t e = pack2(pow2(df.x), pow2(df.y));
+        // d_j for the sum q, and the exponent that is taken, kDown lower
+        const uint64_t t = add2(x, base), down = pack2(-kDown, -kDown), d = mul2(t, c);
+        const uint64_t z = CHECKED ? (ENTROPY ? d : fma2(t, lo, d)) : ENTROPY ? add2(d, down) : fma2(t, lo, fma2(t, c, down));
+        const float2 zf = unpack2(z);
+        const uint64_t e = pack2(pow2(zf.x), pow2(zf.y));
         s[i] = add2(s[i], e);
-        if (ENTROPY) q[i] = fma2(e, CHECKED ? pack2(fmaxf(df.x, kFar), fmaxf(df.y, kFar)) : d, q[i]);
+        if (ENTROPY) q[i] = fma2(e, CHECKED ? pack2(fmaxf(zf.x, kFar), fmaxf(zf.y, kFar)) : d, q[i]);
     }
     __device__ __forceinline__ void add(const uint4& v) {
         if (CHECKED) {
@@ -262,7 +263,8 @@ struct Sums {
     }
     __device__ __forceinline__ void add_one(float x) {
         if (CHECKED && x > limit) raise(x);
-        const float t = x - base_of(m), p = CHECKED ? t * k.c : fmaf(t, k.c, -kDown), d = ENTROPY ? p : fmaf(t, k.lo, p), e = pow2(d);
+        const float t = x - base_of(m), down = CHECKED ? 0.0f : -kDown, d = t * k.c;
+        const float e = pow2(ENTROPY ? d + down : fmaf(t, k.lo, CHECKED ? d : fmaf(t, k.c, down)));
         s[0] = add2(s[0], pack2(e, 0.0f));
         if (ENTROPY) q[0] = fma2(pack2(e, 0.0f), pack2(CHECKED ? fmaxf(d, kFar) : d, 0.0f), q[0]);
     }
@@ -270,7 +272,7 @@ struct Sums {
         const float2 a = unpack2(add2(s[0], s[1])), b = unpack2(add2(q[0], q[1]));
         const float up = CHECKED ? 1.0f : 0x1p20f, sum = a.x + a.y;
         static_assert(kDown == 20.0f, "2^kDown");
-        return {m, sum * up, ENTROPY ? (CHECKED ? b.x + b.y : fmaf(kDown, sum, b.x + b.y) * up) : 0.0f};
+        return {m, sum * up, ENTROPY ? (b.x + b.y) * up : 0.0f};
     }
 };
 
