@@ -382,6 +382,8 @@ POLICY = [  # lens, reduce, advantages per, old, ref, kl, kl_coef, entropy_coef,
     ([3, 2], "token", "token", True, True, "k3", 0.1, 0.02, 0.0, 1.0, 131073, "bf16"),
     ([3, 2], "sequence", "sequence", True, True, "k3", 0.1, 0.02, 3.0, 1.0, 300001, "fp32"),
     ([310], "token", "token", True, False, "k3", 0.0, 0.01, 0.0, 1.0, 60001, "bf16"),
+    ([160], "sum", "sequence", True, True, "k3", 0.05, 0.01, 0.0, 1.0, 30011, "bf16"),  # one CTA per row, large and small
+    ([160], "token", "sequence", True, True, "k3", 0.05, 0.0, 0.0, 1.0, 12007, "fp16"),
 ]
 
 

@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "zero_host.h"
 #include "zero_softmax.cuh"
@@ -239,17 +240,15 @@ __global__ void __launch_bounds__(kLinearThreads, 1)
             const int n = (int)min((int64_t)cols, a.vocab - col0);  // may be 0 or less
             const int64_t y = r < a.rows ? a.targets[r] - col0 : -1;
             float v[BN / 2];
-#pragma unroll
-            for (int j = 0; j < BN / 2; ++j) v[j] = 0.0f;
-            for (int k = 0; k < steps; k += kChunk, acc.next()) {
-                if (!(ok = __all_sync(~0u, mbar_wait(acc_full + 8 * acc.at, acc.phase, &gave_up)))) break;
+            auto take = [&](auto add) {
+                if (!(ok = __all_sync(~0u, mbar_wait(acc_full + 8 * acc.at, acc.phase, &gave_up)))) return;
                 tcgen05_after_sync();
 #pragma unroll
                 for (int j = 0; j < BN / 2; j += 64) {
                     float u[64];
                     tmem_load64(mine + acc.at * BN + j, u);
 #pragma unroll
-                    for (int n = 0; n < 64; ++n) v[j + n] += u[n];
+                    for (int n = 0; n < 64; ++n) v[j + n] = decltype(add)::value ? v[j + n] + u[n] : u[n];
                 }
                 tcgen05_before_sync();
                 __syncwarp();
@@ -257,7 +256,10 @@ __global__ void __launch_bounds__(kLinearThreads, 1)
                     if (CG == 2) mbar_arrive_at(smem_of(acc_empty + 8 * acc.at, 0));
                     else mbar_arrive(acc_empty + 8 * acc.at);
                 }
-            }
+                acc.next();
+            };
+            take(std::false_type());
+            for (int k = kChunk; k < steps && ok; k += kChunk) take(std::true_type());
             if (!ok) break;
             if (n < BN / 2) {
 #pragma unroll

@@ -588,9 +588,11 @@ __device__ __forceinline__ TokenLoss policy_token(const PolicyTokens& a, const T
 // tokens, a quarter masked, with entropy bonus: 235 us the whole call, 1.44 GB, 92% of the copy
 // peak (two passes over the logits: 383 us). Seven warps compute: with ten, and four parts to a
 // slice, 252 us, since registers then spill; with fifteen 325.
-constexpr int kFusedWarps = 7, kFusedThreads = 32 * kFusedWarps;
 constexpr int kChunks = 2, kSlots = 8;  // parts of a slice; most parts that shared memory holds
-constexpr int64_t kFusedBytes = 110 * 1024;  // of a CTA's parts: two CTAs fit an SM
+// Computing warps of a CTA, and how many CTAs an SM then holds, by registers and shared memory.
+constexpr int kFusedWarps = 7, kFusedWarpsSmall = 3;
+constexpr int fused_ctas(int warps) { return warps == kFusedWarps ? 2 : 4; }
+constexpr int64_t fused_room(int warps) { return warps == kFusedWarps ? 110 * 1024 : 54 * 1024; }
 
 template <int THREADS>
 __device__ __forceinline__ void consumers_sync() {
@@ -609,11 +611,12 @@ struct Slot {
     }
 };
 
-template <class T, bool H>
-__global__ void __launch_bounds__(kFusedThreads + 32, 2)
+template <class T, bool H, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
     k_policy_rows(const Rows<T> a, const PolicyTokens p, int size, int per, int slots, float* logp, float* entropy, T* dx, int64_t dstride) {
+    constexpr int kThreads = 32 * WARPS;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ RowStat sm[kFusedWarps], mine[2];
+    __shared__ RowStat sm[WARPS], mine[2];
     __shared__ GradRow shared_row;
     __shared__ bool shared_zero;
     __shared__ int64_t row_at[2], row_y[2];
@@ -628,11 +631,11 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
         gave_up = 0;
         for (int i = 0; i < slots; ++i) {
             mbar_init(full + 8 * i, 1);
-            mbar_init(empty + 8 * i, kFusedWarps);
+            mbar_init(empty + 8 * i, WARPS);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(row_full + 8 * i, 1);
-            mbar_init(row_empty + 8 * i, kFusedWarps);
+            mbar_init(row_empty + 8 * i, WARPS);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -641,7 +644,7 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
     // The kernel before this one sets up the weights; it was itself launched behind the logits'
     // producer, so logits and targets may be read at once, and the rest after it.
     let_next_kernel_start();
-    if (threadIdx.x >= kFusedThreads) {
+    if (threadIdx.x >= kThreads) {
         Slot slot;
         bool ok = true;
         for (int64_t n = 0;; ++n) {
@@ -694,7 +697,7 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
             T* out = dx + t * dstride;
             if (n == 0) wait_for_kernel_before();
             if (y < 0) {
-                zero_row<T, kFusedThreads>(out, a.vocab, rank, size);
+                zero_row<T, kThreads>(out, a.vocab, rank, size);
                 if (threadIdx.x == 0 && rank == 0) {
                     logp[t] = p.loss[t] = p.kl[t] = p.clipped[t] = 0.0f;
                     if (entropy) entropy[t] = 0.0f;
@@ -716,18 +719,18 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
                     ok = ok && mbar_wait(full + 8 * slot.at, slot.phase, &gave_up);
                     const int at = min(s.n, i * per);
                     const uint4* v = parts + slot.at * per;
-                    for_vectors<kFusedThreads>(min(s.n, at + per) - at, [&](int j) { return v[j]; }, [&](int, const uint4& q) { run.add(q); });
+                    for_vectors<kThreads>(min(s.n, at + per) - at, [&](int j) { return v[j]; }, [&](int, const uint4& q) { run.add(q); });
                 }
                 if (threadIdx.x < s.head) run.add_one(x_head);
                 if (threadIdx.x < s.tail) run.add_one(x_tail);
-                return group_join<H, kChecked, kFusedWarps>(run.stat(), a.k, sm, 1);
+                return group_join<H, kChecked, WARPS>(run.stat(), a.k, sm, 1);
             };
             RowStat st;
             bool good = false;
             if (try_fast) {
                 st = sums(std::false_type());
                 good = good_sums<H>(st);
-                if (!good) consumers_sync<kFusedThreads>();
+                if (!good) consumers_sync<kThreads>();
             }
             if (!good) st = sums(std::true_type());
             if (!ok || *(volatile int*)&gave_up) st.s = NAN;  // a copy did not come: no result
@@ -750,7 +753,7 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
                     p.clipped[t] = l.clipped;
                 }
             }
-            consumers_sync<kFusedThreads>();
+            consumers_sync<kThreads>();
             const GradRow r = shared_row;
             const bool zero = shared_zero;
             const int place = place_of(y, a.vocab);
@@ -759,7 +762,7 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
             auto write = [&](auto clamp) {
                 constexpr bool kClamp = decltype(clamp)::value;
                 const GradVector<T, H, kClamp> grad(r, c);
-                if (zero) zero_row<T, kFusedThreads>(out, a.vocab, rank, size);
+                if (zero) zero_row<T, kThreads>(out, a.vocab, rank, size);
                 else write_ends<T, H, kClamp>(s, r, threadIdx.x, x_head, x_tail, out, c, place);
                 for (int i = 0; i < kChunks; ++i, begin.next(slots)) {
                     const int at = min(s.n, i * per), m = min(s.n, at + per) - at;
@@ -767,14 +770,14 @@ __global__ void __launch_bounds__(kFusedThreads + 32, 2)
                     const int from = s.first + at * kVec<T>;  // the chunk's first element
                     if (!zero && fast) {
                         uint4* to = reinterpret_cast<uint4*>(out + from);
-                        for_vectors<kFusedThreads>(m, [&](int j) { return v[j]; }, [&](int j, const uint4& q) { __stcs(to + j, grad(q)); });
+                        for_vectors<kThreads>(m, [&](int j) { return v[j]; }, [&](int j, const uint4& q) { __stcs(to + j, grad(q)); });
                         // the thread that wrote the target's vector sets the target right
                         const int dy = place - from;
-                        if (dy >= 0 && dy < m * kVec<T> && dy / kVec<T> % kFusedThreads == threadIdx.x)
+                        if (dy >= 0 && dy < m * kVec<T> && dy / kVec<T> % kThreads == threadIdx.x)
                             out[place] = narrow<T>(grad_term<H, kClamp>(r, x_y, c, true));
                     } else if (!zero) {
                         const T* e = reinterpret_cast<const T*>(v);
-                        for (int j = threadIdx.x; j < m * kVec<T>; j += kFusedThreads)
+                        for (int j = threadIdx.x; j < m * kVec<T>; j += kThreads)
                             out[from + j] = narrow<T>(grad_term<H, kClamp>(r, widen(e[j]), c, from + j == place));
                     }
                     __syncwarp();
@@ -930,15 +933,31 @@ constexpr int64_t kShortRow = 16384;
 bool short_rows(const zero_logits* x, int sms) { return x->vocab * type_size(x->type) <= kShortRow && x->rows >= 8 * (int64_t)sms; }
 unsigned short_grid(const zero_logits* x) { return (unsigned)((x->rows + kRowThreads / 32 - 1) / (kRowThreads / 32)); }
 
-// Vectors of one part of a CTA's share of a row, and the shared memory for all its parts.
-int64_t fused_part(const zero_logits* x, int size) {
+// How the one-pass kernel takes a row.
+struct FusedPlan {
+    int size = 0;      // CTAs per row; 0: two passes over the row instead
+    int warps = 0;
+    int part = 0;      // vectors of one part of a CTA's slice
+    int slots = 0;     // parts in shared memory: with more than a row's, the next row's copies begin earlier
+};
+
+// CTAs per row as ctas_per_row for few rows, else one, or two where a slice would not fit: four CTAs
+// per row wait for each other longer than a second pass takes (2709 rows of 151936 bf16: 414 us
+// against 347). Rows of half the room go to smaller CTAs, twice as many.
+FusedPlan fused_plan(const zero_logits* x, int sms) {
+    FusedPlan f;
     const int64_t vecs = x->vocab * type_size(x->type) / 16;
-    return ((vecs + size - 1) / size + kChunks - 1) / kChunks;
-}
-int64_t fused_bytes(const zero_logits* x, int size) { return 16 * kChunks * fused_part(x, size); }
-// Parts that fit: with more than a row's, the next row's copies begin before this one is done.
-int fused_slots(const zero_logits* x, int size) {
-    return (int)std::max<int64_t>(kChunks, std::min<int64_t>(kSlots, kFusedBytes / std::max<int64_t>(16, 16 * fused_part(x, size))));
+    const int few = ctas_per_row(x, sms, 2);
+    for (int size = few; size <= std::max(few, 2); size *= 2) {
+        const int64_t part = std::max<int64_t>(1, ((vecs + size - 1) / size + kChunks - 1) / kChunks);
+        if (16 * kChunks * part > fused_room(kFusedWarps)) continue;
+        f.size = size;
+        f.warps = size == 1 && 16 * kChunks * part <= fused_room(kFusedWarpsSmall) ? kFusedWarpsSmall : kFusedWarps;
+        f.part = (int)part;
+        f.slots = (int)std::min<int64_t>(kSlots, fused_room(f.warps) / (16 * part));
+        return f;
+    }
+    return f;
 }
 
 int launch_token_logp(const zero_logits* x, const float* weight, float* logp, float* lse, float* entropy, float* cleared,
@@ -971,29 +990,23 @@ int launch_token_grad(const zero_logits* x, const float* weight, const float* lo
     });
 }
 
-// CTAs per row of the one-pass kernel: as ctas_per_row for few rows, else one, or two where a slice
-// would not fit. 0: the row takes two passes. Four CTAs per row wait for each other longer than the
-// second pass takes (2709 rows of 151936 bf16: 414 us against 330).
-int fused_size(const zero_logits* x, int sms) {
-    const int few = ctas_per_row(x, sms, 2);
-    for (int size = few; size <= std::max(few, 2); size *= 2)
-        if (fused_bytes(x, size) <= kFusedBytes) return size;
-    return 0;
+template <class T, int WARPS>
+int launch_fused(const zero_logits* x, const FusedPlan& f, const PolicyTokens& p, const zero_policy* q, int sms, cudaStream_t s) {
+    auto* kernel = q->entropy_coef != 0.0 ? k_policy_rows<T, true, WARPS> : k_policy_rows<T, false, WARPS>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fused_room(WARPS));
+    if (e != cudaSuccess) return record_cuda_error(e);
+    const int64_t clusters = std::min<int64_t>(x->rows, fused_ctas(WARPS) * sms / f.size);
+    return launch_linked(kernel, (unsigned)(clusters * f.size), 32 * WARPS + 32, (size_t)16 * f.slots * f.part, f.size, s, rows_of<T>(x, nullptr),
+                         p, f.size, f.part, f.slots, q->logp, q->entropy, (T*)q->dlogits, q->dstride);
 }
 
-int launch_policy_rows(const zero_logits* x, const PolicyTokens& p, const zero_policy* q, int sms, cudaStream_t s) {
-    const int size = fused_size(x, sms);
+int launch_policy_rows(const zero_logits* x, const FusedPlan& f, const PolicyTokens& p, const zero_policy* q, int sms, cudaStream_t s) {
     const int rc = by_type(x->type, [&](auto tag) {
         using T = decltype(tag);
         if (short_rows(x, sms))
             return launch_linked(q->entropy_coef != 0.0 ? k_policy_short<T, true> : k_policy_short<T, false>, short_grid(x), kRowThreads, 0, 1, s,
                                  rows_of<T>(x, p.w), p, q->logp, q->entropy, (T*)q->dlogits, q->dstride);
-        auto* kernel = q->entropy_coef != 0.0 ? k_policy_rows<T, true> : k_policy_rows<T, false>;
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFusedBytes);
-        if (e != cudaSuccess) return record_cuda_error(e);
-        const int64_t clusters = std::min<int64_t>(x->rows, 2 * sms / size);
-        return launch_linked(kernel, (unsigned)(clusters * size), kFusedThreads + 32, (size_t)(16 * fused_slots(x, size) * fused_part(x, size)), size, s,
-                             rows_of<T>(x, nullptr), p, size, (int)fused_part(x, size), fused_slots(x, size), q->logp, q->entropy, (T*)q->dlogits, q->dstride);
+        return f.warps == kFusedWarps ? launch_fused<T, kFusedWarps>(x, f, p, q, sms, s) : launch_fused<T, kFusedWarpsSmall>(x, f, p, q, sms, s);
     });
     if (rc) return rc;
     return launch_linked(k_policy_finish, 1, kSetupThreads, 0, 1, s, p);
@@ -1155,7 +1168,8 @@ extern "C" int zero_policy_loss(const zero_logits* x, const zero_policy* p, void
     if (x->rows > 0) {
         k_policy_setup<<<1, kSetupThreads, 0, s>>>(a);
         if ((rc = launched())) return rc;
-        if (fused_size(x, sms)) return launch_policy_rows(x, a, p, sms, s);
+        const FusedPlan f = fused_plan(x, sms);
+        if (f.size) return launch_policy_rows(x, f, a, p, sms, s);
         if ((rc = launch_token_logp(x, a.w, p->logp, a.lse, p->entropy, nullptr, nullptr, sms, s))) return rc;
         k_policy_tokens<<<(int)std::min<int64_t>((x->rows + kRowThreads - 1) / kRowThreads, 1024), kRowThreads, 0, s>>>(a, p->logp, p->entropy);
         if ((rc = launched())) return rc;
