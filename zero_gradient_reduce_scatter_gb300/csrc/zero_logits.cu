@@ -147,8 +147,8 @@ __device__ __forceinline__ int64_t row_of(int size) {
 
 // Forward, bound by reading the logits once: `size` CTAs per row (a cluster; several where there
 // are few rows), each thread kUnroll vectors at a time. 4096 fp16 tokens, a quarter of them masked:
-// 53.9 us, 309 MB, 86% of the copy peak (128 or 512 threads and 2 or 6 vectors lie within 5%); one
-// token 4.4 us, over eight CTAs. Rows of up to kShortRow bytes go to a warp each: a CTA's joining
+// 53.3 us, 309 MB, 87% of the copy peak (128 or 512 threads and 2 or 6 vectors lie within 5%); one
+// token 3.9 us, over eight CTAs. Rows of up to kShortRow bytes go to a warp each: a CTA's joining
 // would take longer than their reading.
 template <class T, bool ENTROPY, int THREADS>
 __global__ void __launch_bounds__(kRowThreads, 5)
@@ -585,9 +585,9 @@ __device__ __forceinline__ TokenLoss policy_token(const PolicyTokens& a, const T
 // again. Two CTAs per SM, each with one slice: a producer warp refills a part of it with the next
 // row as soon as the gradient of this one has been taken from it, so that copies run beside
 // everything else. Rows are handed out one by one (some carry no loss and cost half). 8192 bf16
-// tokens, a quarter masked, with entropy bonus: 235 us the whole call, 1.44 GB, 92% of the copy
-// peak (two passes over the logits: 383 us). Seven warps compute: with ten, and four parts to a
-// slice, 252 us, since registers then spill; with fifteen 325.
+// tokens, a quarter masked, with entropy bonus: 237 us the whole call, 1.44 GB, 91% of the copy peak
+// (two passes over the logits: 383 us). Seven warps compute: with ten, and four parts to a slice,
+// 252 us, since registers then spill; with fifteen 325.
 constexpr int kChunks = 2, kSlots = 8;  // parts of a slice; most parts that shared memory holds
 // Computing warps of a CTA, and how many CTAs an SM then holds, by registers and shared memory.
 constexpr int kFusedWarps = 7, kFusedWarpsSmall = 3;
