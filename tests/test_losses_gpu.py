@@ -546,6 +546,7 @@ def test_side_stream_and_graph():
 LINEAR = [  # T, V, D, ld_hidden, ld_weight
     (1, 1, 8, 8, 8), (1, 9, 3, 8, 8), (1, 50257, 768, 768, 768), (3, 127, 64, 64, 64), (5, 129, 72, 80, 88), (16, 1000, 8, 8, 16),
     (130, 300, 200, 200, 200), (257, 2049, 136, 136, 136), (64, 4096, 1024, 1024, 1024), (300, 777, 1000, 1000, 1008),
+    (300, 20011, 264, 264, 264), (500, 20011, 520, 520, 520), (640, 9001, 64, 64, 64),  # tiles of 128 tokens, and of 256
 ]
 
 

@@ -373,25 +373,35 @@ struct LinearPlan {
     int64_t parts, parts_bytes, bytes;
 };
 
-// Pairs of CTAs once there are tokens for more than one CTA's tile. The width of a tile is the
-// one (of the multiples of 16, for pairs of 32, that an MMA takes) for which the busiest CTA has the fewest columns to go
-// through: few tokens are bound by reading the vocabulary matrix, and 50257 columns over 152 CTAs
-// are three tiles of 112 each rather than one or two of 256. Pairs keep to wide tiles, which
-// their MMAs need to run at full rate.
+// Up to 128 tokens: single CTAs on narrow tiles. Beyond: pairs of CTAs on tiles of 256 tokens, or
+// single CTAs on tiles of 128, whichever has the busiest CTA go through fewer columns; single CTAs
+// count for 8% more, since each loads all of its columns itself (300 tokens x 50257 x 2048: three
+// tiles of 128 in 62 us, two of 256 in 75). The width of a tile is likewise the one, of those that
+// an MMA takes, with the fewest columns for the busiest CTA: 50257 columns over 152 CTAs are three
+// tiles of 112 each rather than one or two of 256. Tiles narrower than 192 would slow the MMAs
+// where these are what bounds.
 LinearPlan linear_plan(int64_t rows, int64_t vocab, int sms) {
-    LinearPlan l;
-    l.pairs = rows > kRowsTile;
-    l.tile_rows = l.pairs ? 2 * kRowsTile : kRowsTile;
-    l.row_tiles = (int32_t)((rows + l.tile_rows - 1) / l.tile_rows);
-    const int workers = std::max(1, l.pairs ? sms / 2 : sms), widest = l.pairs ? 256 : 128;
-    int64_t least = INT64_MAX;
-    l.tile_cols = widest;
-    for (int cols = widest; cols >= (l.pairs ? 224 : 64); cols -= l.pairs ? 32 : 16) {
-        const int64_t tiles = (vocab + cols - 1) / cols * l.row_tiles, most = (tiles + workers - 1) / workers * cols;
-        if (most < least) {
+    LinearPlan l = {};
+    double least = 1e300;
+    auto consider = [&](bool pairs, int widest, int narrowest, int step, double weight) {
+        const int tile_rows = pairs ? 2 * kRowsTile : kRowsTile, workers = std::max(1, pairs ? sms / 2 : sms);
+        const int64_t row_tiles = (rows + tile_rows - 1) / tile_rows;
+        for (int cols = widest; cols >= narrowest; cols -= step) {
+            const int64_t tiles = (vocab + cols - 1) / cols * row_tiles;
+            const double most = (double)((tiles + workers - 1) / workers) * cols * weight;
+            if (most >= least) continue;
             least = most;
+            l.pairs = pairs;
+            l.tile_rows = tile_rows;
+            l.row_tiles = (int32_t)row_tiles;
             l.tile_cols = cols;
         }
+    };
+    if (rows <= kRowsTile) {
+        consider(false, 128, 64, 16, 1.0);
+    } else {
+        consider(true, 256, 224, 32, 1.0);
+        consider(false, 256, 192, 16, 1.08);
     }
     l.col_tiles = (int32_t)((vocab + l.tile_cols - 1) / l.tile_cols);
     l.parts = 2 * (int64_t)l.col_tiles;
@@ -448,6 +458,7 @@ int run_linear(const zero_linear* x, const LinearArgs& a, const LinearPlan& l, f
     if (rc) return rc;
     const bool bf16 = x->type == ZERO_T_BF16;
     if (l.pairs) rc = bf16 ? launch_product<ZERO_T_BF16, 2, 256, ENTROPY>(x, a, s) : launch_product<ZERO_T_FP16, 2, 256, ENTROPY>(x, a, s);
+    else if (l.tile_cols > 128) rc = bf16 ? launch_product<ZERO_T_BF16, 1, 256, ENTROPY>(x, a, s) : launch_product<ZERO_T_FP16, 1, 256, ENTROPY>(x, a, s);
     else rc = bf16 ? launch_product<ZERO_T_BF16, 1, 128, ENTROPY>(x, a, s) : launch_product<ZERO_T_FP16, 1, 128, ENTROPY>(x, a, s);
     if (rc) return rc;
     if (x->rows <= kJoinFewRows)
@@ -457,7 +468,7 @@ int run_linear(const zero_linear* x, const LinearArgs& a, const LinearPlan& l, f
 
 // The workspace of any number of SMs.
 int64_t most_bytes(int64_t rows, int64_t vocab) {
-    const int64_t narrowest = rows > kRowsTile ? 224 : 64;
+    const int64_t narrowest = rows > kRowsTile ? 192 : 64;
     return 12 * 2 * ((vocab + narrowest - 1) / narrowest) * rows + 4 * rows + 16 + 4 * (kMaxGrid + 4 + rows / kRowsTile + 1);
 }
 
