@@ -788,7 +788,8 @@ typedef struct {
     int32_t dst_type;   /* ZERO_T_*                                                           */
 } zero_grad_tensor;
 typedef struct zero_grads zero_grads; /* opaque, library-owned */
-/* Bytes of workspace of a plan over n tensors; negative for n < 1. Host only. */
+/* Bytes of workspace (256-byte aligned device memory) of a plan over n tensors; negative for n < 1.
+ * Host only. */
 int64_t zero_grads_workspace(int64_t n);
 /* Checks the list and uploads its table; waits for `stream` (as zero_init). The device is that
  * of `workspace`. Errors: INVALID_ARG, MISALIGNED, SIZE_MISMATCH, CUDA; *out is NULL then. */

@@ -93,14 +93,6 @@ __device__ __forceinline__ RowStat join(RowStat a, RowStat b, Scale k) {
     return {m, a.s + b.s, ENTROPY ? a.q + b.q : 0.0f};
 }
 
-// One term over the base m.
-template <bool ENTROPY>
-__device__ __forceinline__ void add_term(RowStat& a, float x, Scale k, float m) {
-    const float d = scaled<ENTROPY>(x - m, k), e = pow2(d);
-    a.s += e;
-    if (ENTROPY) a.q = fmaf(e, fmaxf(d, kFar), a.q);
-}
-
 // ---- two fp32 numbers in one instruction -------------------------------------------------
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t r;
