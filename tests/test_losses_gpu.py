@@ -444,6 +444,52 @@ def test_policy_loss(case):
     assert torch.equal(x, q.dlogits) and torch.equal(inplace.loss, q.loss)
 
 
+MANY = [  # as POLICY, with more tokens than a CTA takes at a time: one sequence, a long one among short ones, none
+    ((5001,), "sequence", "sequence", True, True, "k3", 0.05, 0.01, 0.0, 1.0, 40, "bf16"),
+    ((3, 0, 9000, 1, 70, 0), "sequence", "token", True, False, "k1", 0.0, 0.0, 3.0, 0.8, 24, "fp32"),
+    ((40,) * 130, "token", "sequence", False, True, "k2", 0.1, 0.0, 0.0, 1.0, 33, "fp16"),
+]
+
+
+@pytest.mark.parametrize("case", MANY)
+def test_policy_loss_of_many_tokens(case):
+    test_policy_loss(case)
+
+
+@pytest.mark.parametrize("T", [61, 6000])
+@pytest.mark.parametrize("reduce", ["token", "sequence", "sum"])
+def test_tokens_of_no_sequence(T, reduce):
+    """Tokens in front of the first sequence and behind the last change nothing: the same gradients as
+    without them, bit for bit, and the same loss but for one rounding of each."""
+    x, _ = make_logits(T, 33, "fp32", 5)
+    y = make_targets(T, 33, 6)
+    n = T - 8
+    off = torch.tensor([3, 3, 10, 12, n + 3], device=DEV)
+    adv = torch.rand(4, device=DEV, generator=gen(7)) + 0.5  # every term of the loss has one sign
+    q = zg.policy_loss(x, y, adv, offsets=off, reduce=reduce)
+    r = zg.policy_loss(x[3:n + 3], y[3:n + 3], adv, offsets=off - 3, reduce=reduce)
+    assert torch.equal(q.dlogits[3:n + 3], r.dlogits)
+    assert bool((q.dlogits[:3] == 0).all()) and bool((q.dlogits[n + 3:] == 0).all())
+    assert abs(float(q.loss) - float(r.loss)) <= 2.0 ** -22 * abs(float(r.loss))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,V", [(40, 50304), (1300, 600)])
+def test_padding_with_the_lowest_value(T, V, dtype):
+    """Over a vocabulary padded with the type's lowest value or with -inf the terms are the same zeros."""
+    x, _ = make_logits(T, V, dtype, 9)
+    y = make_targets(T, V - 100, 8)
+    adv = torch.randn(T, device=DEV, generator=gen(3))
+    results = []
+    for mask in (torch.finfo(TYPES[dtype]).min, -math.inf):
+        x[:, -100:] = mask
+        f = zg.token_logp(x, y, entropy=True)
+        q = zg.policy_loss(x, y, adv, entropy_coef=0.02)
+        results.append([f.logp, f.lse, f.entropy, q.logp, q.entropy, q.loss, q.dlogits])
+    for a, b in zip(*results):
+        assert torch.equal(a, b) and bool(a.isfinite().all())
+
+
 def test_policy_gradient_against_differences():
     """Central differences of the 64-bit loss in logits of both sequences; the loss is smooth
     here (no ratio near an edge), its third derivatives below 30."""

@@ -106,12 +106,13 @@ __device__ __forceinline__ RowStat cluster_join(RowStat a, int size, Scale k, Ro
     return warp_join<ENTROPY, true, 8>(a, k);
 }
 
-// Whether a row is taken without CHECKED (Sums) first: its target's logit is a base, and a
-// vocabulary padded with -inf, at its end or start, does not make an entropy's sum fail anyway.
-// A function of the row alone, so that its bits are too.
+// Whether a row is taken without CHECKED (Sums) first: its target's logit is a base, and a vocabulary
+// padded with -inf or the type's lowest value, at its end or start, does not make an entropy's sum
+// fail anyway. A function of the row alone, so that its bits are too.
 template <bool ENTROPY, class T>
-__device__ __forceinline__ bool fast_row(const T* x, int64_t vocab, float x_y) {
-    return fabsf(x_y) < INFINITY && !(ENTROPY && (widen(x[0]) == -INFINITY || widen(x[vocab - 1]) == -INFINITY));
+__device__ __forceinline__ bool fast_row(const T* x, int64_t vocab, float x_y, Scale k) {
+    if (ENTROPY && fminf(widen(x[0]) - x_y, widen(x[vocab - 1]) - x_y) * k.c == -INFINITY) return false;
+    return fabsf(x_y) < INFINITY;
 }
 
 // The sums of a row, or of a CTA's share of it, by the THREADS that take it: a CTA's (joined through
@@ -130,7 +131,7 @@ __device__ __forceinline__ RowStat row_sums(const T* x, int64_t vocab, float x_y
         if constexpr (THREADS == 32) return warp_join<ENTROPY, kChecked>(run.stat(), k);
         else return group_join<ENTROPY, kChecked, THREADS / 32>(run.stat(), k, sm, 0);
     };
-    if (fast_row<ENTROPY>(x, vocab, x_y)) {
+    if (fast_row<ENTROPY>(x, vocab, x_y, k)) {
         const RowStat st = sums(std::false_type());
         if (good_sums<ENTROPY>(st)) return st;
         if (THREADS > 32) __syncthreads();
@@ -454,79 +455,78 @@ struct PolicyTokens {
     int32_t kl_kind, reduce, per_sequence;
 };
 
+// The kernels over tokens alone: one cluster of token_ctas(rows) CTAs.
 constexpr int kSetupThreads = 1024;
 
-__device__ __forceinline__ int64_t warp_sum(int64_t x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-    return x;
+// The sequence that token t lies in, -1 in front of the first, `seqs` behind the last: the last one
+// that begins at or before it.
+__device__ __forceinline__ int64_t sequence_of(const int64_t* offsets, int64_t seqs, int64_t t) {
+    int64_t lo = 0, hi = seqs + 1;  // offsets below lo are at most t, those from hi on are more
+    while (lo < hi) {
+        const int64_t mid = lo + (hi - lo) / 2;
+        if (offsets[mid] <= t) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo - 1;
 }
 
-// Weights and advantages of all tokens, by one CTA: a warp per sequence counts, then spreads.
+// Weights and advantages of all tokens: targets are counted, in all and by sequence, then spread. A
+// thread finds its token's sequence by bisection, so that one sequence of all tokens takes no longer
+// than many: 32768 tokens in one sequence took a warp of its own 700 us.
 __global__ void __launch_bounds__(kSetupThreads) k_policy_setup(const PolicyTokens a) {
-    __shared__ unsigned long long total, nonempty;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = kSetupThreads / 32;
+    __shared__ uint32_t counted[2], all[2];  // tokens with a target, sequences that have one: added up in the first CTA's; everyone's copy
+    const cg::cluster_group cl = cg::this_cluster();
+    const int lane = threadIdx.x & 31;
+    const int64_t first = (int64_t)blockIdx.x * kSetupThreads + threadIdx.x, step = (int64_t)gridDim.x * kSetupThreads;
+    const bool by_sequence = a.reduce == ZERO_REDUCE_SEQUENCE;
+    uint32_t* of = reinterpret_cast<uint32_t*>(a.h);  // a sequence's targets, at its first token
+    wait_for_kernel_before();
     let_next_kernel_start();
-    if (threadIdx.x == 0) {
-        total = nonempty = 0;
-        *a.ticket = 0;
+    if (threadIdx.x < 2) counted[threadIdx.x] = 0;
+    if (first == 0) *a.ticket = 0;
+    if (by_sequence)
+        for (int64_t t = first; t < a.rows; t += step) of[t] = 0;
+    cl.sync();
+    uint32_t* sums = cl.map_shared_rank(counted, 0);
+    uint32_t targets = 0, filled = 0;
+    for (int64_t t0 = first - lane; t0 < a.rows; t0 += step) {
+        const int64_t t = t0 + lane;
+        const bool target = t < a.rows && a.targets[t] >= 0;
+        const int64_t s = a.offsets && target ? sequence_of(a.offsets, a.seqs, t) : 0;
+        const bool live = target && (!a.offsets || (s >= 0 && s < a.seqs));
+        targets += live;
+        const unsigned lives = __ballot_sync(~0u, live);
+        if (!by_sequence || !lives) continue;
+        // a warp's tokens are most often of one sequence
+        const int64_t b = live ? clamp_offset(a.offsets[s], 0, a.rows - 1) : 0, b0 = __shfl_sync(~0u, b, __ffs(lives) - 1);
+        if (__all_sync(~0u, !live || b == b0)) {
+            if (lane == 0) filled += atomicAdd(of + b0, (uint32_t)__popc(lives)) == 0;
+        } else if (live) {
+            filled += atomicAdd(of + b, 1u) == 0;
+        }
     }
+    targets = __reduce_add_sync(~0u, targets);
+    filled = __reduce_add_sync(~0u, filled);
+    if (lane == 0 && targets) atomicAdd(sums, targets);
+    if (lane == 0 && filled) atomicAdd(sums + 1, filled);
+    cl.sync();
+    if (threadIdx.x < 2) all[threadIdx.x] = sums[threadIdx.x];
     __syncthreads();
-    // sequences leave no gaps: what lies before the first and behind the last carries no loss
-    const int64_t begin = a.offsets ? clamp_offset(a.offsets[0], 0, a.rows) : 0;
-    const int64_t end = a.offsets ? clamp_offset(a.offsets[a.seqs], begin, a.rows) : a.rows;
-#pragma unroll 4
-    for (int64_t t = threadIdx.x; t < begin; t += kSetupThreads) a.w[t] = 0.0f;
-#pragma unroll 4
-    for (int64_t t = end + threadIdx.x; t < a.rows; t += kSetupThreads) a.w[t] = 0.0f;
-    if (a.offsets) {
-        for (int64_t s = warp; s < a.seqs; s += warps) {
-            const int64_t b = clamp_offset(a.offsets[s], 0, a.rows), e = clamp_offset(a.offsets[s + 1], b, a.rows);
-            int64_t n = 0;
-#pragma unroll 4
-            for (int64_t t = b + lane; t < e; t += 32) n += a.targets[t] >= 0;
-            n = warp_sum(n);
-            if (lane == 0 && n) {
-                atomicAdd(&total, (unsigned long long)n);
-                atomicAdd(&nonempty, 1ull);
-            }
+    const float tokens = (float)max(all[0], 1u), sequences = (float)max(all[1], 1u);
+    const float same = a.reduce == ZERO_REDUCE_TOKEN ? 1.0f / tokens : 1.0f;
+    for (int64_t t = first; t < a.rows; t += step) {
+        const int64_t s = a.offsets ? sequence_of(a.offsets, a.seqs, t) : 0;
+        if (a.offsets && (s < 0 || s >= a.seqs)) {  // in front of the first sequence or behind the last
+            a.w[t] = 0.0f;
+            continue;
         }
-    } else {
-        int64_t n = 0;
-#pragma unroll 4
-        for (int64_t t = threadIdx.x; t < a.rows; t += kSetupThreads) n += a.targets[t] >= 0;
-        n = warp_sum(n);
-        if (lane == 0) atomicAdd(&total, (unsigned long long)n);
+        float w = a.targets[t] >= 0 ? same : 0.0f;
+        if (by_sequence && w != 0.0f) w = 1.0f / (float)__ldcg(of + clamp_offset(a.offsets[s], 0, a.rows - 1)) / sequences;
+        a.w[t] = w;
+        a.adv[t] = a.advantages[a.per_sequence ? s : t];
+        a.loss[t] = NAN;  // until its row is done
     }
-    __syncthreads();
-    const float tokens = (float)(total ? total : 1), filled = (float)(nonempty ? nonempty : 1);
-    if (!a.offsets) {
-        const float w = a.reduce == ZERO_REDUCE_TOKEN ? 1.0f / tokens : 1.0f;
-#pragma unroll 4
-        for (int64_t t = threadIdx.x; t < a.rows; t += kSetupThreads) {
-            a.w[t] = a.targets[t] >= 0 ? w : 0.0f;
-            a.adv[t] = a.advantages[t];
-            a.loss[t] = NAN;  // until its row is done
-        }
-        return;
-    }
-    for (int64_t s = warp; s < a.seqs; s += warps) {
-        const int64_t b = clamp_offset(a.offsets[s], 0, a.rows), e = clamp_offset(a.offsets[s + 1], b, a.rows);
-        float w = a.reduce == ZERO_REDUCE_TOKEN ? 1.0f / tokens : 1.0f;
-        if (a.reduce == ZERO_REDUCE_SEQUENCE) {
-            int64_t n = 0;
-#pragma unroll 4
-            for (int64_t t = b + lane; t < e; t += 32) n += a.targets[t] >= 0;
-            n = warp_sum(n);
-            w = 1.0f / (float)(n ? n : 1) / filled;
-        }
-#pragma unroll 4
-        for (int64_t t = b + lane; t < e; t += 32) {
-            a.w[t] = a.targets[t] >= 0 ? w : 0.0f;
-            a.adv[t] = a.advantages[a.per_sequence ? s : t];
-            a.loss[t] = NAN;
-        }
-    }
+    cl.sync();  // no CTA leaves while another reads its sums
 }
 
 // What a token's loss takes, read ahead of its row's sums.
@@ -641,13 +641,14 @@ __global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
     }
     __syncthreads();
 
-    // The kernel before this one sets up the weights; it was itself launched behind the logits'
-    // producer, so logits and targets may be read at once, and the rest after it.
+    // The kernel before this one sets up the weights; it lets this one start once it has waited for
+    // the logits' producer, so logits and targets may be read at once, and the rest after it.
     let_next_kernel_start();
+    int64_t n = 0;  // rows taken
     if (threadIdx.x >= kThreads) {
         Slot slot;
         bool ok = true;
-        for (int64_t n = 0;; ++n) {
+        for (;; ++n) {
             int64_t t = first + n * clusters;
             if (size == 1 && n > 0) {
                 if (n == 1) wait_for_kernel_before();
@@ -665,7 +666,7 @@ __global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
                 row_y[n & 1] = y;
                 const float x_y = y >= 0 && y < a.vocab ? widen(x[y]) : NAN;
                 row_x[n & 1] = x_y;
-                row_fast[n & 1] = y >= 0 && fast_row<H>(x, a.vocab, x_y);
+                row_fast[n & 1] = y >= 0 && fast_row<H>(x, a.vocab, x_y, a.k);
                 mbar_arrive(row_full + 8 * (n & 1));
             }
             if (t < 0) break;
@@ -680,14 +681,18 @@ __global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
                     slot.next(slots);
                 }
             }
+            __syncwarp();
             if (size > 1) cg::this_cluster().sync();  // the consumers' cluster_join
         }
     } else {
         uint32_t taken = 0;
         Slot begin;  // of the row at hand
         const uint4* parts = reinterpret_cast<const uint4*>(smem);
-        for (int64_t n = 0;; ++n) {
-            const bool got = mbar_wait(row_full + 8 * (n & 1), (uint32_t)(n >> 1) & 1, &gave_up);
+        for (;; ++n) {
+            // Not left early where another wait gave up: the producer announces an end even then, and
+            // all warps have to take the same rows.
+            bool got = mbar_try(row_full + 8 * (n & 1), (uint32_t)(n >> 1) & 1);
+            for (int i = 0; i < 4 * kWaitLimit && !got; ++i) got = mbar_try(row_full + 8 * (n & 1), (uint32_t)(n >> 1) & 1);
             const int64_t t = got ? row_at[n & 1] : -1, y = row_y[n & 1];
             const float x_y = row_x[n & 1];
             const bool try_fast = row_fast[n & 1];
@@ -789,9 +794,18 @@ __global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
             ++taken;
         }
     }
-    if (size > 1) {  // no CTA leaves while another reads its sums
-        __syncwarp();
-        cg::this_cluster().sync();
+    __syncwarp();
+    if (*(volatile int*)&gave_up)  // leave no copy in flight behind: they take microseconds, this a millisecond
+        for (int j = 0; j < 1000; ++j) __nanosleep(1000);
+    if (size > 1) {
+        // after giving up: keep in step with the other CTAs, which get no sums from this one
+        for (; first + n * clusters < a.rows; ++n) {
+            if (a.targets[first + n * clusters] < 0) continue;
+            if (threadIdx.x == 0) mine[0].s = mine[1].s = NAN;
+            __syncwarp();
+            cg::this_cluster().sync();
+        }
+        cg::this_cluster().sync();  // no CTA leaves while another reads its sums
     }
 }
 
@@ -849,13 +863,20 @@ __global__ void __launch_bounds__(kRowThreads) k_policy_tokens(const PolicyToken
     }
 }
 
+// The means, in a fixed order.
 __global__ void __launch_bounds__(kSetupThreads) k_policy_finish(const PolicyTokens a) {
     __shared__ Sum sm[kSetupThreads / 32];
+    __shared__ struct {
+        float loss[2], kl[2];
+        uint32_t targets, clipped;
+    } mine;
+    const cg::cluster_group cl = cg::this_cluster();
+    if (threadIdx.x == 0) mine.targets = mine.clipped = 0;
     wait_for_kernel_before();
     Sum loss, kl;
-    int clipped = 0, n = 0;
+    uint32_t clipped = 0, n = 0;
 #pragma unroll 4
-    for (int64_t t = threadIdx.x; t < a.rows; t += kSetupThreads) {
+    for (int64_t t = (int64_t)blockIdx.x * kSetupThreads + threadIdx.x; t < a.rows; t += (int64_t)gridDim.x * kSetupThreads) {
         loss.add(a.w[t] != 0.0f ? a.loss[t] : 0.0f);
         kl.add(a.kl[t]);
         clipped += a.clipped[t] != 0.0f;
@@ -863,22 +884,36 @@ __global__ void __launch_bounds__(kSetupThreads) k_policy_finish(const PolicyTok
     }
     loss = cta_sum<kSetupThreads>(loss, sm);
     kl = cta_sum<kSetupThreads>(kl, sm);
-    __shared__ unsigned long long total, all_clipped;
-    if (threadIdx.x == 0) total = all_clipped = 0;
-    __syncthreads();
     clipped = __reduce_add_sync(~0u, clipped);
     n = __reduce_add_sync(~0u, n);
     if ((threadIdx.x & 31) == 0) {
-        atomicAdd(&total, (unsigned long long)n);
-        atomicAdd(&all_clipped, (unsigned long long)clipped);
+        atomicAdd(&mine.targets, n);
+        atomicAdd(&mine.clipped, clipped);
     }
-    __syncthreads();
     if (threadIdx.x == 0) {
-        const double tokens = total ? (double)total : 1.0;
+        mine.loss[0] = loss.hi;
+        mine.loss[1] = loss.lo;
+        mine.kl[0] = kl.hi;
+        mine.kl[1] = kl.lo;
+    }
+    cl.sync();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        n = mine.targets;
+        clipped = mine.clipped;
+#pragma unroll 1
+        for (unsigned i = 1; i < gridDim.x; ++i) {
+            const auto* other = cl.map_shared_rank(&mine, i);
+            loss.add(Sum{other->loss[0], other->loss[1]});
+            kl.add(Sum{other->kl[0], other->kl[1]});
+            n += other->targets;
+            clipped += other->clipped;
+        }
+        const double tokens = n ? (double)n : 1.0;
         *a.out_loss = (float)loss.value();
         *a.out_kl = (float)(kl.value() / tokens);
-        *a.out_clip = (float)((double)all_clipped / tokens);
+        *a.out_clip = (float)((double)clipped / tokens);
     }
+    cl.sync();  // no CTA leaves while the first reads its sums
 }
 
 // ---------------------------------------------------------------------------------------
@@ -960,6 +995,13 @@ FusedPlan fused_plan(const zero_logits* x, int sms) {
     return f;
 }
 
+// CTAs of the kernels over tokens alone: a cluster of eight begins 3 us later than one CTA, which
+// it has made up at 2048 tokens (4096 of 50257 in 123 us against 129).
+int token_ctas(int64_t rows) { return rows <= 2048 ? 1 : 8; }
+int launch_finish(const PolicyTokens& p, cudaStream_t s) {
+    return launch_linked(k_policy_finish, (unsigned)token_ctas(p.rows), kSetupThreads, 0, token_ctas(p.rows), s, p);
+}
+
 int launch_token_logp(const zero_logits* x, const float* weight, float* logp, float* lse, float* entropy, float* cleared,
                       uint32_t* counter, int sms, cudaStream_t s) {
     if (x->rows == 0) return ZERO_OK;
@@ -1009,7 +1051,7 @@ int launch_policy_rows(const zero_logits* x, const FusedPlan& f, const PolicyTok
         return f.warps == kFusedWarps ? launch_fused<T, kFusedWarps>(x, f, p, q, sms, s) : launch_fused<T, kFusedWarpsSmall>(x, f, p, q, sms, s);
     });
     if (rc) return rc;
-    return launch_linked(k_policy_finish, 1, kSetupThreads, 0, 1, s, p);
+    return launch_finish(p, s);
 }
 
 int check_dlogits(const zero_logits* x, const void* dx, int64_t dstride) {
@@ -1166,8 +1208,7 @@ extern "C" int zero_policy_loss(const zero_logits* x, const zero_policy* p, void
     a.per_sequence = p->per_sequence;
     const int sms = d.sm_count();
     if (x->rows > 0) {
-        k_policy_setup<<<1, kSetupThreads, 0, s>>>(a);
-        if ((rc = launched())) return rc;
+        if ((rc = launch_linked(k_policy_setup, (unsigned)token_ctas(x->rows), kSetupThreads, 0, token_ctas(x->rows), s, a))) return rc;
         const FusedPlan f = fused_plan(x, sms);
         if (f.size) return launch_policy_rows(x, f, a, p, sms, s);
         if ((rc = launch_token_logp(x, a.w, p->logp, a.lse, p->entropy, nullptr, nullptr, sms, s))) return rc;
@@ -1176,6 +1217,5 @@ extern "C" int zero_policy_loss(const zero_logits* x, const zero_policy* p, void
         rc = launch_token_grad(x, a.w, p->logp, a.lse, p->entropy, a.g, a.entropy_coef != 0.0f ? a.h : nullptr, p->dlogits, p->dstride, sms, s);
         if (rc) return rc;
     }
-    k_policy_finish<<<1, kSetupThreads, 0, s>>>(a);
-    return launched();
+    return launch_finish(a, s);
 }
