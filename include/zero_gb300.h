@@ -680,7 +680,8 @@ int zero_token_logp_backward(const zero_logits* x, const float* logp, const floa
 /* Preference loss (paired log ratios). Tokens are packed; sequence s is tokens
  * [offsets[s], offsets[s + 1]), and pair i is sequence 2i (chosen) against 2i + 1 (rejected).
  *   d_s = sum over the sequence's tokens with a target of (logp_t - ref_logp[t]), divided by
- *         their number where `average` is 1;  m_i = d_2i - d_2i+1
+ *         their number where `average` is 1;  m_i = d_2i - d_2i+1. The sums take logp_t as it was
+ *         before its rounding to fp32.
  *   ZERO_PREF_SIGMOID  -(1 - e) log sigmoid(beta m) - e log sigmoid(-beta m), e = label_smoothing
  *   ZERO_PREF_HINGE    max(0, 1 - beta m)          ZERO_PREF_IPO  (m - 1 / (2 beta))^2
  * loss = the mean over pairs. */

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kLinearThreads, 1)
 template <bool ENTROPY>
 __device__ __forceinline__ void finish(const LinearArgs& a, int64_t t, int64_t y, const RowStat& s, bool gave_up, float* logp, float* lse,
                                        float* entropy) {
-    RowResult r = {0.0f, 0.0f, 0.0f};
+    RowResult r = {0.0f, 0.0f, 0.0f, 0.0f};
     if (y >= 0) {
         r = finish_row<ENTROPY>(s, y < a.vocab ? a.zy[t] : NAN, a.k, a.inv_t);
         if (y >= a.vocab) r.logp = NAN;

@@ -148,12 +148,12 @@ __device__ __forceinline__ int64_t row_of(int size) {
 
 // Forward, bound by reading the logits once: `size` CTAs per row (a cluster; several where there
 // are few rows), each thread kUnroll vectors at a time. 4096 fp16 tokens, a quarter of them masked:
-// 53.3 us, 309 MB, 87% of the copy peak (128 or 512 threads and 2 or 6 vectors lie within 5%); one
-// token 3.9 us, over eight CTAs. Rows of up to kShortRow bytes go to a warp each: a CTA's joining
+// 51.6 us, 309 MB, 90% of the copy peak (128 or 512 threads and 2 or 6 vectors lie within 5%); one
+// token 3.7 us, over eight CTAs. Rows of up to kShortRow bytes go to a warp each: a CTA's joining
 // would take longer than their reading.
 template <class T, bool ENTROPY, int THREADS>
 __global__ void __launch_bounds__(kRowThreads, 5)
-    k_token_logp(const Rows<T> a, int size, float* logp, float* lse, float* entropy, float* cleared, uint32_t* counter) {
+    k_token_logp(const Rows<T> a, int size, float* logp, float* lse, float* entropy, float* low, float* cleared, uint32_t* counter) {
     __shared__ RowStat sm[kRowThreads / 32], mine;
     wait_for_kernel_before();
     let_next_kernel_start();
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kRowThreads, 5)
     if (THREADS == 32 && t >= a.rows) return;
     const int rank = THREADS == 32 ? 0 : (int)(blockIdx.x % size);
     const int64_t y = live_target(a, t);
-    RowResult r = {0.0f, 0.0f, 0.0f};
+    RowResult r = {0.0f, 0.0f, 0.0f, 0.0f};
     const bool first = place_in_group<THREADS>() == 0 && rank == 0;
     if (y >= 0) {
         const T* x = a.x + t * a.stride;
@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kRowThreads, 5)
         logp[t] = r.logp;
         lse[t] = r.lse;
         if (ENTROPY) entropy[t] = r.entropy;
+        if (low) low[t] = r.low;
         if (cleared) cleared[t] = 0.0f;
         if (counter && t == 0) *counter = 0;
     }
@@ -331,7 +332,9 @@ __device__ __forceinline__ int64_t clamp_offset(int64_t o, int64_t lo, int64_t h
 // ---------------------------------------------------------------------------------------
 // Preference loss, between the forward kernel and the gradient's: a CTA per pair sums its two
 // sequences and spreads the gradient over their tokens. g holds 0 for the tokens of no pair
-// (written before). The loss of a pair needs all of its rows, so the logits are read twice: 8192
+// (written before). Sequences sum what their log-probabilities were before they were rounded to
+// fp32 (low): a reward is the small difference of such sums, and 100 roundings of numbers near 10
+// are 3e-6 of it. The loss of a pair needs all of its rows, so the logits are read twice: 8192
 // tokens in 16 pairs, a quarter masked, take 326 us, 94% of the copy peak on their 2.06 GB. One
 // kernel that follows each pair's forward rows with its gradient rows, to read them from L2, took
 // 450 us and more: the L2 gave back 6%, handing out rows cost 20%.
@@ -339,7 +342,7 @@ __device__ __forceinline__ int64_t clamp_offset(int64_t o, int64_t lo, int64_t h
 struct PairArgs {
     const int64_t* targets;
     const int64_t* offsets;
-    const float* logp;
+    const float *logp, *low;
     const float* ref;
     float* g;
     float *pair_loss, *chosen, *rejected, *loss;
@@ -366,9 +369,10 @@ __global__ void __launch_bounds__(kRowThreads) k_pairs(const PairArgs a) {
         int targets = 0;
 #pragma unroll 4
         for (int64_t t = lo + id; t < hi; t += kHalf) {
-            const float lp = a.logp[t], ref = a.ref ? a.ref[t] : 0.0f;
+            const float lp = a.logp[t], low = a.low[t], ref = a.ref ? a.ref[t] : 0.0f;
             if (a.targets[t] < 0) continue;
             sum.add(lp);
+            sum.lo += low;
             if (a.ref) sum.add(-ref);
             ++targets;
         }
@@ -585,7 +589,7 @@ __device__ __forceinline__ TokenLoss policy_token(const PolicyTokens& a, const T
 // again. Two CTAs per SM, each with one slice: a producer warp refills a part of it with the next
 // row as soon as the gradient of this one has been taken from it, so that copies run beside
 // everything else. Rows are handed out one by one (some carry no loss and cost half). 8192 bf16
-// tokens, a quarter masked, with entropy bonus: 237 us the whole call, 1.44 GB, 91% of the copy peak
+// tokens, a quarter masked, with entropy bonus: 232 us the whole call, 1.44 GB, 93% of the copy peak
 // (two passes over the logits: 383 us). Seven warps compute: with ten, and four parts to a slice,
 // 252 us, since registers then spill; with fifteen 325.
 constexpr int kChunks = 2, kSlots = 8;  // parts of a slice; most parts that shared memory holds
@@ -741,7 +745,7 @@ __global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
             if (!ok || *(volatile int*)&gave_up) st.s = NAN;  // a copy did not come: no result
             st = cluster_join<H>(st, size, a.k, mine + (taken & 1));
             if (threadIdx.x == 0) {
-                RowResult r = {0.0f, 0.0f, 0.0f};
+                RowResult r = {0.0f, 0.0f, 0.0f, 0.0f};
                 TokenLoss l = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
                 if (in.w != 0.0f) {
                     r = finish_row<H>(st, x_y, a.k, (float)a.inv_t);
@@ -822,7 +826,7 @@ __global__ void __launch_bounds__(kRowThreads)
     const int64_t y = live_target(a, t);
     T* out = dx + t * dstride;
     const T* x = a.x + t * a.stride;
-    RowResult r = {0.0f, 0.0f, 0.0f};
+    RowResult r = {0.0f, 0.0f, 0.0f, 0.0f};
     TokenLoss l = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     RowStat st = empty_stat();
     float x_y = NAN;
@@ -1002,18 +1006,18 @@ int launch_finish(const PolicyTokens& p, cudaStream_t s) {
     return launch_linked(k_policy_finish, (unsigned)token_ctas(p.rows), kSetupThreads, 0, token_ctas(p.rows), s, p);
 }
 
-int launch_token_logp(const zero_logits* x, const float* weight, float* logp, float* lse, float* entropy, float* cleared,
-                      uint32_t* counter, int sms, cudaStream_t s) {
+int launch_token_logp(const zero_logits* x, const float* weight, float* logp, float* lse, float* entropy, float* low,
+                      float* cleared, uint32_t* counter, int sms, cudaStream_t s) {
     if (x->rows == 0) return ZERO_OK;
     return by_type(x->type, [&](auto tag) {
         using T = decltype(tag);
         const Rows<T> a = rows_of<T>(x, weight);
         if (short_rows(x, sms))
             return launch_linked(entropy ? k_token_logp<T, true, 32> : k_token_logp<T, false, 32>, short_grid(x), kRowThreads, 0, 1, s, a, 1,
-                                 logp, lse, entropy, cleared, counter);
+                                 logp, lse, entropy, low, cleared, counter);
         const int size = ctas_per_row(x, sms);
         return launch_linked(entropy ? k_token_logp<T, true, kRowThreads> : k_token_logp<T, false, kRowThreads>, (unsigned)(x->rows * size),
-                             kRowThreads, 0, size, s, a, size, logp, lse, entropy, cleared, counter);
+                             kRowThreads, 0, size, s, a, size, logp, lse, entropy, low, cleared, counter);
     });
 }
 
@@ -1076,7 +1080,7 @@ extern "C" int zero_token_logp(const zero_logits* x, float* logp, float* lse, fl
     d.need(lse, 4);
     d.optional(entropy, 4);
     if (d.rc) return d.rc;
-    return launch_token_logp(x, nullptr, logp, lse, entropy, nullptr, nullptr, d.sm_count(), (cudaStream_t)stream);
+    return launch_token_logp(x, nullptr, logp, lse, entropy, nullptr, nullptr, nullptr, d.sm_count(), (cudaStream_t)stream);
 }
 
 extern "C" int zero_token_logp_backward(const zero_logits* x, const float* logp, const float* lse, const float* entropy,
@@ -1099,7 +1103,7 @@ extern "C" int zero_token_logp_backward(const zero_logits* x, const float* logp,
 
 extern "C" int64_t zero_preference_workspace(int64_t rows) {
     if (rows < 0 || rows > INT64_MAX / 64) return -1;
-    return 2 * 4 * round_up(rows, 4) + 64;
+    return 3 * 4 * round_up(rows, 4) + 64;
 }
 
 extern "C" int zero_preference_loss(const zero_logits* x, const zero_preference* p, void* workspace, int64_t workspace_bytes,
@@ -1129,15 +1133,16 @@ extern "C" int zero_preference_loss(const zero_logits* x, const zero_preference*
     cudaStream_t s = (cudaStream_t)stream;
     float* lse = (float*)workspace;
     float* g = lse + round_up(x->rows, 4);
-    uint32_t* done = (uint32_t*)(g + round_up(x->rows, 4));
+    float* low = g + round_up(x->rows, 4);
+    uint32_t* done = (uint32_t*)(low + round_up(x->rows, 4));
     const int sms = d.sm_count();
-    const PairArgs a = {x->targets, p->offsets, p->logp, p->ref_logp, g, p->pair_loss, p->chosen_reward, p->rejected_reward, p->loss, done,
+    const PairArgs a = {x->targets, p->offsets, p->logp, low, p->ref_logp, g, p->pair_loss, p->chosen_reward, p->rejected_reward, p->loss, done,
                         x->rows, p->pairs, p->beta, 0.5 / p->beta, p->kind == ZERO_PREF_SIGMOID ? p->label_smoothing : 0.0, p->kind, p->average};
     if (x->rows == 0) {  // no forward kernel that clears the counter
         const cudaError_t e = cudaMemsetAsync(done, 0, 4, s);
         if (e != cudaSuccess) return record_cuda_error(e);
     }
-    if ((rc = launch_token_logp(x, nullptr, p->logp, lse, nullptr, g, done, sms, s))) return rc;
+    if ((rc = launch_token_logp(x, nullptr, p->logp, lse, nullptr, low, g, done, sms, s))) return rc;
     if ((rc = launch_linked(k_pairs, (unsigned)std::min<int64_t>(p->pairs, 1 << 20), kRowThreads, 0, 1, s, a))) return rc;
     return launch_token_grad(x, nullptr, p->logp, lse, nullptr, g, nullptr, p->dlogits, p->dstride, sms, s);
 }
@@ -1211,7 +1216,7 @@ extern "C" int zero_policy_loss(const zero_logits* x, const zero_policy* p, void
         if ((rc = launch_linked(k_policy_setup, (unsigned)token_ctas(x->rows), kSetupThreads, 0, token_ctas(x->rows), s, a))) return rc;
         const FusedPlan f = fused_plan(x, sms);
         if (f.size) return launch_policy_rows(x, f, a, p, sms, s);
-        if ((rc = launch_token_logp(x, a.w, p->logp, a.lse, p->entropy, nullptr, nullptr, sms, s))) return rc;
+        if ((rc = launch_token_logp(x, a.w, p->logp, a.lse, p->entropy, nullptr, nullptr, nullptr, sms, s))) return rc;
         k_policy_tokens<<<(int)std::min<int64_t>((x->rows + kRowThreads - 1) / kRowThreads, 1024), kRowThreads, 0, s>>>(a, p->logp, p->entropy);
         if ((rc = launched())) return rc;
         rc = launch_token_grad(x, a.w, p->logp, a.lse, p->entropy, a.g, a.entropy_coef != 0.0f ? a.h : nullptr, p->dlogits, p->dstride, sms, s);

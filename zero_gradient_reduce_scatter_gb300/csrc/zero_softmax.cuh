@@ -312,6 +312,7 @@ __device__ __forceinline__ RowStat group_join(RowStat a, Scale k, RowStat* sm, i
 
 struct RowResult {
     float logp, lse, entropy;
+    float low;  // what logp was short of before it was rounded
 };
 
 // pow2 errs low by this share on average (measured over 2^24 arguments below 0), and so does a sum
@@ -328,7 +329,7 @@ __device__ __forceinline__ RowResult finish_row(const RowStat& a, float x_y, Sca
     RowResult r;
     if (a.s == 0.0f) {  // nothing but -inf
         r.logp = r.lse = -INFINITY;
-        r.entropy = 0.0f;
+        r.entropy = r.low = 0.0f;
         return r;
     }
     constexpr float kLn2Hi = 2839.0f / 4096.0f, kLn2Lo = 3.1946184945309e-5f;
@@ -339,7 +340,11 @@ __device__ __forceinline__ RowResult finish_row(const RowStat& a, float x_y, Sca
     const float mean = ENTROPY ? a.q / a.s * kLn2 : 0.0f, low = k.lo / k.c;
     const float hi = n * kLn2Hi, lo = logf(f) + fmaf(n, kLn2Lo, fmaf(low, mean, kPow2Low * (1.0f - 1.0f / a.s)));
     const float base = base_of(a.m);
-    r.logp = (x_y - base) * inv_t - hi - lo;
+    const float top = (x_y - base) * inv_t - hi;
+    r.logp = __fsub_rn(top, lo);
+    const float z = __fsub_rn(r.logp, top);
+    r.low = __fsub_rn(__fsub_rn(top, __fsub_rn(r.logp, z)), __fadd_rn(lo, z));
+    if (!(fabsf(r.logp) < INFINITY)) r.low = 0.0f;
     r.lse = fmaf(base, inv_t, hi) + lo;
     r.entropy = hi - fmaf(mean, low, mean) + lo;
     return r;
