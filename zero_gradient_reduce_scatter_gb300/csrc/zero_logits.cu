@@ -70,10 +70,10 @@ struct Slice {
 template <int THREADS>
 __device__ __forceinline__ int place_in_group() { return THREADS == 32 ? threadIdx.x & 31 : threadIdx.x; }
 
-// This thread's vectors of n, kUnroll at a time: `load` first for all of them, then `use`.
+// This thread's vectors of n, from its place `i` on, kUnroll at a time: `load` first for all of them,
+// then `use`.
 template <int THREADS, class L, class U>
-__device__ __forceinline__ void for_vectors(int n, L load, U use) {
-    int i = place_in_group<THREADS>();
+__device__ __forceinline__ void for_vectors(int n, L load, U use, int i = place_in_group<THREADS>()) {
     for (; i + (kUnroll - 1) * THREADS < n; i += kUnroll * THREADS) {
         uint4 q[kUnroll];
 #pragma unroll
@@ -91,6 +91,33 @@ __device__ __forceinline__ void for_vectors(int n, L load, U use) {
             if (i + u * THREADS < n) use(i + u * THREADS, q[u]);
     }
 }
+
+// The part of a row that a thread reads first: its first vectors and its elements at the row's ends,
+// on their way at once with whatever else the row waits for.
+template <class T, int THREADS>
+struct RowStart {
+    uint4 q[kUnroll];
+    T head, tail;
+
+    template <class L>
+    __device__ __forceinline__ RowStart(const Slice<T>& s, const T* x, L load) {
+        const int id = place_in_group<THREADS>();
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (id + u * THREADS < s.n) q[u] = load(id + u * THREADS);
+        if (id < s.head) head = x[id];
+        if (id < s.tail) tail = x[s.tail_at + id];
+    }
+    // for_vectors over all of the thread's vectors
+    template <class L, class U>
+    __device__ __forceinline__ void vectors(int n, L load, U use) const {
+        const int id = place_in_group<THREADS>();
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (id + u * THREADS < n) use(id + u * THREADS, q[u]);
+        for_vectors<THREADS>(n, load, use, id + kUnroll * THREADS);
+    }
+};
 
 // The sums of all CTAs of a cluster (at most 8), joined in a fixed order; valid everywhere. `mine` is
 // shared memory of this CTA, which stays as it is until the cluster's next barrier. A lane reads a
@@ -118,16 +145,20 @@ __device__ __forceinline__ bool fast_row(const T* x, int64_t vocab, float x_y, S
 // The sums of a row, or of a CTA's share of it, by the THREADS that take it: a CTA's (joined through
 // sm, THREADS / 32 entries), or one warp's, which takes the whole row and needs no sm.
 template <int THREADS, bool ENTROPY, class T>
-__device__ __forceinline__ RowStat row_sums(const T* x, int64_t vocab, float x_y, Scale k, int rank, int size, RowStat* sm) {
+__device__ __forceinline__ RowStat row_sums(const T* x, int64_t vocab, int64_t y, float* x_target, Scale k, int rank, int size, RowStat* sm) {
     const Slice<T> s(x, vocab, rank, size);
     const int id = place_in_group<THREADS>();
+    auto load = [&](int i) { return THREADS == 32 ? __ldg(s.v + i) : load_once(s.v + i); };
+    const RowStart<T, THREADS> start(s, x, load);
+    const float x_y = *x_target = y < vocab ? widen(x[y]) : NAN;
     auto sums = [&](auto checked) {
         constexpr bool kChecked = decltype(checked)::value;
         Sums<T, ENTROPY, kChecked> run(k, x_y);
-        for_vectors<THREADS>(s.n, [&](int i) { return THREADS == 32 ? __ldg(s.v + i) : load_once(s.v + i); },
-                             [&](int, const uint4& q) { run.add(q); });
-        if (id < s.head) run.add_one(widen(x[id]));
-        if (id < s.tail) run.add_one(widen(x[s.tail_at + id]));
+        auto use = [&](int, const uint4& q) { run.add(q); };
+        if (kChecked) for_vectors<THREADS>(s.n, load, use);
+        else start.vectors(s.n, load, use);
+        if (id < s.head) run.add_one(widen(start.head));
+        if (id < s.tail) run.add_one(widen(start.tail));
         if constexpr (THREADS == 32) return warp_join<ENTROPY, kChecked>(run.stat(), k);
         else return group_join<ENTROPY, kChecked, THREADS / 32>(run.stat(), k, sm, 0);
     };
@@ -165,8 +196,8 @@ __global__ void __launch_bounds__(kRowThreads, 5)
     const bool first = place_in_group<THREADS>() == 0 && rank == 0;
     if (y >= 0) {
         const T* x = a.x + t * a.stride;
-        const float x_y = y < a.vocab ? widen(x[y]) : NAN;
-        RowStat st = row_sums<THREADS, ENTROPY>(x, a.vocab, x_y, a.k, rank, size, sm);
+        float x_y;
+        RowStat st = row_sums<THREADS, ENTROPY>(x, a.vocab, y, &x_y, a.k, rank, size, sm);
         if (THREADS != 32) st = cluster_join<ENTROPY>(st, size, a.k, &mine);
         if (first) {
             r = finish_row<ENTROPY>(st, x_y, a.k, (float)a.inv_t);
@@ -274,16 +305,14 @@ __device__ __forceinline__ void write_ends(const Slice<T>& s, const GradRow& r, 
 // Backward, bound by reading the logits and writing their gradient: 2048 bf16 rows in 62.9 us, 412
 // MB, 98% of the copy peak. Where the gradient's rows have another alignment than the logits',
 // elements are taken one at a time.
-template <int THREADS, bool H, class T>
-__device__ __forceinline__ void write_grad(float c, const GradRow& r, const T* x, T* out, int64_t vocab, int y, float x_y, int rank, int size) {
-    const Slice<T> s(x, vocab, rank, size);
+template <int THREADS, bool H, class T, class L>
+__device__ __forceinline__ void write_grad(float c, const GradRow& r, const Slice<T>& s, const RowStart<T, THREADS>& start, const T* x, T* out, L load,
+                                           int y, float x_y) {
     const int id = place_in_group<THREADS>();
-    const float x_head = id < s.head ? widen(x[id]) : 0.0f;
-    const float x_tail = id < s.tail ? widen(x[s.tail_at + id]) : 0.0f;
     if (same_alignment(x, out)) {
         const GradVector<T, H> grad(r, c);
         uint4* to = reinterpret_cast<uint4*>(out + s.first);
-        for_vectors<THREADS>(s.n, [&](int i) { return __ldcs(s.v + i); }, [&](int i, const uint4& q) { __stcs(to + i, grad(q)); });
+        start.vectors(s.n, load, [&](int i, const uint4& q) { __stcs(to + i, grad(q)); });
         // the thread that wrote the target's vector sets the target right
         const int at = y - s.first;
         if (at >= 0 && at < s.n * kVec<T> && at / kVec<T> % THREADS == id) out[y] = narrow<T>(grad_term<H>(r, x_y, c, true));
@@ -291,7 +320,7 @@ __device__ __forceinline__ void write_grad(float c, const GradRow& r, const T* x
         for (int j = s.first + id; j < s.first + s.n * kVec<T>; j += THREADS)
             out[j] = narrow<T>(grad_term<H>(r, widen(x[j]), c, j == y));
     }
-    write_ends<T, H>(s, r, id, x_head, x_tail, out, c, y);
+    write_ends<T, H>(s, r, id, id < s.head ? widen(start.head) : 0.0f, id < s.tail ? widen(start.tail) : 0.0f, out, c, y);
 }
 
 template <class T, bool H, int THREADS>
@@ -305,21 +334,25 @@ __global__ void __launch_bounds__(kRowThreads)
     if (THREADS == 32 && t < 0) return;
     const int rank = THREADS == 32 ? 0 : (int)(blockIdx.x % size);
     const int64_t y = live_target(a, t);
-    const float g = y < 0 ? 0.0f : dlogp[t], h = y < 0 || !H ? 0.0f : dentropy[t];
+    const float row_logp = logp[t], row_lse = lse[t], row_entropy = H ? entropy[t] : 0.0f, row_g = dlogp[t], row_h = H ? dentropy[t] : 0.0f;
+    const float g = y < 0 ? 0.0f : row_g, h = y < 0 ? 0.0f : row_h;
     T* out = dx + t * dstride;
-    if ((g == 0.0f && h == 0.0f) || lse[t] == -INFINITY) {
+    if ((g == 0.0f && h == 0.0f) || row_lse == -INFINITY) {
         zero_row<T, THREADS>(out, a.vocab, rank, size);
         return;
     }
     const T* x = a.x + t * a.stride;
+    const Slice<T> s(x, a.vocab, rank, size);
+    auto load = [&](int i) { return __ldcs(s.v + i); };
+    const RowStart<T, THREADS> start(s, x, load);
     const float x_y = y < a.vocab ? widen(x[y]) : NAN;
-    const GradRow r = grad_row(y < a.vocab ? g : NAN, h, x_y, logp[t], lse[t], h != 0.0f ? entropy[t] : 0.0f, a.inv_t);
+    const GradRow r = grad_row(y < a.vocab ? g : NAN, h, x_y, row_logp, row_lse, h != 0.0f ? row_entropy : 0.0f, a.inv_t);
     if (out == x) {  // the target's logit is read before any thread writes it
         if (THREADS == 32) __syncwarp();
         else if (size > 1) cg::this_cluster().sync();
         else __syncthreads();
     }
-    write_grad<THREADS, H>(a.c, r, x, out, a.vocab, place_of(y, a.vocab), x_y, rank, size);
+    write_grad<THREADS, H>(a.c, r, s, start, x, out, load, place_of(y, a.vocab), x_y);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -832,8 +865,7 @@ __global__ void __launch_bounds__(kRowThreads)
     float x_y = NAN;
     if (y >= 0) {
         const TokenIn in(p, t);
-        x_y = y < a.vocab ? widen(x[y]) : NAN;
-        st = row_sums<32, H>(x, a.vocab, x_y, a.k, 0, 1, nullptr);
+        st = row_sums<32, H>(x, a.vocab, y, &x_y, a.k, 0, 1, nullptr);
         r = finish_row<H>(st, x_y, a.k, (float)a.inv_t);
         if (y >= a.vocab) r.logp = NAN;
         l = policy_token(p, in, r.logp, r.entropy);
@@ -850,8 +882,11 @@ __global__ void __launch_bounds__(kRowThreads)
         return;
     }
     const GradRow grad = grad_row(l.g, l.h, st, r.entropy, a.inv_t);
+    const Slice<T> s(x, a.vocab, 0, 1);
+    auto load = [&](int i) { return __ldcs(s.v + i); };
+    const RowStart<T, 32> start(s, x, load);
     __syncwarp();  // the row's ends and its target are read before any lane writes
-    write_grad<32, H>(H ? a.k.c : a.c, grad, x, out, a.vocab, place_of(y, a.vocab), x_y, 0, 1);
+    write_grad<32, H>(H ? a.k.c : a.c, grad, s, start, x, out, load, place_of(y, a.vocab), x_y);
 }
 
 __global__ void __launch_bounds__(kRowThreads) k_policy_tokens(const PolicyTokens a, const float* logp, const float* entropy) {
