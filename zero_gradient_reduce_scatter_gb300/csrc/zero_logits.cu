@@ -853,19 +853,19 @@ __global__ void __launch_bounds__(kRowThreads)
     k_policy_short(const Rows<T> a, const PolicyTokens p, float* logp, float* entropy, T* dx, int64_t dstride) {
     let_next_kernel_start();
     const int64_t t = row_of<32>(1);
-    wait_for_kernel_before();
     if (t >= a.rows) return;
     const int lane = threadIdx.x & 31;
-    const int64_t y = live_target(a, t);
+    const int64_t y = a.targets[t];  // these and the logits may be read at once, as in k_policy_rows
     T* out = dx + t * dstride;
     const T* x = a.x + t * a.stride;
     RowResult r = {0.0f, 0.0f, 0.0f, 0.0f};
     TokenLoss l = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     RowStat st = empty_stat();
     float x_y = NAN;
-    if (y >= 0) {
-        const TokenIn in(p, t);
-        st = row_sums<32, H>(x, a.vocab, y, &x_y, a.k, 0, 1, nullptr);
+    if (y >= 0) st = row_sums<32, H>(x, a.vocab, y, &x_y, a.k, 0, 1, nullptr);
+    wait_for_kernel_before();
+    const TokenIn in(p, t);
+    if (in.w != 0.0f) {
         r = finish_row<H>(st, x_y, a.k, (float)a.inv_t);
         if (y >= a.vocab) r.logp = NAN;
         l = policy_token(p, in, r.logp, r.entropy);
@@ -1086,7 +1086,7 @@ int launch_policy_rows(const zero_logits* x, const FusedPlan& f, const PolicyTok
         using T = decltype(tag);
         if (short_rows(x, sms))
             return launch_linked(q->entropy_coef != 0.0 ? k_policy_short<T, true> : k_policy_short<T, false>, short_grid(x), kRowThreads, 0, 1, s,
-                                 rows_of<T>(x, p.w), p, q->logp, q->entropy, (T*)q->dlogits, q->dstride);
+                                 rows_of<T>(x, nullptr), p, q->logp, q->entropy, (T*)q->dlogits, q->dstride);
         return f.warps == kFusedWarps ? launch_fused<T, kFusedWarps>(x, f, p, q, sms, s) : launch_fused<T, kFusedWarpsSmall>(x, f, p, q, sms, s);
     });
     if (rc) return rc;
