@@ -179,8 +179,8 @@ __device__ __forceinline__ int64_t row_of(int size) {
 
 // Forward, bound by reading the logits once: `size` CTAs per row (a cluster; several where there
 // are few rows), each thread kUnroll vectors at a time. 4096 fp16 tokens, a quarter of them masked:
-// 51.6 us, 309 MB, 90% of the copy peak (128 or 512 threads and 2 or 6 vectors lie within 5%); one
-// token 3.7 us, over eight CTAs. Rows of up to kShortRow bytes go to a warp each: a CTA's joining
+// 50.4 us, 309 MB, 92% of the copy peak (128 or 512 threads and 2 or 6 vectors lie within 5%); one
+// token 3.3 us, over eight CTAs. Rows of up to kShortRow bytes go to a warp each: a CTA's joining
 // would take longer than their reading.
 template <class T, bool ENTROPY, int THREADS>
 __global__ void __launch_bounds__(kRowThreads, 5)
@@ -323,8 +323,11 @@ __device__ __forceinline__ void write_grad(float c, const GradRow& r, const Slic
     write_ends<T, H>(s, r, id, id < s.head ? widen(start.head) : 0.0f, id < s.tail ? widen(start.tail) : 0.0f, out, c, y);
 }
 
+// The CTAs of an SM are bounded for fp32, whose rows bring few bytes per register: 40 registers for a
+// CTA's rows are 174 us for 2039 of 50257 with their forward pass, 32 are 171; 16-bit rows are the
+// faster with all that the compiler takes.
 template <class T, bool H, int THREADS>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, sizeof(T) == 4 ? (THREADS == 32 ? 5 : 8) : 1)
     k_token_grad(const Rows<T> a, int size, const float* logp, const float* lse, const float* entropy, const float* dlogp,
                  const float* dentropy, T* dx, int64_t dstride) {
     wait_for_kernel_before();
@@ -368,7 +371,7 @@ __device__ __forceinline__ int64_t clamp_offset(int64_t o, int64_t lo, int64_t h
 // (written before). Sequences sum what their log-probabilities were before they were rounded to
 // fp32 (low): a reward is the small difference of such sums, and 100 roundings of numbers near 10
 // are 3e-6 of it. The loss of a pair needs all of its rows, so the logits are read twice: 8192
-// tokens in 16 pairs, a quarter masked, take 326 us, 94% of the copy peak on their 2.06 GB. One
+// tokens in 16 pairs, a quarter masked, take 320 us, 96% of the copy peak on their 2.06 GB. One
 // kernel that follows each pair's forward rows with its gradient rows, to read them from L2, took
 // 450 us and more: the L2 gave back 6%, handing out rows cost 20%.
 // ---------------------------------------------------------------------------------------
