@@ -114,6 +114,7 @@ SHAPES = [  # T, V, stride, offset
     (1, 1, None, 0), (1, 50257, None, 0), (3, 7, None, 1), (5, 8, None, 0), (4, 9, 17, 3), (17, 1000, 1008, 0),
     (33, 4099, None, 5), (2, 8192, None, 8), (64, 257, 264, 0), (700, 130, 131, 2), (3, 131072, None, 1),
     (1300, 515, 518, 1), (1217, 3, None, 0), (1251, 4099, None, 0),  # a warp per row
+    (2501, 9001, None, 1),  # forward only, in 16 bits
 ]
 
 

@@ -180,7 +180,7 @@ __device__ __forceinline__ int64_t row_of(int size) {
 // Forward, bound by reading the logits once: `size` CTAs per row (a cluster; several where there
 // are few rows), each thread kUnroll vectors at a time. 4096 fp16 tokens, a quarter of them masked:
 // 50.4 us, 309 MB, 92% of the copy peak (128 or 512 threads and 2 or 6 vectors lie within 5%); one
-// token 3.3 us, over eight CTAs. Rows of up to kShortRow bytes go to a warp each: a CTA's joining
+// token 3.3 us, over eight CTAs. Rows of up to kShortRowRead bytes go to a warp each: a CTA's joining
 // would take longer than their reading.
 template <class T, bool ENTROPY, int THREADS>
 __global__ void __launch_bounds__(kRowThreads, 5)
@@ -1003,11 +1003,16 @@ int ctas_per_row(const zero_logits* x, int sms, int per_sm = kRowCtas) {
     return size;
 }
 
-// Whether each row goes to a warp: short rows, enough of them for every SM. At 16 KB a warp is the
-// faster (8192 rows, forward: 31 us against 42; policy loss 71 against 92), at 32 KB a CTA (policy
-// loss 114 us against 126).
-constexpr int64_t kShortRow = 16384;
-bool short_rows(const zero_logits* x, int sms) { return x->vocab * type_size(x->type) <= kShortRow && x->rows >= 8 * (int64_t)sms; }
+// Whether each row goes to a warp: short rows, enough of them for every SM. 8192 bf16 rows, a warp each
+// against a CTA each: of 16 KB 25.8 us against 30.4 forward, 57 against 63 for the policy loss, the same
+// for the gradient alone; of 32 KB 45.2 against 49.6 forward, but 113 against 83 for the policy loss
+// and 83 against 78 for the gradient; of 64 KB 86 against 80 forward. 2048 rows of 32 KB are the same
+// either way.
+constexpr int64_t kShortRow = 16384, kShortRowRead = 32768;
+bool short_rows(const zero_logits* x, int sms, int64_t most = kShortRow) {
+    const int64_t bytes = x->vocab * type_size(x->type);
+    return bytes <= most && x->rows >= (bytes > kShortRow ? 16 : 8) * (int64_t)sms;
+}
 unsigned short_grid(const zero_logits* x) { return (unsigned)((x->rows + kRowThreads / 32 - 1) / (kRowThreads / 32)); }
 
 // How the one-pass kernel takes a row.
@@ -1050,7 +1055,7 @@ int launch_token_logp(const zero_logits* x, const float* weight, float* logp, fl
     return by_type(x->type, [&](auto tag) {
         using T = decltype(tag);
         const Rows<T> a = rows_of<T>(x, weight);
-        if (short_rows(x, sms))
+        if (short_rows(x, sms, kShortRowRead))
             return launch_linked(entropy ? k_token_logp<T, true, 32> : k_token_logp<T, false, 32>, short_grid(x), kRowThreads, 0, 1, s, a, 1,
                                  logp, lse, entropy, low, cleared, counter);
         const int size = ctas_per_row(x, sms);
