@@ -302,8 +302,8 @@ __device__ __forceinline__ void write_ends(const Slice<T>& s, const GradRow& r, 
     if (i < s.tail) out[s.tail_at + i] = narrow<T>(grad_term<H, CLAMP>(r, x_tail, c, s.tail_at + i == y));
 }
 
-// Backward, bound by reading the logits and writing their gradient: 2048 bf16 rows in 62.9 us, 412
-// MB, 98% of the copy peak. Where the gradient's rows have another alignment than the logits',
+// Backward, bound by reading the logits and writing their gradient: 2048 bf16 rows in 63.5 us, 412
+// MB, 97% of the copy peak (8192 in 245 us, 101%). Where the gradient's rows have another alignment than the logits',
 // elements are taken one at a time.
 template <int THREADS, bool H, class T, class L>
 __device__ __forceinline__ void write_grad(float c, const GradRow& r, const Slice<T>& s, const RowStart<T, THREADS>& start, const T* x, T* out, L load,
