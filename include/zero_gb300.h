@@ -746,7 +746,8 @@ typedef struct {
     float* clip_fraction;     /* [1] share of the targets whose ratio was clipped             */
     float* kl_mean;           /* [1] mean KL over the targets; 0 without ref_logp             */
     float* logp;              /* [rows]                                                       */
-    float* entropy;           /* [rows]; may be NULL when entropy_coef = 0                    */
+    float* entropy;           /* [rows]; may be NULL when entropy_coef = 0, and is written
+                                 wherever it is given                                         */
     void* dlogits;            /* [rows, vocab] as for zero_preference                         */
     int64_t dstride;
 } zero_policy;

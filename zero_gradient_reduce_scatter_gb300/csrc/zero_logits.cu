@@ -651,6 +651,8 @@ struct Slot {
     }
 };
 
+// H: entropies are formed, for the loss or only for the caller, who may want them beside a coefficient
+// of 0.
 template <class T, bool H, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
     k_policy_rows(const Rows<T> a, const PolicyTokens p, int size, int per, int slots, float* logp, float* entropy, T* dx, int64_t dstride) {
@@ -1081,7 +1083,7 @@ int launch_token_grad(const zero_logits* x, const float* weight, const float* lo
 
 template <class T, int WARPS>
 int launch_fused(const zero_logits* x, const FusedPlan& f, const PolicyTokens& p, const zero_policy* q, int sms, cudaStream_t s) {
-    auto* kernel = q->entropy_coef != 0.0 ? k_policy_rows<T, true, WARPS> : k_policy_rows<T, false, WARPS>;
+    auto* kernel = q->entropy ? k_policy_rows<T, true, WARPS> : k_policy_rows<T, false, WARPS>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fused_room(WARPS));
     if (e != cudaSuccess) return record_cuda_error(e);
     const int64_t clusters = std::min<int64_t>(x->rows, fused_ctas(WARPS) * sms / f.size);
@@ -1093,7 +1095,7 @@ int launch_policy_rows(const zero_logits* x, const FusedPlan& f, const PolicyTok
     const int rc = by_type(x->type, [&](auto tag) {
         using T = decltype(tag);
         if (short_rows(x, sms))
-            return launch_linked(q->entropy_coef != 0.0 ? k_policy_short<T, true> : k_policy_short<T, false>, short_grid(x), kRowThreads, 0, 1, s,
+            return launch_linked(q->entropy ? k_policy_short<T, true> : k_policy_short<T, false>, short_grid(x), kRowThreads, 0, 1, s,
                                  rows_of<T>(x, nullptr), p, q->logp, q->entropy, (T*)q->dlogits, q->dstride);
         return f.warps == kFusedWarps ? launch_fused<T, kFusedWarps>(x, f, p, q, sms, s) : launch_fused<T, kFusedWarpsSmall>(x, f, p, q, sms, s);
     });
