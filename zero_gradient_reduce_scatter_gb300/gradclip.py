@@ -34,7 +34,8 @@ class GradClip:
 
     grads: contiguous tensors of one device. dst: where the clipped values go, one tensor of the
     same size each (any of the three types), or None for in place. The plan keeps references to
-    both. A dst tensor must not overlap any gradient but its own.
+    both. A dst tensor must not overlap any gradient but its own. A plan may be dropped right after
+    ``clip``, on whatever stream that ran; one captured in a CUDA graph must live as long as the graph.
     """
 
     def __init__(self, grads, dst=None, stream=None):
@@ -57,9 +58,10 @@ class GradClip:
         size = _lib().zero_grads_workspace(n)
         with _on(stream):
             self.workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        self._home = _handle(stream, dev)  # the stream that the workspace was allocated on
         plan = ctypes.c_void_p()
         _check(_lib().zero_grads_init(ctypes.byref(plan), ctypes.cast(rows, ctypes.c_void_p), n, self.workspace.data_ptr(),
-                                      size, _handle(stream, dev)), "zero_grads_init")
+                                      size, self._home), "zero_grads_init")
         self._plan = plan
 
     @classmethod
@@ -75,10 +77,11 @@ class GradClip:
         the values as they are (scale 1). max_norm may be infinite."""
         with _on(stream):
             norm, scale, norms = _floats(self.device), _floats(self.device), _floats(self.device, len(self.grads))
-        if stream is not None:
-            self.workspace.record_stream(stream)  # not handed out again before this call is done
-        _check(_lib().zero_grads_clip(self._plan, max_norm, norm.data_ptr(), scale.data_ptr(), norms.data_ptr(),
-                                      _handle(stream, self.device)), "zero_grads_clip")
+        handle = _handle(stream, self.device)
+        if handle != self._home:  # the kernels follow the workspace's table: not handed out again before this call is done
+            self.workspace.record_stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+        _check(_lib().zero_grads_clip(self._plan, max_norm, norm.data_ptr(), scale.data_ptr(), norms.data_ptr(), handle),
+               "zero_grads_clip")
         return Clipped(norm, scale, norms)
 
     def close(self):
