@@ -71,3 +71,124 @@ def test_entropy_without_a_coefficient(way):
         tol = tol + 2.0 ** -25
     for d in (r["dlogits"], q.dlogits):
         assert bool(((d.double() - want).abs() <= tol).all())
+
+
+def extremes(way, seed):
+    """Logits whose rows 1, 3, 5 ... hold masks: -inf or the type's lowest value over parts, over all
+    but one token, over the target itself, in the middle of the vocabulary."""
+    T, V, dtype = WAYS[way]
+    low = torch.finfo(TYPES[dtype]).min
+    x, _ = make_logits(T, V, dtype, seed)
+    y = torch.randint(0, V // 2, (T,), device=DEV, generator=gen(seed + 1))
+    x[1, V // 2:] = -math.inf
+    x[3, V // 2:] = low
+    x[5, V // 3:V // 3 + V // 7] = -math.inf     # in the middle
+    y[5] = 1
+    x[7, :] = low                                # nothing allowed, by the lowest value: uniform
+    x[9, :] = -math.inf                          # one token allowed, and it is the target
+    x[9, V - 1] = 2.0
+    y[9] = V - 1
+    x[11, V // 2:] = low                         # the target is masked by the lowest value
+    y[11] = V - 2
+    x[13, V // 2:] = -math.inf                   # the target is masked by -inf
+    y[13] = V - 2
+    return x, y
+
+
+@pytest.mark.parametrize("entropy_coef", [0.0, 0.02])
+@pytest.mark.parametrize("way", WAYS)
+def test_policy_loss_of_masked_rows(way, entropy_coef):
+    T, V, dtype = WAYS[way]
+    x, y = extremes(way, 41)
+    adv = torch.randn(T, device=DEV, generator=gen(43)) + 0.3
+    logq, lp, _, ent = reference(x, y)
+    gone = lp < -1e4                             # a ratio of exactly 0, in fp32 as in 64 bits
+    assert gone.tolist()[:14] == [False] * 11 + [True, False, True]
+    old = torch.where(gone, torch.full_like(lp, -5.0), lp - 0.05).float()
+    q = zg.policy_loss(x, y, adv, old, reduce="sum", entropy_coef=entropy_coef)
+    A, near = adv.double(), torch.where(gone, torch.zeros_like(lp), lp)
+    r = torch.exp(lp - old.double())
+    live = torch.where(gone & (A < 0), torch.zeros_like(A), torch.ones_like(A))   # below the clip: no gradient, a constant loss
+    surrogate = torch.where(gone & (A < 0), -0.8 * A, -r * A)
+    E = bound(x) * (1 + near.abs())
+    size = r * A.abs() + entropy_coef * (1 + ent)
+    check(q.logp[~gone], lp[~gone], bound(x)[~gone], "logp")
+    assert bool((q.logp[gone] < -1e4).all())
+    assert abs(float(q.loss) - float((surrogate - entropy_coef * ent).sum())) <= float((2 * E * size + 2.0 ** -20 * (surrogate.abs() + entropy_coef * ent)).sum())
+    g = -r * A * live
+    h = torch.full_like(g, -entropy_coef) if entropy_coef else None
+    want = reference_grad(logq, y, g, h, ent, 1.0)
+    p = torch.exp(logq)
+    hot = torch.zeros_like(p).scatter_(1, y[:, None], 1.0)
+    plogp = torch.where(p > 0, p * logq.abs(), torch.zeros_like(p))
+    tol = ((4 * E * size + 2.0 ** -21 * size)[:, None] * (p + hot) + (2 * E * entropy_coef)[:, None] * plogp)
+    tol = tol + UNIT[dtype] * want.abs() + 2.0 ** -100 + (2.0 ** -25 if dtype == "fp16" else 0.0)
+    err = (q.dlogits.double() - want).abs()
+    bad = ~(err <= tol)
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:3].tolist(), q.dlogits[bad][:3].tolist(), want[bad][:3].tolist())
+    inplace = zg.policy_loss(x, y, adv, old, reduce="sum", entropy_coef=entropy_coef, out=x)
+    assert torch.equal(x, q.dlogits) and torch.equal(inplace.loss, q.loss)
+
+
+@pytest.mark.parametrize("entropy_coef", [0.0, 0.02])
+@pytest.mark.parametrize("way", WAYS)
+def test_policy_loss_of_rows_without_a_value(way, entropy_coef):
+    """NaN, +inf, a target past the vocabulary: NaN for that token and in the loss, and every other row's
+    gradient bit for bit what it is without them; a row of -inf alone: gradient 0."""
+    T, V, dtype = WAYS[way]
+    x, _ = make_logits(T, V, dtype, 51)
+    y = torch.randint(0, V, (T,), device=DEV, generator=gen(52))
+    adv = torch.randn(T, device=DEV, generator=gen(53))
+    old = (reference(x, y)[1] - 0.05).float()
+    kw = dict(reduce="sum", entropy_coef=entropy_coef)
+    bad = [2, 4, 6, 8]
+    x[2, V // 3] = math.nan
+    x[4, V // 3] = math.inf
+    y[6] = V + 3
+    x[8, y[8]] = math.nan
+    x[10, :] = -math.inf
+    masked = y.clone()
+    masked[bad] = -1
+    want = zg.policy_loss(x, masked, adv, old, **kw)
+    assert bool(want.loss.isfinite()) and want.logp[10] == -math.inf and bool((want.dlogits[10] == 0).all())
+    assert bool((want.dlogits[bad] == 0).all()) and bool(want.dlogits.isfinite().all())
+    q = zg.policy_loss(x, y, adv, old, **kw)
+    assert bool(q.loss.isnan()) and bool(q.logp[bad].isnan().all()) and bool(q.dlogits[bad].isnan().all())
+    rest = torch.ones(T, dtype=torch.bool, device=DEV)
+    rest[bad] = False
+    assert torch.equal(q.dlogits[rest], want.dlogits[rest]) and torch.equal(q.logp[rest], want.logp[rest])
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_preference_loss_of_extreme_rows(way):
+    """Masked rows in two pairs; in a third a target that cannot be scored: NaN in that pair and the mean,
+    nothing in the others."""
+    T, V, dtype = WAYS[way]
+    x, y = extremes(way, 61)
+    y[11], y[13] = 3, 4                          # targets among the allowed tokens
+    x[0, V // 3] = math.nan
+    off = torch.tensor([0, 1, 2, 8, T - 2, T - 2, T], device=DEV)
+    logq, lp, _, ent = reference(x, y)
+    E = bound(x) * (1 + lp.abs())
+    ref = (torch.where(lp.isfinite(), lp, torch.zeros_like(lp)) - 0.01).float()
+    r = zg.preference_loss(x, y, off, ref, beta=0.1)
+    assert bool(r.loss.isnan()) and bool(r.pair_loss[0].isnan()) and bool(r.dlogits[:2].isnan().all())
+    check(r.logp[1:], lp[1:], bound(x)[1:], "logp")
+    for i, (a, b, c) in ((1, (2, 8, T - 2)), (2, (T - 2, T - 2, T))):
+        d = (lp - ref.double())
+        m, err = float(d[a:b].sum() - d[b:c].sum()), float(E[a:c].sum())
+        loss = math.log1p(math.exp(-0.1 * m))
+        assert abs(float(r.pair_loss[i]) - loss) <= 0.1 * err + 2.0 ** -22
+        dm = -0.1 / (1 + math.exp(0.1 * m)) / 3
+        for lo, hi, s in ((a, b, dm), (b, c, -dm)):
+            if lo == hi:
+                continue
+            g = torch.full((hi - lo,), s, device=DEV, dtype=torch.float64)
+            want = reference_grad(logq[lo:hi], y[lo:hi], g, None, ent[lo:hi], 1.0)
+            p = torch.exp(logq[lo:hi])
+            hot = torch.zeros_like(p).scatter_(1, y[lo:hi, None], 1.0)
+            # the coefficient follows the margin with a slope below beta times itself
+            tol = abs(s) * (2 * E[lo:hi, None] + 0.1 * err + 2.0 ** -22) * (p + hot) + UNIT[dtype] * want.abs() + 2.0 ** -100
+            if dtype == "fp16":
+                tol = tol + 2.0 ** -25
+            assert bool(((r.dlogits[lo:hi].double() - want).abs() <= tol).all()), (i, lo)

@@ -831,7 +831,8 @@ __global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
                     if (lane == 0) mbar_arrive(empty + 8 * begin.at);  // this warp has done with the part
                 }
             };
-            if (H && !good) write(std::true_type());  // this slice may hold -inf
+            // -inf in this slice, or a base that another CTA's slice raised far above this one's values
+            if (H && !(good && st.m == base_of(x_y))) write(std::true_type());
             else write(std::false_type());
             ++taken;
         }
