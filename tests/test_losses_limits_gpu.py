@@ -192,3 +192,23 @@ def test_preference_loss_of_extreme_rows(way):
             if dtype == "fp16":
                 tol = tol + 2.0 ** -25
             assert bool(((r.dlogits[lo:hi].double() - want).abs() <= tol).all()), (i, lo)
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_masked_target_under_the_current_policy(way):
+    """Without old_logp the ratio is 1, also where the target's probability is 0; NaN stays NaN."""
+    T, V, dtype = WAYS[way]
+    x, _ = make_logits(T, V, dtype, 71)
+    y = torch.randint(0, V // 2, (T,), device=DEV, generator=gen(72))
+    x[1, V // 2:] = -math.inf
+    y[1] = V - 1
+    adv = torch.full((T,), 0.5, device=DEV)
+    q = zg.policy_loss(x, y, adv, reduce="sum")
+    assert q.logp[1] == -math.inf and abs(float(q.loss) + 0.5 * T) <= 2.0 ** -22 * T
+    logq, _, _, ent = reference(x, y)
+    want = reference_grad(logq, y, -adv.double(), None, ent, 1.0)[1]
+    p = torch.exp(logq[1])
+    tol = 0.5 * (2 * bound(x)[1] + 2.0 ** -21) * p + UNIT[dtype] * want.abs() + 2.0 ** -100 + (2.0 ** -25 if dtype == "fp16" else 0.0)
+    assert bool(((q.dlogits[1].double() - want).abs() <= tol).all())
+    x[2, 5] = math.nan
+    assert bool(zg.policy_loss(x, y, adv, reduce="sum").loss.isnan())

@@ -582,7 +582,8 @@ struct TokenLoss {
 
 __device__ __forceinline__ TokenLoss policy_token(const PolicyTokens& a, const TokenIn& in, float logp, float entropy) {
     TokenLoss r;
-    const float w = in.w, A = in.adv, ratio = expf(logp - (a.old_logp ? in.old : logp));
+    // without old_logp the ratio is 1, of a log-probability of -inf too; a NaN stays
+    const float w = in.w, A = in.adv, ratio = a.old_logp ? expf(logp - in.old) : logp == logp ? 1.0f : logp;
     const float plain = -ratio * A, clip = -fminf(fmaxf(ratio, a.lo), a.hi) * A;
     float loss = !(plain < clip) ? plain : clip;  // a NaN stays
     bool off = (A > 0.0f && ratio > a.hi) || (A < 0.0f && ratio < a.lo);
