@@ -212,3 +212,16 @@ def test_masked_target_under_the_current_policy(way):
     assert bool(((q.dlogits[1].double() - want).abs() <= tol).all())
     x[2, 5] = math.nan
     assert bool(zg.policy_loss(x, y, adv, reduce="sum").loss.isnan())
+
+
+def test_kl_of_a_masked_target_is_infinite():
+    """exp(d) - d - 1 at d = inf, the third estimator where the policy gives a target no probability."""
+    x, _ = make_logits(20, 300, "bf16", 81)
+    y = torch.randint(0, 150, (20,), device=DEV, generator=gen(82))
+    x[4, 150:] = -math.inf
+    y[4] = 200
+    zero = torch.zeros(20, device=DEV)
+    for kl in ("k2", "k3"):
+        assert float(zg.policy_loss(x, y, zero, zero - 5, zero - 5, kl=kl).kl) == math.inf
+    x[5, 3] = math.nan
+    assert bool(zg.policy_loss(x, y, zero, zero - 5, zero - 5).kl.isnan())

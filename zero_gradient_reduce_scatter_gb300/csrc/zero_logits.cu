@@ -604,7 +604,7 @@ __device__ __forceinline__ TokenLoss policy_token(const PolicyTokens& a, const T
             dkl = -d;
         } else {
             const float e = expm1f(d);
-            r.kl = e - d;
+            r.kl = e < INFINITY ? e - d : e;  // not inf - inf where the target has no probability
             dkl = -e;
         }
         if (a.kl_coef != 0.0f) {
