@@ -225,3 +225,17 @@ def test_kl_of_a_masked_target_is_infinite():
         assert float(zg.policy_loss(x, y, zero, zero - 5, zero - 5, kl=kl).kl) == math.inf
     x[5, 3] = math.nan
     assert bool(zg.policy_loss(x, y, zero, zero - 5, zero - 5).kl.isnan())
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_no_advantage_beside_a_ratio_past_fp32(way):
+    """Advantage 0, as in a group whose rewards are all equal: no surrogate whatever the ratio, of which
+    exp(logp - old_logp) may be no fp32 number."""
+    T, V, dtype = WAYS[way]
+    x, _ = make_logits(T, V, dtype, 91)
+    y = torch.randint(0, V, (T,), device=DEV, generator=gen(92))
+    adv = torch.zeros(T, device=DEV)
+    old = torch.full((T,), -5.0, device=DEV)
+    old[1] = -200.0
+    q = zg.policy_loss(x, y, adv, old, reduce="sum")
+    assert float(q.loss) == 0 and float(q.clip_fraction) == 0 and bool((q.dlogits == 0).all())

@@ -584,7 +584,8 @@ __device__ __forceinline__ TokenLoss policy_token(const PolicyTokens& a, const T
     TokenLoss r;
     // without old_logp the ratio is 1, of a log-probability of -inf too; a NaN stays
     const float w = in.w, A = in.adv, ratio = a.old_logp ? expf(logp - in.old) : logp == logp ? 1.0f : logp;
-    const float plain = -ratio * A, clip = -fminf(fmaxf(ratio, a.lo), a.hi) * A;
+    // a ratio past fp32 times an advantage of 0 is 0
+    const float plain = A == 0.0f && ratio == INFINITY ? 0.0f : -ratio * A, clip = -fminf(fmaxf(ratio, a.lo), a.hi) * A;
     float loss = !(plain < clip) ? plain : clip;  // a NaN stays
     bool off = (A > 0.0f && ratio > a.hi) || (A < 0.0f && ratio < a.lo);
     if (a.dual > 0.0f && A < 0.0f && ratio > a.dual) {
