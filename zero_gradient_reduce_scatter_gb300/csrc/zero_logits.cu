@@ -143,12 +143,13 @@ __device__ __forceinline__ bool fast_row(const T* x, int64_t vocab, float x_y, S
 }
 
 // The sums of a row, or of a CTA's share of it, by the THREADS that take it: a CTA's (joined through
-// sm, THREADS / 32 entries), or one warp's, which takes the whole row and needs no sm.
-template <int THREADS, bool ENTROPY, class T>
+// sm, THREADS / 32 entries), or one warp's, which takes the whole row and needs no sm. WRITTEN: the
+// kernel writes the row afterwards (a gradient in place), so not through the read-only path.
+template <int THREADS, bool ENTROPY, bool WRITTEN, class T>
 __device__ __forceinline__ RowStat row_sums(const T* x, int64_t vocab, int64_t y, float* x_target, Scale k, int rank, int size, RowStat* sm) {
     const Slice<T> s(x, vocab, rank, size);
     const int id = place_in_group<THREADS>();
-    auto load = [&](int i) { return THREADS == 32 ? __ldg(s.v + i) : load_once(s.v + i); };
+    auto load = [&](int i) { return WRITTEN ? s.v[i] : THREADS == 32 ? __ldg(s.v + i) : load_once(s.v + i); };
     const RowStart<T, THREADS> start(s, x, load);
     const float x_y = *x_target = y < vocab ? widen(x[y]) : NAN;
     auto sums = [&](auto checked) {
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kRowThreads, 5)
     if (y >= 0) {
         const T* x = a.x + t * a.stride;
         float x_y;
-        RowStat st = row_sums<THREADS, ENTROPY>(x, a.vocab, y, &x_y, a.k, rank, size, sm);
+        RowStat st = row_sums<THREADS, ENTROPY, false>(x, a.vocab, y, &x_y, a.k, rank, size, sm);
         if (THREADS != 32) st = cluster_join<ENTROPY>(st, size, a.k, &mine);
         if (first) {
             r = finish_row<ENTROPY>(st, x_y, a.k, (float)a.inv_t);
@@ -870,7 +871,7 @@ __global__ void __launch_bounds__(kRowThreads)
     TokenLoss l = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     RowStat st = empty_stat();
     float x_y = NAN;
-    if (y >= 0) st = row_sums<32, H>(x, a.vocab, y, &x_y, a.k, 0, 1, nullptr);
+    if (y >= 0) st = row_sums<32, H, true>(x, a.vocab, y, &x_y, a.k, 0, 1, nullptr);
     wait_for_kernel_before();
     const TokenIn in(p, t);
     if (in.w != 0.0f) {
