@@ -25,8 +25,10 @@ class Workspace:
 
 
 class Tensor(types.SimpleNamespace):
+    at = 1 << 16
+
     def data_ptr(self):
-        return 1 << 16
+        return self.at
 
     def is_contiguous(self):
         return True
@@ -50,14 +52,14 @@ def world(monkeypatch):
     def empty(*a, **kw):
         made.append(Workspace())
         return made[-1]
-    fake = types.SimpleNamespace(empty=empty, uint8=None, cuda=types.SimpleNamespace(current_stream=lambda device=None: Stream(current[0])))
+    fake = types.SimpleNamespace(empty=empty, uint8=None, Tensor=Tensor, cuda=types.SimpleNamespace(current_stream=lambda device=None: Stream(current[0])))
     monkeypatch.setattr(gradclip, "torch", fake)
     monkeypatch.setattr(gradclip, "_lib", lambda: lib)
     monkeypatch.setattr(gradclip, "_on", lambda stream: losses._NOTHING)
     monkeypatch.setattr(gradclip, "_floats", lambda device, *shape: Tensor())
     monkeypatch.setattr(gradclip, "_handle", lambda stream, device: current[0] if stream is None else stream.cuda_stream)
     grad = Tensor(is_cuda=True, dtype=torch.float32, device=types.SimpleNamespace(index=0))
-    return types.SimpleNamespace(make=lambda **kw: gradclip.GradClip([grad], **kw), current=current, used=used, made=made)
+    return types.SimpleNamespace(make=lambda **kw: gradclip.GradClip([grad], **kw), current=current, used=used, made=made, grad=grad)
 
 
 def test_the_workspace_is_recorded_on_every_stream_that_uses_it(world):
@@ -75,3 +77,16 @@ def test_the_workspace_is_recorded_on_every_stream_that_uses_it(world):
     side.clip(1.0)
     side.clip(1.0, stream=Stream(5))
     assert world.made[1].streams == [9]
+
+
+def test_gradients_made_anew_are_noticed(world):
+    """zero_grad() sets gradients to None and the next backward makes others: handed to clip, they are refused."""
+    plan = world.make()
+    kw = dict(is_cuda=True, dtype=world.grad.dtype, device=world.grad.device)
+    plan.clip(1.0, grads=[world.grad])
+    plan.clip(1.0, grads=(g for g in [Tensor(**kw)]))      # a view of the same values
+    assert world.used == [0, 0]
+    for grads in ([Tensor(at=1 << 18, **kw)], [None], [], [world.grad, world.grad]):
+        with pytest.raises(ValueError):
+            plan.clip(1.0, grads=grads)
+    assert world.used == [0, 0]

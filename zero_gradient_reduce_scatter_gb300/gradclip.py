@@ -34,7 +34,10 @@ class GradClip:
 
     grads: contiguous tensors of one device. dst: where the clipped values go, one tensor of the
     same size each (any of the three types), or None for in place. The plan keeps references to
-    both. A dst tensor must not overlap any gradient but its own. A plan may be dropped right after
+    both, and their addresses: gradients must stay the same tensors from call to call, which
+    ``optimizer.zero_grad(set_to_none=False)`` or ``p.grad.zero_()`` does and torch's default,
+    gradients set to None and made anew, does not (``clip(..., grads=)`` checks it).
+    A dst tensor must not overlap any gradient but its own. A plan may be dropped right after
     ``clip``, on whatever stream that ran; one captured in a CUDA graph must live as long as the graph.
     """
 
@@ -72,9 +75,19 @@ class GradClip:
             raise ValueError(f"the optimizer has {len(opt.numel)} tensors, got {len(grads)}")
         return cls(grads, [opt.tensor_view(buf, i) for i in range(len(opt.numel))], stream=stream)
 
-    def clip(self, max_norm: float, stream=None) -> Clipped:
+    def clip(self, max_norm: float, stream=None, grads=None) -> Clipped:
         """Measure, and write gradient * min(1, max_norm / norm). A norm that is not finite leaves
-        the values as they are (scale 1). max_norm may be infinite."""
+        the values as they are (scale 1). max_norm may be infinite: then the values are only
+        measured and packed. grads: the gradients as the caller holds them now (``[p.grad for p in
+        params]``); ValueError where one is not the plan's, whose old values would be clipped instead."""
+        if grads is not None:
+            now = list(grads)
+            if len(now) != len(self.grads):
+                raise ValueError(f"the plan has {len(self.grads)} gradients, got {len(now)}")
+            for i, (a, b) in enumerate(zip(now, self.grads)):
+                if a is not b and not (isinstance(a, torch.Tensor) and a.data_ptr() == b.data_ptr() and a.dtype == b.dtype
+                                       and a.numel() == b.numel() and a.is_contiguous()):
+                    raise ValueError(f"grads[{i}] is not the tensor that the plan was made for")
         with _on(stream):
             norm, scale, norms = _floats(self.device), _floats(self.device), _floats(self.device, len(self.grads))
         handle = _handle(stream, self.device)
