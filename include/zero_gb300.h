@@ -636,7 +636,8 @@ double zero_state_bytes_per_param(int stage, int M, double param_bytes, double g
  *    is enqueued on `stream` and the call returns; every pointer is device memory of one GPU
  *    (or managed memory), which the call finds from its first buffer and makes current; a
  *    pointer elsewhere, or a stream of another GPU, returns INVALID_ARG before anything is
- *    enqueued. The calls only launch kernels, so they can be captured in a CUDA graph.
+ *    enqueued. The calls only enqueue work on the stream (kernels; for a preference loss of no
+ *    rows also a 4-byte clear), so they can be captured in a CUDA graph.
  *  - Logits of token t are the row z_t = x_t / temperature, x_t[j] at logits[t * stride + j].
  *    Rows may have any alignment that their element type has: an odd vocabulary is as good as
  *    a padded one. Elements past `vocab` in a row are never read nor written.
@@ -717,6 +718,8 @@ int zero_preference_loss(const zero_logits* x, const zero_preference* p, void* w
  *   L = max(-r A, -clamp(r, 1 - clip_low, 1 + clip_high) A), and for A < 0 with dual_clip > 0
  *       at most -dual_clip A;  L += kl_coef KL - entropy_coef entropy
  *   KL, with d = ref_logp - logp: ZERO_KL_K1 -d, ZERO_KL_K2 d^2 / 2, ZERO_KL_K3 exp(d) - d - 1
+ * A target of probability 0 (logp = -inf) has r = 0, or 1 without old_logp, and an infinite KL_K2
+ * and KL_K3; an r that is no fp32 number times A = 0 is 0.
  * loss = sum of w_t L_t: w = 1 / (number of targets) (ZERO_REDUCE_TOKEN), 1 / (targets of the
  * token's sequence x sequences that have any) (ZERO_REDUCE_SEQUENCE), or 1 (ZERO_REDUCE_SUM).
  * The gradient follows r inside and on the clip's edges and is 0 past them; old_logp, ref_logp

@@ -239,3 +239,21 @@ def test_no_advantage_beside_a_ratio_past_fp32(way):
     old[1] = -200.0
     q = zg.policy_loss(x, y, adv, old, reduce="sum")
     assert float(q.loss) == 0 and float(q.clip_fraction) == 0 and bool((q.dlogits == 0).all())
+
+
+def test_pairs_of_no_tokens_in_a_graph():
+    """A batch of no rows is captured like any other."""
+    x, y = torch.empty((0, 40), device=DEV, dtype=torch.bfloat16), torch.empty(0, dtype=torch.int64, device=DEV)
+    off = torch.zeros(2 * 700 + 1, dtype=torch.int64, device=DEV)
+    want = zg.preference_loss(x, y, off)
+    import gc
+    gc.collect()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = zg.preference_loss(x, y, off)
+    for _ in range(2):
+        r.loss.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(r.loss, want.loss) and abs(float(r.loss) - math.log(2)) <= 2.0 ** -23

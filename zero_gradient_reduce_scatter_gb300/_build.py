@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libzero_gb300.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
-# The bounds-checked variant (every kernel index tested before use; for tests).
+# The bounds-checked variant (every index of the step's kernels tested before use; for tests). The
+# kernels of the losses and of the clipping are the same in both.
 CHECKED_LIB_PATH = os.path.join(BUILD_DIR, "libzero_gb300_checked.so")
 
 SOURCES = ["zero_kernels.cu", "zero_api.cpp", "zero_noalloc.cu", "zero_logits.cu", "zero_linear.cu", "zero_grads.cu"]

@@ -86,7 +86,6 @@ public:
         int n = 0;
         return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev_) == cudaSuccess && n > 0 ? n : 1;
     }
-    int device() const { return dev_; }
 
 private:
     int prev_ = -1, dev_ = -1;

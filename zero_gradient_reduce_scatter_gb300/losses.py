@@ -10,9 +10,11 @@ into a model.
 The calls marshal arguments; the arithmetic runs in the library's kernels (there is no CPU
 fallback). They allocate their results with torch on the stream they run on and return once the
 work is enqueued. ``stream`` is a torch.cuda.Stream (default: the current one of the logits'
-device); inputs made on another stream need the usual event or stream wait, and results belong
-to the stream the call ran on. include/zero_gb300.h states every formula and what the calls do
-with masked tokens, infinities and NaN.
+device); inputs made on another stream need the usual event or stream wait, and have to live until
+the work is done (or record_stream); results belong to the stream the call ran on. No call takes
+part in autograd: results carry no graph, whether or not the logits require a gradient.
+include/zero_gb300.h states every formula and what the calls do with masked tokens, infinities
+and NaN.
 
 A target below 0 marks a token without a loss: its row of logits is not read and its gradient
 row is zero.
