@@ -257,3 +257,23 @@ def test_pairs_of_no_tokens_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(r.loss, want.loss) and abs(float(r.loss) - math.log(2)) <= 2.0 ** -23
+
+
+@pytest.mark.parametrize("temperature", [1.0, 0.7])
+@pytest.mark.parametrize("T,V", [(60000, 67), (1000, 1031)])
+def test_entropy_beside_an_unlikely_target(T, V, temperature):
+    """One token takes nearly all of the probability and the target is up to e^50 times less likely: the
+    entropy, small, keeps the bound that the roundings of log p have."""
+    x = torch.randn((T, V), device=DEV, generator=gen(1))
+    y = torch.randint(1, V, (T,), device=DEV, generator=gen(2))
+    x[:, 0] = x[:, 1:].amax(1) + 3 * torch.rand(T, device=DEV, generator=gen(4)) + 1
+    gap = torch.linspace(0.0, 50.0, T, device=DEV) * temperature
+    x.scatter_(1, y[:, None], (x[:, 0] - gap)[:, None])
+    f = zg.token_logp(x, y, entropy=True, temperature=temperature)
+    _, lp, lse, ent = reference(x, y, temperature)
+    E = bound(x, temperature)
+    check(f.entropy, ent, E * (1 + ent), "entropy")
+    check(f.lse, lse, E, "lse")
+    check(f.logp, lp, E, "logp")
+    q = zg.policy_loss(x, y, torch.ones(T, device=DEV), entropy_coef=0.02, temperature=temperature)
+    check(q.entropy, ent, E * (1 + ent), "entropy")

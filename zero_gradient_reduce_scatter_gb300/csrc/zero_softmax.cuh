@@ -197,8 +197,12 @@ __device__ __forceinline__ void narrow2<float>(uint4& v, int i, float2 f) {
 // One thread's sums over a row.
 // Not CHECKED: over a base that is given and stays, usually the target's logit: no comparing, no
 // rescaling, and the parts of a row are plain sums. The sums are floating-point, so a base well
-// below the maximum is as good, until 2^60; and an entropy's sum meets 0 times -inf at a logit of
-// -inf. Both show in the result, and the row is then taken again, CHECKED: the base follows the
+// below the maximum is as good, until 2^60. An entropy is the difference of log s and q / s, which
+// are both as large as the distance of the row's mass from its base, and so are the roundings of q:
+// off by 4e-7 (root mean square) where the target is the likely token, as in any fp32 form, by 2e-6
+// where it is 2^30 times less likely, and by 4e-6, past the bound of a row's other roundings, at
+// 2^60; so with ENTROPY until 2^30. And its sum meets 0 times -inf at a logit of -inf. All of these
+// show in the result, and the row is then taken again, CHECKED: the base follows the
 // maximum (only once a value exceeds it by 2^40: comparing costs less than rescaling) and
 // differences are kept finite.
 // pow2 errs low below 0 and high above it, by 5e-8 and 3e-8 on average: over a base that is not the
@@ -271,7 +275,7 @@ struct Sums {
 // Whether sums that were not CHECKED are good.
 template <bool ENTROPY>
 __device__ __forceinline__ bool good_sums(const RowStat& a) {
-    return a.s < 0x1p60f && (!ENTROPY || a.q == a.q);
+    return ENTROPY ? a.s < 0x1p30f && a.q == a.q : a.s < 0x1p60f;
 }
 
 // Joins the parts of a warp's lanes (the first N of them) in a fixed order; valid in every lane.
