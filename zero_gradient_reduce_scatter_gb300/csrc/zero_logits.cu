@@ -135,7 +135,10 @@ __device__ __forceinline__ RowStat cluster_join(RowStat a, int size, Scale k, Ro
 
 // Whether a row is taken without CHECKED (Sums) first: its target's logit is a base, and a vocabulary
 // padded with -inf or the type's lowest value, at its end or start, does not make an entropy's sum
-// fail anyway. A function of the row alone, so that its bits are too.
+// fail anyway. -inf elsewhere in the vocabulary shows in the sum only, and the row is then taken twice:
+// with an entropy, 4096 x 50257 bf16 token_logp 65 us without a mask, 70 with one at the end, 122 with one
+// in the middle, policy_loss 140, 160 and 212; 8192 x 4000 token_logp 16, 19 and 26, policy_loss 34, 37 and
+// 45. A function of the row alone, so that its bits are too.
 template <bool ENTROPY, class T>
 __device__ __forceinline__ bool fast_row(const T* x, int64_t vocab, float x_y, Scale k) {
     if (ENTROPY && fminf(widen(x[0]) - x_y, widen(x[vocab - 1]) - x_y) * k.c == -INFINITY) return false;
