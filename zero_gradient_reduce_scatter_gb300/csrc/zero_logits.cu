@@ -12,126 +12,11 @@
 #include <cstdint>
 #include <type_traits>
 
-#include <cooperative_groups.h>
-
-#include "zero_host.h"
-#include "zero_softmax.cuh"
-#include "zero_sum.cuh"
+#include "zero_rows.cuh"
 #include "zero_tcgen05.cuh"
 
 namespace zg {
 namespace {
-
-namespace cg = cooperative_groups;
-
-constexpr int kRowThreads = 256;
-constexpr int kRowCtas = 12;  // CTAs of an SM up to which short batches cut their rows
-constexpr int kUnroll = 4;  // 16-byte loads of a thread on their way at a time
-
-// Logits as the kernels take them.
-template <class T>
-struct Rows {
-    const T* x;
-    const int64_t* targets;
-    const float* weight;  // nullptr, or 0 for rows that carry no loss
-    int64_t rows, vocab, stride;
-    Scale k;              // log2(e) / temperature
-    float c;              // the same in one number, for gradients
-    double inv_t;         // 1 / temperature
-};
-
-template <class T>
-__device__ __forceinline__ int64_t live_target(const Rows<T>& a, int64_t t) {
-    return a.weight && a.weight[t] == 0.0f ? -1 : a.targets[t];
-}
-
-// A row as the CTAs of a cluster share it: up to 7 elements before the first 16-byte boundary
-// (the first CTA's), `n` whole vectors of each CTA from element `first` on, and up to 7 elements
-// behind the last (the last CTA's). A row of an odd vocabulary starts at any even address.
-template <class T>
-struct Slice {
-    int head, n, first, tail_at, tail;
-    const uint4* v;  // this CTA's vectors
-
-    __device__ __forceinline__ Slice(const T* x, int64_t vocab, int rank, int size) {
-        const int len = (int)vocab, to = (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T);
-        const int before = min(to, len), vecs = (len - before) / kVec<T>, per = (vecs + size - 1) / size;
-        const int lo = min(per * rank, vecs);
-        n = min(per, vecs - lo);
-        first = before + lo * kVec<T>;
-        tail_at = before + vecs * kVec<T>;
-        head = rank == 0 ? before : 0;
-        tail = rank == size - 1 ? len - tail_at : 0;
-        v = reinterpret_cast<const uint4*>(x + first);
-    }
-};
-
-// A thread's place among the THREADS that share a row: those of a CTA, or of a warp.
-template <int THREADS>
-__device__ __forceinline__ int place_in_group() { return THREADS == 32 ? threadIdx.x & 31 : threadIdx.x; }
-
-// This thread's vectors of n, from its place `i` on, kUnroll at a time: `load` first for all of them,
-// then `use`.
-template <int THREADS, class L, class U>
-__device__ __forceinline__ void for_vectors(int n, L load, U use, int i = place_in_group<THREADS>()) {
-    for (; i + (kUnroll - 1) * THREADS < n; i += kUnroll * THREADS) {
-        uint4 q[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) q[u] = load(i + u * THREADS);
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) use(i + u * THREADS, q[u]);
-    }
-    if (i < n) {
-        uint4 q[kUnroll - 1];
-#pragma unroll
-        for (int u = 0; u < kUnroll - 1; ++u)
-            if (i + u * THREADS < n) q[u] = load(i + u * THREADS);
-#pragma unroll
-        for (int u = 0; u < kUnroll - 1; ++u)
-            if (i + u * THREADS < n) use(i + u * THREADS, q[u]);
-    }
-}
-
-// The part of a row that a thread reads first: its first vectors and its elements at the row's ends,
-// on their way at once with whatever else the row waits for.
-template <class T, int THREADS>
-struct RowStart {
-    uint4 q[kUnroll];
-    T head, tail;
-
-    template <class L>
-    __device__ __forceinline__ RowStart(const Slice<T>& s, const T* x, L load) {
-        const int id = place_in_group<THREADS>();
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            if (id + u * THREADS < s.n) q[u] = load(id + u * THREADS);
-        if (id < s.head) head = x[id];
-        if (id < s.tail) tail = x[s.tail_at + id];
-    }
-    // for_vectors over all of the thread's vectors
-    template <class L, class U>
-    __device__ __forceinline__ void vectors(int n, L load, U use) const {
-        const int id = place_in_group<THREADS>();
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            if (id + u * THREADS < n) use(id + u * THREADS, q[u]);
-        for_vectors<THREADS>(n, load, use, id + kUnroll * THREADS);
-    }
-};
-
-// The sums of all CTAs of a cluster (at most 8), joined in a fixed order; valid everywhere. `mine` is
-// shared memory of this CTA, which stays as it is until the cluster's next barrier. A lane reads a
-// CTA's sums, so that their latencies are one.
-template <bool ENTROPY>
-__device__ __forceinline__ RowStat cluster_join(RowStat a, int size, Scale k, RowStat* mine) {
-    if (size == 1) return a;
-    cg::cluster_group cl = cg::this_cluster();
-    if (threadIdx.x == 0) *mine = a;
-    cl.sync();
-    const int lane = threadIdx.x & 7;
-    a = lane < size ? *cl.map_shared_rank(mine, lane) : empty_stat();
-    return warp_join<ENTROPY, true, 8>(a, k);
-}
 
 // Whether a row is taken without CHECKED (Sums) first: its target's logit is a base, and a vocabulary
 // padded with -inf or the type's lowest value, at its end or start, does not make an entropy's sum
@@ -174,13 +59,6 @@ __device__ __forceinline__ RowStat row_sums(const T* x, int64_t vocab, int64_t y
     return sums(std::true_type());
 }
 
-// The row and the part of it that this thread works on: `size` CTAs per row, or (THREADS = 32) a
-// warp each.
-template <int THREADS>
-__device__ __forceinline__ int64_t row_of(int size) {
-    return THREADS == 32 ? (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5) : blockIdx.x / size;
-}
-
 // Forward, bound by reading the logits once: `size` CTAs per row (a cluster; several where there
 // are few rows), each thread kUnroll vectors at a time. 4096 fp16 tokens, a quarter of them masked:
 // 50.4 us, 309 MB, 92% of the copy peak (128 or 512 threads and 2 or 6 vectors lie within 5%); one
@@ -219,12 +97,6 @@ __global__ void __launch_bounds__(kRowThreads, 5)
     if (THREADS != 32 && size > 1 && y >= 0) cg::this_cluster().sync();  // no CTA leaves while another reads its sums
 }
 
-// dx_j = g [j = y] - 2^d_j (ka + kb d_j) with d_j = (x_j - base) c - off, so that 2^d_j is p_j or
-// a multiple of it that ka and kb make up for.
-struct GradRow {
-    float g, ka, kb, base, off;
-};
-
 // From what zero_token_logp gave. log p is rebuilt from whichever is the smaller number and so
 // the more exact in fp32: the target's log-probability (base = its logit) or lse.
 __device__ __forceinline__ GradRow grad_row(float g, float h, float x_y, float logp, float lse, float entropy, double inv_t) {
@@ -249,55 +121,8 @@ __device__ __forceinline__ GradRow grad_row(float g, float h, const RowStat& a, 
     return {g * i, f * (h == 0.0f ? g : fmaf(h, entropy - log2f(a.s) * kLn2, g)), f * h * kLn2, base_of(a.m), 0.0f};
 }
 
-// One element, in the very operations of GradVector: the bits do not depend on alignment. CLAMP:
-// the row may hold -inf, whose term 2^d (ka + kb d) is 0 times -inf.
-template <bool H, bool CLAMP = H>
-__device__ __forceinline__ float grad_term(const GradRow& r, float x, float c, bool target) {
-    const float d = fmaf(x - r.base, c, -r.off);
-    const float f = __fmul_rn(pow2(d), H ? fmaf(-r.kb, CLAMP ? fmaxf(d, kFar) : d, -r.ka) : -r.ka);
-    return target ? __fadd_rn(f, r.g) : f;
-}
-
-// The same for 16 bytes of a row that do not hold the target, or before it is set right.
-template <class T, bool H, bool CLAMP = H>
-struct GradVector {
-    const uint64_t base, c, off, ka, kb;  // twice each
-
-    __device__ __forceinline__ GradVector(const GradRow& r, float c)
-        : base(pack2(-r.base, -r.base)), c(pack2(c, c)), off(pack2(-r.off, -r.off)), ka(pack2(-r.ka, -r.ka)), kb(pack2(-r.kb, -r.kb)) {}
-
-    __device__ __forceinline__ uint4 operator()(const uint4& x) const {
-        uint4 out;
-#pragma unroll
-        for (int i = 0; i < kVec<T> / 2; ++i) {
-            const uint64_t d = fma2(add2(widen2<T>(x, i), base), c, off);
-            const float2 df = unpack2(d);
-            const uint64_t e = pack2(pow2(df.x), pow2(df.y));
-            const uint64_t b = CLAMP ? pack2(fmaxf(df.x, kFar), fmaxf(df.y, kFar)) : d;
-            narrow2<T>(out, i, unpack2(mul2(e, H ? fma2(kb, b, ka) : ka)));
-        }
-        return out;
-    }
-};
-
 // The target's place in a row that has it, or a place that no slice reaches.
 __device__ __forceinline__ int place_of(int64_t y, int64_t vocab) { return y < vocab ? (int)y : -1; }
-
-// Zeros into this CTA's share of a row.
-template <class T, int THREADS>
-__device__ __forceinline__ void zero_row(T* out, int64_t vocab, int rank, int size) {
-    const Slice<T> s(out, vocab, rank, size);
-    const int id = place_in_group<THREADS>();
-    uint4* v = const_cast<uint4*>(s.v);
-    for (int i = id; i < s.n; i += THREADS) __stcs(v + i, make_uint4(0, 0, 0, 0));
-    if (id < s.head) out[id] = narrow<T>(0.0f);
-    if (id < s.tail) out[s.tail_at + id] = narrow<T>(0.0f);
-}
-
-template <class T>
-__device__ __forceinline__ bool same_alignment(const T* a, const T* b) {
-    return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0;
-}
 
 // The elements of a row that no vector holds.
 template <class T, bool H, bool CLAMP = H>
@@ -360,13 +185,6 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 4 ? (THREADS == 32 ?
         else __syncthreads();
     }
     write_grad<THREADS, H>(a.c, r, s, start, x, out, load, place_of(y, a.vocab), x_y);
-}
-
-// ---------------------------------------------------------------------------------------
-// Losses over tokens.
-// ---------------------------------------------------------------------------------------
-__device__ __forceinline__ int64_t clamp_offset(int64_t o, int64_t lo, int64_t hi) {
-    return o < lo ? lo : (o > hi ? hi : o);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -484,94 +302,19 @@ __global__ void __launch_bounds__(kRowThreads) k_pairs(const PairArgs a) {
 // Policy loss.
 // ---------------------------------------------------------------------------------------
 // What a token's loss needs beside its row: its weight (0: no loss) and its advantage.
-struct PolicyTokens {
-    const int64_t* targets;
-    const int64_t* offsets;
+struct PolicyTokens : TokenWeights {
+    static constexpr bool kClips = true;
     const float* advantages;
     const float *old_logp, *ref_logp;
-    float *w, *adv;              // [rows]
-    float *lse, *g, *h;          // [rows]
-    float *loss, *kl, *clipped;  // [rows]
+    float* adv;            // [rows]
+    float *lse, *g, *h;    // [rows]
+    float *kl, *clipped;   // [rows]
     float *out_loss, *out_clip, *out_kl;
-    uint32_t* ticket;            // the next row of the one-pass kernel
-    int64_t rows, seqs;
     float lo, hi, dual, kl_coef, entropy_coef;
-    int32_t kl_kind, reduce, per_sequence;
+    int32_t kl_kind, per_sequence;
+
+    __device__ __forceinline__ void spread(int64_t t, int64_t s) const { adv[t] = advantages[per_sequence ? s : t]; }
 };
-
-// The kernels over tokens alone: one cluster of token_ctas(rows) CTAs.
-constexpr int kSetupThreads = 1024;
-
-// The sequence that token t lies in, -1 in front of the first, `seqs` behind the last: the last one
-// that begins at or before it.
-__device__ __forceinline__ int64_t sequence_of(const int64_t* offsets, int64_t seqs, int64_t t) {
-    int64_t lo = 0, hi = seqs + 1;  // offsets below lo are at most t, those from hi on are more
-    while (lo < hi) {
-        const int64_t mid = lo + (hi - lo) / 2;
-        if (offsets[mid] <= t) lo = mid + 1;
-        else hi = mid;
-    }
-    return lo - 1;
-}
-
-// Weights and advantages of all tokens: targets are counted, in all and by sequence, then spread. A
-// thread finds its token's sequence by bisection, so that one sequence of all tokens takes no longer
-// than many: 32768 tokens in one sequence took a warp of its own 700 us.
-__global__ void __launch_bounds__(kSetupThreads) k_policy_setup(const PolicyTokens a) {
-    __shared__ uint32_t counted[2], all[2];  // tokens with a target, sequences that have one: added up in the first CTA's; everyone's copy
-    const cg::cluster_group cl = cg::this_cluster();
-    const int lane = threadIdx.x & 31;
-    const int64_t first = (int64_t)blockIdx.x * kSetupThreads + threadIdx.x, step = (int64_t)gridDim.x * kSetupThreads;
-    const bool by_sequence = a.reduce == ZERO_REDUCE_SEQUENCE;
-    uint32_t* of = reinterpret_cast<uint32_t*>(a.h);  // a sequence's targets, at its first token
-    wait_for_kernel_before();
-    let_next_kernel_start();
-    if (threadIdx.x < 2) counted[threadIdx.x] = 0;
-    if (first == 0) *a.ticket = 0;
-    if (by_sequence)
-        for (int64_t t = first; t < a.rows; t += step) of[t] = 0;
-    cl.sync();
-    uint32_t* sums = cl.map_shared_rank(counted, 0);
-    uint32_t targets = 0, filled = 0;
-    for (int64_t t0 = first - lane; t0 < a.rows; t0 += step) {
-        const int64_t t = t0 + lane;
-        const bool target = t < a.rows && a.targets[t] >= 0;
-        const int64_t s = a.offsets && target ? sequence_of(a.offsets, a.seqs, t) : 0;
-        const bool live = target && (!a.offsets || (s >= 0 && s < a.seqs));
-        targets += live;
-        const unsigned lives = __ballot_sync(~0u, live);
-        if (!by_sequence || !lives) continue;
-        // a warp's tokens are most often of one sequence
-        const int64_t b = live ? clamp_offset(a.offsets[s], 0, a.rows - 1) : 0, b0 = __shfl_sync(~0u, b, __ffs(lives) - 1);
-        if (__all_sync(~0u, !live || b == b0)) {
-            if (lane == 0) filled += atomicAdd(of + b0, (uint32_t)__popc(lives)) == 0;
-        } else if (live) {
-            filled += atomicAdd(of + b, 1u) == 0;
-        }
-    }
-    targets = __reduce_add_sync(~0u, targets);
-    filled = __reduce_add_sync(~0u, filled);
-    if (lane == 0 && targets) atomicAdd(sums, targets);
-    if (lane == 0 && filled) atomicAdd(sums + 1, filled);
-    cl.sync();
-    if (threadIdx.x < 2) all[threadIdx.x] = sums[threadIdx.x];
-    __syncthreads();
-    const float tokens = (float)max(all[0], 1u), sequences = (float)max(all[1], 1u);
-    const float same = a.reduce == ZERO_REDUCE_TOKEN ? 1.0f / tokens : 1.0f;
-    for (int64_t t = first; t < a.rows; t += step) {
-        const int64_t s = a.offsets ? sequence_of(a.offsets, a.seqs, t) : 0;
-        if (a.offsets && (s < 0 || s >= a.seqs)) {  // in front of the first sequence or behind the last
-            a.w[t] = 0.0f;
-            continue;
-        }
-        float w = a.targets[t] >= 0 ? same : 0.0f;
-        if (by_sequence && w != 0.0f) w = 1.0f / (float)__ldcg(of + clamp_offset(a.offsets[s], 0, a.rows - 1)) / sequences;
-        a.w[t] = w;
-        a.adv[t] = a.advantages[a.per_sequence ? s : t];
-        a.loss[t] = NAN;  // until its row is done
-    }
-    cl.sync();  // no CTA leaves while another reads its sums
-}
 
 // What a token's loss takes, read ahead of its row's sums.
 struct TokenIn {
@@ -914,104 +657,9 @@ __global__ void __launch_bounds__(kRowThreads) k_policy_tokens(const PolicyToken
     }
 }
 
-// The means, in a fixed order.
-__global__ void __launch_bounds__(kSetupThreads) k_policy_finish(const PolicyTokens a) {
-    __shared__ Sum sm[kSetupThreads / 32];
-    __shared__ struct {
-        float loss[2], kl[2];
-        uint32_t targets, clipped;
-    } mine;
-    const cg::cluster_group cl = cg::this_cluster();
-    if (threadIdx.x == 0) mine.targets = mine.clipped = 0;
-    wait_for_kernel_before();
-    Sum loss, kl;
-    uint32_t clipped = 0, n = 0;
-#pragma unroll 4
-    for (int64_t t = (int64_t)blockIdx.x * kSetupThreads + threadIdx.x; t < a.rows; t += (int64_t)gridDim.x * kSetupThreads) {
-        loss.add(a.w[t] != 0.0f ? a.loss[t] : 0.0f);
-        kl.add(a.kl[t]);
-        clipped += a.clipped[t] != 0.0f;
-        n += a.w[t] != 0.0f;
-    }
-    loss = cta_sum<kSetupThreads>(loss, sm);
-    kl = cta_sum<kSetupThreads>(kl, sm);
-    clipped = __reduce_add_sync(~0u, clipped);
-    n = __reduce_add_sync(~0u, n);
-    if ((threadIdx.x & 31) == 0) {
-        atomicAdd(&mine.targets, n);
-        atomicAdd(&mine.clipped, clipped);
-    }
-    if (threadIdx.x == 0) {
-        mine.loss[0] = loss.hi;
-        mine.loss[1] = loss.lo;
-        mine.kl[0] = kl.hi;
-        mine.kl[1] = kl.lo;
-    }
-    cl.sync();
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        n = mine.targets;
-        clipped = mine.clipped;
-#pragma unroll 1
-        for (unsigned i = 1; i < gridDim.x; ++i) {
-            const auto* other = cl.map_shared_rank(&mine, i);
-            loss.add(Sum{other->loss[0], other->loss[1]});
-            kl.add(Sum{other->kl[0], other->kl[1]});
-            n += other->targets;
-            clipped += other->clipped;
-        }
-        const double tokens = n ? (double)n : 1.0;
-        *a.out_loss = (float)loss.value();
-        *a.out_kl = (float)(kl.value() / tokens);
-        *a.out_clip = (float)((double)clipped / tokens);
-    }
-    cl.sync();  // no CTA leaves while the first reads its sums
-}
-
 // ---------------------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------------------
-int check_logits(const zero_logits* x) {
-    if (!x || x->rows < 0 || x->rows > INT32_MAX || x->vocab < 1 || x->vocab > (1 << 30) || x->stride < x->vocab || !type_ok(x->type)) return ZERO_ERR_INVALID_ARG;
-    if (!temperature_ok(x->temperature)) return ZERO_ERR_INVALID_ARG;
-    if (x->rows > 0 && x->stride > INT64_MAX / 8 / x->rows) return ZERO_ERR_INVALID_ARG;
-    return ZERO_OK;
-}
-
-void need_logits(CallDevice& d, const zero_logits* x) {
-    d.need(x->logits, type_size(x->type));
-    d.need(x->targets, 8);
-}
-
-template <class T>
-Rows<T> rows_of(const zero_logits* x, const float* weight) {
-    Rows<T> a;
-    a.x = (const T*)x->logits;
-    a.targets = x->targets;
-    a.weight = weight;
-    a.rows = x->rows;
-    a.vocab = x->vocab;
-    a.stride = x->stride;
-    a.k = make_scale(x->temperature);
-    a.c = (float)(1.4426950408889634 / x->temperature);
-    a.inv_t = 1.0 / x->temperature;
-    return a;
-}
-
-template <class F>
-int by_type(int32_t type, F f) {
-    if (type == ZERO_T_BF16) return f(__nv_bfloat16());
-    if (type == ZERO_T_FP16) return f(__half());
-    return f(float());
-}
-
-// CTAs per row: 1 where the rows fill the GPU, else the row is cut (into at most 8, of 4 KB at
-// least), while every SM has at most `per_sm`.
-int ctas_per_row(const zero_logits* x, int sms, int per_sm = kRowCtas) {
-    int size = 1;
-    while (size < 8 && 2 * size * x->rows <= per_sm * (int64_t)sms && x->vocab * type_size(x->type) / (2 * size) >= 4096) size *= 2;
-    return size;
-}
-
 // Whether each row goes to a warp: short rows, enough of them for every SM. 8192 bf16 rows, a warp each
 // against a CTA each: of 16 KB 25.8 us against 30.4 forward, 57 against 63 for the policy loss, the same
 // for the gradient alone; of 32 KB 45.2 against 49.6 forward, but 113 against 83 for the policy loss
@@ -1051,11 +699,8 @@ FusedPlan fused_plan(const zero_logits* x, int sms) {
     return f;
 }
 
-// CTAs of the kernels over tokens alone: a cluster of eight begins 3 us later than one CTA, which
-// it has made up at 2048 tokens (4096 of 50257 in 123 us against 129).
-int token_ctas(int64_t rows) { return rows <= 2048 ? 1 : 8; }
 int launch_finish(const PolicyTokens& p, cudaStream_t s) {
-    return launch_linked(k_policy_finish, (unsigned)token_ctas(p.rows), kSetupThreads, 0, token_ctas(p.rows), s, p);
+    return launch_linked(k_token_finish<PolicyTokens>, (unsigned)token_ctas(p.rows), kSetupThreads, 0, token_ctas(p.rows), s, p);
 }
 
 int launch_token_logp(const zero_logits* x, const float* weight, float* logp, float* lse, float* entropy, float* low,
@@ -1109,14 +754,6 @@ int launch_policy_rows(const zero_logits* x, const FusedPlan& f, const PolicyTok
     if (rc) return rc;
     return launch_finish(p, s);
 }
-
-int check_dlogits(const zero_logits* x, const void* dx, int64_t dstride) {
-    if (dstride < x->vocab || (x->rows > 0 && dstride > INT64_MAX / 8 / x->rows)) return ZERO_ERR_INVALID_ARG;
-    if (dx == x->logits && x->rows > 0 && dstride != x->stride) return ZERO_ERR_INVALID_ARG;
-    return ZERO_OK;
-}
-
-int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 }  // namespace
 }  // namespace zg
@@ -1246,6 +883,7 @@ extern "C" int zero_policy_loss(const zero_logits* x, const zero_policy* p, void
     a.lse = f + 2 * n;
     a.g = f + 3 * n;
     a.h = f + 4 * n;
+    a.of = (uint32_t*)a.h;  // free until the rows
     a.loss = f + 5 * n;
     a.kl = f + 6 * n;
     a.clipped = f + 7 * n;
@@ -1265,7 +903,7 @@ extern "C" int zero_policy_loss(const zero_logits* x, const zero_policy* p, void
     a.per_sequence = p->per_sequence;
     const int sms = d.sm_count();
     if (x->rows > 0) {
-        if ((rc = launch_linked(k_policy_setup, (unsigned)token_ctas(x->rows), kSetupThreads, 0, token_ctas(x->rows), s, a))) return rc;
+        if ((rc = launch_linked(k_token_setup<PolicyTokens>, (unsigned)token_ctas(x->rows), kSetupThreads, 0, token_ctas(x->rows), s, a))) return rc;
         const FusedPlan f = fused_plan(x, sms);
         if (f.size) return launch_policy_rows(x, f, a, p, sms, s);
         if ((rc = launch_token_logp(x, a.w, p->logp, a.lse, p->entropy, nullptr, nullptr, nullptr, sms, s))) return rc;
