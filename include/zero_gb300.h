@@ -778,6 +778,62 @@ int64_t zero_linear_logp_workspace(int64_t rows, int64_t vocab);
 int zero_linear_logp(const zero_linear* x, float* logp, float* lse, float* entropy, void* workspace,
                      int64_t workspace_bytes, void* stream);
 
+/* The k largest logits of every token, the largest first and the lower place first among equal ones (0 and
+ * -0 are equal): what a teacher hands to a student, or the alternatives to a token.
+ *   index[t * k + i]  the i-th one's place in the vocabulary
+ *   logp[t * k + i]   its log-probability z_t[index] - lse_t
+ *   lse[t]            log sum_j exp(z_t[j])
+ *   rest[t]           log of the probability outside the k, summed over them alone; -inf for none
+ * x->targets may be NULL: every row counts. Where a target is below 0 its row is not read, its indices are
+ * -1 and its results 0; which token a target is does not matter. A row of -inf alone has -inf throughout and
+ * the lowest places; of a row that holds NaN the numbers are ranked, with index -1 where they are fewer
+ * than k, and all its other results are NaN, as those of a row that holds +inf. Reads each row once.
+ * 1 <= k <= min(vocab, 512). Errors: INVALID_ARG, MISALIGNED, CUDA. */
+int zero_top_logits(const zero_logits* x, int64_t k, int64_t* index, float* logp, float* lse,
+                    float* rest, void* stream);
+
+/* The rows of a vocabulary matrix for a batch's tokens, scaled: out[t] = scale * weight[tokens[t]],
+ * computed in fp32 and rounded once. A token below 0 (padding) gets a row of zeros; a token >= vocab
+ * is not followed and gets a row of NaN.
+ *  out  device [rows, dim] of x->type, rows ld_out elements apart (>= dim); overlaps no input
+ * Errors: INVALID_ARG, MISALIGNED, CUDA. */
+typedef struct {
+    const void* weight;      /* device [vocab, dim] of `type`, aligned to the element size    */
+    const int64_t* tokens;   /* device [rows]                                                 */
+    int64_t rows;            /* 0 .. 2^31 - 1                                                 */
+    int64_t vocab, dim;      /* 1 .. 2^30                                                     */
+    int64_t ld_weight;       /* elements from one row to the next, >= dim                     */
+    int32_t type;            /* ZERO_T_*                                                      */
+    double scale;            /* finite in fp32                                                */
+} zero_embed;
+int zero_embedding(const zero_embed* x, void* out, int64_t ld_out, void* stream);
+
+/* The gradient of a function of those rows on the matrix:
+ *   dweight[v] = scale * sum of dhidden[t] over the t with tokens[t] = v, in ascending t
+ * written, with zeros in the rows of no token, or (accumulate = 1) added to what dweight holds, whose
+ * rows of no token are then neither read nor written: the gradient of a matrix that is also the output
+ * matrix. Sums in fp32 (of 32 rows at most, then of such sums), rounded once to out_type. A token
+ * outside [0, vocab) has no gradient. With views of a flat gradient buffer as dweight the result is
+ * in its place for a step. dhidden and dweight do not overlap.
+ * Rows whose addresses and lengths are multiples of 16 bytes are read and written so, others element
+ * by element. Errors: INVALID_ARG, MISALIGNED, SIZE_MISMATCH (workspace too small), CUDA. */
+typedef struct {
+    const int64_t* tokens;   /* device [rows]                                                 */
+    const void* dhidden;     /* device [rows, dim] of `type`, aligned to the element size     */
+    void* dweight;           /* device [vocab, dim] of `out_type`                             */
+    int64_t rows;            /* 0 .. 2^31 - 1                                                 */
+    int64_t vocab, dim;      /* 1 .. 2^30                                                     */
+    int64_t ld_hidden, ld_weight;  /* >= dim                                                  */
+    int32_t type, out_type;  /* ZERO_T_*                                                      */
+    double scale;            /* finite in fp32                                                */
+    int32_t accumulate;
+} zero_embed_grad;
+/* Bytes of workspace (16-byte aligned device memory, contents free before and after the call);
+ * negative for invalid sizes. Host only. */
+int64_t zero_embedding_backward_workspace(int64_t rows, int64_t vocab, int64_t dim, int32_t type);
+int zero_embedding_backward(const zero_embed_grad* x, void* workspace, int64_t workspace_bytes,
+                            void* stream);
+
 /* Global L2 norm over many separate tensors, and clipping:
  *   norm = sqrt(sum over all tensors of all squares), scale = max_norm / norm where norm >
  *   max_norm, else 1 (also when the norm is not finite: the values then pass unchanged, and a

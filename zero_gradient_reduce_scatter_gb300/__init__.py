@@ -149,6 +149,10 @@ SIGNATURES = {
     "zero_policy_loss": (ctypes.c_int, [_P, _P, _P, _I64, _P]),
     "zero_linear_logp_workspace": (_I64, [_I64, _I64]),
     "zero_linear_logp": (ctypes.c_int, [_P] * 5 + [_I64, _P]),
+    "zero_top_logits": (ctypes.c_int, [_P, _I64] + [_P] * 5),
+    "zero_embedding": (ctypes.c_int, [_P, _P, _I64, _P]),
+    "zero_embedding_backward_workspace": (_I64, [_I64, _I64, _I64, _I32]),
+    "zero_embedding_backward": (ctypes.c_int, [_P, _P, _I64, _P]),
     "zero_grads_workspace": (_I64, [_I64]),
     "zero_grads_init": (ctypes.c_int, [ctypes.POINTER(_P), _P, _I64, _P, _I64, _P]),
     "zero_grads_clip": (ctypes.c_int, [_P, ctypes.c_double, _P, _P, _P, _P]),
@@ -626,7 +630,9 @@ class ZeroOptimizer:
 # process-per-rank mode (one process per GPU); imported last: it builds on the names above
 from .sharded import ShardedZeroOptimizer  # noqa: E402
 
-# training losses and gradient clipping: what stands before the step
+# training losses, the embedding of tokens and gradient clipping: what stands before the step
+from .embed import embedding, embedding_backward  # noqa: E402
+from .distill import TopLogits, top_logits  # noqa: E402
 from .gradclip import Clipped, GradClip  # noqa: E402
 from .losses import (PolicyLoss, PreferenceLoss, TokenLogp, linear_logp, policy_loss, preference_loss,  # noqa: E402
                      token_logp, token_logp_backward)

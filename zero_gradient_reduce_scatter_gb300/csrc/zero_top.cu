@@ -1,0 +1,680 @@
+// zero_top.cu -- the k largest logits of every token with their log-probabilities, for sm_103a.
+//
+// Bound by reading [rows, vocab] logits once, beside the sums of a softmax (zero_softmax.cuh). A row is
+// read as a stream of chunks that stay in registers. The first chunk gives a threshold that at least k
+// of its values reach; what lies above the threshold so far is kept as a candidate in shared memory,
+// everything else goes into the sum of the rest at once, so that the mass outside the k is a sum of its
+// own and not a difference. Where the candidates grow too many they are cut back to about k and the
+// threshold rises. In the end they are sorted: by value, the lower place first among equal ones.
+
+#include <climits>
+
+#include "zero_rows.cuh"
+
+namespace zg {
+namespace {
+
+constexpr int kTopMost = 512;  // largest k
+
+// fp32 values as whole numbers in the same order, and back. 0 and -0 are equal; NaN does not occur.
+__device__ __forceinline__ uint32_t key_of(float x) {
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+    return __uint_as_float(key ^ ((uint32_t)((int32_t)~key >> 31) | 0x80000000u));
+}
+constexpr uint32_t kKeyLow = 0x007FFFFFu;  // -inf
+
+// A candidate: its value's key above, and below it the complement of its place, so that a larger one is the
+// better and no two are equal.
+__device__ __forceinline__ uint64_t candidate(float x, int place) { return (uint64_t)key_of(x) << 32 | (uint32_t)~place; }
+
+// What the THREADS that share a row (a CTA's, or a warp's) hold in shared memory.
+template <int THREADS, int CAP>
+struct TopSpace {
+    uint64_t cand[CAP];
+    int n;  // candidates; counts on past CAP where they did not fit
+    int sums[2][THREADS / 32];
+    float floats[THREADS / 32];
+    // for the cluster's first CTA
+    int kept;
+    float low, rest;
+};
+
+// Candidates to which they are cut back.
+__host__ __device__ constexpr int top_few(int k) { return k + k / 8 + 16; }
+
+template <class T, int THREADS, int CAP>
+struct TopRow {
+    using Space = TopSpace<THREADS, CAP>;
+    static constexpr int kRoom = CAP - 16;  // the ends of a row always fit
+    Space& sm;
+    const Scale scale;
+    const int k, id;
+    int turn = 0;           // of sm.sums
+    int n = 0;              // candidates
+    bool have = false;      // whether there is a threshold: at least k candidates are not below it
+    float low = -INFINITY;  // the threshold, and the base of the sum
+    uint64_t s[2];          // sum of 2^((x - low) C) over what is no candidate
+    uint64_t base, c2, lo2;
+
+    __device__ __forceinline__ TopRow(Space& sm, Scale scale, int k) : sm(sm), scale(scale), k(k), id(place_in_group<THREADS>()) {
+        s[0] = s[1] = base = pack2(0.0f, 0.0f);
+        c2 = pack2(scale.c, scale.c);
+        lo2 = pack2(scale.lo, scale.lo);
+        if (id == 0) sm.n = 0;
+        sync();
+    }
+    static __device__ __forceinline__ void sync() {
+        if (THREADS == 32) __syncwarp();
+        else __syncthreads();
+    }
+    // The sum over the group, in all of its threads. Also a barrier.
+    __device__ __forceinline__ int total(int x) {
+        x = __reduce_add_sync(~0u, x);
+        if (THREADS == 32) {
+            __syncwarp();
+            return x;
+        }
+        int* a = sm.sums[turn];
+        turn ^= 1;
+        if ((id & 31) == 0) a[id >> 5] = x;
+        __syncthreads();
+        x = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) x += a[w];
+        return x;
+    }
+    __device__ __forceinline__ uint32_t largest(uint32_t x) {
+        x = __reduce_max_sync(~0u, x);
+        if (THREADS == 32) return x;
+        int* a = sm.sums[turn];
+        turn ^= 1;
+        if ((id & 31) == 0) a[id >> 5] = (int)x;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) x = max(x, (uint32_t)a[w]);
+        return x;
+    }
+
+    // A key that at least k of a set reach, and at most `most` where keys alone can do that: else the
+    // k-th largest. count(v): this thread's members that are not below v. At least k reach lo, fewer
+    // than k reach hi; n: how many reach the result, INT_MAX if that was not counted.
+    template <class F>
+    __device__ __forceinline__ uint32_t cut(F count, uint32_t lo, uint32_t hi, int most, int& reach) {
+        while (reach > most && hi - lo > 1) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            const int c = total(count(value_of(mid)));
+            if (c >= k) {
+                lo = mid;
+                reach = c;
+            } else {
+                hi = mid;
+            }
+        }
+        return lo;
+    }
+    // The last place of the first `need` members of a set; count(p): this thread's members up to place p.
+    template <class F>
+    __device__ __forceinline__ int cut_places(F count, int need) {
+        int lo = -1, hi = 1 << 30;  // fewer than `need` up to lo, at least as many up to hi: a vocabulary's places are below
+        while (hi - lo > 1) {
+            const int mid = lo + (hi - lo) / 2;
+            if (total(count(mid)) >= need) hi = mid;
+            else lo = mid;
+        }
+        return hi;
+    }
+
+    // The sum taken to a higher base.
+    __device__ __forceinline__ void raise_base(float to) {
+        const float f = pow2(scaled<false>(low - base_of(to), scale));
+        s[0] = mul2(s[0], pack2(f, f));
+        s[1] = mul2(s[1], pack2(f, f));
+        low = to;
+        base = pack2(-base_of(to), -base_of(to));
+    }
+    __device__ __forceinline__ void add_one(float x) {
+        s[0] = add2(s[0], pack2(pow2(scaled<false>(x - base_of(low), scale)), 0.0f));
+    }
+    __device__ __forceinline__ void add(const uint4& v) {
+#pragma unroll
+        for (int i = 0; i < kVec<T> / 2; ++i) {
+            const uint64_t t = add2(widen2<T>(v, i), base);
+            const float2 z = unpack2(fma2(t, lo2, mul2(t, c2)));
+            s[i & 1] = add2(s[i & 1], pack2(pow2(z.x), pow2(z.y)));
+        }
+    }
+    __device__ __forceinline__ void keep(float x, int place) {
+        const int at = atomicAdd(&sm.n, 1);
+        if (at < CAP) sm.cand[at] = candidate(x, place);
+    }
+
+    // Cuts the candidates back to at most top_few(k), the k best among them.
+    __device__ __forceinline__ void cut_back() {
+        constexpr int kMine = CAP / THREADS;
+        const int few = top_few(k);
+        if (n <= few) return;
+        uint64_t mine[kMine];
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            mine[i] = id + i * THREADS < n ? sm.cand[id + i * THREADS] : 0;
+            best = max(best, (uint32_t)(mine[i] >> 32));
+        }
+        best = largest(best);
+        auto reaches = [&](float v) {
+            const uint32_t key = key_of(v);
+            int c = 0;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) c += (uint32_t)(mine[i] >> 32) >= key;
+            return c;
+        };
+        int reach = n;
+        const uint32_t key = cut(reaches, have ? max(key_of(low), kKeyLow) : kKeyLow, best + 1, few, reach);
+        int last = INT_MAX;  // among those of the key itself
+        if (reach > few) {
+            int above = 0;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) above += (uint32_t)(mine[i] >> 32) > key;
+            above = total(above);
+            last = cut_places(
+                [&](int p) {
+                    int c = 0;
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) c += (uint32_t)(mine[i] >> 32) == key && (int)~(uint32_t)mine[i] <= p;
+                    return c;
+                },
+                k - above);
+        }
+        raise_base(value_of(key));
+        have = true;
+        sync();
+        if (id == 0) sm.n = 0;
+        sync();
+        int kept = 0;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            if (mine[i] == 0) continue;
+            const uint32_t its = (uint32_t)(mine[i] >> 32);
+            if (its > key || (its == key && (int)~(uint32_t)mine[i] <= last)) {
+                sm.cand[atomicAdd(&sm.n, 1)] = mine[i];
+                ++kept;
+            } else {
+                add_one(value_of(its));
+            }
+        }
+        n = total(kept);
+    }
+
+    // Takes a chunk: `present` says which of this thread's vectors there are, vector u begins at place at + u * step.
+    // full: all threads have all of theirs.
+    __device__ __forceinline__ void chunk(uint4* q, const bool* present, int at, int step, bool full) {
+        if (have && n > CAP / 2) cut_back();
+        float limit = low;  // kept: values above it ..
+        int last = -1;      // .. and equal ones up to this place
+        const int before = n;
+        bool done = false;
+        if (have) {
+            int mine = 0;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (present[u] && max_of<T>(q[u]) > limit) mine += push(q[u], at + u * step, limit, last);
+            n += total(mine);
+            done = n <= kRoom;
+        } else {
+            int there = 0;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) there += present[u] ? kVec<T> : 0;
+            if (total(there) <= kRoom - n) {  // all of it fits
+                limit = -INFINITY;
+                last = INT_MAX;
+            } else {
+                limit = first_limit(q, present, full);
+                last = INT_MAX;
+            }
+            int mine = 0;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (present[u]) mine += push(q[u], at + u * step, limit, last);
+            n += total(mine);
+            done = n <= kRoom;
+        }
+        if (!done) {  // more than fit: the chunk's own k best, and the candidates cut back
+            sync();
+            if (id == 0) sm.n = before;
+            n = before;
+            sync();
+            cut_back();
+            pick(q, present, at, step, limit, last);
+            int mine = 0;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (present[u]) mine += push(q[u], at + u * step, limit, last);
+            n += total(mine);
+        }
+        if (limit > low || !have) {
+            if (n - before >= k || have) {
+                // at least k candidates are not below the limit
+                if (limit > low) raise_base(limit);
+                have = have || n - before >= k;
+            }
+        }
+        if (have) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (!present[u]) continue;
+                if (!(max_of<T>(q[u]) < limit)) strike(q[u], at + u * step, limit, last);
+                add(q[u]);
+            }
+        } else {  // no threshold yet: everything but NaN was kept
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (present[u]) add_missing(q[u]);
+        }
+    }
+
+private:
+    static __device__ __forceinline__ bool kept(float x, int place, float limit, int last) { return x > limit || (x == limit && place <= last); }
+
+    __device__ __forceinline__ int push(const uint4& v, int at, float limit, int last) {
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < kVec<T> / 2; ++i) {
+            const float2 x = unpack2(widen2<T>(v, i));
+            if (kept(x.x, at + 2 * i, limit, last)) {
+                keep(x.x, at + 2 * i);
+                ++c;
+            }
+            if (kept(x.y, at + 2 * i + 1, limit, last)) {
+                keep(x.y, at + 2 * i + 1);
+                ++c;
+            }
+        }
+        return c;
+    }
+    // -inf in the place of what was kept.
+    __device__ __forceinline__ void strike(uint4& v, int at, float limit, int last) {
+#pragma unroll
+        for (int i = 0; i < kVec<T> / 2; ++i) {
+            float2 x = unpack2(widen2<T>(v, i));
+            if (kept(x.x, at + 2 * i, limit, last)) x.x = -INFINITY;
+            if (kept(x.y, at + 2 * i + 1, limit, last)) x.y = -INFINITY;
+            narrow2<T>(v, i, x);
+        }
+    }
+    __device__ __forceinline__ void add_missing(const uint4& v) {
+#pragma unroll
+        for (int i = 0; i < kVec<T> / 2; ++i) {
+            const float2 x = unpack2(widen2<T>(v, i));
+            if (x.x != x.x || x.y != x.y) s[0] = pack2(NAN, NAN);
+        }
+    }
+
+    // A value that at least k of the chunk reach, and not many more: by the maxima of groups of four.
+    __device__ __forceinline__ float first_limit(const uint4* q, const bool* present, bool full) {
+        constexpr int kGroups = kVec<T> / 4;
+        float top[kUnroll * kGroups];
+        float most = -INFINITY, least = INFINITY;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                const float2 a = unpack2(widen2<T>(q[u], 2 * g)), b = unpack2(widen2<T>(q[u], 2 * g + 1));
+                const float m = fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y));  // a NaN is passed over
+                top[u * kGroups + g] = present[u] && m == m ? m : -INFINITY;
+                most = fmaxf(most, top[u * kGroups + g]);
+                least = fminf(least, top[u * kGroups + g]);
+            }
+        }
+        const uint32_t best = largest(key_of(most));
+        // each thread has a group that reaches the least of all threads' largest
+        uint32_t lo = kKeyLow;
+        if (full) lo = ~largest(~key_of(k <= THREADS ? most : least));
+        int reach = INT_MAX;
+        const uint32_t key = cut(
+            [&](float v) {
+                int c = 0;
+#pragma unroll
+                for (int i = 0; i < kUnroll * kGroups; ++i) c += top[i] >= v;
+                return c;
+            },
+            lo, best + 1, k + k / 4 + 8, reach);
+        return value_of(key);
+    }
+
+    // The limit that the chunk's k best are kept by. At least k values are above (limit, last), or fewer and all fit.
+    __device__ __forceinline__ void pick(const uint4* q, const bool* present, int at, int step, float& limit, int& last) {
+        auto members = [&](auto is) {
+            int c = 0;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (!present[u]) continue;
+#pragma unroll
+                for (int i = 0; i < kVec<T> / 2; ++i) {
+                    const float2 x = unpack2(widen2<T>(q[u], i));
+                    c += is(x.x, at + u * step + 2 * i) + is(x.y, at + u * step + 2 * i + 1);
+                }
+            }
+            return c;
+        };
+        if (have) {  // the candidates' threshold may have risen
+            limit = low;
+            last = -1;
+        }
+        const int few = min(top_few(k), kRoom - n);
+        int reach = total(members([&](float x, int p) { return (int)kept(x, p, limit, last); }));
+        if (reach <= few) return;
+        uint32_t best = 0;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (!present[u]) continue;
+            const float m = max_of<T>(q[u]);
+            if (m == m) best = max(best, key_of(m));
+        }
+        best = largest(best);
+        const uint32_t from = last < 0 ? key_of(limit) + 1 : max(key_of(limit), kKeyLow);
+        const uint32_t key = cut([&](float v) { return members([&](float x, int) { return (int)(x >= v); }); }, from, best + 1, few, reach);
+        limit = value_of(key);
+        last = INT_MAX;
+        if (reach > few) {
+            const float v = limit;
+            const int above = total(members([&](float x, int) { return (int)(x > v); }));
+            last = cut_places([&](int most) { return members([&](float x, int p) { return (int)(x == v && p <= most); }); }, k - above);
+        }
+    }
+};
+
+// Sorts the first n of a list of at most N, the largest first; by one warp in registers or by all threads in place.
+// 0 fills up, and is smaller than any candidate.
+template <int R>
+__device__ __forceinline__ void sort_in_warp(uint64_t* list, int n) {
+    const int lane = threadIdx.x & 31;
+    uint64_t v[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = r * 32 + lane < n ? list[r * 32 + lane] : 0;
+#pragma unroll
+    for (int size = 2; size <= 32 * R; size *= 2) {
+#pragma unroll
+        for (int stride = size / 2; stride > 0; stride /= 2) {
+            if (stride >= 32) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int o = r ^ (stride / 32);
+                    if (o > r) {
+                        const bool down = ((r * 32 + lane) & size) == 0;
+                        const uint64_t a = v[r], b = v[o];
+                        if ((a < b) == down) {
+                            v[r] = b;
+                            v[o] = a;
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const uint64_t other = __shfl_xor_sync(~0u, v[r], stride);
+                    const bool down = ((r * 32 + lane) & size) == 0, first = (lane & stride) == 0;
+                    const bool greater = other > v[r];
+                    if (greater == (first == down)) v[r] = other;
+                }
+            }
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (r * 32 + lane < n) list[r * 32 + lane] = v[r];
+}
+
+template <int THREADS>
+__device__ __forceinline__ void sort_in_place(uint64_t* list, int n, int size_all) {
+    for (int i = n + threadIdx.x; i < size_all; i += THREADS) list[i] = 0;
+    __syncthreads();
+    for (int size = 2; size <= size_all; size *= 2) {
+        for (int stride = size / 2; stride > 0; stride /= 2) {
+            for (int p = threadIdx.x; p < size_all / 2; p += THREADS) {
+                const int i = 2 * p - (p & (stride - 1)), j = i + stride;
+                const uint64_t a = list[i], b = list[j];
+                if ((a < b) == ((i & size) == 0)) {
+                    list[i] = b;
+                    list[j] = a;
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// log s in two numbers, hi exact (as in finish_row), for s in fp32's range; sums of pow2 err low.
+__device__ __forceinline__ float2 log_parts(float s) {
+    constexpr float kLn2Hi = 2839.0f / 4096.0f, kLn2Lo = 3.1946184945309e-5f;
+    const uint32_t bits = __float_as_uint(s);
+    const bool plain = s >= 0x1p-126f && s < INFINITY;
+    const float n = plain ? (float)((int)(bits >> 23) - 127) : 0.0f, f = plain ? __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u) : s;
+    return make_float2(n * kLn2Hi, logf(f) + fmaf(n, kLn2Lo, kPow2Low));
+}
+
+struct TopOut {
+    int64_t* index;
+    float *logp, *lse, *rest;
+};
+
+template <class T, int THREADS, int CAP>
+__global__ void __launch_bounds__(kRowThreads, THREADS == 32 ? 3 : 4) k_top_rows(const Rows<T> a, int k, int size, const TopOut out) {
+    using Row = TopRow<T, THREADS, CAP>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    typename Row::Space& sm = reinterpret_cast<typename Row::Space*>(smem)[THREADS == 32 ? threadIdx.x >> 5 : 0];
+    wait_for_kernel_before();
+    let_next_kernel_start();
+    const int64_t t = row_of<THREADS>(size);
+    if (THREADS == 32 && t >= a.rows) return;
+    const int rank = THREADS == 32 ? 0 : (int)(blockIdx.x % size), id = place_in_group<THREADS>();
+    if (a.targets && a.targets[t] < 0) {
+        if (rank == 0) {
+            for (int i = id; i < k; i += THREADS) {
+                out.index[t * k + i] = -1;
+                out.logp[t * k + i] = 0.0f;
+            }
+            if (id == 0) out.lse[t] = out.rest[t] = 0.0f;
+        }
+        return;
+    }
+    const T* x = a.x + t * a.stride;
+    const Slice<T> part(x, a.vocab, rank, size);
+    uint4 q[kUnroll];
+    bool present[kUnroll];
+    auto load = [&](int from) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = from + id + u * THREADS;
+            if (i < part.n) q[u] = THREADS == 32 ? __ldg(part.v + i) : load_once(part.v + i);
+        }
+    };
+    load(0);
+    Row row(sm, a.k, k);
+    {
+        int mine = 0;
+        if (id < part.head) {
+            const float v = widen(x[id]);
+            if (v == v) {
+                row.keep(v, id);
+                mine = 1;
+            } else {
+                row.s[0] = pack2(NAN, NAN);
+            }
+        }
+        if (part.head) row.n += row.total(mine);
+    }
+    for (int from = 0; from < part.n; from += kUnroll * THREADS) {
+        uint4 v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            v[u] = q[u];
+            present[u] = from + id + u * THREADS < part.n;
+        }
+        load(from + kUnroll * THREADS);
+        row.chunk(v, present, part.first + (from + id) * kVec<T>, THREADS * kVec<T>, from + kUnroll * THREADS <= part.n);
+    }
+    if (part.tail) {
+        int mine = 0;
+        if (id < part.tail) {
+            const float v = widen(x[part.tail_at + id]);
+            if (row.have ? v > row.low : v == v) {
+                row.keep(v, part.tail_at + id);
+                mine = 1;
+            } else if (row.have || v != v) {
+                row.add_one(v);
+            }
+        }
+        row.n += row.total(mine);
+    }
+    row.cut_back();
+
+    // The sum of what is no candidate, and the other CTAs' candidates and sums.
+    auto group_sum = [&](float v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+        if (THREADS == 32) return v;
+        Row::sync();
+        if ((id & 31) == 0) sm.floats[id >> 5] = v;
+        Row::sync();
+        v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) v += sm.floats[w];
+        return v;
+    };
+    float lows[8], rests[8];
+    if (THREADS != 32 && size > 1) {
+        cg::cluster_group cl = cg::this_cluster();
+        const float2 s2 = unpack2(add2(row.s[0], row.s[1]));
+        const float mine = group_sum(s2.x + s2.y);
+        if (id == 0) {
+            sm.kept = row.n;
+            sm.low = row.low;
+            sm.rest = mine;
+        }
+        cl.sync();
+        if (rank == 0) {
+            for (int r = 1; r < size; ++r) {
+                const typename Row::Space* other = cl.map_shared_rank(&sm, r);
+                const int more = other->kept;
+                if (row.n + more > Row::kRoom) row.cut_back();
+                for (int i = id; i < more; i += THREADS) sm.cand[row.n + i] = other->cand[i];
+                row.n += more;
+                Row::sync();
+                if (id == 0) sm.n = row.n;
+                Row::sync();
+            }
+            row.cut_back();
+        }
+#pragma unroll
+        for (int r = 1; r < 8; ++r) {
+            lows[r] = -INFINITY;
+            rests[r] = 0.0f;
+            if (rank == 0 && r < size) {
+                const typename Row::Space* other = cl.map_shared_rank(&sm, r);
+                lows[r] = other->low;
+                rests[r] = other->rest;
+            }
+        }
+        cl.sync();  // the others may leave
+        if (rank != 0) return;
+    }
+    Row::sync();
+    const int n = row.n;
+    if (THREADS == 32 || n <= 128) {
+        if (THREADS == 32 || id < 32) {
+            if (n <= 64) sort_in_warp<2>(sm.cand, n);
+            else sort_in_warp<4>(sm.cand, n);
+        }
+        Row::sync();
+    } else if (THREADS != 32) {
+        int all = 256;
+        while (all < n) all *= 2;
+        sort_in_place<THREADS>(sm.cand, n, all);
+    }
+    // The rest over a base that none of its terms exceeds, and all over the row's maximum.
+    const float top = n > 0 ? value_of((uint32_t)(sm.cand[0] >> 32)) : -INFINITY;
+    float under = row.low;
+    if (n > k) under = fmaxf(under, value_of((uint32_t)(sm.cand[k] >> 32)));
+    if (THREADS != 32 && size > 1) {
+#pragma unroll
+        for (int r = 1; r < 8; ++r) under = fmaxf(under, lows[r]);
+    }
+    const float top_base = base_of(top), under_base = base_of(under);
+    row.raise_base(under);
+    const float2 s2 = unpack2(add2(row.s[0], row.s[1]));
+    float rest = s2.x + s2.y, sel = 0.0f;
+    for (int i = id; i < n; i += THREADS) {
+        const float v = value_of((uint32_t)(sm.cand[i] >> 32));
+        if (i < k) sel += pow2(scaled<false>(v - top_base, a.k));
+        else rest += pow2(scaled<false>(v - under_base, a.k));
+    }
+    rest = group_sum(rest);
+    sel = group_sum(sel);
+    if (THREADS != 32 && size > 1) {
+#pragma unroll
+        for (int r = 1; r < 8; ++r) rest += r < size ? rests[r] * pow2(scaled<false>(lows[r] - under_base, a.k)) : 0.0f;
+    }
+    const float inv_t = (float)a.inv_t;
+    const float total = sel + rest * pow2(scaled<false>(under_base - top_base, a.k));
+    const float2 all = log_parts(total), outside = log_parts(rest);
+    const bool nothing = total == 0.0f;  // -inf alone
+    for (int i = id; i < k; i += THREADS) {
+        const uint64_t its = i < n ? sm.cand[i] : 0;
+        const float v = value_of((uint32_t)(its >> 32));
+        out.index[t * k + i] = i < n ? (int64_t)(int)~(uint32_t)its : -1;
+        out.logp[t * k + i] = i >= n ? NAN : nothing ? -INFINITY : ((v - top_base) * inv_t - all.x) - all.y;
+    }
+    if (id == 0) {
+        out.lse[t] = nothing ? -INFINITY : fmaf(top_base, inv_t, all.x) + all.y;
+        out.rest[t] = rest == 0.0f && total == total ? -INFINITY : ((under_base - top_base) * inv_t + (outside.x - all.x)) + (outside.y - all.y);
+    }
+}
+
+template <class T, int THREADS, int CAP>
+int launch_top(const zero_logits* x, int k, int size, const TopOut& out, unsigned grid, cudaStream_t s) {
+    constexpr size_t bytes = sizeof(TopSpace<THREADS, CAP>) * (THREADS == 32 ? kRowThreads / 32 : 1);
+    auto* kernel = k_top_rows<T, THREADS, CAP>;
+    if (bytes > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e != cudaSuccess) return record_cuda_error(e);
+    }
+    return launch_linked(kernel, grid, kRowThreads, bytes, size, s, rows_of<T>(x, nullptr), k, size, out);
+}
+
+// Rows of up to this many bytes, enough of them for every SM and short lists: a warp each.
+constexpr int64_t kTopShort = 16384;
+constexpr int kTopShortMost = 64;
+
+}  // namespace
+}  // namespace zg
+
+using namespace zg;
+
+extern "C" int zero_top_logits(const zero_logits* x, int64_t k, int64_t* index, float* logp, float* lse, float* rest, void* stream) {
+    int rc = check_logits(x);
+    if (!rc && (k < 1 || k > kTopMost || k > x->vocab)) rc = ZERO_ERR_INVALID_ARG;
+    if (rc || x->rows == 0) return rc;
+    CallDevice d(x->logits, stream);
+    d.need(x->logits, type_size(x->type));
+    d.optional(x->targets, 8);
+    d.need(index, 8);
+    d.need(logp, 4);
+    d.need(lse, 4);
+    d.need(rest, 4);
+    if (d.rc) return d.rc;
+    const int sms = d.sm_count(), most = (int)k;
+    const TopOut out = {index, logp, lse, rest};
+    cudaStream_t s = (cudaStream_t)stream;
+    return by_type(x->type, [&](auto tag) {
+        using T = decltype(tag);
+        if (x->vocab * type_size(x->type) <= kTopShort && most <= kTopShortMost && x->rows >= 8 * (int64_t)sms)
+            return launch_top<T, 32, 256>(x, most, 1, out, (unsigned)((x->rows + kRowThreads / 32 - 1) / (kRowThreads / 32)), s);
+        const int size = ctas_per_row(x, sms);
+        const unsigned grid = (unsigned)(x->rows * size);
+        return most <= 128 ? launch_top<T, kRowThreads, 512>(x, most, size, out, grid, s) : launch_top<T, kRowThreads, 2048>(x, most, size, out, grid, s);
+    });
+}
