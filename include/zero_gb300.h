@@ -792,6 +792,57 @@ int zero_linear_logp(const zero_linear* x, float* logp, float* lse, float* entro
 int zero_top_logits(const zero_logits* x, int64_t k, int64_t* index, float* logp, float* lse,
                     float* rest, void* stream);
 
+/* Distillation: the divergence of the student's q = softmax(z) from a teacher's most likely tokens, per
+ * token with a target. Entry i of a token's list is the place index[t * k + i] with the teacher's
+ * log-probability teacher_logp[t * k + i], at the same temperature; one whose index is below 0 or whose
+ * log-probability is -inf is not there (lists may be shorter than k). With p_i and q_i an entry's two
+ * probabilities, and the rest of the vocabulary
+ *   ZERO_TAIL_REST         as one more entry: q_rest = sum of q outside the list, p_rest =
+ *                          exp(teacher_rest[t]), or max(1 - sum p_i, 2^-24) where teacher_rest is NULL;
+ *                          no entry where the list is the whole vocabulary
+ *   ZERO_TAIL_DROP         left out of D (its q still lowers the list's)
+ *   ZERO_TAIL_RENORMALISE  the same, with p_i / sum p_i for p_i
+ *   ZERO_DISTILL_FORWARD   D = sum p (log p - log q)
+ *   ZERO_DISTILL_REVERSE   D = sum q (log q - log p)                          (with ZERO_TAIL_REST only)
+ *   ZERO_DISTILL_JS        D = mix sum p (log p - log m) + (1 - mix) sum q (log q - log m),
+ *                          m = mix p + (1 - mix) q                            (with ZERO_TAIL_REST only)
+ * L_t = kl_coef D - ce_coef log q_target, loss = sum of w_t L_t with the weights of zero_policy_loss; a
+ * coefficient of 0 leaves its term out, also an infinite one. A p = 0 or q = 0 adds 0 where it is the
+ * factor; D is infinite where a p > 0 meets q = 0 (forward) or a q > 0 meets p_rest = 0 (reverse, whose
+ * gradient is then not defined). The rest's sum is formed over the rest alone, to full precision where
+ * it is small.
+ * A token whose list names a place twice or one past the vocabulary, or whose target is past it, has
+ * NaN results and a NaN gradient row. Reads and writes each row of logits once where it fits in shared
+ * memory, else it reads it twice. */
+#define ZERO_DISTILL_FORWARD 0
+#define ZERO_DISTILL_REVERSE 1
+#define ZERO_DISTILL_JS      2
+#define ZERO_TAIL_REST        0
+#define ZERO_TAIL_DROP        1
+#define ZERO_TAIL_RENORMALISE 2
+typedef struct {
+    const int64_t* index;       /* device [rows, k]                                           */
+    const float* teacher_logp;  /* device [rows, k]                                           */
+    const float* teacher_rest;  /* device [rows], or NULL                                     */
+    const int64_t* offsets;     /* as for zero_policy                                         */
+    int64_t seqs, k;            /* 1 <= k <= min(vocab, 512); vocab <= 2^20                   */
+    double mix;                 /* in (0, 1)                                                  */
+    double kl_coef, ce_coef;    /* finite in fp32                                             */
+    int32_t kind;               /* ZERO_DISTILL_*                                             */
+    int32_t tail;               /* ZERO_TAIL_*                                                */
+    int32_t reduce;             /* ZERO_REDUCE_*                                              */
+    /* results, device */
+    float* loss;                /* [1]                                                        */
+    float* kl;                  /* [1] mean D over the targets                                */
+    float* token_kl;            /* [rows] D                                                   */
+    float* logp;                /* [rows] log q_target                                        */
+    void* dlogits;              /* [rows, vocab] as for zero_preference                       */
+    int64_t dstride;
+} zero_distill;
+int64_t zero_distill_workspace(int64_t rows);
+int zero_distill_loss(const zero_logits* x, const zero_distill* p, void* workspace,
+                      int64_t workspace_bytes, void* stream);
+
 /* The rows of a vocabulary matrix for a batch's tokens, scaled: out[t] = scale * weight[tokens[t]],
  * computed in fp32 and rounded once. A token below 0 (padding) gets a row of zeros; a token >= vocab
  * is not followed and gets a row of NaN.

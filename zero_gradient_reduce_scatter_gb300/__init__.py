@@ -150,6 +150,8 @@ SIGNATURES = {
     "zero_linear_logp_workspace": (_I64, [_I64, _I64]),
     "zero_linear_logp": (ctypes.c_int, [_P] * 5 + [_I64, _P]),
     "zero_top_logits": (ctypes.c_int, [_P, _I64] + [_P] * 5),
+    "zero_distill_workspace": (_I64, [_I64]),
+    "zero_distill_loss": (ctypes.c_int, [_P, _P, _P, _I64, _P]),
     "zero_embedding": (ctypes.c_int, [_P, _P, _I64, _P]),
     "zero_embedding_backward_workspace": (_I64, [_I64, _I64, _I64, _I32]),
     "zero_embedding_backward": (ctypes.c_int, [_P, _P, _I64, _P]),
@@ -632,7 +634,7 @@ from .sharded import ShardedZeroOptimizer  # noqa: E402
 
 # training losses, the embedding of tokens and gradient clipping: what stands before the step
 from .embed import embedding, embedding_backward  # noqa: E402
-from .distill import TopLogits, top_logits  # noqa: E402
+from .distill import DistillLoss, TopLogits, distill_loss, top_logits  # noqa: E402
 from .gradclip import Clipped, GradClip  # noqa: E402
 from .losses import (PolicyLoss, PreferenceLoss, TokenLogp, linear_logp, policy_loss, preference_loss,  # noqa: E402
                      token_logp, token_logp_backward)

@@ -22,8 +22,8 @@ LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 # kernels of the losses and of the clipping are the same in both.
 CHECKED_LIB_PATH = os.path.join(BUILD_DIR, "libzero_gb300_checked.so")
 
-SOURCES = ["zero_kernels.cu", "zero_api.cpp", "zero_noalloc.cu", "zero_logits.cu", "zero_linear.cu", "zero_top.cu", "zero_embed.cu",
-           "zero_grads.cu"]
+SOURCES = ["zero_kernels.cu", "zero_api.cpp", "zero_noalloc.cu", "zero_logits.cu", "zero_linear.cu", "zero_top.cu", "zero_distill.cu",
+           "zero_embed.cu", "zero_grads.cu"]
 HEADERS = ["zero_internal.h", "zero_host.h", "zero_softmax.cuh", "zero_sum.cuh", "zero_rows.cuh", "zero_tcgen05.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

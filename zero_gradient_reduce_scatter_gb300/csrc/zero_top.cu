@@ -37,6 +37,7 @@ struct TopSpace {
     int n;  // candidates; counts on past CAP where they did not fit
     int sums[2][THREADS / 32];
     float floats[THREADS / 32];
+    unsigned long long gone[THREADS / 32];
     // for the cluster's first CTA
     int kept;
     float low, rest;
@@ -194,6 +195,9 @@ struct TopRow {
         if (id == 0) sm.n = 0;
         sync();
         int kept = 0;
+        // Candidates lie in no fixed order: what is dropped is added up in whole numbers, of 2^-44 of the
+        // threshold's own term, so that equal calls give equal bits.
+        unsigned long long gone = 0;
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             if (mine[i] == 0) continue;
@@ -202,10 +206,20 @@ struct TopRow {
                 sm.cand[atomicAdd(&sm.n, 1)] = mine[i];
                 ++kept;
             } else {
-                add_one(value_of(its));
+                gone += __float2ull_rn(pow2(scaled<false>(value_of(its) - base_of(low), scale)) * 0x1p44f);
             }
         }
+        const unsigned high = __reduce_add_sync(~0u, (unsigned)(gone >> 22)), rest = __reduce_add_sync(~0u, (unsigned)gone & 0x3FFFFFu);
+        gone = ((unsigned long long)high << 22) + rest;
+        if (THREADS > 32 && (id & 31) == 0) sm.gone[id >> 5] = gone;
         n = total(kept);
+        if (id == 0) {
+            if (THREADS > 32) {
+                gone = 0;
+                for (int w = 0; w < THREADS / 32; ++w) gone += sm.gone[w];
+            }
+            s[0] = add2(s[0], pack2(__ull2float_rn(gone) * 0x1p-44f, 0.0f));
+        }
     }
 
     // Takes a chunk: `present` says which of this thread's vectors there are, vector u begins at place at + u * step.
@@ -493,7 +507,7 @@ __global__ void __launch_bounds__(kRowThreads, THREADS == 32 ? 3 : 4) k_top_rows
         }
     };
     load(0);
-    Row row(sm, a.k, k);
+    Row row(sm, a.k, k + 1);  // one more: the largest of the rest, the base of its sum
     {
         int mine = 0;
         if (id < part.head) {
@@ -597,12 +611,8 @@ __global__ void __launch_bounds__(kRowThreads, THREADS == 32 ? 3 : 4) k_top_rows
     }
     // The rest over a base that none of its terms exceeds, and all over the row's maximum.
     const float top = n > 0 ? value_of((uint32_t)(sm.cand[0] >> 32)) : -INFINITY;
-    float under = row.low;
-    if (n > k) under = fmaxf(under, value_of((uint32_t)(sm.cand[k] >> 32)));
-    if (THREADS != 32 && size > 1) {
-#pragma unroll
-        for (int r = 1; r < 8; ++r) under = fmaxf(under, lows[r]);
-    }
+    // (its largest: every CTA's threshold is one that k + 1 candidates reach)
+    const float under = n > k ? value_of((uint32_t)(sm.cand[k] >> 32)) : row.low;
     const float top_base = base_of(top), under_base = base_of(under);
     row.raise_base(under);
     const float2 s2 = unpack2(add2(row.s[0], row.s[1]));
