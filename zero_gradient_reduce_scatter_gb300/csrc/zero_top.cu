@@ -1,13 +1,16 @@
 // zero_top.cu -- the k largest logits of every token with their log-probabilities, for sm_103a.
 //
 // Bound by reading [rows, vocab] logits once, beside the sums of a softmax (zero_softmax.cuh). A row is
-// read as a stream of chunks that stay in registers. The first chunk gives a threshold that at least k
-// of its values reach; what lies above the threshold so far is kept as a candidate in shared memory,
-// everything else goes into the sum of the rest at once, so that the mass outside the k is a sum of its
-// own and not a difference. Where the candidates grow too many they are cut back to about k and the
-// threshold rises. In the end they are sorted: by value, the lower place first among equal ones.
+// read as a stream without a barrier: every thread leaves the largest value and the sum of each segment
+// of a few vectors of its own. The largest values give a threshold that more than k values of the row
+// reach, and hardly more; the few segments that reach it are read again (from L2), their values above it
+// become candidates, and their sums are formed once more without those. So the probability outside the k
+// is a sum of its own, not a difference. The candidates are sorted: by value, the lower place first among
+// equal ones. Rows that this does not fit (floods of equal values, nothing but -inf, values too far
+// apart for one base) are taken again chunk by chunk, in a way that holds for all (TopRow::chunk).
 
 #include <climits>
+#include <type_traits>
 
 #include "zero_rows.cuh"
 
@@ -30,25 +33,43 @@ constexpr uint32_t kKeyLow = 0x007FFFFFu;  // -inf
 // better and no two are equal.
 __device__ __forceinline__ uint64_t candidate(float x, int place) { return (uint64_t)key_of(x) << 32 | (uint32_t)~place; }
 
-// What the THREADS that share a row (a CTA's, or a warp's) hold in shared memory.
+// What the THREADS that share a row (a CTA's, or a warp's) hold in shared memory, and behind it the largest value and the
+// sum of every thread's segments, [segments][THREADS] each.
+constexpr int kSegments = 16, kShortSegments = 32;
 template <int THREADS, int CAP>
 struct TopSpace {
-    uint64_t cand[CAP];
-    int n;  // candidates; counts on past CAP where they did not fit
+    // segments that reach the threshold: about as many as values, which are k + k / 4 and some more
+    static constexpr int kHot = THREADS == 32 ? 160 : CAP == 512 ? 384 : CAP == 1024 ? 512 : 1024;
+    alignas(16) uint64_t cand[CAP];
+    int n;                   // candidates; counts on past CAP where they did not fit
+    int hots;
+    uint32_t hot[kHot];      // segment * THREADS + thread
+    uint32_t keys[2 * THREADS];  // of every thread's largest values, of half its vectors each
     int sums[2][THREADS / 32];
-    float floats[THREADS / 32];
+    float2 floats[THREADS / 32];
+    float bases[THREADS / 32];
     unsigned long long gone[THREADS / 32];
+    uint32_t key;            // the threshold's
     // for the cluster's first CTA
     int kept;
     float low, rest;
+
+    __device__ __forceinline__ float* largest() { return reinterpret_cast<float*>(this + 1); }
 };
 
 // Candidates to which they are cut back.
 __host__ __device__ constexpr int top_few(int k) { return k + k / 8 + 16; }
 
+// What a row has come to: candidates, the threshold, and this thread's sum over it as a base.
+struct Taken {
+    int n;
+    float low, sum;
+};
+
 template <class T, int THREADS, int CAP>
 struct TopRow {
     using Space = TopSpace<THREADS, CAP>;
+    static constexpr int kRanked = THREADS == 32 ? 128 : CAP <= 1024 ? 2 * THREADS : 0;  // so many candidates are ranked by counting
     static constexpr int kRoom = CAP - 16;  // the ends of a row always fit
     Space& sm;
     const Scale scale;
@@ -64,8 +85,24 @@ struct TopRow {
         s[0] = s[1] = base = pack2(0.0f, 0.0f);
         c2 = pack2(scale.c, scale.c);
         lo2 = pack2(scale.lo, scale.lo);
-        if (id == 0) sm.n = 0;
         sync();
+        if (id == 0) sm.n = sm.hots = 0;
+        sync();
+    }
+    // What has been taken of a row.
+    __device__ __forceinline__ TopRow(Space& sm, Scale scale, int k, const Taken& t) : sm(sm), scale(scale), k(k), id(place_in_group<THREADS>()) {
+        s[0] = pack2(t.sum, 0.0f);
+        s[1] = pack2(0.0f, 0.0f);
+        base = pack2(-base_of(t.low), -base_of(t.low));
+        c2 = pack2(scale.c, scale.c);
+        lo2 = pack2(scale.lo, scale.lo);
+        n = t.n;
+        low = t.low;
+        have = n >= k;
+    }
+    __device__ __forceinline__ Taken taken() const {
+        const float2 f = unpack2(add2(s[0], s[1]));
+        return {n, low, f.x + f.y};
     }
     static __device__ __forceinline__ void sync() {
         if (THREADS == 32) __syncwarp();
@@ -222,6 +259,248 @@ struct TopRow {
         }
     }
 
+    // ---- the usual way -----------------------------------------------------------------
+    // A segment is `vectors` vectors of a thread, THREADS apart; the row's are numbered through. 2^(x C - from - kDown),
+    // with the product inside the fused operation, so that differences of any large values are kept.
+    __device__ __forceinline__ void term(uint64_t (&sum)[2], int i, uint64_t x, uint64_t from) const {
+        const float2 z = unpack2(fma2(x, lo2, fma2(x, c2, from)));
+        sum[i & 1] = add2(sum[i & 1], pack2(pow2(z.x), pow2(z.y)));
+    }
+
+    // A whole row, or a CTA's share of it, of which each thread has a vector. False: it has to be taken the other way.
+    __device__ __forceinline__ bool fast(const Slice<T>& part, const T* x, int vectors) {
+        const int per = vectors * THREADS, segments = (part.n + per - 1) / per;
+        float* const tops = sm.largest();
+        float* const segs = tops + segments * THREADS;
+        float halves[2] = {-INFINITY, -INFINITY}, base_c = 0.0f;
+        uint64_t from = 0;
+        float least = INFINITY;  // of the segments' largest values
+        float top = -INFINITY;
+        uint64_t sum[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
+        constexpr int kStep = kUnroll * THREADS;
+        const int steps = (part.n + kStep - 1) / kStep;
+        int left = vectors;  // of the segment at hand
+        float* its_top = tops + id;
+        float* its_sum = segs + id;
+        auto load = [&](uint4* q, int c) {
+            const uint4* v = part.v + c * kStep + id;
+            if ((c + 1) * kStep <= part.n) {
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) q[u] = THREADS == 32 ? __ldg(v + u * THREADS) : load_once(v + u * THREADS);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    q[u] = lowest();
+                    if (c * kStep + id + u * THREADS < part.n) q[u] = THREADS == 32 ? __ldg(v + u * THREADS) : load_once(v + u * THREADS);
+                }
+            }
+        };
+        auto use = [&](const uint4* q, int c) {
+            const float half = largest_of(q), other = largest_of(q + kUnroll / 2), its = fmaxf(half, other);
+            halves[0] = fmaxf(halves[0], half);
+            halves[1] = fmaxf(halves[1], other);
+            top = fmaxf(top, its);
+            if (c == 0) {  // the base: the least of the warp's largest first values
+                float low = its;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(~0u, low, o));
+                base_c = low * scale.c;
+                from = pack2(-base_c - kDown, -base_c - kDown);
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+#pragma unroll
+                for (int i = 0; i < kVec<T> / 2; ++i) term(sum, i, widen2<T>(q[u], i), from);
+                if (THREADS == 32) {  // a segment each
+                    const int at = (c * kUnroll + u) * THREADS;
+                    if (at < part.n) {
+                        const float2 f = unpack2(add2(sum[0], sum[1]));
+                        const float largest = fmaxf(-INFINITY, max_of<T>(q[u]));
+                        tops[at + id] = largest;
+                        segs[at + id] = f.x + f.y;
+                        if (at + id < part.n) least = fminf(least, largest);
+                    }
+                    sum[0] = sum[1] = pack2(0.0f, 0.0f);
+                }
+            }
+            if (THREADS > 32) {
+                left -= kUnroll;
+                if (left == 0 || c == steps - 1) {
+                    const float2 f = unpack2(add2(sum[0], sum[1]));
+                    *its_top = top;
+                    *its_sum = f.x + f.y;
+                    its_top += THREADS;
+                    its_sum += THREADS;
+                    if ((c / (vectors / kUnroll)) * per + id < part.n) least = fminf(least, top);
+                    sum[0] = sum[1] = pack2(0.0f, 0.0f);
+                    top = -INFINITY;
+                    left = vectors;
+                }
+            }
+        };
+        {
+            uint4 a[kUnroll], b[kUnroll];
+            load(a, 0);
+            for (int c = 0;;) {  // the next vectors are on their way beside these
+                if (c + 1 < steps) load(b, c + 1);
+                use(a, c);
+                if (++c >= steps) break;
+                if (c + 1 < steps) load(a, c + 1);
+                use(b, c);
+                if (++c >= steps) break;
+            }
+        }
+        if ((id & 31) == 0) sm.bases[id >> 5] = base_c;
+
+        // the threshold
+        const float most = fmaxf(halves[0], halves[1]);
+        float limit;
+        if (kRanked > 0 && THREADS > 32) {  // by the threads' largest values, which one warp looks through
+            sm.keys[id] = key_of(halves[0]);
+            sm.keys[THREADS + id] = key_of(halves[1]);
+            sync();
+            if (id < 32) {
+                constexpr int kEach = 2 * THREADS / 32;
+                uint32_t mine[kEach], lo = ~0u, hi = 0;
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) {
+                    mine[i] = sm.keys[id + 32 * i];
+                    lo = min(lo, mine[i]);
+                    hi = max(hi, mine[i]);
+                }
+                lo = __reduce_min_sync(~0u, lo);
+                hi = __reduce_max_sync(~0u, hi) + 1;
+                int reach = 2 * THREADS;
+                while (reach > k + 4 && hi - lo > 1) {
+                    const uint32_t mid = lo + (hi - lo) / 2;
+                    int c = 0;
+#pragma unroll
+                    for (int i = 0; i < kEach; ++i) c += mine[i] >= mid;
+                    c = __reduce_add_sync(~0u, c);
+                    if (c >= k) {
+                        lo = mid;
+                        reach = c;
+                    } else {
+                        hi = mid;
+                    }
+                }
+                if (id == 0) sm.key = lo;
+            }
+            sync();
+            limit = value_of(sm.key);
+        } else {  // by the segments' largest values
+            const int groups = THREADS == 32 ? part.n : (segments - 1) * THREADS + min(THREADS, part.n - (segments - 1) * per);
+            if (groups < 2 * k) return false;
+            const uint32_t best = largest(key_of(most)), lo = ~largest(~key_of(k <= THREADS ? most : least));
+            int reach = INT_MAX;
+            const uint32_t key = cut(
+                [&](float v) {
+                    int c = 0;
+                    for (int g = 0; g < segments; ++g) c += tops[g * THREADS + id] >= v;
+                    return c;
+                },
+                lo, best + 1, k + k / 4 + 8, reach);
+            limit = value_of(key);
+        }
+        // not -inf, and no base so far above it that its terms are too small to count, or so far below that they overflow
+        const float gap = fabsf(base_c) < INFINITY ? base_of_rest(limit, base_c) : INFINITY;
+        if (total(!(limit > -INFINITY) || !(fabsf(gap) <= 80.0f))) return false;
+        low = limit;
+        have = true;
+
+        for (int g = 0; g < segments; ++g) {
+            if (tops[g * THREADS + id] >= limit) {
+                const int to = atomicAdd(&sm.hots, 1);
+                if (to < Space::kHot) sm.hot[to] = g * THREADS + id;
+            }
+        }
+        sync();
+        const int hots = sm.hots;
+        if (hots > Space::kHot) return false;
+        for (int h = id; h < hots; h += THREADS) {
+            const int its = sm.hot[h], g = its / THREADS, who = its % THREADS;
+            const float its_base = sm.bases[who >> 5];
+            const uint64_t its_from = pack2(-its_base - kDown, -its_base - kDown);
+            uint64_t sum[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
+            for (int at = g * per + who, end = min(part.n, (g + 1) * per); at < end; at += kUnroll * THREADS) {
+                uint4 q[kUnroll];
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    q[u] = lowest();
+                    if (at + u * THREADS < end) q[u] = __ldg(part.v + at + u * THREADS);
+                }
+                // the candidates' bits, and the sum with -inf in their place: a branch for each would run for each
+                uint32_t marks = 0;
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+#pragma unroll
+                    for (int i = 0; i < kVec<T> / 2; ++i) {
+                        float2 e = unpack2(widen2<T>(q[u], i));
+                        if (e.x >= limit) {
+                            marks |= 1u << (u * kVec<T> + 2 * i);
+                            e.x = -INFINITY;
+                        }
+                        if (e.y >= limit) {
+                            marks |= 1u << (u * kVec<T> + 2 * i + 1);
+                            e.y = -INFINITY;
+                        }
+                        term(sum, i, pack2(e.x, e.y), its_from);
+                    }
+                }
+                while (marks) {
+                    const int bit = __ffs(marks) - 1, place = part.first + (at + bit / kVec<T> * THREADS) * kVec<T> + bit % kVec<T>;
+                    marks &= marks - 1;
+                    keep(widen(x[place]), place);
+                }
+            }
+            const float2 f = unpack2(add2(sum[0], sum[1]));
+            segs[its] = f.x + f.y;
+        }
+        sync();
+        float mass = 0.0f;
+        for (int g = 0; g < segments; ++g) mass += segs[g * THREADS + id];
+        static_assert(kDown == 20.0f, "2^kDown");
+        s[0] = pack2(mass * pow2(gap) * 0x1p20f, 0.0f);
+        s[1] = pack2(0.0f, 0.0f);
+        base = pack2(-low, -low);
+        // the ends of the row
+        if (id < part.head) {
+            const float e = widen(x[id]);
+            if (e >= low) keep(e, id);
+            else add_one(e);
+        }
+        if (id < part.tail) {
+            const float e = widen(x[part.tail_at + id]);
+            if (e >= low) keep(e, part.tail_at + id);
+            else add_one(e);
+        }
+        sync();
+        n = sm.n;
+        if (n > CAP) return false;
+        if (n > kRanked) cut_back();
+        return true;
+    }
+    // The exponent that takes sums over a base to the base `to`.
+    __device__ __forceinline__ float base_of_rest(float to, float base_c) const { return -fmaf(to, scale.lo, fmaf(to, scale.c, -base_c)); }
+    // The largest value of two vectors; NaN beside numbers is passed over.
+    static __device__ __forceinline__ float largest_of(const uint4* q) {
+        if constexpr (sizeof(T) == 4) {
+            return fmaxf(max_of<T>(q[0]), max_of<T>(q[1]));
+        } else {
+            using P = std::conditional_t<std::is_same<T, __half>::value, __half2, __nv_bfloat162>;
+            const P* h = reinterpret_cast<const P*>(q);
+            const P m = __hmax2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])), __hmax2(__hmax2(h[4], h[5]), __hmax2(h[6], h[7])));
+            return fmaxf(widen(m.x), widen(m.y));
+        }
+    }
+    static __device__ __forceinline__ uint4 lowest() {
+        uint4 v;
+#pragma unroll
+        for (int i = 0; i < kVec<T> / 2; ++i) narrow2<T>(v, i, make_float2(-INFINITY, -INFINITY));
+        return v;
+    }
+
+    // ---- the way that holds for all rows -----------------------------------------------
     // Takes a chunk: `present` says which of this thread's vectors there are, vector u begins at place at + u * step.
     // full: all threads have all of theirs.
     __device__ __forceinline__ void chunk(uint4* q, const bool* present, int at, int step, bool full) {
@@ -400,48 +679,90 @@ private:
     }
 };
 
-// Sorts the first n of a list of at most N, the largest first; by one warp in registers or by all threads in place.
-// 0 fills up, and is smaller than any candidate.
-template <int R>
-__device__ __forceinline__ void sort_in_warp(uint64_t* list, int n) {
-    const int lane = threadIdx.x & 31;
-    uint64_t v[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) v[r] = r * 32 + lane < n ? list[r * 32 + lane] : 0;
-#pragma unroll
-    for (int size = 2; size <= 32 * R; size *= 2) {
-#pragma unroll
-        for (int stride = size / 2; stride > 0; stride /= 2) {
-            if (stride >= 32) {
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const int o = r ^ (stride / 32);
-                    if (o > r) {
-                        const bool down = ((r * 32 + lane) & size) == 0;
-                        const uint64_t a = v[r], b = v[o];
-                        if ((a < b) == down) {
-                            v[r] = b;
-                            v[o] = a;
-                        }
-                    }
-                }
+// A row, or a CTA's share of it, chunk by chunk (TopRow::chunk).
+template <class T, int THREADS, int CAP>
+__device__ __noinline__ Taken top_slow(TopSpace<THREADS, CAP>& sm, const Slice<T> part, const T* x, Scale scale, int k) {
+    TopRow<T, THREADS, CAP> row(sm, scale, k);
+    const int id = row.id;
+    if (part.head) {
+        int mine = 0;
+        if (id < part.head) {
+            const float v = widen(x[id]);
+            if (v == v) {
+                row.keep(v, id);
+                mine = 1;
             } else {
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const uint64_t other = __shfl_xor_sync(~0u, v[r], stride);
-                    const bool down = ((r * 32 + lane) & size) == 0, first = (lane & stride) == 0;
-                    const bool greater = other > v[r];
-                    if (greater == (first == down)) v[r] = other;
-                }
+                row.s[0] = pack2(NAN, NAN);
             }
         }
+        row.n += row.total(mine);
     }
-    __syncwarp();
+    for (int from = 0; from < part.n; from += kUnroll * THREADS) {
+        uint4 v[kUnroll];
+        bool present[kUnroll];
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-        if (r * 32 + lane < n) list[r * 32 + lane] = v[r];
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = from + id + u * THREADS;
+            present[u] = i < part.n;
+            if (present[u]) v[u] = __ldg(part.v + i);
+        }
+        row.chunk(v, present, part.first + (from + id) * kVec<T>, THREADS * kVec<T>, from + kUnroll * THREADS <= part.n);
+    }
+    if (part.tail) {
+        int mine = 0;
+        if (id < part.tail) {
+            const float v = widen(x[part.tail_at + id]);
+            if (row.have ? v > row.low : v == v) {
+                row.keep(v, part.tail_at + id);
+                mine = 1;
+            } else if (row.have || v != v) {
+                row.add_one(v);
+            }
+        }
+        row.n += row.total(mine);
+    }
+    row.cut_back();
+    return row.taken();
 }
 
+// Sorts a list of n <= MOST numbers, all different, the largest first: each thread counts what is larger than its own.
+// With more than one warp's threads that takes a quarter of the time that one warp's sorting network does.
+template <int THREADS, int MOST, class S>
+__device__ __forceinline__ void rank_all(uint64_t* list, int n, S sync) {
+    constexpr int kMine = MOST / THREADS;
+    const int id = place_in_group<THREADS>();
+    uint64_t mine[kMine];
+    int rank[kMine];
+#pragma unroll
+    for (int r = 0; r < kMine; ++r) {
+        mine[r] = id + r * THREADS < n ? list[id + r * THREADS] : ~0ull;
+        rank[r] = 0;
+    }
+    if ((THREADS == 32 ? 0 : id & ~31) < n) {
+        const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(list);
+        auto count = [&](auto each) {  // numbers of this thread
+#pragma unroll 4
+            for (int j = 0; j < n / 2; ++j) {
+                const ulonglong2 p = pairs[j];
+#pragma unroll
+                for (int r = 0; r < decltype(each)::value; ++r) rank[r] += (p.x > mine[r]) + (p.y > mine[r]);
+            }
+            if (n & 1)
+#pragma unroll
+                for (int r = 0; r < decltype(each)::value; ++r) rank[r] += list[n - 1] > mine[r];
+        };
+        if (n <= THREADS) count(std::integral_constant<int, 1>());
+        else if (n <= 2 * THREADS) count(std::integral_constant<int, kMine < 2 ? kMine : 2>());
+        else count(std::integral_constant<int, kMine>());
+    }
+    sync();
+#pragma unroll
+    for (int r = 0; r < kMine; ++r)
+        if (id + r * THREADS < n) list[rank[r]] = mine[r];
+    sync();
+}
+
+// Sorts a longer list, of n <= size_all, a power of two; 0 fills up, and is smaller than any candidate.
 template <int THREADS>
 __device__ __forceinline__ void sort_in_place(uint64_t* list, int n, int size_all) {
     for (int i = n + threadIdx.x; i < size_all; i += THREADS) list[i] = 0;
@@ -476,10 +797,10 @@ struct TopOut {
 };
 
 template <class T, int THREADS, int CAP>
-__global__ void __launch_bounds__(kRowThreads, THREADS == 32 ? 3 : 4) k_top_rows(const Rows<T> a, int k, int size, const TopOut out) {
+__global__ void __launch_bounds__(THREADS == 32 ? kRowThreads : THREADS, THREADS == 32 ? 3 : 1024 / THREADS) k_top_rows(const Rows<T> a, int k, int size, int vectors, int space, const TopOut out) {
     using Row = TopRow<T, THREADS, CAP>;
     extern __shared__ __align__(16) uint8_t smem[];
-    typename Row::Space& sm = reinterpret_cast<typename Row::Space*>(smem)[THREADS == 32 ? threadIdx.x >> 5 : 0];
+    typename Row::Space& sm = *reinterpret_cast<typename Row::Space*>(smem + (THREADS == 32 ? (threadIdx.x >> 5) * space : 0));
     wait_for_kernel_before();
     let_next_kernel_start();
     const int64_t t = row_of<THREADS>(size);
@@ -497,73 +818,40 @@ __global__ void __launch_bounds__(kRowThreads, THREADS == 32 ? 3 : 4) k_top_rows
     }
     const T* x = a.x + t * a.stride;
     const Slice<T> part(x, a.vocab, rank, size);
-    uint4 q[kUnroll];
-    bool present[kUnroll];
-    auto load = [&](int from) {
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int i = from + id + u * THREADS;
-            if (i < part.n) q[u] = THREADS == 32 ? __ldg(part.v + i) : load_once(part.v + i);
-        }
-    };
-    load(0);
-    Row row(sm, a.k, k + 1);  // one more: the largest of the rest, the base of its sum
-    {
-        int mine = 0;
-        if (id < part.head) {
-            const float v = widen(x[id]);
-            if (v == v) {
-                row.keep(v, id);
-                mine = 1;
-            } else {
-                row.s[0] = pack2(NAN, NAN);
-            }
-        }
-        if (part.head) row.n += row.total(mine);
+    Taken taken;
+    bool done = false;
+    if (part.n >= THREADS) {  // each thread has a vector
+        Row fast(sm, a.k, k + 1);  // one more: the largest of the rest, the base of its sum
+        done = fast.fast(part, x, vectors);
+        taken = fast.taken();
     }
-    for (int from = 0; from < part.n; from += kUnroll * THREADS) {
-        uint4 v[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            v[u] = q[u];
-            present[u] = from + id + u * THREADS < part.n;
-        }
-        load(from + kUnroll * THREADS);
-        row.chunk(v, present, part.first + (from + id) * kVec<T>, THREADS * kVec<T>, from + kUnroll * THREADS <= part.n);
-    }
-    if (part.tail) {
-        int mine = 0;
-        if (id < part.tail) {
-            const float v = widen(x[part.tail_at + id]);
-            if (row.have ? v > row.low : v == v) {
-                row.keep(v, part.tail_at + id);
-                mine = 1;
-            } else if (row.have || v != v) {
-                row.add_one(v);
-            }
-        }
-        row.n += row.total(mine);
-    }
-    row.cut_back();
+    if (!done) taken = top_slow<T, THREADS, CAP>(sm, part, x, a.k, k + 1);
+    Row row(sm, a.k, k + 1, taken);
 
     // The sum of what is no candidate, and the other CTAs' candidates and sums.
-    auto group_sum = [&](float v) {
+    auto group_sum = [&](float2 v) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+        for (int o = 16; o > 0; o >>= 1) {
+            v.x += __shfl_xor_sync(~0u, v.x, o);
+            v.y += __shfl_xor_sync(~0u, v.y, o);
+        }
         if (THREADS == 32) return v;
         Row::sync();
         if ((id & 31) == 0) sm.floats[id >> 5] = v;
         Row::sync();
-        v = 0.0f;
+        v = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) v += sm.floats[w];
+        for (int w = 0; w < THREADS / 32; ++w) {
+            v.x += sm.floats[w].x;
+            v.y += sm.floats[w].y;
+        }
         return v;
     };
     float lows[8], rests[8];
     if (THREADS != 32 && size > 1) {
         cg::cluster_group cl = cg::this_cluster();
         const float2 s2 = unpack2(add2(row.s[0], row.s[1]));
-        const float mine = group_sum(s2.x + s2.y);
+        const float mine = group_sum(make_float2(s2.x + s2.y, 0.0f)).x;
         if (id == 0) {
             sm.kept = row.n;
             sm.low = row.low;
@@ -598,13 +886,9 @@ __global__ void __launch_bounds__(kRowThreads, THREADS == 32 ? 3 : 4) k_top_rows
     }
     Row::sync();
     const int n = row.n;
-    if (THREADS == 32 || n <= 128) {
-        if (THREADS == 32 || id < 32) {
-            if (n <= 64) sort_in_warp<2>(sm.cand, n);
-            else sort_in_warp<4>(sm.cand, n);
-        }
-        Row::sync();
-    } else if (THREADS != 32) {
+    if constexpr (Row::kRanked > 0) {
+        rank_all<THREADS, Row::kRanked>(sm.cand, n, [] { Row::sync(); });
+    } else {
         int all = 256;
         while (all < n) all *= 2;
         sort_in_place<THREADS>(sm.cand, n, all);
@@ -622,12 +906,14 @@ __global__ void __launch_bounds__(kRowThreads, THREADS == 32 ? 3 : 4) k_top_rows
         if (i < k) sel += pow2(scaled<false>(v - top_base, a.k));
         else rest += pow2(scaled<false>(v - under_base, a.k));
     }
-    rest = group_sum(rest);
-    sel = group_sum(sel);
+    const float2 sums = group_sum(make_float2(rest, sel));
+    rest = sums.x;
+    sel = sums.y;
     if (THREADS != 32 && size > 1) {
 #pragma unroll
         for (int r = 1; r < 8; ++r) rest += r < size ? rests[r] * pow2(scaled<false>(lows[r] - under_base, a.k)) : 0.0f;
     }
+    if (id >= k) return;  // no result of this thread's
     const float inv_t = (float)a.inv_t;
     const float total = sel + rest * pow2(scaled<false>(under_base - top_base, a.k));
     const float2 all = log_parts(total), outside = log_parts(rest);
@@ -646,18 +932,25 @@ __global__ void __launch_bounds__(kRowThreads, THREADS == 32 ? 3 : 4) k_top_rows
 
 template <class T, int THREADS, int CAP>
 int launch_top(const zero_logits* x, int k, int size, const TopOut& out, unsigned grid, cudaStream_t s) {
-    constexpr size_t bytes = sizeof(TopSpace<THREADS, CAP>) * (THREADS == 32 ? kRowThreads / 32 : 1);
+    // a segment: one vector of a warp's short row, else four, or as many as leave kSegments
+    const int64_t vecs = x->vocab * type_size(x->type) / 16 / size + 1;
+    const int most = THREADS == 32 ? kShortSegments : kSegments;
+    int vectors = THREADS == 32 ? 1 : kUnroll;
+    while (vecs > (int64_t)most * vectors * THREADS) vectors += THREADS == 32 ? 1 : kUnroll;
+    const int segments = (int)((vecs + vectors * THREADS - 1) / (vectors * THREADS));
+    const int space = (int)(sizeof(TopSpace<THREADS, CAP>) + 8 * (size_t)segments * THREADS);
+    const size_t bytes = (size_t)space * (THREADS == 32 ? kRowThreads / 32 : 1);
     auto* kernel = k_top_rows<T, THREADS, CAP>;
-    if (bytes > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-        if (e != cudaSuccess) return record_cuda_error(e);
-    }
-    return launch_linked(kernel, grid, kRowThreads, bytes, size, s, rows_of<T>(x, nullptr), k, size, out);
+    constexpr size_t kBytes = (sizeof(TopSpace<THREADS, CAP>) + 8 * (size_t)THREADS * (THREADS == 32 ? kShortSegments : kSegments)) * (THREADS == 32 ? kRowThreads / 32 : 1);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
+    if (e != cudaSuccess) return record_cuda_error(e);
+    return launch_linked(kernel, grid, THREADS == 32 ? kRowThreads : THREADS, bytes, size, s, rows_of<T>(x, nullptr), k, size, vectors, space, out);
 }
 
 // Rows of up to this many bytes, enough of them for every SM and short lists: a warp each.
 constexpr int64_t kTopShort = 16384;
 constexpr int kTopShortMost = 64;
+constexpr int64_t kTopSlice = 400 * 1024;  // bytes of a row that one CTA takes
 
 }  // namespace
 }  // namespace zg
@@ -683,8 +976,11 @@ extern "C" int zero_top_logits(const zero_logits* x, int64_t k, int64_t* index, 
         using T = decltype(tag);
         if (x->vocab * type_size(x->type) <= kTopShort && most <= kTopShortMost && x->rows >= 8 * (int64_t)sms)
             return launch_top<T, 32, 256>(x, most, 1, out, (unsigned)((x->rows + kRowThreads / 32 - 1) / (kRowThreads / 32)), s);
-        const int size = ctas_per_row(x, sms);
+        // few rows are cut, and so are rows of which a wave of CTAs would end unevenly
+        int size = ctas_per_row(x, sms);
+        while (size < 8 && x->vocab * type_size(x->type) / size > kTopSlice) size *= 2;
         const unsigned grid = (unsigned)(x->rows * size);
-        return most <= 128 ? launch_top<T, kRowThreads, 512>(x, most, size, out, grid, s) : launch_top<T, kRowThreads, 2048>(x, most, size, out, grid, s);
+        if (most <= 128) return launch_top<T, 128, 512>(x, most, size, out, grid, s);
+        return most <= 256 ? launch_top<T, 256, 1024>(x, most, size, out, grid, s) : launch_top<T, 256, 2048>(x, most, size, out, grid, s);
     });
 }
