@@ -267,12 +267,44 @@ struct TopRow {
         sum[i & 1] = add2(sum[i & 1], pack2(pow2(z.x), pow2(z.y)));
     }
 
+    // A key that at least k of the threads' keys reach and at most four more, or more that equal it. By a warp.
+    __device__ __forceinline__ uint32_t few_reach() const {
+        constexpr int kEach = 2 * THREADS / 32;
+        uint32_t mine[kEach], lo = ~0u, hi = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            mine[i] = sm.keys[id + 32 * i];
+            lo = min(lo, mine[i]);
+            hi = max(hi, mine[i]);
+        }
+        lo = __reduce_min_sync(~0u, lo);
+        hi = __reduce_max_sync(~0u, hi) + 1;
+        int reach = 2 * THREADS;
+        while (reach > k + 4 && hi - lo > 1) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            int c = 0;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) c += mine[i] >= mid;
+            c = __reduce_add_sync(~0u, c);
+            if (c >= k) {
+                lo = mid;
+                reach = c;
+            } else {
+                hi = mid;
+            }
+        }
+        return lo;
+    }
+
     // A whole row, or a CTA's share of it, of which each thread has a vector. False: it has to be taken the other way.
     __device__ __forceinline__ bool fast(const Slice<T>& part, const T* x, int vectors) {
         const int per = vectors * THREADS, segments = (part.n + per - 1) / per;
         float* const tops = sm.largest();
         float* const segs = tops + segments * THREADS;
         float halves[2] = {-INFINITY, -INFINITY}, base_c = 0.0f;
+        T head, tail;  // read before they are wanted
+        if (id < part.head) head = x[id];
+        if (id < part.tail) tail = x[part.tail_at + id];
         uint64_t from = 0;
         float least = INFINITY;  // of the segments' largest values
         float top = -INFINITY;
@@ -360,31 +392,8 @@ struct TopRow {
             sm.keys[THREADS + id] = key_of(halves[1]);
             sync();
             if (id < 32) {
-                constexpr int kEach = 2 * THREADS / 32;
-                uint32_t mine[kEach], lo = ~0u, hi = 0;
-#pragma unroll
-                for (int i = 0; i < kEach; ++i) {
-                    mine[i] = sm.keys[id + 32 * i];
-                    lo = min(lo, mine[i]);
-                    hi = max(hi, mine[i]);
-                }
-                lo = __reduce_min_sync(~0u, lo);
-                hi = __reduce_max_sync(~0u, hi) + 1;
-                int reach = 2 * THREADS;
-                while (reach > k + 4 && hi - lo > 1) {
-                    const uint32_t mid = lo + (hi - lo) / 2;
-                    int c = 0;
-#pragma unroll
-                    for (int i = 0; i < kEach; ++i) c += mine[i] >= mid;
-                    c = __reduce_add_sync(~0u, c);
-                    if (c >= k) {
-                        lo = mid;
-                        reach = c;
-                    } else {
-                        hi = mid;
-                    }
-                }
-                if (id == 0) sm.key = lo;
+                const uint32_t key = few_reach();
+                if (id == 0) sm.key = key;
             }
             sync();
             limit = value_of(sm.key);
@@ -403,16 +412,26 @@ struct TopRow {
             limit = value_of(key);
         }
         // not -inf, and no base so far above it that its terms are too small to count, or so far below that they overflow
-        const float gap = fabsf(base_c) < INFINITY ? base_of_rest(limit, base_c) : INFINITY;
-        if (total(!(limit > -INFINITY) || !(fabsf(gap) <= 80.0f))) return false;
+        bool good = limit > -INFINITY;
+        float gap = 0.0f;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) {
+            const float its = base_of_rest(limit, sm.bases[w]);
+            good = good && fabsf(its) <= 80.0f;
+            if (w == id >> 5) gap = its;
+        }
+        if (!good) return false;
         low = limit;
         have = true;
 
-        for (int g = 0; g < segments; ++g) {
-            if (tops[g * THREADS + id] >= limit) {
-                const int to = atomicAdd(&sm.hots, 1);
-                if (to < Space::kHot) sm.hot[to] = g * THREADS + id;
-            }
+        // the segments that reach it: one place on the list for all of a thread's
+        uint32_t marks = 0;
+#pragma unroll 4
+        for (int g = 0; g < segments; ++g) marks |= (uint32_t)(tops[g * THREADS + id] >= limit) << g;
+        if (marks) {
+            int to = atomicAdd(&sm.hots, __popc(marks));
+            for (; marks; marks &= marks - 1, ++to)
+                if (to < Space::kHot) sm.hot[to] = (__ffs(marks) - 1) * THREADS + id;
         }
         sync();
         const int hots = sm.hots;
@@ -465,12 +484,12 @@ struct TopRow {
         base = pack2(-low, -low);
         // the ends of the row
         if (id < part.head) {
-            const float e = widen(x[id]);
+            const float e = widen(head);
             if (e >= low) keep(e, id);
             else add_one(e);
         }
         if (id < part.tail) {
-            const float e = widen(x[part.tail_at + id]);
+            const float e = widen(tail);
             if (e >= low) keep(e, part.tail_at + id);
             else add_one(e);
         }
@@ -950,7 +969,6 @@ int launch_top(const zero_logits* x, int k, int size, const TopOut& out, unsigne
 // Rows of up to this many bytes, enough of them for every SM and short lists: a warp each.
 constexpr int64_t kTopShort = 16384;
 constexpr int kTopShortMost = 64;
-constexpr int64_t kTopSlice = 400 * 1024;  // bytes of a row that one CTA takes
 
 }  // namespace
 }  // namespace zg
@@ -976,9 +994,7 @@ extern "C" int zero_top_logits(const zero_logits* x, int64_t k, int64_t* index, 
         using T = decltype(tag);
         if (x->vocab * type_size(x->type) <= kTopShort && most <= kTopShortMost && x->rows >= 8 * (int64_t)sms)
             return launch_top<T, 32, 256>(x, most, 1, out, (unsigned)((x->rows + kRowThreads / 32 - 1) / (kRowThreads / 32)), s);
-        // few rows are cut, and so are rows of which a wave of CTAs would end unevenly
-        int size = ctas_per_row(x, sms);
-        while (size < 8 && x->vocab * type_size(x->type) / size > kTopSlice) size *= 2;
+        const int size = ctas_per_row(x, sms);
         const unsigned grid = (unsigned)(x->rows * size);
         if (most <= 128) return launch_top<T, 128, 512>(x, most, size, out, grid, s);
         return most <= 256 ? launch_top<T, 256, 1024>(x, most, size, out, grid, s) : launch_top<T, 256, 2048>(x, most, size, out, grid, s);
