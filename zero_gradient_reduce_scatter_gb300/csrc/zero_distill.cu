@@ -17,6 +17,8 @@
 
 #include <climits>
 
+#include <type_traits>
+
 #include "zero_rows.cuh"
 
 namespace zg {
@@ -40,20 +42,21 @@ struct DistillTokens : TokenWeights {
     __device__ __forceinline__ void spread(int64_t, int64_t) const {}
 };
 
-// What a CTA holds of a token's list in shared memory: the bitmap, then the entries.
+// What a CTA holds of a token's list in shared memory: a bitmap of the vocabulary, and the entries.
 struct List {
     uint32_t* bits;
-    float *x, *lp;  // the student's logit, the teacher's log-probability; later x: the gradient
-    int* place;     // -1: not there
+    float *x, *lp;  // the student's logit, later the gradient; the teacher's log-probability
+    int* place;     // kNotThere, or kPastVocab
     int k;
 
-    __device__ __forceinline__ List(uint8_t* smem, int words, int k) : k(k) {
+    __device__ __forceinline__ List(uint8_t* smem, int words, int k, int buffer = 0) : k(k) {
         bits = reinterpret_cast<uint32_t*>(smem);
-        x = reinterpret_cast<float*>(bits + words);
+        x = reinterpret_cast<float*>(bits + words) + 3 * k * buffer;
         lp = x + k;
         place = reinterpret_cast<int*>(lp + k);
     }
 };
+constexpr int kNotThere = -1, kPastVocab = -2;
 __host__ __device__ constexpr int bitmap_words(int64_t vocab) { return (int)((vocab + 8 + 31) / 32); }
 
 // Whether place j is in the list. Bits begin `shift` before the vocabulary, so that a vector's are neighbours in a byte.
@@ -124,106 +127,166 @@ struct DistillRow {
     float base, factor;
     float target;  // the target's gradient
     bool target_listed;
+    bool zero;     // no loss: a row of zeros
 };
 
-// What the row's sums and its list come to, by one warp. rest: the sums outside the list. Writes the token's
-// results (`first`: this CTA does) and the list's gradients over list.x.
-__device__ __forceinline__ DistillRow finish_list(const DistillTokens& a, const List& list, const RowStat& rest, bool bad, int64_t t, int64_t y,
-                                                  float x_y, int64_t vocab, Scale k, float inv_t, bool first) {
-    const int lane = threadIdx.x & 31;
-    const float w = a.w[t];
-    // the row's maximum, and the list's sums
-    float top = rest.s != 0.0f ? rest.m : -INFINITY;
+// A warp's share of a list: its largest logit, the sum of 2^((x - it) C), the teacher's mass, and how many entries there
+// are, 1024 more where the target is one. Before the barrier that finish_list's threads pass.
+template <int THREADS>
+__device__ __forceinline__ void sum_list(const List& list, Scale k, int64_t y, float4* shares) {
+    float top = -INFINITY, mass = 0.0f, sum = 0.0f;
     int count = 0;
-    float mass = 0.0f;
-    for (int i = lane; i < list.k; i += 32) {
+    bool target = false;
+    for (int i = threadIdx.x; i < list.k; i += THREADS) {
         if (list.place[i] < 0) continue;
         ++count;
+        target = target || list.place[i] == y;
         top = fmaxf(top, list.x[i]);
         mass += expf(list.lp[i]);
     }
+    if ((threadIdx.x & ~31) < list.k) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    count = __reduce_add_sync(~0u, count);
-    mass = warp_add(mass);
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        for (int i = threadIdx.x; i < list.k; i += THREADS)
+            if (list.place[i] >= 0) sum += pow2(scaled<false>(list.x[i] - base_of(top), k));
+        sum = warp_add(sum);
+        mass = warp_add(mass);
+        count = __reduce_add_sync(~0u, count) + (__any_sync(~0u, target) ? 1024 : 0);
+    }
+    if ((threadIdx.x & 31) == 0) shares[threadIdx.x >> 5] = make_float4(top, sum, mass, __int_as_float(count));
+}
+
+// What the row's sums and its list come to. rest: the sums outside the list. Writes the token's results (`first`: this CTA
+// does) and the gradients of this thread's entries over list.x. Valid in all threads.
+template <int THREADS, class S>
+__device__ __forceinline__ DistillRow finish_list(const DistillTokens& a, const List& list, const RowStat& rest, bool bad, int64_t t, int64_t y,
+                                                  float x_y, int64_t vocab, Scale k, float inv_t, bool first, const float4* shares, float2* parts,
+                                                  S sync) {
+    constexpr int kWarps = THREADS / 32;
+    const float w = a.w[t];
+    float top = rest.s != 0.0f ? rest.m : -INFINITY, mass = 0.0f, total = 0.0f;
+    int count = 0;
+    const int warps = min(kWarps, (list.k + 31) / 32);
+    for (int i = 0; i < warps; ++i) {
+        const float4 v = shares[i];
+        top = fmaxf(top, v.x);
+        mass += v.z;
+        count += __float_as_int(v.w);
+    }
+    DistillRow r;
+    r.target_listed = count >= 1024;  // more often where it is listed twice, which is bad
+    count &= 1023;
     const float base = base_of(top), rest_base = base_of(rest.m), up = pow2(scaled<false>(rest_base - base, k));
-    float total = 0.0f;
-    for (int i = lane; i < list.k; i += 32)
-        if (list.place[i] >= 0) total += pow2(scaled<false>(list.x[i] - base, k));
-    total = warp_add(total) + (rest.s != 0.0f ? rest.s * up : 0.0f);
+    for (int i = 0; i < warps; ++i) total += shares[i].y != 0.0f ? shares[i].y * pow2(scaled<false>(base_of(shares[i].x) - base, k)) : 0.0f;
+    if (rest.s != 0.0f) total += rest.s * up;
     if (bad || y >= vocab) total = NAN;
     const bool nothing = total == 0.0f;  // -inf alone
     const float2 all = log_parts(total);
     const bool with_rest = a.tail == ZERO_TAIL_REST && count < vocab;
-    const float shift = a.tail == ZERO_TAIL_RENORMALISE && count > 0 ? logf(mass) : 0.0f;
+    const float shift = a.tail == ZERO_TAIL_RENORMALISE && count > 0 ? logf(mass) : 0.0f, over = nothing ? 0.0f : 1.0f / total;
     auto logq = [&](float x) { return nothing ? -INFINITY : ((x - base) * inv_t - all.x) - all.y; };
     float d = 0.0f, c = 0.0f;
-    for (int i = lane; i < list.k; i += 32) {
-        if (list.place[i] < 0) continue;
-        const float x = list.x[i], lp = list.lp[i] - shift, lq = logq(x);
-        const float q = nothing ? 0.0f : pow2(scaled<false>(x - base, k)) / total;
-        const Part part = entry_part(a.kind, a.mix, expf(lp), q, lp - lq);
-        d += part.d;
-        c += part.c;
+    if ((threadIdx.x & ~31) < list.k) {
+        for (int i = threadIdx.x; i < list.k; i += THREADS) {
+            if (list.place[i] < 0) continue;
+            const float x = list.x[i], lp = list.lp[i] - shift, q = pow2(scaled<false>(x - base, k)) * over;
+            const Part part = entry_part(a.kind, a.mix, expf(lp), q, lp - logq(x));
+            d += part.d;
+            c += part.c;
+        }
+        d = warp_add(d);
+        c = warp_add(c);
     }
-    d = warp_add(d);
-    c = warp_add(c);
+    if ((threadIdx.x & 31) == 0) parts[threadIdx.x >> 5] = make_float2(d, c);
+    sync();
+    d = c = 0.0f;
+    for (int i = 0; i < warps; ++i) {
+        d += parts[i].x;
+        c += parts[i].y;
+    }
     Part outside = {0.0f, 0.0f};
     if (with_rest) {
         const float lp = a.teacher_rest ? a.teacher_rest[t] : logf(fmaxf(1.0f - mass, 0x1p-24f));
         const float2 own = log_parts(rest.s);
         const float lq = nothing || rest.s == 0.0f ? -INFINITY : ((rest_base - base) * inv_t + (own.x - all.x)) + (own.y - all.y);
-        const float q = nothing ? 0.0f : rest.s != 0.0f ? rest.s * up / total : 0.0f;
+        const float q = rest.s != 0.0f ? rest.s * up * over : 0.0f;
         const float p = mass == mass ? expf(lp) : NAN;
         if (!(lp == -INFINITY && lq == -INFINITY)) outside = entry_part(a.kind, a.mix, p, q, lp - lq);
         d += outside.d;
         c += outside.c;
     }
-    const float logp = y < vocab ? logq(x_y) : NAN;
     // a coefficient of 0 leaves its term out, also where that is infinite
     const float g = w * a.kl_coef * inv_t, h = w * a.ce_coef * inv_t;
     const float share = (a.ce_coef != 0.0f ? h : 0.0f) - (a.kl_coef != 0.0f ? g * c : 0.0f);
-    DistillRow r;
     r.base = rest_base;
     r.factor = 0.0f;  // outside the list there is nothing above -inf
     if (rest.s != 0.0f) {
-        r.factor = share * up / total;
+        r.factor = share * up * over;
         if (with_rest && a.kl_coef != 0.0f) r.factor += g * outside.c / rest.s;
     }
     if (total != total) r.factor = NAN;
-    r.target_listed = false;
-    for (int i = lane; i < list.k; i += 32) {
+    for (int i = threadIdx.x; i < list.k; i += THREADS) {
         if (list.place[i] < 0) continue;
-        const float x = list.x[i], lp = list.lp[i] - shift;
-        const float q = nothing ? 0.0f : pow2(scaled<false>(x - base, k)) / total;
+        const float x = list.x[i], lp = list.lp[i] - shift, q = pow2(scaled<false>(x - base, k)) * over;
         float v = share * q;
         if (a.kl_coef != 0.0f) v += g * entry_part(a.kind, a.mix, expf(lp), q, lp - logq(x)).c;
-        if (list.place[i] == y) {
-            v -= h;
-            r.target_listed = true;
-        }
+        if (list.place[i] == y) v -= h;
         list.x[i] = nothing ? 0.0f : v;
     }
-    r.target_listed = __any_sync(~0u, r.target_listed);
+    r.zero = w == 0.0f || nothing;
     r.target = nothing ? 0.0f : fmaf(pow2(scaled<false>(x_y - rest_base, k)), r.factor, -h);
-    if (first && lane == 0) {
+    if (first && threadIdx.x == 0) {
+        const float logp = y < vocab ? logq(x_y) : NAN;
         float loss = 0.0f;
         if (a.kl_coef != 0.0f) loss += a.kl_coef * d;
         if (a.ce_coef != 0.0f) loss -= a.ce_coef * logp;
         if (total != total) loss = d = NAN;
-        a.loss[t] = loss * w;
-        a.kl[t] = d;
-        a.logp[t] = logp;
+        a.loss[t] = w != 0.0f ? loss * w : 0.0f;
+        a.kl[t] = w != 0.0f ? d : 0.0f;
+        a.logp[t] = w != 0.0f ? logp : 0.0f;
     }
     return r;
+}
+
+// Whether sums that were not CHECKED are good: the rest may be any share of the base's term.
+__device__ __forceinline__ bool good_rest(const RowStat& a) { return a.s > 0x1p-60f && a.s < 0x1p60f; }
+
+// The list's gradients and the target's over what the vectors left there, by the CTA that wrote their places.
+template <class T, int THREADS>
+__device__ __forceinline__ void write_entries(const List& list, const DistillRow& r, const Slice<T>& s, T* out, int64_t y, int64_t vocab) {
+    auto ours = [&](int64_t j) {
+        return (j >= s.first && j < s.first + s.n * kVec<T>) || (s.head && j < s.head) || (s.tail && j >= s.tail_at);
+    };
+    for (int i = threadIdx.x; i < list.k; i += THREADS)
+        if (list.place[i] >= 0 && ours(list.place[i])) out[list.place[i]] = narrow<T>(r.factor == r.factor ? list.x[i] : NAN);
+    if (threadIdx.x == 0 && !r.target_listed && y < vocab && ours(y)) out[y] = narrow<T>(r.target);
+}
+
+// Entry i of token t's list into shared memory.
+template <class T>
+__device__ __forceinline__ void take_entry(const DistillTokens& p, const List& list, const T* x, int64_t vocab, int64_t t, int i) {
+    const int64_t j = p.index[t * p.k + i];
+    const float lp = p.teacher[t * p.k + i];
+    const bool there = j >= 0 && lp != -INFINITY, past = j >= vocab;
+    if (there && !past) list.x[i] = widen(x[j]);
+    list.lp[i] = lp;
+    list.place[i] = !there ? kNotThere : past ? kPastVocab : (int)j;
+}
+// Its bit into the bitmap. False: it names a place twice or past the vocabulary.
+__device__ __forceinline__ bool mark_entry(const List& list, int i, int shift) {
+    const int j = list.place[i];
+    if (j < 0) return j != kPastVocab;
+    const uint32_t bit = 1u << ((j + shift) & 31);
+    return !(atomicOr(list.bits + ((j + shift) >> 5), bit) & bit);
 }
 
 // Any row: read once for the rest's sum and again for the gradient, by `size` CTAs (a cluster).
 template <class T, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_distill_rows(const Rows<T> a, const DistillTokens p, int size, T* dx, int64_t dstride) {
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ RowStat sm[THREADS / 32], mine;
-    __shared__ DistillRow shared_row;
+    __shared__ float4 shares[THREADS / 32];
+    __shared__ float2 sums_of[THREADS / 32];
     __shared__ int shared_bad;
     wait_for_kernel_before();
     let_next_kernel_start();
@@ -248,22 +311,10 @@ __global__ void __launch_bounds__(THREADS) k_distill_rows(const Rows<T> a, const
     const float x_y = y < a.vocab ? widen(x[y]) : NAN;
     const int shift = (kVec<T> - (s.tail_at % kVec<T>)) % kVec<T>;
     for (int i = id; i < p.k; i += THREADS) {
-        const int64_t j = p.index[t * p.k + i];
-        const float lp = p.teacher[t * p.k + i];
-        int place = -1;
-        if (j >= 0 && lp != -INFINITY) {
-            if (j >= a.vocab) {
-                shared_bad = 1;
-            } else {
-                place = (int)j;
-                const uint32_t bit = 1u << ((place + shift) & 31);
-                if (atomicOr(list.bits + ((place + shift) >> 5), bit) & bit) shared_bad = 1;  // twice in the list
-                list.x[i] = widen(x[j]);
-                list.lp[i] = lp;
-            }
-        }
-        list.place[i] = place;
+        take_entry(p, list, x, a.vocab, t, i);
+        if (!mark_entry(list, i, shift)) shared_bad = 1;
     }
+    sum_list<THREADS>(list, a.k, y, shares);
     __syncthreads();
     auto sums = [&](auto checked) {
         constexpr bool kChecked = decltype(checked)::value;
@@ -283,17 +334,13 @@ __global__ void __launch_bounds__(THREADS) k_distill_rows(const Rows<T> a, const
     bool good = false;
     if (fabsf(x_y) < INFINITY) {
         st = sums(std::false_type());
-        good = st.s > 0x1p-60f && st.s < 0x1p60f;
+        good = good_rest(st);
         if (!good) __syncthreads();
     }
     if (!good) st = sums(std::true_type());
     st = cluster_join<false>(st, size, a.k, &mine);
-    if (id < 32) {
-        const DistillRow r = finish_list(p, list, st, shared_bad != 0, t, y, x_y, a.vocab, a.k, (float)a.inv_t, rank == 0);
-        if (id == 0) shared_row = r;
-    }
-    __syncthreads();
-    const DistillRow r = shared_row;
+    const DistillRow r = finish_list<THREADS>(p, list, st, shared_bad != 0, t, y, x_y, a.vocab, a.k, (float)a.inv_t, rank == 0, shares, sums_of,
+                                              [] { __syncthreads(); });
     const GradRow grad = {0.0f, -r.factor, 0.0f, r.base, 0.0f};
     if (same_alignment(x, out)) {
         const GradVector<T, false> vector(grad, a.c);
@@ -305,14 +352,251 @@ __global__ void __launch_bounds__(THREADS) k_distill_rows(const Rows<T> a, const
     if (id < s.head) out[id] = narrow<T>(grad_term<false>(grad, widen(start.head), a.c, false));
     if (id < s.tail) out[s.tail_at + id] = narrow<T>(grad_term<false>(grad, widen(start.tail), a.c, false));
     __syncthreads();
-    // the list's entries and the target, by the CTA that wrote their places
-    auto ours = [&](int64_t j) {
-        return (j >= s.first && j < s.first + s.n * kVec<T>) || (s.head && j < s.head) || (s.tail && j >= s.tail_at);
-    };
-    for (int i = id; i < p.k; i += THREADS)
-        if (list.place[i] >= 0 && ours(list.place[i])) out[list.place[i]] = narrow<T>(r.factor == r.factor ? list.x[i] : NAN);
-    if (id == 0 && !r.target_listed && y < a.vocab && ours(y)) out[y] = narrow<T>(r.target);
+    write_entries<T, THREADS>(list, r, s, out, y, a.vocab);
     if (size > 1) cg::this_cluster().sync();  // no CTA leaves while another reads its sums
+}
+
+// Forward and backward in one pass over each row, as k_policy_rows takes it: the row's slice comes to shared memory by bulk
+// copies, is read for the rest's sum as it arrives, and again for the gradient; a producer warp refills each part with the
+// next row's as soon as it has been read. It reads the list too, a row ahead, and looks for places that are named twice; the
+// list's places in shared memory then become -inf, so that the sum over the row is the rest's.
+template <class T, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
+    k_distill_fused(const Rows<T> a, const DistillTokens p, int size, int per, int slots, T* dx, int64_t dstride) {
+    constexpr int kThreads = 32 * WARPS;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ RowStat sm[WARPS], mine[2];
+    __shared__ float4 shares[WARPS];
+    __shared__ float2 sums_of[WARPS];
+    __shared__ uint32_t end_listed[16];  // elements that no vector holds: the number of the row whose list has them
+    __shared__ int shared_bad[2];
+    __shared__ int64_t row_at[2], row_y[2];
+    __shared__ float row_x[2];  // the target's logit
+    __shared__ uint64_t bars[2 * kSlots + 4];
+    __shared__ int gave_up;
+    const uint32_t full = smem_addr(bars), empty = full + 8 * kSlots, row_full = empty + 8 * kSlots, row_empty = row_full + 16;
+    const int rank = (int)(blockIdx.x % size), lane = threadIdx.x & 31, words = bitmap_words(a.vocab);
+    const int64_t first = blockIdx.x / size, clusters = gridDim.x / size;
+    uint8_t* const lists = smem + (size_t)16 * slots * per;
+    uint32_t* const bits = reinterpret_cast<uint32_t*>(lists);
+    if (threadIdx.x == 0) {
+        gave_up = 0;
+        shared_bad[0] = shared_bad[1] = 0;
+        for (int i = 0; i < 16; ++i) end_listed[i] = 0;
+        for (int i = 0; i < slots; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, WARPS);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(row_full + 8 * i, 1);
+            mbar_init(row_empty + 8 * i, WARPS);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    for (int i = threadIdx.x; i < words; i += kThreads + 32) bits[i] = 0;
+    __syncthreads();
+
+    // As in k_policy_rows: what the caller gives may be read at once, the weights after the kernel before this one.
+    let_next_kernel_start();
+    int64_t n = 0;  // rows taken
+    if (threadIdx.x >= kThreads) {
+        Slot slot;
+        bool ok = true;
+        // The next row and its target; its list is read a row ahead, behind this row's copies.
+        int64_t t = -1, y = -1;
+        auto next = [&](int64_t i) {
+            t = first + i * clusters;
+            if (size == 1 && i > 0) {
+                if (i == 1) wait_for_kernel_before();
+                if (lane == 0) t = (int64_t)gridDim.x + (int64_t)atomicAdd(p.ticket, 1u);
+                t = __shfl_sync(~0u, t, 0);
+            }
+            if (t >= a.rows) t = -1;
+            ok = ok && mbar_wait(row_empty + 8 * (i & 1), ((uint32_t)(i >> 1) & 1) ^ 1, &gave_up);
+            ok = __all_sync(~0u, ok);
+            if (!ok) t = -1;
+            y = t >= 0 ? a.targets[t] : -1;
+            if (y < 0) return;
+            const List list(lists, words, p.k, i & 1);
+            const T* x = a.x + t * a.stride;
+#pragma unroll 4
+            for (int e = lane; e < p.k; e += 32) take_entry(p, list, x, a.vocab, t, e);
+            __syncwarp();
+            bool bad = false;
+            for (int e = lane; e < p.k; e += 32) bad = !mark_entry(list, e, 0) || bad;
+            __syncwarp();
+            for (int e = lane; e < p.k; e += 32)
+                if (list.place[e] >= 0) list.bits[list.place[e] >> 5] = 0;
+            bad = __any_sync(~0u, bad);
+            if (lane == 0) shared_bad[i & 1] = bad;
+            __syncwarp();
+        };
+        for (next(0);; ++n) {
+            const int64_t y_now = y;
+            const T* x = a.x + t * a.stride;
+            if (lane == 0) {
+                row_at[n & 1] = t;
+                row_y[n & 1] = y;
+                row_x[n & 1] = y >= 0 && y < a.vocab ? widen(x[y]) : NAN;
+                mbar_arrive(row_full + 8 * (n & 1));
+            }
+            if (t < 0) break;
+            if (y >= 0 && lane == 0) {
+                const Slice<T> s(x, a.vocab, rank, size);
+                for (int i = 0; i < kChunks; ++i) {
+                    ok = ok && mbar_wait(empty + 8 * slot.at, slot.phase ^ 1, &gave_up);
+                    const int at = min(s.n, i * per), bytes = 16 * (min(s.n, at + per) - at);
+                    mbar_expect(full + 8 * slot.at, ok ? bytes : 0);
+                    if (ok && bytes) bulk_load(smem_addr(smem) + 16 * slot.at * per, s.v + at, bytes, full + 8 * slot.at);
+                    slot.next(slots);
+                }
+            }
+            __syncwarp();
+            // the consumers' cluster_join, which does not wait for the list
+            if (size > 1 && y_now >= 0) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+            next(n + 1);
+            if (size > 1 && y_now >= 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        }
+    } else {
+        uint32_t taken = 0;
+        Slot begin;  // of the row at hand
+        const uint4* parts = reinterpret_cast<const uint4*>(smem);
+        for (;; ++n) {
+            // Not left early where another wait gave up (k_policy_rows)
+            bool got = mbar_try(row_full + 8 * (n & 1), (uint32_t)(n >> 1) & 1);
+            for (int i = 0; i < 4 * kWaitLimit && !got; ++i) got = mbar_try(row_full + 8 * (n & 1), (uint32_t)(n >> 1) & 1);
+            const int64_t t = got ? row_at[n & 1] : -1, y = row_y[n & 1];
+            const float x_y = row_x[n & 1];
+            auto release = [&] {  // this warp has done with the row's numbers and its list
+                __syncwarp();
+                if (lane == 0) mbar_arrive(row_empty + 8 * (n & 1));
+            };
+            if (t < 0) break;
+            T* out = dx + t * dstride;
+            if (n == 0) wait_for_kernel_before();
+            if (y < 0) {
+                zero_row<T, kThreads>(out, a.vocab, rank, size);
+                if (threadIdx.x == 0 && rank == 0) p.loss[t] = p.kl[t] = p.logp[t] = 0.0f;
+                release();
+                continue;
+            }
+            const T* x = a.x + t * a.stride;
+            const Slice<T> s(x, a.vocab, rank, size);
+            const List list(lists, words, p.k, n & 1);
+            const float x_head = threadIdx.x < s.head ? widen(x[threadIdx.x]) : 0.0f;
+            const float x_tail = threadIdx.x < s.tail ? widen(x[s.tail_at + threadIdx.x]) : 0.0f;
+            sum_list<kThreads>(list, a.k, y, shares);
+            for (int i = threadIdx.x; i < p.k; i += kThreads) {
+                const int j = list.place[i];
+                if (j >= 0 && j < s.head) end_listed[j] = taken + 1;
+                if (j >= s.tail_at && s.tail) end_listed[8 + j - s.tail_at] = taken + 1;
+            }
+            bool ok = true, struck = false;
+            // -inf in the places of the list that part i of the slice has, once it is there
+            auto strike_list = [&](int i, const Slot& slot) {
+                ok = ok && mbar_wait(full + 8 * slot.at, slot.phase, &gave_up);
+                const int at = min(s.n, i * per), from = s.first + at * kVec<T>, m = (min(s.n, at + per) - at) * kVec<T>;
+                T* v = reinterpret_cast<T*>(smem) + (size_t)slot.at * per * kVec<T>;
+                for (int e = threadIdx.x; e < p.k; e += kThreads) {
+                    const int j = list.place[e] - from;
+                    if (list.place[e] >= 0 && j >= 0 && j < m) v[j] = narrow<T>(-INFINITY);
+                }
+                consumers_sync<kThreads>();
+            };
+            auto sums = [&](auto checked) {
+                constexpr bool kChecked = decltype(checked)::value;
+                Sums<T, false, kChecked> run(a.k, x_y);
+                Slot slot = begin;
+                for (int i = 0; i < kChunks; ++i, slot.next(slots)) {
+                    if (!struck) strike_list(i, slot);
+                    const int at = min(s.n, i * per);
+                    const uint4* v = parts + slot.at * per;
+                    for_vectors<kThreads>(min(s.n, at + per) - at, [&](int j) { return v[j]; }, [&](int, const uint4& q) { run.add(q); });
+                }
+                if (threadIdx.x < s.head && end_listed[threadIdx.x] != taken + 1) run.add_one(x_head);
+                if (threadIdx.x < s.tail && end_listed[8 + threadIdx.x] != taken + 1) run.add_one(x_tail);
+                struck = true;
+                return group_join<false, kChecked, WARPS>(run.stat(), a.k, sm, 1);
+            };
+            RowStat st;
+            bool good = false;
+            if (fabsf(x_y) < INFINITY) {
+                st = sums(std::false_type());
+                good = good_rest(st);
+                if (!good) consumers_sync<kThreads>();
+            }
+            if (!good) st = sums(std::true_type());
+            if (!ok || *(volatile int*)&gave_up) st.s = NAN;  // a copy did not come: no result
+            st = cluster_join<false>(st, size, a.k, mine + (taken & 1));
+            const DistillRow r = finish_list<kThreads>(p, list, st, shared_bad[n & 1] != 0, t, y, x_y, a.vocab, a.k, (float)a.inv_t, rank == 0, shares, sums_of,
+                                                       [] { consumers_sync<kThreads>(); });
+            const GradRow grad = {0.0f, -r.factor, 0.0f, r.base, 0.0f};
+            const bool fast = same_alignment(x, out);
+            if (r.zero) {
+                zero_row<T, kThreads>(out, a.vocab, rank, size);
+            } else {
+                if (threadIdx.x < s.head) out[threadIdx.x] = narrow<T>(grad_term<false>(grad, x_head, a.c, false));
+                if (threadIdx.x < s.tail) out[s.tail_at + threadIdx.x] = narrow<T>(grad_term<false>(grad, x_tail, a.c, false));
+            }
+            const GradVector<T, false> vector(grad, a.c);
+            for (int i = 0; i < kChunks; ++i, begin.next(slots)) {
+                const int at = min(s.n, i * per), m = min(s.n, at + per) - at;
+                const uint4* v = parts + begin.at * per;
+                const int from = s.first + at * kVec<T>;  // the chunk's first element
+                if (!r.zero && fast) {
+                    uint4* to = reinterpret_cast<uint4*>(out + from);
+                    for_vectors<kThreads>(m, [&](int j) { return v[j]; }, [&](int j, const uint4& q) { __stcs(to + j, vector(q)); });
+                } else if (!r.zero) {
+                    const T* e = reinterpret_cast<const T*>(v);
+                    for (int j = threadIdx.x; j < m * kVec<T>; j += kThreads) out[from + j] = narrow<T>(grad_term<false>(grad, widen(e[j]), a.c, false));
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // -inf was written to it
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + 8 * begin.at);  // this warp has done with the part
+            }
+            consumers_sync<kThreads>();
+            if (!r.zero) write_entries<T, kThreads>(list, r, s, out, y, a.vocab);
+            release();
+            ++taken;
+        }
+    }
+    __syncwarp();
+    if (*(volatile int*)&gave_up)  // leave no copy in flight behind: they take microseconds, this a millisecond
+        for (int j = 0; j < 1000; ++j) __nanosleep(1000);
+    if (size > 1) {
+        // after giving up: keep in step with the other CTAs, which get no sums from this one
+        for (; first + n * clusters < a.rows; ++n) {
+            if (a.targets[first + n * clusters] < 0) continue;
+            if (threadIdx.x == 0) mine[0].s = mine[1].s = NAN;
+            __syncwarp();
+            cg::this_cluster().sync();
+        }
+        cg::this_cluster().sync();  // no CTA leaves while another reads its sums
+    }
+}
+
+constexpr int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
+
+// Rows of up to this many bytes are read twice, by small CTAs.
+constexpr int64_t kDistillShort = 16384;
+constexpr int64_t kDistillSpare = 2048;  // two CTAs of an SM have this much more than k_policy_rows takes
+
+template <class T, int THREADS>
+int launch_distill_rows(const Rows<T>& rows, int size, const DistillTokens& a, const zero_distill* p, size_t smem, cudaStream_t s) {
+    auto* kernel = k_distill_rows<T, THREADS>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * bitmap_words(kDistillVocab) + 24 * kListMost + 16);
+    if (e != cudaSuccess) return record_cuda_error(e);
+    return launch_linked(kernel, (unsigned)(rows.rows * size), THREADS, smem, size, s, rows, a, size, (T*)p->dlogits, p->dstride);
+}
+
+template <class T, int WARPS>
+int launch_distill_fused(const Rows<T>& rows, const FusedPlan& f, const DistillTokens& a, const zero_distill* p, size_t extra, int sms, cudaStream_t s) {
+    auto* kernel = k_distill_fused<T, WARPS>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(fused_room(WARPS) + kDistillSpare));
+    if (e != cudaSuccess) return record_cuda_error(e);
+    const int64_t clusters = std::min<int64_t>(rows.rows, fused_ctas(WARPS) * sms / f.size);
+    return launch_linked(kernel, (unsigned)(clusters * f.size), 32 * WARPS + 32, (size_t)16 * f.slots * f.part + extra, f.size, s, rows, a, f.size, f.part,
+                         f.slots, (T*)p->dlogits, p->dstride);
 }
 
 }  // namespace
@@ -381,15 +665,16 @@ extern "C" int zero_distill_loss(const zero_logits* x, const zero_distill* p, vo
     const int sms = d.sm_count(), ctas = token_ctas(x->rows);
     if (x->rows > 0) {
         if ((rc = launch_linked(k_token_setup<DistillTokens>, (unsigned)ctas, kSetupThreads, 0, ctas, s, a))) return rc;
+        const size_t extra = (size_t)up16(4 * (int64_t)bitmap_words(x->vocab) + 24 * (int64_t)a.k);
+        const FusedPlan f = x->vocab * type_size(x->type) > kDistillShort ? fused_plan(x, sms, (int64_t)extra, kDistillSpare) : FusedPlan();
         rc = by_type(x->type, [&](auto tag) {
             using T = decltype(tag);
-            auto* kernel = k_distill_rows<T, kRowThreads>;
-            const size_t smem = (size_t)4 * bitmap_words(x->vocab) + 12 * (size_t)a.k;
-            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(4 * bitmap_words(kDistillVocab) + 12 * kListMost));
-            if (e != cudaSuccess) return record_cuda_error(e);
-            const int size = ctas_per_row(x, sms, smem > 16384 ? 4 : kRowCtas / 2);
-            return launch_linked(kernel, (unsigned)(x->rows * size), kRowThreads, smem, size, s, rows_of<T>(x, nullptr), a, size, (T*)p->dlogits,
-                                 p->dstride);
+            const Rows<T> rows = rows_of<T>(x, nullptr);
+            if (f.size)
+                return f.warps == kFusedWarps ? launch_distill_fused<T, kFusedWarps>(rows, f, a, p, extra, sms, s)
+                                              : launch_distill_fused<T, kFusedWarpsSmall>(rows, f, a, p, extra, sms, s);
+            if (x->vocab * type_size(x->type) <= kDistillShort && x->rows >= 8 * (int64_t)sms) return launch_distill_rows<T, 64>(rows, 1, a, p, extra, s);
+            return launch_distill_rows<T, kRowThreads>(rows, ctas_per_row(x, sms, extra > 16384 ? 4 : kRowCtas / 2), a, p, extra, s);
         });
         if (rc) return rc;
     }

@@ -13,7 +13,6 @@
 #include <type_traits>
 
 #include "zero_rows.cuh"
-#include "zero_tcgen05.cuh"
 
 namespace zg {
 namespace {
@@ -377,29 +376,6 @@ __device__ __forceinline__ TokenLoss policy_token(const PolicyTokens& a, const T
 // tokens, a quarter masked, with entropy bonus: 232 us the whole call, 1.44 GB, 93% of the copy peak
 // (two passes over the logits: 383 us). Seven warps compute: with ten, and four parts to a slice,
 // 252 us, since registers then spill; with fifteen 325.
-constexpr int kChunks = 2, kSlots = 8;  // parts of a slice; most parts that shared memory holds
-// Computing warps of a CTA, and how many CTAs an SM then holds, by registers and shared memory.
-constexpr int kFusedWarps = 7, kFusedWarpsSmall = 3;
-constexpr int fused_ctas(int warps) { return warps == kFusedWarps ? 2 : 4; }
-constexpr int64_t fused_room(int warps) { return warps == kFusedWarps ? 110 * 1024 : 54 * 1024; }
-
-template <int THREADS>
-__device__ __forceinline__ void consumers_sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
-}
-
-// Place and phase in a ring of a number of slots.
-struct Slot {
-    int at = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next(int slots) {
-        if (++at == slots) {
-            at = 0;
-            phase ^= 1;
-        }
-    }
-};
-
 // H: entropies are formed, for the loss or only for the caller, who may want them beside a coefficient
 // of 0.
 template <class T, bool H, int WARPS>
@@ -671,33 +647,6 @@ bool short_rows(const zero_logits* x, int sms, int64_t most = kShortRow) {
     return bytes <= most && x->rows >= (bytes > kShortRow ? 16 : 8) * (int64_t)sms;
 }
 unsigned short_grid(const zero_logits* x) { return (unsigned)((x->rows + kRowThreads / 32 - 1) / (kRowThreads / 32)); }
-
-// How the one-pass kernel takes a row.
-struct FusedPlan {
-    int size = 0;      // CTAs per row; 0: two passes over the row instead
-    int warps = 0;
-    int part = 0;      // vectors of one part of a CTA's slice
-    int slots = 0;     // parts in shared memory: with more than a row's, the next row's copies begin earlier
-};
-
-// CTAs per row as ctas_per_row for few rows, else one, or two where a slice would not fit: four CTAs
-// per row wait for each other longer than a second pass takes (2709 rows of 151936 bf16: 414 us
-// against 347). Rows of half the room go to smaller CTAs, twice as many.
-FusedPlan fused_plan(const zero_logits* x, int sms) {
-    FusedPlan f;
-    const int64_t vecs = x->vocab * type_size(x->type) / 16;
-    const int few = ctas_per_row(x, sms, 2);
-    for (int size = few; size <= std::max(few, 2); size *= 2) {
-        const int64_t part = std::max<int64_t>(1, ((vecs + size - 1) / size + kChunks - 1) / kChunks);
-        if (16 * kChunks * part > fused_room(kFusedWarps)) continue;
-        f.size = size;
-        f.warps = size == 1 && 16 * kChunks * part <= fused_room(kFusedWarpsSmall) ? kFusedWarpsSmall : kFusedWarps;
-        f.part = (int)part;
-        f.slots = (int)std::min<int64_t>(kSlots, fused_room(f.warps) / (16 * part));
-        return f;
-    }
-    return f;
-}
 
 int launch_finish(const PolicyTokens& p, cudaStream_t s) {
     return launch_linked(k_token_finish<PolicyTokens>, (unsigned)token_ctas(p.rows), kSetupThreads, 0, token_ctas(p.rows), s, p);

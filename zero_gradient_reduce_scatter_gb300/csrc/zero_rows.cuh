@@ -12,6 +12,7 @@
 #include "zero_host.h"
 #include "zero_softmax.cuh"
 #include "zero_sum.cuh"
+#include "zero_tcgen05.cuh"
 
 namespace zg {
 namespace {
@@ -190,6 +191,32 @@ __device__ __forceinline__ bool same_alignment(const T* a, const T* b) {
 __device__ __forceinline__ int64_t clamp_offset(int64_t o, int64_t lo, int64_t hi) {
     return o < lo ? lo : (o > hi ? hi : o);
 }
+
+// ---- one pass over rows that stay in shared memory ------------------------------------------
+// What kernels share that bring a row's slice to shared memory by bulk copies, sum over it as it arrives,
+// and read it again for the gradient, while a producer warp brings the next row in behind it.
+constexpr int kChunks = 2, kSlots = 8;  // parts of a slice; most parts that shared memory holds
+// Computing warps of a CTA, and how many CTAs an SM then holds, by registers and shared memory.
+constexpr int kFusedWarps = 7, kFusedWarpsSmall = 3;
+constexpr int fused_ctas(int warps) { return warps == kFusedWarps ? 2 : 4; }
+constexpr int64_t fused_room(int warps) { return warps == kFusedWarps ? 110 * 1024 : 54 * 1024; }
+
+template <int THREADS>
+__device__ __forceinline__ void consumers_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+
+// Place and phase in a ring of a number of slots.
+struct Slot {
+    int at = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int slots) {
+        if (++at == slots) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+};
 
 // The weights of a batch's tokens in a loss that is a weighted sum over them.
 struct TokenWeights {
@@ -375,6 +402,34 @@ inline int ctas_per_row(const zero_logits* x, int sms, int per_sm = kRowCtas) {
     int size = 1;
     while (size < 8 && 2 * size * x->rows <= per_sm * (int64_t)sms && x->vocab * type_size(x->type) / (2 * size) >= 4096) size *= 2;
     return size;
+}
+
+// How the one-pass kernel takes a row.
+struct FusedPlan {
+    int size = 0;      // CTAs per row; 0: two passes over the row instead
+    int warps = 0;
+    int part = 0;      // vectors of one part of a CTA's slice
+    int slots = 0;     // parts in shared memory: with more than a row's, the next row's copies begin earlier
+};
+
+// CTAs per row as ctas_per_row for few rows, else one, or two where a slice would not fit: four CTAs
+// per row wait for each other longer than a second pass takes (2709 rows of 151936 bf16: 414 us
+// against 347). Rows of half the room go to smaller CTAs, twice as many.
+// `reserve`: bytes of shared memory that a kernel needs beside the slices; `spare`: what its larger CTAs may take over the room.
+inline FusedPlan fused_plan(const zero_logits* x, int sms, int64_t reserve = 0, int64_t spare = 0) {
+    FusedPlan f;
+    const int64_t vecs = x->vocab * type_size(x->type) / 16;
+    const int few = ctas_per_row(x, sms, 2);
+    for (int size = few; size <= std::max(few, 2); size *= 2) {
+        const int64_t part = std::max<int64_t>(1, ((vecs + size - 1) / size + kChunks - 1) / kChunks);
+        if (16 * kChunks * part > fused_room(kFusedWarps) + spare - reserve) continue;
+        f.size = size;
+        f.warps = size == 1 && 16 * kChunks * part <= fused_room(kFusedWarpsSmall) - reserve ? kFusedWarpsSmall : kFusedWarps;
+        f.part = (int)part;
+        f.slots = (int)std::min<int64_t>(kSlots, (fused_room(f.warps) + (f.warps == kFusedWarps ? spare : 0) - reserve) / (16 * part));
+        return f;
+    }
+    return f;
 }
 
 // CTAs of the kernels over tokens alone: a cluster of eight begins 3 us later than one CTA, which
