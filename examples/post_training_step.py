@@ -1,12 +1,17 @@
-"""Preference or policy training of a tiny language model, end to end on one GPU.
+"""Preference, policy or distillation training of a tiny language model, end to end on one GPU.
 
-    python examples/post_training_step.py [preference|policy] [steps]
+    python examples/post_training_step.py [preference|policy|distill] [steps]
 
 Each step is what a post-training loop does around the optimizer: the frozen reference model's
 log-probabilities without its logits (``linear_logp``), the trained model's loss with its gradient
 on the logits (``preference_loss`` or ``policy_loss``), autograd for the parameters' gradients,
 their global norm and clipping straight into the flat gradient buffer (``GradClip.into``), and one
 ZeRO step, whose bf16 parameters go back to the model.
+
+Distillation has a teacher of its own in place of the reference: its most likely tokens
+(``top_logits``), the student's divergence from them with its gradient (``distill_loss``), and the
+embedding's rows and their gradient by the library too (``embedding``, ``embedding_backward``), added to
+the gradient that the output product leaves on the same matrix.
 
 The model predicts the next token from the last two (embeddings, one hidden layer, the embedding
 again as the vocabulary matrix). The task is synthetic: answers made of even tokens are preferred.
@@ -33,8 +38,12 @@ class Model:
 
     def hidden(self, tokens):
         """[T, DIM] states that predict the token after each of `tokens`."""
-        wte, w1, w2 = self.params
-        pair = torch.cat([wte[tokens], wte[tokens.roll(1)]], 1)
+        wte = self.params[0]
+        return self.states(torch.cat([wte[tokens], wte[tokens.roll(1)]], 1))
+
+    def states(self, pair):
+        """The same from the rows of each token and of the one before it, [T, 2 DIM]."""
+        _, w1, w2 = self.params
         return torch.nn.functional.gelu(pair @ w1) @ w2
 
     def load(self, flat):
@@ -62,6 +71,41 @@ def batch(generator):
     return torch.cat(tokens), torch.cat(targets), offsets
 
 
+def both(tokens):
+    """Each token, and behind them the token before each."""
+    return torch.cat([tokens, tokens.roll(1)])
+
+
+def distill(model, teacher, tokens, targets, offsets, **kw):
+    """The distillation loss of a batch; its gradients are added to the parameters' own."""
+    wte = model.params[0]
+    with torch.no_grad():
+        top = zg.top_logits(teacher.hidden(tokens) @ teacher.params[0].T, 16, targets)
+    rows = zg.embedding(wte.detach(), both(tokens)).requires_grad_()
+    logits = model.states(rows.view(2, -1, DIM).transpose(0, 1).reshape(-1, 2 * DIM)) @ wte.T
+    r = zg.distill_loss(logits.detach(), targets, top.index, top.logp, top.rest, offsets=offsets, **kw)
+    logits.backward(r.dlogits)  # the output product's part of wte's gradient
+    zg.embedding_backward(both(tokens), rows.grad, VOCAB, out=wte.grad, accumulate=True)  # and the embedding's
+    return r
+
+
+def prefer(kind, model, reference, tokens, targets, offsets):
+    """The preference or policy loss of a batch; its gradients are added to the parameters' own."""
+    wte = model.params[0]
+    with torch.no_grad():
+        ref = zg.linear_logp(reference.hidden(tokens), reference.params[0], targets).logp
+        old = zg.linear_logp(model.hidden(tokens), wte.detach(), targets).logp if kind == "policy" else None
+    logits = model.hidden(tokens) @ wte.T
+    if kind == "preference":
+        r = zg.preference_loss(logits.detach(), targets, offsets, ref, beta=0.2)
+    else:
+        advantages = torch.tensor([1.0, -1.0] * PAIRS, device="cuda")
+        r = zg.policy_loss(logits.detach(), targets, advantages, old, ref, offsets=offsets, clip_high=0.28, kl_coef=0.02,
+                           entropy_coef=0.001, reduce="sequence")
+    logits.backward(r.dlogits)
+    return r
+
+
 def train(kind="preference", steps=20, seed=0):
     """Returns each step's (loss, gradient norm before clipping, log-probability of the good answers
     above the bad ones', mean over pairs)."""
@@ -77,22 +121,16 @@ def train(kind="preference", steps=20, seed=0):
     clip = zg.GradClip.into(opt, [p.grad for p in model.params], flat)
     reference = Model.__new__(Model)
     reference.params = frozen
+    teacher = Model(torch.Generator(device="cuda").manual_seed(seed + 1)) if kind == "distill" else None
     log = []
     for _ in range(steps):
         tokens, targets, offsets = batch(g)
-        with torch.no_grad():
-            ref = zg.linear_logp(reference.hidden(tokens), frozen[0], targets).logp
-            old = zg.linear_logp(model.hidden(tokens), model.params[0].detach(), targets).logp if kind == "policy" else None
-        logits = model.hidden(tokens) @ model.params[0].T
-        if kind == "preference":
-            r = zg.preference_loss(logits.detach(), targets, offsets, ref, beta=0.2)
-        else:
-            advantages = torch.tensor([1.0, -1.0] * PAIRS, device="cuda")
-            r = zg.policy_loss(logits.detach(), targets, advantages, old, ref, offsets=offsets, clip_high=0.28, kl_coef=0.02,
-                               entropy_coef=0.001, reduce="sequence")
         for p in model.params:
             p.grad.zero_()
-        logits.backward(r.dlogits)
+        if kind == "distill":
+            r = distill(model, teacher, tokens, targets, offsets, reduce="sequence", ce_coef=0.1)
+        else:
+            r = prefer(kind, model, reference, tokens, targets, offsets)
         c = clip.clip(1.0)
         opt.step([flat], zg.Hyper(lr=2e-3, weight_decay=0.0))
         model.load(opt.params())

@@ -81,13 +81,29 @@ __device__ __forceinline__ void strike(uint4& v, uint32_t marks) {
     }
 }
 
-// log s as hi + lo (finish_row's reduction), hi exact.
-__device__ __forceinline__ float2 log_parts(float s) {
+// log s as hi + lo (finish_row's reduction), hi exact; `share` of it are terms whose pow2 errs low.
+__device__ __forceinline__ float2 log_parts(float s, float share = 1.0f) {
     constexpr float kLn2Hi = 2839.0f / 4096.0f, kLn2Lo = 3.1946184945309e-5f;
     const uint32_t bits = __float_as_uint(s);
     const bool plain = s >= 0x1p-126f && s < INFINITY;
     const float n = plain ? (float)((int)(bits >> 23) - 127) : 0.0f, f = plain ? __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u) : s;
-    return make_float2(n * kLn2Hi, logf(f) + fmaf(n, kLn2Lo, kPow2Low));
+    return make_float2(n * kLn2Hi, logf(f) + fmaf(n, kLn2Lo, kPow2Low * share));
+}
+
+// 1 / temperature in two numbers.
+__device__ __forceinline__ float2 inverse(double inv_t) { return make_float2((float)inv_t, (float)(inv_t - (double)(float)inv_t)); }
+
+// (x - base) / temperature in two numbers. A divergence of a few tenths is the sum of differences of
+// log-probabilities near 10, whose own roundings would be 1e-6 of it.
+__device__ __forceinline__ float2 over_base(float x, float base, float2 inv_t) {
+    const float d = __fsub_rn(x, base), z = __fsub_rn(d, x), lost = __fsub_rn(__fsub_rn(x, __fsub_rn(d, z)), __fadd_rn(base, z));
+    const float hi = __fmul_rn(d, inv_t.x);
+    return make_float2(hi, __fmaf_rn(d, inv_t.x, -hi) + __fmaf_rn(d, inv_t.y, lost * inv_t.x));
+}
+// log p - log q, log p = lp - shift, log q = z - log s, with z in two numbers as above.
+__device__ __forceinline__ float log_ratio(float lp, float shift, float2 z, float2 log_s) {
+    const float d = __fsub_rn(lp, z.x), w = __fsub_rn(d, lp), lost = __fsub_rn(__fsub_rn(lp, __fsub_rn(d, w)), __fadd_rn(z.x, w));
+    return fabsf(d) < INFINITY ? __fadd_rn(__fadd_rn(d, log_s.x), ((lost + log_s.y) - z.y) - shift) : d;
 }
 
 __device__ __forceinline__ float warp_add(float v) {
@@ -160,7 +176,7 @@ __device__ __forceinline__ void sum_list(const List& list, Scale k, int64_t y, f
 // does) and the gradients of this thread's entries over list.x. Valid in all threads.
 template <int THREADS, class S>
 __device__ __forceinline__ DistillRow finish_list(const DistillTokens& a, const List& list, const RowStat& rest, bool bad, int64_t t, int64_t y,
-                                                  float x_y, int64_t vocab, Scale k, float inv_t, bool first, const float4* shares, float2* parts,
+                                                  float x_y, int64_t vocab, Scale k, float2 inv_t, bool first, const float4* shares, float2* parts,
                                                   S sync) {
     constexpr int kWarps = THREADS / 32;
     const float w = a.w[t];
@@ -181,16 +197,17 @@ __device__ __forceinline__ DistillRow finish_list(const DistillTokens& a, const 
     if (rest.s != 0.0f) total += rest.s * up;
     if (bad || y >= vocab) total = NAN;
     const bool nothing = total == 0.0f;  // -inf alone
-    const float2 all = log_parts(total);
+    const float over = nothing ? 0.0f : 1.0f / total;
+    const float2 all = log_parts(total, 1.0f - over);
     const bool with_rest = a.tail == ZERO_TAIL_REST && count < vocab;
-    const float shift = a.tail == ZERO_TAIL_RENORMALISE && count > 0 ? logf(mass) : 0.0f, over = nothing ? 0.0f : 1.0f / total;
-    auto logq = [&](float x) { return nothing ? -INFINITY : ((x - base) * inv_t - all.x) - all.y; };
+    const float shift = a.tail == ZERO_TAIL_RENORMALISE && count > 0 ? logf(mass) : 0.0f;
+    auto ratio = [&](float lp, float x) { return nothing ? INFINITY : log_ratio(lp, shift, over_base(x, base, inv_t), all); };
     float d = 0.0f, c = 0.0f;
     if ((threadIdx.x & ~31) < list.k) {
         for (int i = threadIdx.x; i < list.k; i += THREADS) {
             if (list.place[i] < 0) continue;
-            const float x = list.x[i], lp = list.lp[i] - shift, q = pow2(scaled<false>(x - base, k)) * over;
-            const Part part = entry_part(a.kind, a.mix, expf(lp), q, lp - logq(x));
+            const float x = list.x[i], lp = list.lp[i], q = pow2(scaled<false>(x - base, k)) * over;
+            const Part part = entry_part(a.kind, a.mix, expf(lp - shift), q, ratio(lp, x));
             d += part.d;
             c += part.c;
         }
@@ -208,15 +225,15 @@ __device__ __forceinline__ DistillRow finish_list(const DistillTokens& a, const 
     if (with_rest) {
         const float lp = a.teacher_rest ? a.teacher_rest[t] : logf(fmaxf(1.0f - mass, 0x1p-24f));
         const float2 own = log_parts(rest.s);
-        const float lq = nothing || rest.s == 0.0f ? -INFINITY : ((rest_base - base) * inv_t + (own.x - all.x)) + (own.y - all.y);
-        const float q = rest.s != 0.0f ? rest.s * up * over : 0.0f;
-        const float p = mass == mass ? expf(lp) : NAN;
-        if (!(lp == -INFINITY && lq == -INFINITY)) outside = entry_part(a.kind, a.mix, p, q, lp - lq);
+        const bool none = nothing || rest.s == 0.0f;  // no q
+        const float q = none ? 0.0f : rest.s * up * over, p = mass == mass ? expf(lp) : NAN;
+        const float r_rest = none ? INFINITY : log_ratio(lp, 0.0f, over_base(rest_base, base, inv_t), make_float2(all.x - own.x, all.y - own.y));
+        if (!(lp == -INFINITY && none)) outside = entry_part(a.kind, a.mix, p, q, r_rest);
         d += outside.d;
         c += outside.c;
     }
     // a coefficient of 0 leaves its term out, also where that is infinite
-    const float g = w * a.kl_coef * inv_t, h = w * a.ce_coef * inv_t;
+    const float g = w * a.kl_coef * inv_t.x, h = w * a.ce_coef * inv_t.x;
     const float share = (a.ce_coef != 0.0f ? h : 0.0f) - (a.kl_coef != 0.0f ? g * c : 0.0f);
     r.base = rest_base;
     r.factor = 0.0f;  // outside the list there is nothing above -inf
@@ -227,16 +244,17 @@ __device__ __forceinline__ DistillRow finish_list(const DistillTokens& a, const 
     if (total != total) r.factor = NAN;
     for (int i = threadIdx.x; i < list.k; i += THREADS) {
         if (list.place[i] < 0) continue;
-        const float x = list.x[i], lp = list.lp[i] - shift, q = pow2(scaled<false>(x - base, k)) * over;
+        const float x = list.x[i], lp = list.lp[i], q = pow2(scaled<false>(x - base, k)) * over;
         float v = share * q;
-        if (a.kl_coef != 0.0f) v += g * entry_part(a.kind, a.mix, expf(lp), q, lp - logq(x)).c;
+        if (a.kl_coef != 0.0f) v += g * entry_part(a.kind, a.mix, expf(lp - shift), q, ratio(lp, x)).c;
         if (list.place[i] == y) v -= h;
         list.x[i] = nothing ? 0.0f : v;
     }
     r.zero = w == 0.0f || nothing;
     r.target = nothing ? 0.0f : fmaf(pow2(scaled<false>(x_y - rest_base, k)), r.factor, -h);
     if (first && threadIdx.x == 0) {
-        const float logp = y < vocab ? logq(x_y) : NAN;
+        const float2 z = over_base(x_y, base, inv_t);
+        const float logp = y >= vocab ? NAN : nothing || x_y == -INFINITY ? -INFINITY : __fsub_rn(z.x, all.x) + (z.y - all.y);
         float loss = 0.0f;
         if (a.kl_coef != 0.0f) loss += a.kl_coef * d;
         if (a.ce_coef != 0.0f) loss -= a.ce_coef * logp;
@@ -339,7 +357,7 @@ __global__ void __launch_bounds__(THREADS) k_distill_rows(const Rows<T> a, const
     }
     if (!good) st = sums(std::true_type());
     st = cluster_join<false>(st, size, a.k, &mine);
-    const DistillRow r = finish_list<THREADS>(p, list, st, shared_bad != 0, t, y, x_y, a.vocab, a.k, (float)a.inv_t, rank == 0, shares, sums_of,
+    const DistillRow r = finish_list<THREADS>(p, list, st, shared_bad != 0, t, y, x_y, a.vocab, a.k, inverse(a.inv_t), rank == 0, shares, sums_of,
                                               [] { __syncthreads(); });
     const GradRow grad = {0.0f, -r.factor, 0.0f, r.base, 0.0f};
     if (same_alignment(x, out)) {
@@ -528,7 +546,7 @@ __global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
             if (!good) st = sums(std::true_type());
             if (!ok || *(volatile int*)&gave_up) st.s = NAN;  // a copy did not come: no result
             st = cluster_join<false>(st, size, a.k, mine + (taken & 1));
-            const DistillRow r = finish_list<kThreads>(p, list, st, shared_bad[n & 1] != 0, t, y, x_y, a.vocab, a.k, (float)a.inv_t, rank == 0, shares, sums_of,
+            const DistillRow r = finish_list<kThreads>(p, list, st, shared_bad[n & 1] != 0, t, y, x_y, a.vocab, a.k, inverse(a.inv_t), rank == 0, shares, sums_of,
                                                        [] { consumers_sync<kThreads>(); });
             const GradRow grad = {0.0f, -r.factor, 0.0f, r.base, 0.0f};
             const bool fast = same_alignment(x, out);
