@@ -125,11 +125,11 @@ __device__ __forceinline__ Part entry_part(int kind, float b, float p, float q, 
     // log p - log m and log q - log m from r alone
     float pm, qm;
     if (r > 0.0f) {
-        const float m = logf(fmaf(1.0f - b, expf(-r), b));
+        const float m = log1pf((1.0f - b) * expm1f(-r));
         pm = -m;
         qm = -(r + m);
     } else {
-        const float m = logf(fmaf(b, expf(r), 1.0f - b));
+        const float m = log1pf(b * expm1f(r));
         pm = r - m;
         qm = -m;
     }
@@ -266,6 +266,44 @@ __device__ __forceinline__ DistillRow finish_list(const DistillTokens& a, const 
     return r;
 }
 
+// The rest's sum over a base that is given and stays, the list's largest logit: near the row's mass, so that exponents and
+// their roundings are small (over the target's logit, as elsewhere, an unlikely target cost 7e-7 of a divergence). Where the
+// rest is not good_rest, the sum is formed once more over its own maximum (Sums, CHECKED).
+template <class T>
+struct RestSums {
+    const float m;
+    const uint64_t base, c, lo;
+    uint64_t s[2];
+    const Scale k;
+
+    __device__ __forceinline__ RestSums(Scale k, float m) : m(m), base(pack2(-m, -m)), c(pack2(k.c, k.c)), lo(pack2(k.lo, k.lo)), k(k) {
+        s[0] = s[1] = pack2(0.0f, 0.0f);
+    }
+    __device__ __forceinline__ void add(const uint4& v) {
+#pragma unroll
+        for (int i = 0; i < kVec<T> / 2; ++i) {
+            const uint64_t t = add2(widen2<T>(v, i), base);
+            const float2 z = unpack2(fma2(t, lo, mul2(t, c)));
+            s[i & 1] = add2(s[i & 1], pack2(pow2(z.x), pow2(z.y)));
+        }
+    }
+    __device__ __forceinline__ void add_one(float x) { s[0] = add2(s[0], pack2(pow2(scaled<false>(x - m, k)), 0.0f)); }
+    __device__ __forceinline__ RowStat stat() const {
+        const float2 f = unpack2(add2(s[0], s[1]));
+        return {m, f.x + f.y, 0.0f};
+    }
+};
+template <class T, bool CHECKED>
+using SumsOf = std::conditional_t<CHECKED, Sums<T, false, true>, RestSums<T>>;
+
+// The list's largest logit (sum_list), after a barrier.
+template <int THREADS>
+__device__ __forceinline__ float list_top(const float4* shares, int k) {
+    float top = -INFINITY;
+    for (int i = 0; i < min(THREADS / 32, (k + 31) / 32); ++i) top = fmaxf(top, shares[i].x);
+    return top;
+}
+
 // Whether sums that were not CHECKED are good: the rest may be any share of the base's term.
 __device__ __forceinline__ bool good_rest(const RowStat& a) { return a.s > 0x1p-60f && a.s < 0x1p60f; }
 
@@ -334,9 +372,10 @@ __global__ void __launch_bounds__(THREADS) k_distill_rows(const Rows<T> a, const
     }
     sum_list<THREADS>(list, a.k, y, shares);
     __syncthreads();
+    const float listed_top = list_top<THREADS>(shares, p.k);
     auto sums = [&](auto checked) {
         constexpr bool kChecked = decltype(checked)::value;
-        Sums<T, false, kChecked> run(a.k, x_y);
+        SumsOf<T, kChecked> run(a.k, listed_top);
         auto use = [&](int i, uint4 q) {
             const uint32_t marks = vector_bits<T>(list.bits, s.first + i * kVec<T>, shift);
             if (marks) strike<T>(q, marks);
@@ -350,7 +389,7 @@ __global__ void __launch_bounds__(THREADS) k_distill_rows(const Rows<T> a, const
     };
     RowStat st;
     bool good = false;
-    if (fabsf(x_y) < INFINITY) {
+    if (fabsf(listed_top) < INFINITY) {
         st = sums(std::false_type());
         good = good_rest(st);
         if (!good) __syncthreads();
@@ -521,12 +560,14 @@ __global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
                 }
                 consumers_sync<kThreads>();
             };
+            strike_list(0, begin);
+            const float listed_top = list_top<kThreads>(shares, p.k);
             auto sums = [&](auto checked) {
                 constexpr bool kChecked = decltype(checked)::value;
-                Sums<T, false, kChecked> run(a.k, x_y);
+                SumsOf<T, kChecked> run(a.k, listed_top);
                 Slot slot = begin;
                 for (int i = 0; i < kChunks; ++i, slot.next(slots)) {
-                    if (!struck) strike_list(i, slot);
+                    if (i > 0 && !struck) strike_list(i, slot);
                     const int at = min(s.n, i * per);
                     const uint4* v = parts + slot.at * per;
                     for_vectors<kThreads>(min(s.n, at + per) - at, [&](int j) { return v[j]; }, [&](int, const uint4& q) { run.add(q); });
@@ -538,7 +579,7 @@ __global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
             };
             RowStat st;
             bool good = false;
-            if (fabsf(x_y) < INFINITY) {
+            if (fabsf(listed_top) < INFINITY) {
                 st = sums(std::false_type());
                 good = good_rest(st);
                 if (!good) consumers_sync<kThreads>();
