@@ -623,11 +623,12 @@ int zero_grad_norm_noalloc(const void* const* grads, int M, const int64_t* bucke
 double zero_state_bytes_per_param(int stage, int M, double param_bytes, double grad_bytes,
                                   double optim_bytes);
 
-/* ---- Training losses and gradient clipping ---------------------------------------------
+/* ---- Training losses, distillation, embedding and gradient clipping ----------------------
  * What stands directly before an optimizer step of a language model, as calls of their own:
  * the log-probability of given tokens (from logits, or from hidden states and the vocabulary
- * matrix without any logits in memory), a preference loss or a clipped policy loss with its
- * gradient on the logits, and the global norm and clipping of gradients that are still
+ * matrix without any logits in memory), a preference loss, a clipped policy loss or a distillation
+ * loss with its gradient on the logits, the most likely tokens that a distillation keeps of its
+ * teacher, the embedding of tokens with its gradient, and the global norm and clipping of gradients that are still
  * separate tensors, written in place or into the flat gradient buffer of a step. The pages
  * define none of these; they start where the gradients exist.
  *

@@ -89,7 +89,8 @@ struct LaneOld {
 };
 
 // ---------------------------------------------------------------------------------------
-// Forward: a warp per kRowSlices slices of a token's row.
+// Forward: a warp per kRowSlices slices of a token's row. 16384 x 2048 bf16 12.3 us, bound by memory (12.8 us from HBM alone; the
+// matrix' frequent rows stay in L2); one token 1.6 us.
 // ---------------------------------------------------------------------------------------
 constexpr int kRowSlices = 4;
 
@@ -131,7 +132,8 @@ __global__ void __launch_bounds__(kEmbedThreads)
 // share each: once to count its own tokens and those below them, which is where its part of the order
 // begins, and once to write its positions there. A warp takes a contiguous share of the positions with
 // counters of its own, and lanes of one token rank themselves, so the order is that of the positions, and
-// equal calls give equal bits. Rows of no token are zeroed by their owner meanwhile.
+// equal calls give equal bits. Rows of no token are zeroed by their owner meanwhile, which bounds it where there are many: 370 MB
+// in 62 us. 65536 positions alone take 18 us, bound by reading them from L2 (38 clusters, twice); each CTA for itself 31.
 // ---------------------------------------------------------------------------------------
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSortWidth = 1600;  // most tokens of a cluster: 205 KB of counters
@@ -268,7 +270,9 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs a) {
 // a block's rows, run by run. A token's run that lies in one block is written at once; one that
 // goes on in others leaves its part in the workspace, and the warp that ends last adds the parts up, in
 // their order: first those within kGroup blocks, then the groups'. So a token that is all of the batch
-// is as well spread over the GPU as one that occurs twice.
+// is as well spread over the GPU as one that occurs twice. 65536 rows of 2048 bf16, tokens as text has them, added to a matrix:
+// 97 us with the sort, 60% of the copy peak on 398 MB; rows in registers, eight ahead and then none, 140. The rest is the warps'
+// first rows and the joins of runs.
 // ---------------------------------------------------------------------------------------
 constexpr int kGroup = 32;  // blocks
 constexpr int kAhead = 8;        // rows of a warp on their way at a time
@@ -582,15 +586,15 @@ int check_embed(int64_t rows, int64_t vocab, double scale) {
     return rows < 0 || rows > INT32_MAX || vocab < 1 || vocab > (1 << 30) || !std::isfinite((float)scale) ? ZERO_ERR_INVALID_ARG : ZERO_OK;
 }
 
-// Positions of a block: as many as leave 4096 warps, 8 to 128. Fewer leave SMs without work, and with more
-// blocks more runs are cut: 65536 positions of 2048 bf16 numbers 205 us in blocks of 32.
+// Positions of a block: as many as leave 4096 warps, 8 to 128. Fewer leave SMs without work, and with more blocks more runs
+// are cut: 65536 positions of 2048 bf16 numbers 97 us in blocks of 128 or 64, 104 of 32.
 int block_of(int64_t rows, int64_t slices) {
     int block = 8;
     while (block < kBlockMost && rows * slices / (2 * block) >= 4096) block *= 2;
     return block;
 }
-// Batches from here on have their positions read by a cluster of four CTAs instead of by each: 65536 positions are sorted in
-// 31 us by one.
+// Batches from here on have their positions read by a cluster of four CTAs instead of by each (k_embed_sort). Clusters leave some
+// SMs over, which the zeroing of a smaller batch's matrix misses: 16384 positions into 412 MB 98 us without, 114 with.
 constexpr int64_t kSortShared = 32768;
 
 // The backward's workspace.

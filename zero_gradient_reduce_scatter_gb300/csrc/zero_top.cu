@@ -260,7 +260,7 @@ struct TopRow {
     }
 
     // ---- the usual way -----------------------------------------------------------------
-    // A segment is `vectors` vectors of a thread, THREADS apart; the row's are numbered through. 2^(x C - from - kDown),
+    // A segment is `vectors` vectors of a thread, THREADS apart; the row's are numbered through. 2^(x C - from),
     // with the product inside the fused operation, so that differences of any large values are kept.
     __device__ __forceinline__ void term(uint64_t (&sum)[2], int i, uint64_t x, uint64_t from) const {
         const float2 z = unpack2(fma2(x, lo2, fma2(x, c2, from)));
@@ -337,7 +337,7 @@ struct TopRow {
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(~0u, low, o));
                 base_c = low * scale.c;
-                from = pack2(-base_c - kDown, -base_c - kDown);
+                from = pack2(-base_c, -base_c);
             }
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
@@ -439,7 +439,7 @@ struct TopRow {
         for (int h = id; h < hots; h += THREADS) {
             const int its = sm.hot[h], g = its / THREADS, who = its % THREADS;
             const float its_base = sm.bases[who >> 5];
-            const uint64_t its_from = pack2(-its_base - kDown, -its_base - kDown);
+            const uint64_t its_from = pack2(-its_base, -its_base);
             uint64_t sum[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
             for (int at = g * per + who, end = min(part.n, (g + 1) * per); at < end; at += kUnroll * THREADS) {
                 uint4 q[kUnroll];
@@ -478,8 +478,7 @@ struct TopRow {
         sync();
         float mass = 0.0f;
         for (int g = 0; g < segments; ++g) mass += segs[g * THREADS + id];
-        static_assert(kDown == 20.0f, "2^kDown");
-        s[0] = pack2(mass * pow2(gap) * 0x1p20f, 0.0f);
+        s[0] = pack2(mass * pow2(gap), 0.0f);
         s[1] = pack2(0.0f, 0.0f);
         base = pack2(-low, -low);
         // the ends of the row
@@ -815,6 +814,10 @@ struct TopOut {
     float *logp, *lse, *rest;
 };
 
+// A CTA of 128 threads per row (256 for k > 128), several per short batch's row, or a warp per short row. 8192 x 50257 bf16 with a
+// quarter masked, k = 64: 140 us, 66% of the copy peak on 624 MB; k = 8 unmasked 140 us, 87%. The stream alone keeps up with
+// HBM; what a row does after it (threshold, segments read again, ranking) is a chain of latencies of 9 us, behind which eight
+// CTAs of an SM hide three quarters: with four of 256 threads 206 us. Loads run a step ahead of the sums (170 us without).
 template <class T, int THREADS, int CAP>
 __global__ void __launch_bounds__(THREADS == 32 ? kRowThreads : THREADS, THREADS == 32 ? 3 : 1024 / THREADS) k_top_rows(const Rows<T> a, int k, int size, int vectors, int space, const TopOut out) {
     using Row = TopRow<T, THREADS, CAP>;
@@ -949,26 +952,27 @@ __global__ void __launch_bounds__(THREADS == 32 ? kRowThreads : THREADS, THREADS
     }
 }
 
+// Rows of up to this many bytes, enough of them for every SM and short lists: a warp each. 8192 x 4000 bf16, k = 20: 28 us.
+constexpr int64_t kTopShort = 16384;
+constexpr int kTopShortMost = 64;
+
 template <class T, int THREADS, int CAP>
 int launch_top(const zero_logits* x, int k, int size, const TopOut& out, unsigned grid, cudaStream_t s) {
     // a segment: one vector of a warp's short row, else four, or as many as leave kSegments
-    const int64_t vecs = x->vocab * type_size(x->type) / 16 / size + 1;
-    const int most = THREADS == 32 ? kShortSegments : kSegments;
+    constexpr int kMost = THREADS == 32 ? kShortSegments : kSegments;
+    static_assert(kTopShort <= 16 * 32 * kShortSegments, "a warp's row has a segment for every vector");
+    const int64_t vecs = (x->vocab * type_size(x->type) / 16 + size - 1) / size;
     int vectors = THREADS == 32 ? 1 : kUnroll;
-    while (vecs > (int64_t)most * vectors * THREADS) vectors += THREADS == 32 ? 1 : kUnroll;
+    while (vecs > (int64_t)kMost * vectors * THREADS) vectors += kUnroll;
     const int segments = (int)((vecs + vectors * THREADS - 1) / (vectors * THREADS));
     const int space = (int)(sizeof(TopSpace<THREADS, CAP>) + 8 * (size_t)segments * THREADS);
     const size_t bytes = (size_t)space * (THREADS == 32 ? kRowThreads / 32 : 1);
     auto* kernel = k_top_rows<T, THREADS, CAP>;
-    constexpr size_t kBytes = (sizeof(TopSpace<THREADS, CAP>) + 8 * (size_t)THREADS * (THREADS == 32 ? kShortSegments : kSegments)) * (THREADS == 32 ? kRowThreads / 32 : 1);
+    constexpr size_t kBytes = (sizeof(TopSpace<THREADS, CAP>) + 8 * (size_t)THREADS * kMost) * (THREADS == 32 ? kRowThreads / 32 : 1);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBytes);
     if (e != cudaSuccess) return record_cuda_error(e);
     return launch_linked(kernel, grid, THREADS == 32 ? kRowThreads : THREADS, bytes, size, s, rows_of<T>(x, nullptr), k, size, vectors, space, out);
 }
-
-// Rows of up to this many bytes, enough of them for every SM and short lists: a warp each.
-constexpr int64_t kTopShort = 16384;
-constexpr int kTopShortMost = 64;
 
 }  // namespace
 }  // namespace zg
