@@ -81,26 +81,7 @@ __device__ __forceinline__ void strike(uint4& v, uint32_t marks) {
     }
 }
 
-// log s as hi + lo (finish_row's reduction), hi exact; `share` of it are terms whose pow2 errs low.
-__device__ __forceinline__ float2 log_parts(float s, float share = 1.0f) {
-    constexpr float kLn2Hi = 2839.0f / 4096.0f, kLn2Lo = 3.1946184945309e-5f;
-    const uint32_t bits = __float_as_uint(s);
-    const bool plain = s >= 0x1p-126f && s < INFINITY;
-    const float n = plain ? (float)((int)(bits >> 23) - 127) : 0.0f, f = plain ? __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u) : s;
-    return make_float2(n * kLn2Hi, logf(f) + fmaf(n, kLn2Lo, kPow2Low * share));
-}
-
-// 1 / temperature in two numbers.
-__device__ __forceinline__ float2 inverse(double inv_t) { return make_float2((float)inv_t, (float)(inv_t - (double)(float)inv_t)); }
-
-// (x - base) / temperature in two numbers. A divergence of a few tenths is the sum of differences of
-// log-probabilities near 10, whose own roundings would be 1e-6 of it.
-__device__ __forceinline__ float2 over_base(float x, float base, float2 inv_t) {
-    const float d = __fsub_rn(x, base), z = __fsub_rn(d, x), lost = __fsub_rn(__fsub_rn(x, __fsub_rn(d, z)), __fadd_rn(base, z));
-    const float hi = __fmul_rn(d, inv_t.x);
-    return make_float2(hi, __fmaf_rn(d, inv_t.x, -hi) + __fmaf_rn(d, inv_t.y, lost * inv_t.x));
-}
-// log p - log q, log p = lp - shift, log q = z - log s, with z in two numbers as above.
+// log p - log q, log p = lp - shift, log q = z - log s, with z in two numbers (over_base).
 __device__ __forceinline__ float log_ratio(float lp, float shift, float2 z, float2 log_s) {
     const float d = __fsub_rn(lp, z.x), w = __fsub_rn(d, lp), lost = __fsub_rn(__fsub_rn(lp, __fsub_rn(d, w)), __fadd_rn(z.x, w));
     return fabsf(d) < INFINITY ? __fadd_rn(__fadd_rn(d, log_s.x), ((lost + log_s.y) - z.y) - shift) : d;

@@ -800,15 +800,6 @@ __device__ __forceinline__ void sort_in_place(uint64_t* list, int n, int size_al
     }
 }
 
-// log s in two numbers, hi exact (as in finish_row), for s in fp32's range; sums of pow2 err low.
-__device__ __forceinline__ float2 log_parts(float s) {
-    constexpr float kLn2Hi = 2839.0f / 4096.0f, kLn2Lo = 3.1946184945309e-5f;
-    const uint32_t bits = __float_as_uint(s);
-    const bool plain = s >= 0x1p-126f && s < INFINITY;
-    const float n = plain ? (float)((int)(bits >> 23) - 127) : 0.0f, f = plain ? __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u) : s;
-    return make_float2(n * kLn2Hi, logf(f) + fmaf(n, kLn2Lo, kPow2Low));
-}
-
 struct TopOut {
     int64_t* index;
     float *logp, *lse, *rest;
@@ -936,19 +927,24 @@ __global__ void __launch_bounds__(THREADS == 32 ? kRowThreads : THREADS, THREADS
         for (int r = 1; r < 8; ++r) rest += r < size ? rests[r] * pow2(scaled<false>(lows[r] - under_base, a.k)) : 0.0f;
     }
     if (id >= k) return;  // no result of this thread's
-    const float inv_t = (float)a.inv_t;
+    const float2 inv_t = inverse(a.inv_t);
     const float total = sel + rest * pow2(scaled<false>(under_base - top_base, a.k));
-    const float2 all = log_parts(total), outside = log_parts(rest);
+    const float2 all = log_parts(total, 1.0f - 1.0f / total), outside = log_parts(rest);
     const bool nothing = total == 0.0f;  // -inf alone
     for (int i = id; i < k; i += THREADS) {
         const uint64_t its = i < n ? sm.cand[i] : 0;
         const float v = value_of((uint32_t)(its >> 32));
         out.index[t * k + i] = i < n ? (int64_t)(int)~(uint32_t)its : -1;
-        out.logp[t * k + i] = i >= n ? NAN : nothing ? -INFINITY : ((v - top_base) * inv_t - all.x) - all.y;
+        const float2 z = over_base(v, top_base, inv_t);
+        out.logp[t * k + i] = i >= n ? NAN : nothing || v == -INFINITY ? -INFINITY : __fsub_rn(z.x, all.x) + (z.y - all.y);
     }
     if (id == 0) {
-        out.lse[t] = nothing ? -INFINITY : fmaf(top_base, inv_t, all.x) + all.y;
-        out.rest[t] = rest == 0.0f && total == total ? -INFINITY : ((under_base - top_base) * inv_t + (outside.x - all.x)) + (outside.y - all.y);
+        const float2 z = over_base(under_base, top_base, inv_t);
+        out.lse[t] = nothing ? -INFINITY : fmaf(top_base, inv_t.x, all.x) + fmaf(top_base, inv_t.y, all.y);
+        // from the smaller of the two probabilities
+        out.rest[t] = rest == 0.0f && total == total ? -INFINITY
+                      : sel < 0.5f * total           ? log1pf(-sel / total)
+                                                     : __fadd_rn(z.x, outside.x - all.x) + (z.y + (outside.y - all.y));
     }
 }
 
