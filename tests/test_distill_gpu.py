@@ -196,7 +196,7 @@ SHAPES = [  # T, V, k, stride, offset
     (1, 1, 1, None, 0), (1, 50257, 32, None, 0), (3, 7, 7, None, 1), (5, 8, 3, None, 0), (4, 9, 1, 17, 3), (2, 600, 512, 601, 5),
     (17, 1000, 64, 1008, 0), (33, 4099, 65, None, 5), (64, 257, 5, 264, 0), (2, 151936, 300, None, 1), (330, 50257, 64, None, 0),
     (310, 9001, 20, 9002, 1), (1300, 515, 64, 518, 1), (1217, 3, 2, None, 0), (400, 30011, 8, None, 2), (310, 80001, 40, None, 0),
-    (160, 151937, 24, None, 0),
+    (160, 151937, 24, None, 0), (310, 50257, 512, None, 1), (700, 20011, 500, None, 0), (1300, 8001, 3, None, 0),
 ]
 
 
@@ -382,6 +382,44 @@ def test_equal_calls_streams_and_graphs(V):
     y.copy_(y.roll(3))
     g.replay()
     assert all(torch.equal(a, b) for a, b in zip(held, zg.distill_loss(x, y, index, lp, rest, ce_coef=0.1)))
+
+
+def test_rows_past_two_to_the_31_elements():
+    T, V, k = 43001, 50257, 4
+    x = torch.zeros((T, V), device=DEV, dtype=torch.bfloat16)
+    x[-3:] = torch.randn((3, V), device=DEV, generator=gen(1)).bfloat16()
+    y = torch.full((T,), -1, dtype=torch.int64, device=DEV)
+    y[-3:] = torch.tensor([5, 50256, 77], device=DEV)
+    top = zg.top_logits(x, k, y)
+    z = torch.log_softmax(x[-3:].double(), 1)
+    want = torch.sort(z, dim=1, descending=True, stable=True)
+    # log-probabilities near 10, off by E = 2^-22 (8 + R + log V) with R below 10
+    assert torch.equal(top.index[-3:], want.indices[:, :k]) and bool((top.index[:-3] == -1).all())
+    assert float((top.logp[-3:] - want.values[:, :k]).abs().max()) <= 2.0 ** -22 * 29 * 13
+    index, lp = top.index, (top.logp - 0.1).contiguous()
+    r = zg.distill_loss(x, y, index, lp)
+    w = torch.full((3,), 1.0 / 3, dtype=torch.float64, device=DEV)
+    D, _, grad, dtol, _, gtol = reference(x[-3:], y[-3:], index[-3:], lp[-3:], None, w, "forward", "rest", 0.5, 1.0, 0.0, 1.0)
+    close(r.token_kl[-3:], D, dtol, "token_kl")
+    close(r.dlogits[-3:], grad, gtol + UNIT["bf16"] * grad.abs(), "dlogits")
+    assert int(r.dlogits[:-3].count_nonzero()) == 0
+
+
+def test_two_calls_at_once():
+    """On two streams, each with what it allocates for itself."""
+    x, y, index, lp, rest = data(900, 50257, 32, "bf16", 1)
+    x2, y2, index2, lp2, rest2 = data(500, 30011, 100, "bf16", 2)
+    want, want2 = zg.distill_loss(x, y, index, lp, rest), zg.distill_loss(x2, y2, index2, lp2, rest2, kind="js")
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = zg.distill_loss(x, y, index, lp, rest, stream=a)
+        got2 = zg.distill_loss(x2, y2, index2, lp2, rest2, kind="js", stream=b)
+        top = zg.top_logits(x2, 50, stream=b)
+        top2 = zg.top_logits(x, 50, stream=a)
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(got, want)) and all(torch.equal(u, v) for u, v in zip(got2, want2))
+        assert torch.equal(top.index, zg.top_logits(x2, 50).index) and torch.equal(top2.logp, zg.top_logits(x, 50).logp)
 
 
 def test_refusals():

@@ -222,6 +222,27 @@ def test_into_the_flat_gradient():
     assert bool((opt.tensor_view(flat, 1) == 0).all())
 
 
+def test_offsets_past_two_to_the_31_elements():
+    V, D = 70001, 32768
+    w = torch.zeros((V, D), device=DEV, dtype=torch.bfloat16)
+    w[-1] = torch.randn(D, device=DEV, generator=gen(1)).bfloat16()
+    w[-2] = 3.0
+    t = torch.tensor([V - 1, 0, V - 2, V - 1], device=DEV)
+    out = zg.embedding(w, t)
+    assert torch.equal(out, w[t])
+    d = zg.embedding_backward(t, out, V, out=w)
+    assert torch.equal(d[-1], 2 * out[0]) and bool((d[-2] == 3).all()) and int(d[:-2].count_nonzero()) == 0
+    del w, d
+    dh = torch.zeros((V, D), device=DEV, dtype=torch.bfloat16)  # as many tokens
+    dh[-1] = 1.0
+    dh[-2, 1] = 2.0
+    d = zg.embedding_backward(torch.arange(V, device=DEV) % 3, dh, 4)
+    want = torch.zeros((4, D), device=DEV, dtype=torch.bfloat16)
+    want[(V - 1) % 3] = 1.0
+    want[(V - 2) % 3, 1] = 2.0
+    assert torch.equal(d, want)
+
+
 def test_refusals():
     w = torch.zeros((10, 16), device=DEV)
     t = torch.zeros(4, dtype=torch.int64, device=DEV)

@@ -78,6 +78,7 @@ SHAPES = [  # T, V, k, stride, offset
     (2, 500, 500, None, 0), (2, 600, 512, 601, 5), (17, 1000, 64, 1008, 0), (33, 4099, 65, None, 5), (2, 8192, 128, None, 8),
     (2, 8192, 129, None, 8), (64, 257, 5, 264, 0), (3, 131072, 300, None, 1), (700, 50257, 64, None, 0), (400, 9001, 200, 9002, 1),
     (1300, 515, 64, 518, 1), (1217, 3, 2, None, 0), (1251, 4099, 40, None, 0), (1300, 240, 33, None, 0), (1300, 257, 64, None, 3),
+    (2, 3000001, 100, None, 1), (2, 3000001, 512, None, 0),
     (1300, 8192, 60, None, 0), (1300, 4096, 64, None, 0), (1250, 8190, 7, None, 0), (1250, 8191, 33, 8200, 0),  # a warp each
 ]
 
