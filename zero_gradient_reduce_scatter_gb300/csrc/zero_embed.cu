@@ -132,8 +132,8 @@ __global__ void __launch_bounds__(kEmbedThreads)
 // share each: once to count its own tokens and those below them, which is where its part of the order
 // begins, and once to write its positions there. A warp takes a contiguous share of the positions with
 // counters of its own, and lanes of one token rank themselves, so the order is that of the positions, and
-// equal calls give equal bits. Rows of no token are zeroed by their owner meanwhile, which bounds it where there are many: 370 MB
-// in 62 us. 65536 positions alone take 18 us, bound by reading them from L2 (38 clusters, twice); each CTA for itself 31.
+// equal calls give equal bits. 65536 positions take 18 us, bound by reading them from L2 (33 clusters, twice); each CTA for
+// itself 31.
 // ---------------------------------------------------------------------------------------
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSortWidth = 1600;  // most tokens of a cluster: 205 KB of counters
@@ -143,30 +143,16 @@ struct SortArgs {
     int64_t rows, vocab;
     int width, size;            // tokens and CTAs of a cluster
     int32_t *position, *token;  // [rows] in order
-    int32_t *begin, *count;     // [vocab] of tokens that there are: a token's place and number in the order
+    int32_t *begin, *count;     // [vocab] a token's place and number in the order
     int64_t* live;              // [1] length of the order
     uint32_t* counters;         // to be zeroed
     int64_t n_counters;
-    uint8_t* zero;              // the matrix where its rows of no token are zeroed, or nullptr
-    int64_t row_bytes, stride_bytes;
-    int element;                // bytes
 };
-
-__device__ __forceinline__ void zero_bytes(uint8_t* p, int64_t bytes, int element, int lane) {
-    const int64_t head = min((int64_t)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15), bytes), vecs = (bytes - head) / 16;
-    auto one = [&](int64_t at) {
-        if (element == 2) *reinterpret_cast<uint16_t*>(p + at) = 0;
-        else *reinterpret_cast<uint32_t*>(p + at) = 0;
-    };
-    if (lane * element < head) one(lane * element);
-    for (int64_t i = lane; i < vecs; i += 32) __stcs(reinterpret_cast<uint4*>(p + head) + i, make_uint4(0, 0, 0, 0));
-    if (head + 16 * vecs + lane * element < bytes) one(head + 16 * vecs + lane * element);
-}
 
 __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs a) {
     extern __shared__ int32_t counts[];  // [kSortWarps][width]
     __shared__ int32_t warp_sum[kSortWarps];
-    __shared__ int32_t mine_of[kSortWidth], total_of[kSortWidth];  // of the CTA's share, of all
+    __shared__ int32_t mine_of[kSortWidth];  // of the CTA's share
     __shared__ uint32_t below_mine;
     cg::cluster_group cl = cg::this_cluster();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = (int)(blockIdx.x % a.size);
@@ -212,7 +198,6 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs a) {
             n[i] += x;
             if (r < rank) before[i] += x;
         }
-        total_of[b] = n[i];
     }
     int32_t scan = n[0] + n[1];
 #pragma unroll
@@ -228,7 +213,7 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs a) {
     for (int i = 0; i < 2; ++i) {
         const int b = 2 * threadIdx.x + i;
         if (b < a.width) {
-            if (rank == 0 && n[i] > 0) {
+            if (rank == 0 && lo + b < hi) {
                 a.begin[lo + b] = at;
                 a.count[lo + b] = n[i];
             }
@@ -260,9 +245,6 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs a) {
         }
         __syncwarp();
     }
-    if (a.zero)
-        for (int64_t v = lo + rank * kSortWarps + warp; v < hi; v += kSortWarps * a.size)
-            if (total_of[v - lo] == 0) zero_bytes(a.zero + v * a.stride_bytes, a.row_bytes, a.element, lane);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -278,6 +260,7 @@ constexpr int kGroup = 32;  // blocks
 constexpr int kAhead = 8;        // rows of a warp on their way at a time
 constexpr int kLoose = 4;        // the same where they are loaded element by element
 constexpr int kBlockMost = 128;  // positions of a block
+constexpr int64_t kZeroBytes = 16384;  // of the rows of no token that a warp looks after
 
 struct SumArgs {
     const int32_t *position, *token, *begin, *count;
@@ -287,7 +270,28 @@ struct SumArgs {
     int64_t dim, width, ldh, ldw, slices, units;
     int block;
     float scale;
+    // the rows of no token, `zero_rows` to a unit behind the blocks' units
+    uint8_t* zero;  // the matrix, or nullptr where it is added to
+    int64_t vocab, zero_units, row_bytes, stride_bytes;
+    int zero_rows, element;
 };
+
+__device__ __forceinline__ void zero_bytes(uint8_t* p, int64_t bytes, int element, int lane) {
+    const int64_t head = min((int64_t)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15), bytes), vecs = (bytes - head) / 16;
+    auto one = [&](int64_t at) {
+        if (element == 2) *reinterpret_cast<uint16_t*>(p + at) = 0;
+        else *reinterpret_cast<uint32_t*>(p + at) = 0;
+    };
+    if (lane * element < head) one(lane * element);
+    for (int64_t i = lane; i < vecs; i += 32) __stcs(reinterpret_cast<uint4*>(p + head) + i, make_uint4(0, 0, 0, 0));
+    if (head + 16 * vecs + lane * element < bytes) one(head + 16 * vecs + lane * element);
+}
+// Zeros into those of a unit's rows that have no token.
+__device__ __forceinline__ void zero_unit(const SumArgs& a, int64_t unit, int lane) {
+    const int64_t first = unit * a.zero_rows;
+    unsigned none = __ballot_sync(~0u, lane < a.zero_rows && first + lane < a.vocab && a.count[first + lane] == 0);
+    for (; none; none &= none - 1) zero_bytes(a.zero + (first + __ffs(none) - 1) * a.stride_bytes, a.row_bytes, a.element, lane);
+}
 
 // The lane's numbers of one part.
 template <class T, bool VEC>
@@ -464,8 +468,12 @@ __global__ void __launch_bounds__(kEmbedThreads) k_embed_sums(const SumArgs a, c
     Runs<T, O, true, ADD> run(a, dw);
     const int lane = run.lane;
     const int64_t live = *a.live, step = (int64_t)gridDim.x * (kEmbedThreads / 32);
-    for (int64_t unit = (int64_t)blockIdx.x * (kEmbedThreads / 32) + (threadIdx.x >> 5); unit < a.units; unit += step) {
-        if (!run.begin(unit, live)) return;
+    for (int64_t unit = (int64_t)blockIdx.x * (kEmbedThreads / 32) + (threadIdx.x >> 5); unit < a.units + a.zero_units; unit += step) {
+        if (unit >= a.units) {
+            zero_unit(a, unit - a.units, lane);
+            continue;
+        }
+        if (!run.begin(unit, live)) continue;
         const int n = run.n;
         for (int i0 = 0; i0 < n + kAhead; i0 += 32) {
             const int i = i0 + lane;
@@ -527,8 +535,12 @@ __global__ void __launch_bounds__(kEmbedThreads, 2) k_embed_sums_loose(const Sum
     Runs<T, O, false, ADD> run(a, dw);
     const int lane = run.lane;
     const int64_t live = *a.live, step = (int64_t)gridDim.x * (kEmbedThreads / 32);
-    for (int64_t unit = (int64_t)blockIdx.x * (kEmbedThreads / 32) + (threadIdx.x >> 5); unit < a.units; unit += step) {
-        if (!run.begin(unit, live)) return;
+    for (int64_t unit = (int64_t)blockIdx.x * (kEmbedThreads / 32) + (threadIdx.x >> 5); unit < a.units + a.zero_units; unit += step) {
+        if (unit >= a.units) {
+            zero_unit(a, unit - a.units, lane);
+            continue;
+        }
+        if (!run.begin(unit, live)) continue;
         const T* mine = dh + element<T, false>(run.slice, lane, 0);
         for (int k0 = 0; k0 < run.n; k0 += 32) {
             const int m = min(32, run.n - k0);
@@ -694,17 +706,13 @@ extern "C" int zero_embedding_backward(const zero_embed_grad* x, void* workspace
     a.live = (int64_t*)(ws + s.live);
     a.counters = (uint32_t*)(ws + s.counters);
     a.n_counters = s.n_counters;
-    a.zero = x->accumulate ? nullptr : (uint8_t*)x->dweight;
-    a.element = (int)type_size(x->out_type);
-    a.row_bytes = x->dim * a.element;
-    a.stride_bytes = x->ld_weight * a.element;
     const size_t smem = (size_t)4 * kSortWarps * a.width;
     const cudaError_t e = cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kSortWarps * kSortWidth);
     if (e != cudaSuccess) return record_cuda_error(e);
     cudaStream_t st = (cudaStream_t)stream;
     const int64_t grid = (x->vocab + a.width - 1) / a.width * a.size;
     int rc = launch_linked(k_embed_sort, (unsigned)grid, kSortThreads, smem, a.size, st, a);
-    if (rc || x->rows == 0) return rc;
+    if (rc) return rc;
     SumArgs u;
     u.position = a.position;
     u.token = a.token;
@@ -723,7 +731,14 @@ extern "C" int zero_embedding_backward(const zero_embed_grad* x, void* workspace
     u.units = s.blocks * s.slices;
     u.block = s.block;
     u.scale = (float)x->scale;
-    const int64_t ctas = std::min((u.units + kEmbedThreads / 32 - 1) / (kEmbedThreads / 32), (int64_t)sms * 1024);
+    u.element = (int)type_size(x->out_type);
+    u.row_bytes = x->dim * u.element;
+    u.stride_bytes = x->ld_weight * u.element;
+    u.zero = x->accumulate ? nullptr : (uint8_t*)x->dweight;
+    u.vocab = x->vocab;
+    u.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(32, kZeroBytes / u.row_bytes));
+    u.zero_units = x->accumulate ? 0 : (x->vocab + u.zero_rows - 1) / u.zero_rows;
+    const int64_t ctas = std::min((u.units + u.zero_units + kEmbedThreads / 32 - 1) / (kEmbedThreads / 32), (int64_t)sms * 1024);
     return by_type(x->type, [&](auto tag) {
         using T = decltype(tag);
         return by_type(x->out_type, [&](auto out) {
