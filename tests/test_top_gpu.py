@@ -206,3 +206,15 @@ def test_no_rows_and_refusals():
     for t in (0.0, -1.0, math.nan, math.inf):
         with pytest.raises(zg.ZeroError):
             zg.top_logits(x, 3, temperature=t)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("k", [1, 7, 31, 32, 64])
+def test_a_warps_row_of_equal_maxima(k, dtype):
+    """Rows of a warp each in which all of its 32 lanes find the same largest value, so that their threshold is known
+    without a step of search; each row over another base."""
+    T, V = 1300, 2048
+    x = torch.randn((T, V), device=DEV, generator=gen(5)).clamp(-3, 3) + torch.arange(T, device=DEV)[:, None] % 50
+    per = 16 // torch.empty(0, dtype=TYPES[dtype]).element_size()
+    x[:, per - 1:32 * per:per] = (4.0 + torch.arange(T, device=DEV) % 50)[:, None]  # in every lane's first 16 bytes
+    check(x.to(TYPES[dtype]), k)

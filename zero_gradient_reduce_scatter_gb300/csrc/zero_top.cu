@@ -383,6 +383,7 @@ struct TopRow {
             }
         }
         if ((id & 31) == 0) sm.bases[id >> 5] = base_c;
+        if (THREADS == 32) __syncwarp();  // a warp's threshold may take no other barrier (equal maxima in all lanes)
 
         // the threshold
         const float most = fmaxf(halves[0], halves[1]);
