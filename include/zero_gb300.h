@@ -551,7 +551,9 @@ int zero_set_max_ctas(zero_ctx* ctx, int ctas);
  *                        a bucket reduced a second time), a gather after a gather into a
  *                        disjoint destination. It still completes after its predecessor, so
  *                        stream order holds for whatever is enqueued later. The library
- *                        decides this from its own launches; the caller guarantees the rest:
+ *                        decides this from its own launches (also those of its calls without
+ *                        a context: a bucket behind embedding_backward or a clipping on its
+ *                        stream waits for them first); the caller guarantees the rest:
  *                        the kernel that the caller enqueues on the stream directly before
  *                        such a call must not write what the call reads (gradient slices;
  *                        the parameter shards) nor access what it writes. Work ordered by an

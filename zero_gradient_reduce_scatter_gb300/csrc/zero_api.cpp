@@ -79,6 +79,7 @@ struct zero_ctx {
     int overlap = ZERO_OVERLAP_NONE;
     uint64_t seq = 0;
     uint64_t chain_seq = ~0ull;
+    uint64_t chain_others = 0;  // launches_without_context of the stream
     cudaStream_t chain_stream = nullptr;
     int chain_kind = -1;
     uintptr_t chain_lo = 0, chain_hi = 0;
@@ -95,7 +96,14 @@ struct zero_ctx {
 
 namespace {
 thread_local int g_last_cuda_error = 0;
+constexpr int kStreamCounters = 64;
+std::atomic<uint64_t> g_without_context[kStreamCounters];
 }  // namespace
+
+std::atomic<uint64_t>& zg::launches_without_context(cudaStream_t s) {
+    const uintptr_t at = s == cudaStreamLegacy ? 0 : reinterpret_cast<uintptr_t>(s);  // both name the default stream
+    return g_without_context[(at >> 4 ^ at >> 10 ^ at) % kStreamCounters];
+}
 
 int zg::record_cuda_error(cudaError_t e) {
     g_last_cuda_error = (int)e;
@@ -367,11 +375,12 @@ zg::StepArgs base_args(zero_ctx* c) {
 // Programmatic-launch mode of a per-bucket kernel of `kind` about to be launched on s.
 // It may overlap its predecessor (wait last) only under ZERO_OVERLAP_BUCKETS, when the
 // caller allows it for this launch and the library's previous kernel launch was a
-// per-bucket launch of the same kind on the same stream, with nothing launched since.
+// per-bucket launch of the same kind on the same stream, with nothing launched since: neither
+// by this context nor, on that stream, by a call without one.
 int pdl_mode(const zero_ctx* c, int kind, cudaStream_t s, bool may_overlap) {
     if (c->overlap == ZERO_OVERLAP_NONE) return zg::kPdlNone;
     if (c->overlap == ZERO_OVERLAP_BUCKETS && may_overlap && c->chain_seq == c->seq && c->chain_stream == s &&
-        c->chain_kind == kind)
+        c->chain_kind == kind && c->chain_others == zg::launches_without_context(s).load(std::memory_order_relaxed))
         return zg::kPdlWaitLast;
     return zg::kPdlWaitFirst;
 }
@@ -379,6 +388,7 @@ int pdl_mode(const zero_ctx* c, int kind, cudaStream_t s, bool may_overlap) {
 // After a per-bucket launch: a successor of the same kind may overlap it.
 void note_chain(zero_ctx* c, int kind, cudaStream_t s, uintptr_t lo = 0, uintptr_t hi = 0) {
     c->chain_seq = c->seq;
+    c->chain_others = zg::launches_without_context(s).load(std::memory_order_relaxed);
     c->chain_stream = s;
     c->chain_kind = kind;
     c->chain_lo = lo;

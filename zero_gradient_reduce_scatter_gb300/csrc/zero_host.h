@@ -111,6 +111,7 @@ int launch_linked(void (*kernel)(P...), unsigned grid, unsigned threads, size_t 
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
+    launches_without_context(s).fetch_add(1, std::memory_order_relaxed);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
     return e == cudaSuccess ? ZERO_OK : record_cuda_error(e);
 }

@@ -2,6 +2,7 @@
 // (zero_kernels.cu). Not part of the public ABI.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -192,6 +193,11 @@ enum KernelVariant : int {
 
 // Records a CUDA error for zero_last_cuda_error() and returns ZERO_ERR_CUDA.
 int record_cuda_error(cudaError_t e);
+
+// How often a call without a context (losses, embedding, clipping) has launched a kernel on `s`, or on
+// another stream that shares its counter. Such a kernel may write the gradient that a bucket kernel behind it
+// reads, so a bucket kernel does not overlap its predecessor across one (pdl_mode).
+std::atomic<uint64_t>& launches_without_context(cudaStream_t s);
 
 // Threads per CTA of a kernel variant, and its CTAs-per-SM cap (0 = occupancy limit).
 int variant_threads(int variant);
