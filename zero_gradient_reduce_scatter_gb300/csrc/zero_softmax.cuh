@@ -367,11 +367,11 @@ __device__ __forceinline__ float2 log_parts(float s, float share = 1.0f) {
 __device__ __forceinline__ float2 inverse(double inv_t) { return make_float2((float)inv_t, (float)(inv_t - (double)(float)inv_t)); }
 
 // (x - base) / temperature in two numbers, for what is a small difference of log-probabilities near 10, whose own roundings
-// would be 1e-6 of it.
+// would be 1e-6 of it. Past fp32 (logits at the type's lowest value, a temperature below 1) it is infinite, with nothing beside it.
 __device__ __forceinline__ float2 over_base(float x, float base, float2 inv_t) {
     const float d = __fsub_rn(x, base), z = __fsub_rn(d, x), lost = __fsub_rn(__fsub_rn(x, __fsub_rn(d, z)), __fadd_rn(base, z));
     const float hi = __fmul_rn(d, inv_t.x);
-    return make_float2(hi, __fmaf_rn(d, inv_t.x, -hi) + __fmaf_rn(d, inv_t.y, lost * inv_t.x));
+    return make_float2(hi, fabsf(hi) < INFINITY ? __fmaf_rn(d, inv_t.x, -hi) + __fmaf_rn(d, inv_t.y, lost * inv_t.x) : 0.0f);
 }
 
 }  // namespace zg
