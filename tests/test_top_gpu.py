@@ -218,3 +218,25 @@ def test_a_warps_row_of_equal_maxima(k, dtype):
     per = 16 // torch.empty(0, dtype=TYPES[dtype]).element_size()
     x[:, per - 1:32 * per:per] = (4.0 + torch.arange(T, device=DEV) % 50)[:, None]  # in every lane's first 16 bytes
     check(x.to(TYPES[dtype]), k)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T,V,live,k", [(8, 50257, 5, 64), (8, 3000, 5, 400), (1300, 3001, 3, 30), (8, 50257, 5, 400), (8, 300, 1, 2)])
+def test_nan_and_infinity_beside_masked_places(T, V, live, k, dtype):
+    """Lists that reach into the places at -inf: a row that holds NaN or +inf has no results there either, one
+    that does not has -inf."""
+    x = torch.full((T, V), -math.inf, device=DEV)
+    at = torch.stack([torch.randperm(V, device=DEV, generator=gen(i))[:live] for i in range(T)])
+    x.scatter_(1, at, torch.randn((T, live), device=DEV, generator=gen(7)))
+    x[0, V // 2] = math.nan
+    x[1, V - 1] = math.inf
+    x[2, 0], x[2, V // 3] = math.inf, math.nan
+    x[3] = -math.inf
+    x[3, V // 2] = math.nan
+    x = x.to(TYPES[dtype])
+    r = zg.top_logits(x, k)
+    for a in (r.logp, r.lse, r.rest):
+        assert bool(a[:4].isnan().all())
+    check(x[4:], k)
+    loss = zg.distill_loss(x, torch.zeros(T, dtype=torch.int64, device=DEV), r.index, r.logp, r.rest)
+    assert bool(loss.dlogits[:4].isnan().all()) and bool(loss.token_kl[:4].isnan().all())

@@ -937,7 +937,8 @@ __global__ void __launch_bounds__(THREADS == 32 ? kRowThreads : THREADS, THREADS
         const float v = value_of((uint32_t)(its >> 32));
         out.index[t * k + i] = i < n ? (int64_t)(int)~(uint32_t)its : -1;
         const float2 z = over_base(v, top_base, inv_t);
-        out.logp[t * k + i] = i >= n ? NAN : nothing || v == -INFINITY ? -INFINITY : __fsub_rn(z.x, all.x) + (z.y - all.y);
+        // a row that holds NaN or +inf (total is NaN) has no results, also where -inf is listed
+        out.logp[t * k + i] = i >= n || total != total ? NAN : nothing || v == -INFINITY ? -INFINITY : __fsub_rn(z.x, all.x) + (z.y - all.y);
     }
     if (id == 0) {
         const float2 z = over_base(under_base, top_base, inv_t);
