@@ -127,6 +127,54 @@ struct DistillRow {
     bool zero;     // no loss: a row of zeros
 };
 
+// e^x, 1 at most, in units of 2^-48, off by 2^-39 of itself and a unit: x = n ln 2 + r with ln 2 in three parts (Cody and Waite),
+// u = e^(r / 64) - 1 by its Taylor terms, the first two of them in two numbers, and six times u -> 2u + u^2.
+__device__ __forceinline__ uint64_t fixed_exp(float x) {
+    if (!(x > -80.0f)) return 0;
+    if (x >= 0.0f) return 1ull << 48;
+    constexpr float kLn2[3] = {2839.0f / 4096.0f, 3.19461832987e-5f, 1.64659497e-12f};
+    const float n = rintf(x * kLog2e), r = __fmaf_rn(-n, kLn2[0], x), d = __fmul_rn(-n, kLn2[1]), z = __fadd_rn(r, d), e = __fsub_rn(z, r);
+    const float lost = __fadd_rn(__fsub_rn(r, __fsub_rn(z, e)), __fsub_rn(d, e));
+    const float m = z * 0x1p-6f, m_lo = (lost + __fmaf_rn(-n, kLn2[1], -d) - n * kLn2[2]) * 0x1p-6f;
+    const float half = 0.5f * m, q = __fmul_rn(half, m), cube = m * m * m * fmaf(m, fmaf(m, 1.0f / 120.0f, 1.0f / 24.0f), 1.0f / 6.0f);
+    float u = __fadd_rn(m, q), u_lo = __fsub_rn(q, __fsub_rn(u, m)) + (cube + __fmaf_rn(half, m, -q) + fmaf(m, m_lo, m_lo));
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+        const float p = __fmul_rn(u, u), p_lo = fmaf(2.0f * u, u_lo, __fmaf_rn(u, u, -p)), two = 2.0f * u;
+        u = __fadd_rn(two, p);
+        u_lo = __fsub_rn(p, __fsub_rn(u, two)) + (p_lo + 2.0f * u_lo);
+    }
+    const float up = __int_as_float(((int)n + 127 + 48) << 23);
+    return (uint64_t)(__float2ll_rn(up) + __float2ll_rn(u * up) + __float2ll_rn(u_lo * up));
+}
+
+// What the teacher's log-probability of the rest is formed from: the number that is given, or what the list leaves of 1, in units of
+// 2^-48. Whole numbers lose nothing and have no order: the reverse form weighs this logarithm by the student's own rest, and from
+// a sum of expf it was off by 9% at a rest of 1e-6.
+constexpr unsigned long long kWhole = 1ull << 48;
+struct TeacherRest {
+    unsigned long long left;  // kWhole before its row
+    float given;
+};
+// By the warps that have no part in sum_list first. logp(i): entry i's, -inf where it is not there.
+template <int THREADS, class F>
+__device__ __forceinline__ void take_rest(const DistillTokens& p, int64_t t, TeacherRest& rest, F logp) {
+    const int at = THREADS - 1 - threadIdx.x;
+    if ((at & ~31) >= p.k || p.tail != ZERO_TAIL_REST) return;
+    if (p.teacher_rest) {
+        if (at == 0) rest.given = p.teacher_rest[t];
+        return;
+    }
+    uint64_t mass = 0;
+    for (int i = at; i < p.k; i += THREADS) mass += fixed_exp(logp(i));
+    const uint32_t low = (uint32_t)mass & 0x3FFFFFFu, high = (uint32_t)(mass >> 26);  // of 8 entries: 32 of either are below 2^32
+    mass = ((uint64_t)__reduce_add_sync(~0u, high) << 26) + __reduce_add_sync(~0u, low);
+    if ((at & 31) == 0) atomicAdd(&rest.left, 0ull - mass);
+}
+__device__ __forceinline__ float its_logp(const DistillTokens& p, const TeacherRest& rest) {
+    return p.teacher_rest ? rest.given : logf(fmaxf(__ll2float_rn((int64_t)rest.left) * 0x1p-48f, 0x1p-24f));
+}
+
 // A warp's share of a list: its largest logit, the sum of 2^((x - it) C), the teacher's mass, and how many entries there
 // are, 1024 more where the target is one. Before the barrier that finish_list's threads pass.
 template <int THREADS>
@@ -157,8 +205,8 @@ __device__ __forceinline__ void sum_list(const List& list, Scale k, int64_t y, f
 // does) and the gradients of this thread's entries over list.x. Valid in all threads.
 template <int THREADS, class S>
 __device__ __forceinline__ DistillRow finish_list(const DistillTokens& a, const List& list, const RowStat& rest, bool bad, int64_t t, int64_t y,
-                                                  float x_y, int64_t vocab, Scale k, float2 inv_t, bool first, const float4* shares, float2* parts,
-                                                  S sync) {
+                                                  float x_y, int64_t vocab, Scale k, float2 inv_t, bool first, const float4* shares,
+                                                  const TeacherRest& teacher, float2* parts, S sync) {
     constexpr int kWarps = THREADS / 32;
     const float w = a.w[t];
     float top = rest.s != 0.0f ? rest.m : -INFINITY, mass = 0.0f, total = 0.0f;
@@ -204,7 +252,7 @@ __device__ __forceinline__ DistillRow finish_list(const DistillTokens& a, const 
     }
     Part outside = {0.0f, 0.0f};
     if (with_rest) {
-        const float lp = a.teacher_rest ? a.teacher_rest[t] : logf(fmaxf(1.0f - mass, 0x1p-24f));
+        const float lp = its_logp(a, teacher);
         const float2 own = log_parts(rest.s);
         const bool none = nothing || rest.s == 0.0f;  // no q
         const float q = none ? 0.0f : rest.s * up * over, p = mass == mass ? expf(lp) : NAN;
@@ -327,6 +375,7 @@ __global__ void __launch_bounds__(THREADS) k_distill_rows(const Rows<T> a, const
     __shared__ float4 shares[THREADS / 32];
     __shared__ float2 sums_of[THREADS / 32];
     __shared__ int shared_bad;
+    __shared__ TeacherRest teacher;
     wait_for_kernel_before();
     let_next_kernel_start();
     const int64_t t = blockIdx.x / size;
@@ -345,7 +394,10 @@ __global__ void __launch_bounds__(THREADS) k_distill_rows(const Rows<T> a, const
     const int words = bitmap_words(a.vocab);
     const List list(smem, words, p.k);
     for (int i = id; i < words; i += THREADS) list.bits[i] = 0;
-    if (id == 0) shared_bad = 0;
+    if (id == 0) {
+        shared_bad = 0;
+        teacher.left = kWhole;
+    }
     __syncthreads();
     const float x_y = y < a.vocab ? widen(x[y]) : NAN;
     const int shift = (kVec<T> - (s.tail_at % kVec<T>)) % kVec<T>;
@@ -354,6 +406,7 @@ __global__ void __launch_bounds__(THREADS) k_distill_rows(const Rows<T> a, const
         if (!mark_entry(list, i, shift)) shared_bad = 1;
     }
     sum_list<THREADS>(list, a.k, y, shares);
+    take_rest<THREADS>(p, t, teacher, [&](int i) { return p.index[t * p.k + i] >= 0 ? p.teacher[t * p.k + i] : -INFINITY; });
     __syncthreads();
     const float listed_top = list_top<THREADS>(shares, p.k);
     auto sums = [&](auto checked) {
@@ -379,8 +432,8 @@ __global__ void __launch_bounds__(THREADS) k_distill_rows(const Rows<T> a, const
     }
     if (!good) st = sums(std::true_type());
     st = cluster_join<false>(st, size, a.k, &mine);
-    const DistillRow r = finish_list<THREADS>(p, list, st, shared_bad != 0, t, y, x_y, a.vocab, a.k, inverse(a.inv_t), rank == 0, shares, sums_of,
-                                              [] { __syncthreads(); });
+    const DistillRow r = finish_list<THREADS>(p, list, st, shared_bad != 0, t, y, x_y, a.vocab, a.k, inverse(a.inv_t), rank == 0, shares,
+                                              teacher, sums_of, [] { __syncthreads(); });
     const GradRow grad = {0.0f, -r.factor, 0.0f, r.base, 0.0f};
     if (same_alignment(x, out)) {
         const GradVector<T, false> vector(grad, a.c);
@@ -414,6 +467,7 @@ __global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
     __shared__ int shared_bad[2];
     __shared__ int64_t row_at[2], row_y[2];
     __shared__ float row_x[2];  // the target's logit
+    __shared__ TeacherRest teacher[2];  // a row's, and the next one's
     __shared__ uint64_t bars[2 * kSlots + 4];
     __shared__ int gave_up;
     const uint32_t full = smem_addr(bars), empty = full + 8 * kSlots, row_full = empty + 8 * kSlots, row_empty = row_full + 16;
@@ -424,6 +478,7 @@ __global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
     if (threadIdx.x == 0) {
         gave_up = 0;
         shared_bad[0] = shared_bad[1] = 0;
+        teacher[0].left = teacher[1].left = kWhole;
         for (int i = 0; i < 16; ++i) end_listed[i] = 0;
         for (int i = 0; i < slots; ++i) {
             mbar_init(full + 8 * i, 1);
@@ -528,6 +583,7 @@ __global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
             const float x_head = threadIdx.x < s.head ? widen(x[threadIdx.x]) : 0.0f;
             const float x_tail = threadIdx.x < s.tail ? widen(x[s.tail_at + threadIdx.x]) : 0.0f;
             sum_list<kThreads>(list, a.k, y, shares);
+            take_rest<kThreads>(p, t, teacher[taken & 1], [&](int i) { return list.place[i] != kNotThere ? list.lp[i] : -INFINITY; });
             for (int i = threadIdx.x; i < p.k; i += kThreads) {
                 const int j = list.place[i];
                 if (j >= 0 && j < s.head) end_listed[j] = taken + 1;
@@ -572,8 +628,8 @@ __global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
             if (!good) st = sums(std::true_type());
             if (!ok || *(volatile int*)&gave_up) st.s = NAN;  // a copy did not come: no result
             st = cluster_join<false>(st, size, a.k, mine + (taken & 1));
-            const DistillRow r = finish_list<kThreads>(p, list, st, shared_bad[n & 1] != 0, t, y, x_y, a.vocab, a.k, inverse(a.inv_t), rank == 0, shares, sums_of,
-                                                       [] { consumers_sync<kThreads>(); });
+            const DistillRow r = finish_list<kThreads>(p, list, st, shared_bad[n & 1] != 0, t, y, x_y, a.vocab, a.k, inverse(a.inv_t), rank == 0, shares,
+                                                       teacher[taken & 1], sums_of, [] { consumers_sync<kThreads>(); });
             const GradRow grad = {0.0f, -r.factor, 0.0f, r.base, 0.0f};
             const bool fast = same_alignment(x, out);
             if (r.zero) {
@@ -599,6 +655,7 @@ __global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
                 if (lane == 0) mbar_arrive(empty + 8 * begin.at);  // this warp has done with the part
             }
             consumers_sync<kThreads>();
+            if (threadIdx.x == 0) teacher[taken & 1].left = kWhole;  // it is not wanted before the next row's barriers
             if (!r.zero) write_entries<T, kThreads>(list, r, s, out, y, a.vocab);
             release();
             ++taken;
