@@ -201,6 +201,22 @@ __device__ __forceinline__ void sum_list(const List& list, Scale k, int64_t y, f
     if ((threadIdx.x & 31) == 0) shares[threadIdx.x >> 5] = make_float4(top, sum, mass, __int_as_float(count));
 }
 
+// What log p is formed with where the list is renormalised, log p = lp - base - shift, for lists whose sum fp32 does not hold
+// (unnormalised logits, a distribution's far tail): over the largest lp. Each warp for itself, once the list is in shared memory.
+__device__ __forceinline__ float2 far_mass(const float* lp, const int* place, int k) {
+    const int lane = threadIdx.x & 31;
+    float base = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+    for (int i = lane; i < k; i += 32)
+        if (place[i] >= 0) base = fmaxf(base, lp[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) base = fmaxf(base, __shfl_xor_sync(~0u, base, o));
+#pragma unroll 1
+    for (int i = lane; i < k; i += 32)
+        if (place[i] >= 0) sum += expf(lp[i] - base);
+    return make_float2(base, logf(warp_add(sum)));
+}
+
 // What the row's sums and its list come to. rest: the sums outside the list. Writes the token's results (`first`: this CTA
 // does) and the gradients of this thread's entries over list.x. Valid in all threads.
 template <int THREADS, class S>
@@ -229,13 +245,21 @@ __device__ __forceinline__ DistillRow finish_list(const DistillTokens& a, const 
     const float over = nothing ? 0.0f : 1.0f / total;
     const float2 all = log_parts(total, 1.0f - over);
     const bool with_rest = a.tail == ZERO_TAIL_REST && count < vocab;
-    const float shift = a.tail == ZERO_TAIL_RENORMALISE && count > 0 ? logf(mass) : 0.0f;
+    float lp_base = 0.0f, shift = 0.0f;  // log p = lp - lp_base - shift
+    if (a.tail == ZERO_TAIL_RENORMALISE && count > 0) {
+        shift = logf(mass);
+        if (!(mass > 0x1p-90f && mass < 0x1p90f)) {
+            const float2 far = far_mass(list.lp, list.place, list.k);
+            lp_base = far.x;
+            shift = far.y;
+        }
+    }
     auto ratio = [&](float lp, float x) { return nothing ? INFINITY : log_ratio(lp, shift, over_base(x, base, inv_t), all); };
     float d = 0.0f, c = 0.0f;
     if ((threadIdx.x & ~31) < list.k) {
         for (int i = threadIdx.x; i < list.k; i += THREADS) {
             if (list.place[i] < 0) continue;
-            const float x = list.x[i], lp = list.lp[i], q = pow2(scaled<false>(x - base, k)) * over;
+            const float x = list.x[i], lp = list.lp[i] - lp_base, q = pow2(scaled<false>(x - base, k)) * over;
             const Part part = entry_part(a.kind, a.mix, expf(lp - shift), q, ratio(lp, x));
             d += part.d;
             c += part.c;
@@ -273,7 +297,7 @@ __device__ __forceinline__ DistillRow finish_list(const DistillTokens& a, const 
     if (total != total) r.factor = NAN;
     for (int i = threadIdx.x; i < list.k; i += THREADS) {
         if (list.place[i] < 0) continue;
-        const float x = list.x[i], lp = list.lp[i], q = pow2(scaled<false>(x - base, k)) * over;
+        const float x = list.x[i], lp = list.lp[i] - lp_base, q = pow2(scaled<false>(x - base, k)) * over;
         float v = share * q;
         if (a.kl_coef != 0.0f) v += g * entry_part(a.kind, a.mix, expf(lp - shift), q, ratio(lp, x)).c;
         if (list.place[i] == y) v -= h;
