@@ -1,6 +1,8 @@
-"""distill_loss on lists at the edge of what the call allows: renormalised lists whose probabilities, or whose sum, pass fp32.
+"""distill_loss on lists at the edge of what the call allows: renormalised lists whose probabilities, or whose sum, pass fp32; mixtures of nearly one side.
 Against test_distill_gpu's reference; its tolerances, in which a renormalised log-probability lp - log sum exp is off by
 its own rounding and that of lp at its distance from the list's largest, which count as |log p| does."""
+import math
+
 import pytest
 import torch
 
@@ -57,3 +59,49 @@ def test_renormalised_lists_of_unequal_parts():
     y[4] = y[5] = 3
     r = zg.distill_loss(x, y, index, lp, None, tail="renormalise")
     assert bool(r.dlogits[4:6].isnan().all()) and bool(r.token_kl[4:6].isnan().all()) and bool(r.dlogits[6:].isfinite().all())
+
+
+@pytest.mark.parametrize("T,V,k,dtype", [(12, 3000, 20, "fp32"), (12, 50257, 64, "bf16"), (320, 20011, 300, "fp32")])
+@pytest.mark.parametrize("mix", [0.2, 0.999, 1 - 1e-5, 1 - 1e-7, 1 - 1e-9, 1 - 2.0 ** -53])
+def test_mixtures_of_little_student(mix, T, V, k, dtype):
+    """The gradient is of the size of 1 - mix and right relative to that: an entry's c = (1 - mix) q log(q / m) is off by r's own error,
+    by 2^-20 of the logarithm and by its q's. A teacher that is sure of its list has log(q / m) = -log(1 - mix) for the rest."""
+    x, y, index, lp, rest = data(T, V, k, dtype, 9, short=False)
+    rest[0] = -math.inf
+    other = 1.0 - mix
+    logq = torch.log_softmax(x.double(), 1)
+    member = torch.zeros((T, V), dtype=torch.bool, device=DEV).scatter_(1, index, True)
+    lqr = torch.logsumexp(logq.masked_fill(member, -math.inf), 1, keepdim=True)
+    lq, P = torch.cat([logq.gather(1, index), lqr], 1), torch.cat([lp, rest[:, None]], 1).double()
+    p, q, r = P.exp(), lq.exp(), P - lq
+    qm = torch.where(r > 0, -(r + torch.log1p(other * torch.expm1(-r))), -torch.log(other + mix * torch.exp(r)))
+    qm = torch.where(r.abs() < 0.1, -torch.log1p(mix * torch.expm1(r)), qm)  # so that nothing cancels
+    c = other * q * qm
+    C = c.sum(1, keepdim=True)
+    entry = torch.full((T, V), k, dtype=torch.int64, device=DEV).scatter_(1, index, torch.arange(k, device=DEV).expand(T, k))
+    cond, prob = torch.where(member, 1.0, torch.exp(logq - lqr)), logq.exp()
+    E = 2.0 ** -22 * (36 + math.log(V)) + 2.0 ** -24 * V / 256
+    l = E * (2 + torch.where(P.isfinite(), P, 0.0).abs() + lq.abs())
+    ctol = other * q * (l + 2.0 ** -20 * (qm.abs() + 1)) * (1 + qm.abs()) + 2 * E * c.abs()
+    w = weights(y, None, "sum")
+    got = zg.distill_loss(x, y, index, lp, rest, kind="js", mix=mix, reduce="sum")
+    grad = (c.gather(1, entry) * cond - C * prob) * w[:, None]
+    gtol = ctol.gather(1, entry) * cond + (ctol.sum(1, keepdim=True) + 2 * E * C.abs()) * prob
+    close(got.dlogits, grad, gtol + UNIT[dtype] * grad.abs() + 2.0 ** -110, "dlogits")
+
+
+@pytest.mark.parametrize("mix", [1e-300, 1e-50, 1e-30, 1e-9, 1e-4, 1 - 1e-4, 1 - 1e-9, 1 - 2.0 ** -53])
+def test_mixtures_of_any_size(mix):
+    """Also where one side has no probability in an entry: a teacher sure of its list, a student without the rest, a logit of -inf."""
+    T, V, k = 12, 3000, 20
+    x, y, index, lp, rest = data(T, V, k, "fp32", 9, short=False)
+    rest[0] = -math.inf
+    only = torch.full((V,), -math.inf, device=DEV)
+    only[index[1]] = x[1, index[1]]
+    x[1], y[1] = only, index[1, 0]
+    x[2, index[2, 3]], y[2] = -math.inf, index[2, 4]
+    w = weights(y, None, "sum")
+    D, logp, grad, dtol, ltol, gtol = reference(x, y, index, lp, rest, w, "js", "rest", mix, 1.0, 0.0, 1.0)
+    r = zg.distill_loss(x, y, index, lp, rest, kind="js", mix=mix, reduce="sum")
+    close(r.token_kl, D, dtol, "token_kl")
+    close(r.dlogits, grad, gtol + UNIT["fp32"] * grad.abs(), "dlogits")

@@ -15,7 +15,7 @@
 // still has its rest to full precision, and the places of S are left out by a bitmap of the vocabulary
 // in shared memory, 16 bytes of the row to a byte of it.
 
-#include <climits>
+#include <cfloat>
 
 #include <type_traits>
 
@@ -36,7 +36,7 @@ struct DistillTokens : TokenWeights {
     float* clipped = nullptr;
     float* out_clip = nullptr;
     int k;
-    float mix, kl_coef, ce_coef;
+    float mix, student, kl_coef, ce_coef;  // shares of a mixture: neither is 0
     int32_t kind, tail;
 
     __device__ __forceinline__ void spread(int64_t, int64_t) const {}
@@ -97,24 +97,19 @@ __device__ __forceinline__ float warp_add(float v) {
 struct Part {
     float d, c;
 };
-__device__ __forceinline__ Part entry_part(int kind, float b, float p, float q, float r) {
+// b: the teacher's share of a mixture, s the student's, 1 - b.
+__device__ __forceinline__ Part entry_part(int kind, float b, float s, float p, float q, float r) {
     if (kind == ZERO_DISTILL_FORWARD) return {p > 0.0f || p != p ? p * r : 0.0f, -p};
     if (kind == ZERO_DISTILL_REVERSE) {
         const float d = q > 0.0f || q != q ? -q * r : 0.0f;
         return {d, d};
     }
-    // log p - log m and log q - log m from r alone
-    float pm, qm;
-    if (r > 0.0f) {
-        const float m = log1pf((1.0f - b) * expm1f(-r));
-        pm = -m;
-        qm = -(r + m);
-    } else {
-        const float m = log1pf(b * expm1f(r));
-        pm = r - m;
-        qm = -m;
-    }
-    const float c = q > 0.0f || q != q ? (1.0f - b) * q * qm : 0.0f;
+    // log p - log m and log q - log m from r alone: the logarithm of the mixture in units of the larger side, that of a small sum where
+    // 1 - s or 1 - b would have lost it
+    const float x = r > 0.0f ? s * expm1f(-r) : b * expm1f(r);
+    const float m = x < -0.5f ? logf(r > 0.0f ? fmaf(s, expf(-r), b) : fmaf(b, expf(r), s)) : log1pf(x);
+    const float pm = r > 0.0f ? -m : r - m, qm = r > 0.0f ? -(r + m) : -m;
+    const float c = q > 0.0f || q != q ? s * q * qm : 0.0f;
     return {(p > 0.0f || p != p ? b * p * pm : 0.0f) + c, c};
 }
 
@@ -260,7 +255,7 @@ __device__ __forceinline__ DistillRow finish_list(const DistillTokens& a, const 
         for (int i = threadIdx.x; i < list.k; i += THREADS) {
             if (list.place[i] < 0) continue;
             const float x = list.x[i], lp = list.lp[i] - lp_base, q = pow2(scaled<false>(x - base, k)) * over;
-            const Part part = entry_part(a.kind, a.mix, expf(lp - shift), q, ratio(lp, x));
+            const Part part = entry_part(a.kind, a.mix, a.student, expf(lp - shift), q, ratio(lp, x));
             d += part.d;
             c += part.c;
         }
@@ -281,7 +276,7 @@ __device__ __forceinline__ DistillRow finish_list(const DistillTokens& a, const 
         const bool none = nothing || rest.s == 0.0f;  // no q
         const float q = none ? 0.0f : rest.s * up * over, p = mass == mass ? expf(lp) : NAN;
         const float r_rest = none ? INFINITY : log_ratio(lp, 0.0f, over_base(rest_base, base, inv_t), make_float2(all.x - own.x, all.y - own.y));
-        if (!(lp == -INFINITY && none)) outside = entry_part(a.kind, a.mix, p, q, r_rest);
+        if (!(lp == -INFINITY && none)) outside = entry_part(a.kind, a.mix, a.student, p, q, r_rest);
         d += outside.d;
         c += outside.c;
     }
@@ -299,7 +294,7 @@ __device__ __forceinline__ DistillRow finish_list(const DistillTokens& a, const 
         if (list.place[i] < 0) continue;
         const float x = list.x[i], lp = list.lp[i] - lp_base, q = pow2(scaled<false>(x - base, k)) * over;
         float v = share * q;
-        if (a.kl_coef != 0.0f) v += g * entry_part(a.kind, a.mix, expf(lp - shift), q, ratio(lp, x)).c;
+        if (a.kl_coef != 0.0f) v += g * entry_part(a.kind, a.mix, a.student, expf(lp - shift), q, ratio(lp, x)).c;
         if (list.place[i] == y) v -= h;
         list.x[i] = nothing ? 0.0f : v;
     }
@@ -782,7 +777,8 @@ extern "C" int zero_distill_loss(const zero_logits* x, const zero_distill* p, vo
     a.out_loss = p->loss;
     a.out_kl = p->kl;
     a.k = (int)p->k;
-    a.mix = (float)p->mix;
+    a.mix = std::max((float)p->mix, FLT_MIN);
+    a.student = (float)(1.0 - p->mix);
     a.kl_coef = (float)p->kl_coef;
     a.ce_coef = (float)p->ce_coef;
     a.kind = p->kind;
