@@ -866,7 +866,8 @@ int zero_embedding(const zero_embed* x, void* out, int64_t ld_out, void* stream)
  *   dweight[v] = scale * sum of dhidden[t] over the t with tokens[t] = v, in ascending t
  * written, with zeros in the rows of no token, or (accumulate = 1) added to what dweight holds, whose
  * rows of no token are then neither read nor written: the gradient of a matrix that is also the output
- * matrix. Sums in fp32 (of 32 rows at most, then of such sums), rounded once to out_type. A token
+ * matrix. Sums in fp32 (of 32 rows at most, then of such sums; of a token's rows in a block of positions
+ * the last, 8 at most, one by one), rounded once to out_type. A token
  * outside [0, vocab) has no gradient. With views of a flat gradient buffer as dweight the result is
  * in its place for a step. dhidden and dweight do not overlap.
  * Rows whose addresses and lengths are multiples of 16 bytes are read and written so, others element

@@ -270,3 +270,27 @@ def test_refusals():
             zg.embedding(w, t, scale=scale)
         with pytest.raises(zg.ZeroError):
             zg.embedding_backward(t, dh, 10, scale=scale)
+
+
+def depth_rows(T, D, n):
+    """1 and then rows of a little less than half its last bit, n to a block: added one by one they are all lost."""
+    dh = torch.full((T, D), 2.0 ** -24 * 0.99, device=DEV)
+    dh[::n] = 1.0
+    return dh
+
+
+@pytest.mark.parametrize("D,ld", [(2048, 2048), (2047, 2047)])
+def test_sums_are_no_deeper_than_stated(D, ld):
+    """Sums of 32 rows at most, then of such sums: of 128 rows of a block 31 are added to the 1 in it, where a chain of all
+    would lose 127. One token with rows in one block, and one with rows in all."""
+    T, V = 33000, 5
+    dh = depth_rows(T, D, 128)
+    for t in (torch.zeros(T, dtype=torch.int64, device=DEV), torch.arange(T, device=DEV) // 8192):
+        got = zg.embedding_backward(t, dh, V)
+        want, tol = reference(t, dh, V, 1.0, None)
+        assert bool(((got.double() - want).abs() <= tol + U * want.abs()).all())
+    one = torch.full((T,), -1, dtype=torch.int64, device=DEV)
+    one[:128] = 3
+    got = zg.embedding_backward(one, dh, V)
+    want, tol = reference(one, dh, V, 1.0, None)
+    assert bool(((got.double() - want).abs() <= tol + U * want.abs()).all())

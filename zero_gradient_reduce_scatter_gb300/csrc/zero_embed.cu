@@ -261,6 +261,7 @@ constexpr int kGroup = 32;  // blocks
 constexpr int kAhead = 8;        // rows of a warp on their way at a time
 constexpr int kLoose = 4;        // the same where they are loaded element by element
 constexpr int kBlockMost = 128;  // positions of a block
+constexpr int kChain = 32;       // of which so many are added one to another
 constexpr int64_t kZeroBytes = 16384;  // of the rows of no token that a warp looks after
 
 struct SumArgs {
@@ -356,6 +357,27 @@ __device__ __forceinline__ bool last_of(uint32_t* done, uint32_t n, int lane) {
     return before == n - 1;
 }
 
+// A lane's sums of a run's earlier chains in a block. In shared memory, where registers for them would cost an SM one of its CTAs
+// (16384 x 767 fp32 55 us against 51); in registers, where shared memory would (65536 x 2048 bf16 added to fp32 142 against 126).
+template <int N, bool SHARED>
+struct Chains {
+    struct Room {
+        uint64_t at[N][32];
+    };
+    uint64_t (*const at)[32];
+    __device__ __forceinline__ Chains(Room* of) : at(of[threadIdx.x >> 5].at) {}
+    __device__ __forceinline__ uint64_t& operator[](int i) { return at[i][threadIdx.x & 31]; }
+};
+template <int N>
+struct Chains<N, false> {
+    struct Room {};
+    uint64_t v[N];
+    __device__ __forceinline__ Chains(Room*) {}
+    __device__ __forceinline__ uint64_t& operator[](int i) { return v[i]; }
+};
+template <class T, bool VEC, bool ADD>
+using ChainsOf = Chains<kVec<T> / 2, !(VEC && ADD)>;
+
 // One warp's work on the runs of a block: what both kernels below do with the rows that they bring.
 template <class T, class O, bool VEC, bool ADD>
 struct Runs {
@@ -367,10 +389,12 @@ struct Runs {
     int n;
     int32_t left;
     uint64_t sum[P / 2];
+    ChainsOf<T, VEC, ADD> chains;
+    bool chained;           // whether they hold anything
     bool started, carried;  // a run has ended in this block; one that came from the left has
     int32_t last;           // the token of a run that goes on to the right
 
-    __device__ __forceinline__ Runs(const SumArgs& a, O* dw) : a(a), dw(dw), lane(threadIdx.x & 31) {}
+    __device__ __forceinline__ Runs(const SumArgs& a, O* dw, typename ChainsOf<T, VEC, ADD>::Room* room) : a(a), dw(dw), lane(threadIdx.x & 31), chains(room) {}
 
     // False: no such block. Rows of `live` positions.
     __device__ __forceinline__ bool begin(int64_t unit, int64_t live) {
@@ -380,7 +404,7 @@ struct Runs {
         if (first >= live) return false;
         n = (int)min((int64_t)a.block, live - first);
         left = first > 0 ? a.token[first - 1] : -1;
-        started = carried = false;
+        started = carried = chained = false;
         last = -1;
         clear();
         return true;
@@ -388,6 +412,20 @@ struct Runs {
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int i = 0; i < P / 2; ++i) sum[i] = 0;
+    }
+    // Every kChain positions: roundings grow with the additions that a sum goes through.
+    __device__ __forceinline__ void end_chain() {
+#pragma unroll
+        for (int i = 0; i < P / 2; ++i) chains[i] = chained ? add2(chains[i], sum[i]) : sum[i];
+        chained = true;
+        clear();
+    }
+    // Before the few rows among which the run ends.
+    __device__ __forceinline__ void add_chains(bool ends) {
+        if (!chained || !ends) return;
+        chained = false;
+#pragma unroll
+        for (int i = 0; i < P / 2; ++i) sum[i] = add2(chains[i], sum[i]);
     }
     __device__ __forceinline__ O* at(int64_t v) const { return dw + v * a.ldw + element<T, VEC>(slice, lane, 0); }
     __device__ __forceinline__ int64_t in_row() const { return a.dim - element<T, VEC>(slice, lane, 0); }
@@ -419,7 +457,10 @@ struct Runs {
             if (side == 0 ? !carried : last < 0) continue;
             const int32_t y = side == 0 ? left : last;
             const int64_t part = 2 * b + (side == 0 || (!started && left == y) ? 0 : 1);
-            if (side == 1) put_part<T, VEC>(a.part + part * a.width, slice, lane, a.dim, sum);
+            if (side == 1) {
+                add_chains(true);
+                put_part<T, VEC>(a.part + part * a.width, slice, lane, a.dim, sum);
+            }
             // the blocks of this run, all of them and those of this block's group
             const int64_t begin = a.begin[y], b0 = begin / a.block, b1 = (begin + a.count[y] - 1) / a.block;
             const int64_t g = b / kGroup, from = max(b0, g * kGroup), to = min(b1, (g + 1) * kGroup - 1);
@@ -459,14 +500,15 @@ struct EmbedRing {
 };
 
 template <class T, class O, bool ADD>
-__global__ void __launch_bounds__(kEmbedThreads) k_embed_sums(const SumArgs a, const T* dh, O* dw) {
+__global__ void __launch_bounds__(kEmbedThreads, !ADD && sizeof(T) == 4 ? 4 : 0) k_embed_sums(const SumArgs a, const T* dh, O* dw) {
     extern __shared__ __align__(16) uint8_t smem[];
     using Ring = EmbedRing<T, O, ADD>;
     using Old = LaneOld<T, O, true>;
     Ring& ring = reinterpret_cast<Ring*>(smem)[threadIdx.x >> 5];
     wait_for_kernel_before();
     let_next_kernel_start();
-    Runs<T, O, true, ADD> run(a, dw);
+    __shared__ typename ChainsOf<T, true, ADD>::Room room[kEmbedThreads / 32];
+    Runs<T, O, true, ADD> run(a, dw, room);
     const int lane = run.lane;
     const int64_t live = *a.live, step = (int64_t)gridDim.x * (kEmbedThreads / 32);
     for (int64_t unit = (int64_t)blockIdx.x * (kEmbedThreads / 32) + (threadIdx.x >> 5); unit < a.units + a.zero_units; unit += step) {
@@ -510,7 +552,9 @@ __global__ void __launch_bounds__(kEmbedThreads) k_embed_sums(const SumArgs a, c
 #pragma unroll
         for (int e = 0; e < kAhead - 1; ++e) bring(e, e, ring.ends[0] >> e & 1);
         for (int e0 = 0; e0 < n; e0 += kAhead) {
+            if (e0 > 0 && e0 % kChain == 0) run.end_chain();
             const unsigned ends = __funnelshift_r(ring.ends[e0 / 32], ring.ends[e0 / 32 + 1], e0 & 31);
+            run.add_chains(ends & ((1u << kAhead) - 1));
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 if (e0 + u >= n) break;
@@ -533,7 +577,8 @@ template <class T, class O, bool ADD>
 __global__ void __launch_bounds__(kEmbedThreads, 2) k_embed_sums_loose(const SumArgs a, const T* dh, O* dw) {
     wait_for_kernel_before();
     let_next_kernel_start();
-    Runs<T, O, false, ADD> run(a, dw);
+    __shared__ typename ChainsOf<T, false, ADD>::Room room[kEmbedThreads / 32];
+    Runs<T, O, false, ADD> run(a, dw, room);
     const int lane = run.lane;
     const int64_t live = *a.live, step = (int64_t)gridDim.x * (kEmbedThreads / 32);
     for (int64_t unit = (int64_t)blockIdx.x * (kEmbedThreads / 32) + (threadIdx.x >> 5); unit < a.units + a.zero_units; unit += step) {
@@ -543,7 +588,8 @@ __global__ void __launch_bounds__(kEmbedThreads, 2) k_embed_sums_loose(const Sum
         }
         if (!run.begin(unit, live)) continue;
         const T* mine = dh + element<T, false>(run.slice, lane, 0);
-        for (int k0 = 0; k0 < run.n; k0 += 32) {
+        for (int k0 = 0; k0 < run.n; k0 += kChain) {
+            if (k0 > 0) run.end_chain();
             const int m = min(32, run.n - k0);
             const int64_t at = run.first + k0 + lane;
             const int32_t pos = lane < m ? a.position[at] : 0, tok = lane < m ? a.token[at] : -1;
@@ -556,6 +602,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 2) k_embed_sums_loose(const Sum
 #pragma unroll
                 for (int u = 0; u < kLoose; ++u)  // past the last row the first of all, which is not used
                     r[u].load(mine + __shfl_sync(~0u, pos, k + u) * a.ldh, true, run.in_row());
+                run.add_chains(ends >> k & ((1u << kLoose) - 1));
 #pragma unroll
                 for (int u = 0; u < kLoose; ++u) {
                     if (k + u >= m) break;
