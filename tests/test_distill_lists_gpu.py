@@ -105,3 +105,28 @@ def test_mixtures_of_any_size(mix):
     r = zg.distill_loss(x, y, index, lp, rest, kind="js", mix=mix, reduce="sum")
     close(r.token_kl, D, dtol, "token_kl")
     close(r.dlogits, grad, gtol + UNIT["fp32"] * grad.abs(), "dlogits")
+
+
+@pytest.mark.parametrize("mix", [0.1, 0.2, 0.8])
+@pytest.mark.parametrize("T,V", [(6, 5000), (6, 50257), (320, 20001)])
+def test_mixtures_by_differences(mix, T, V):
+    """The gradient of unequal mixtures against central differences of D itself, written here from m = mix p + (1 - mix) q alone."""
+    x, y, index, lp, rest = data(T, V, 16, "fp32", 5, short=False)
+    w = weights(y, None, "token")
+    member = torch.zeros((T, V), dtype=torch.bool, device=DEV).scatter_(1, index, True)
+    P = torch.cat([lp, rest[:, None]], 1).double()
+
+    def loss(z):
+        logq = torch.log_softmax(z, 1)
+        lq = torch.cat([logq.gather(1, index), torch.logsumexp(logq.masked_fill(member, -math.inf), 1, keepdim=True)], 1)
+        p, q = P.exp(), lq.exp()
+        lm = torch.log(mix * p + (1 - mix) * q)
+        return float((w * (mix * p * (P - lm) + (1 - mix) * q * (lq - lm)).sum(1)).sum())
+
+    r = zg.distill_loss(x, y, index, lp, rest, kind="js", mix=mix)
+    assert abs(r.loss.item() - loss(x.double())) <= 2.0 ** -18 * (1 + loss(x.double()))
+    g = torch.Generator(device=DEV).manual_seed(9)
+    d = torch.randn((T, V), device=DEV, generator=g, dtype=torch.float64).scatter_(1, index, 3.0)
+    slope = (loss(x.double() + 1e-4 * d) - loss(x.double() - 1e-4 * d)) / 2e-4
+    # third derivatives times 1e-8, and gradients off by 2^-18 of themselves
+    assert abs(slope - float((r.dlogits.double() * d).sum())) <= 1e-5 * float((r.dlogits.double() * d).abs().sum()) + 1e-7
