@@ -790,7 +790,10 @@ int zero_linear_logp(const zero_linear* x, float* logp, float* lse, float* entro
  * x->targets may be NULL: every row counts. Where a target is below 0 its row is not read, its indices are
  * -1 and its results 0; which token a target is does not matter. A row of -inf alone has -inf throughout and
  * the lowest places; of a row that holds NaN the numbers are ranked, with index -1 where they are fewer
- * than k, and all its other results are NaN, as those of a row that holds +inf. Reads each row once.
+ * than k, and all its other results are NaN, as those of a row that holds +inf, also for the places at -inf
+ * of its list. A logit so far below the row's largest that z passes fp32 (the type's lowest value at a
+ * temperature below 1) has a log-probability of -inf. Reads each row once; a row of equal values, of few
+ * numbers among -inf or of values too far apart for one base, twice.
  * 1 <= k <= min(vocab, 512). Errors: INVALID_ARG, MISALIGNED, CUDA. */
 int zero_top_logits(const zero_logits* x, int64_t k, int64_t* index, float* logp, float* lse,
                     float* rest, void* stream);
@@ -804,13 +807,14 @@ int zero_top_logits(const zero_logits* x, int64_t k, int64_t* index, float* logp
  *                          exp(teacher_rest[t]), or max(1 - sum p_i, 2^-24) where teacher_rest is NULL;
  *                          no entry where the list is the whole vocabulary
  *   ZERO_TAIL_DROP         left out of D (its q still lowers the list's)
- *   ZERO_TAIL_RENORMALISE  the same, with p_i / sum p_i for p_i
+ *   ZERO_TAIL_RENORMALISE  the same, with p_i / sum p_i for p_i, whatever their size (a constant in
+ *                          teacher_logp, as unnormalised logits have one, leaves the result as it is)
  *   ZERO_DISTILL_FORWARD   D = sum p (log p - log q)
  *   ZERO_DISTILL_REVERSE   D = sum q (log q - log p)                          (with ZERO_TAIL_REST only)
  *   ZERO_DISTILL_JS        D = mix sum p (log p - log m) + (1 - mix) sum q (log q - log m),
  *                          m = mix p + (1 - mix) q                            (with ZERO_TAIL_REST only)
  * L_t = kl_coef D - ce_coef log q_target, loss = sum of w_t L_t with the weights of zero_policy_loss; a
- * coefficient of 0 leaves its term out, also an infinite one. A p = 0 or q = 0 adds 0 where it is the
+ * coefficient of 0 leaves its term out, also an infinite one. 1 - sum p_i is off by 2^-38 absolutely. A p = 0 or q = 0 adds 0 where it is the
  * factor; D is infinite where a p > 0 meets q = 0 (forward) or a q > 0 meets p_rest = 0 (reverse, whose
  * gradient is then not defined). The rest's sum is formed over the rest alone, to full precision where
  * it is small.

@@ -385,7 +385,7 @@ __device__ __forceinline__ bool mark_entry(const List& list, int i, int shift) {
 }
 
 // Any row: read once for the rest's sum and again for the gradient, by `size` CTAs (a cluster). Bound by HBM where rows are wide:
-// 2039 x 151936 bf16, lists of 128, 264 us, 78% of the copy peak on the three passes' 1.4 GB (61% on two). With 512 threads and two
+// 2039 x 151936 bf16, lists of 128, 263 us, 78% of the copy peak on the three passes' 1.4 GB (61% on two). With 512 threads and two
 // CTAs an SM, so that L2 could hold the rows until the second reading, 296.
 template <class T, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_distill_rows(const Rows<T> a, const DistillTokens p, int size, T* dx, int64_t dstride) {
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(THREADS) k_distill_rows(const Rows<T> a, const
 // copies, is read for the rest's sum as it arrives, and again for the gradient; a producer warp refills each part with the
 // next row's as soon as it has been read. It reads the list too, a row ahead, and looks for places that are named twice; the
 // list's places in shared memory then become -inf, so that the sum over the row is the rest's. 8192 x 50257 bf16 in lists of 64,
-// a quarter masked: 278 us, 77% of the copy peak on 1.45 GB (the same rows read twice: 304; policy_loss, which has no list to
+// a quarter masked: 280 us, 76% of the copy peak on 1.45 GB (the same rows read twice: 304; policy_loss, which has no list to
 // look at between its two readings, 232). A bitmap tested for every 16 bytes instead of -inf in place: 286.
 template <class T, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(32 * WARPS + 32, fused_ctas(WARPS))
 
 constexpr int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
 
-// Rows of up to this many bytes are read twice, by small CTAs: 8192 x 4000 bf16 53 us by 64 threads, 77 by 256.
+// Rows of up to this many bytes are read twice, by small CTAs: 8192 x 4000 bf16 54 us by 64 threads, 77 by 256.
 constexpr int64_t kDistillShort = 16384;
 constexpr int64_t kDistillSpare = 2048;  // two CTAs of an SM have this much more than k_policy_rows takes
 

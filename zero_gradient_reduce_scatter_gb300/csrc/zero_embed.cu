@@ -89,8 +89,8 @@ struct LaneOld {
 };
 
 // ---------------------------------------------------------------------------------------
-// Forward: a warp per kRowSlices slices of a token's row. 16384 x 2048 bf16 12.3 us, bound by memory (12.8 us from HBM alone; the
-// matrix' frequent rows stay in L2); one token 1.6 us.
+// Forward: a warp per kRowSlices slices of a token's row. 16384 x 2048 bf16 11.6 us, bound by memory (12.8 us from HBM alone; the
+// matrix' frequent rows stay in L2); one token 1.8 us.
 // ---------------------------------------------------------------------------------------
 constexpr int kRowSlices = 4;
 
@@ -132,8 +132,8 @@ __global__ void __launch_bounds__(kEmbedThreads)
 // share each: once to count its own tokens and those below them, which is where its part of the order
 // begins, and once to write its positions there. A warp takes a contiguous share of the positions with
 // counters of its own, and lanes of one token rank themselves, so the order is that of the positions, and
-// equal calls give equal bits. 65536 positions take 18 us, bound by reading them from L2 (33 clusters, twice); each CTA for
-// itself 31.
+// equal calls give equal bits. 65536 positions take 18 us, a chain of latencies: 33 clusters read 35 MB of positions from L2, which
+// would be 3 us at its rate, between rounds over 32 counters a token and their barriers; each CTA for itself 31.
 // ---------------------------------------------------------------------------------------
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSortWidth = 1600;  // most tokens of a cluster: 205 KB of counters

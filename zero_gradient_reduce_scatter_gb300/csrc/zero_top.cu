@@ -807,7 +807,7 @@ struct TopOut {
 };
 
 // A CTA of 128 threads per row (256 for k > 128), several per short batch's row, or a warp per short row. 8192 x 50257 bf16 with a
-// quarter masked, k = 64: 140 us, 66% of the copy peak on 624 MB; k = 8 unmasked 140 us, 87%. The stream alone keeps up with
+// quarter masked, k = 64: 142 us, 65% of the copy peak on 624 MB; k = 8 unmasked 143 us, 85%. The stream alone keeps up with
 // HBM; what a row does after it (threshold, segments read again, ranking) is a chain of latencies of 9 us, behind which eight
 // CTAs of an SM hide three quarters: with four of 256 threads 206 us. Loads run a step ahead of the sums (170 us without).
 template <class T, int THREADS, int CAP>
@@ -950,7 +950,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? kRowThreads : THREADS, THREADS
     }
 }
 
-// Rows of up to this many bytes, enough of them for every SM and short lists: a warp each. 8192 x 4000 bf16, k = 20: 28 us.
+// Rows of up to this many bytes, enough of them for every SM and short lists: a warp each. 8192 x 4000 bf16, k = 20: 30 us.
 constexpr int64_t kTopShort = 16384;
 constexpr int kTopShortMost = 64;
 
