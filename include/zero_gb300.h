@@ -814,10 +814,10 @@ int zero_top_logits(const zero_logits* x, int64_t k, int64_t* index, float* logp
  *   ZERO_DISTILL_JS        D = mix sum p (log p - log m) + (1 - mix) sum q (log q - log m),
  *                          m = mix p + (1 - mix) q                            (with ZERO_TAIL_REST only)
  * L_t = kl_coef D - ce_coef log q_target, loss = sum of w_t L_t with the weights of zero_policy_loss; a
- * coefficient of 0 leaves its term out, also an infinite one. 1 - sum p_i is off by 2^-38 absolutely. A p = 0 or q = 0 adds 0 where it is the
+ * coefficient of 0 leaves its term out, also an infinite one. A p = 0 or q = 0 adds 0 where it is the
  * factor; D is infinite where a p > 0 meets q = 0 (forward) or a q > 0 meets p_rest = 0 (reverse, whose
  * gradient is then not defined). The rest's sum is formed over the rest alone, to full precision where
- * it is small.
+ * it is small; 1 - sum p_i is off by 2^-38.
  * A token whose list names a place twice or one past the vocabulary, or whose target is past it, has
  * NaN results and a NaN gradient row. Reads and writes each row of logits once where it fits in shared
  * memory, else it reads it twice. */
